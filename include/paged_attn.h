@@ -57,7 +57,10 @@ enum pa_dtype {
   PA_BF16 = 1,      /* bfloat16                                  */
   PA_FP8_E4M3 = 2,  /* OCP fp8 e4m3fn codes (1 byte per element) */
   PA_F32 = 3,       /* float32                                   */
-  PA_I32 = 4        /* int32                                     */
+  PA_I32 = 4,       /* int32                                     */
+  PA_FP4_E2M1X2 = 5 /* two OCP fp4 e2m1 codes a byte, the even
+                       element in the low nibble (shapes and
+                       strides count bytes)                      */
 };
 
 /* Status codes. */
@@ -346,6 +349,109 @@ int paged_attn_mla_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t
                                   int32_t max_query_len, size_t* bytes);
 int paged_attn_mla_reserve(int32_t num_seqs, int32_t num_q_heads, int32_t kv_dtype, int32_t max_query_len);
 
+/*
+ * The 4-bit KV cache.  K and V each consist of
+ *   codes   PA_FP4_E2M1X2 [NB, 16, Hkv, D / 2]: two e2m1 codes a byte (sign, two
+ *           exponent bits of bias 1, one mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4,
+ *           6), the even feature in the low nibble;
+ *   scales  PA_FP8_E4M3 [NB, Hkv, 16, D / 16]: one e4m3fn code for 16 consecutive
+ *           features of a (slot, head) row;
+ *   k_scale (v_scale), one positive fp32 scale a tensor.
+ * A feature's value is e2m1 * e4m3 * k_scale; it takes 4.5 bits.
+ *
+ * paged_attn_cache_write_q4 - write new tokens' K and V rows, quantised.
+ *
+ *   key, value      bf16 [T, Hkv, D]; stride[2] == 1, other strides multiples of 8
+ *                   elements, data 16-byte aligned.  D a multiple of 16 up to 512,
+ *                   Hkv at most 4096, T at most 2^30, NB below 2^31.
+ *   slot_mapping    int32 [T] contiguous, as for paged_attn_cache_write.
+ *   k_cache, v_cache  codes (above): stride[3] == 1, other strides multiples of 8
+ *                   bytes, data 8-byte aligned.
+ *   k_group_scales, v_group_scales  scales (above), any positive strides.
+ *   For every group x of 16 features: amax = max |x|, S = e4m3fn(amax / (6 k_scale)),
+ *   codes e2m1(x / (S k_scale)).  The products 6 k_scale and S k_scale are rounded to
+ *   fp32, the quotients are IEEE fp32 divisions, both encodings round to nearest even
+ *   and saturate (448 and 6).  A code takes its feature's sign.  S = 0 stores codes 0;
+ *   a NaN in a group stores the e4m3fn NaN as S (the whole group reads back as NaN)
+ *   and codes 0; an infinity saturates S and its own code.
+ *
+ * paged_attn_cache_read_q4 - the rows at slot_mapping, dequantised: key[t], value[t]
+ * (bf16 [T, Hkv, D], written) = bf16(fp32(e2m1 * e4m3 * scale)).  A negative slot
+ * leaves its rows as they were.
+ *
+ * Errors, padding slots and out-of-range slots as for paged_attn_cache_write; k_scale
+ * and v_scale must be positive and finite.  Asynchronous; both allocate nothing.
+ */
+int paged_attn_cache_write_q4(const pa_tensor_t* key, const pa_tensor_t* value, const pa_tensor_t* slot_mapping,
+                              const pa_tensor_t* k_cache, const pa_tensor_t* v_cache,
+                              const pa_tensor_t* k_group_scales, const pa_tensor_t* v_group_scales, float k_scale,
+                              float v_scale, pa_stream_t stream);
+int paged_attn_cache_read_q4(const pa_tensor_t* slot_mapping, const pa_tensor_t* k_cache, const pa_tensor_t* v_cache,
+                             const pa_tensor_t* k_group_scales, const pa_tensor_t* v_group_scales, float k_scale,
+                             float v_scale, const pa_tensor_t* key, const pa_tensor_t* value, pa_stream_t stream);
+
+/*
+ * Operations on whole pages.  They work on any paged cache of this library.
+ *
+ *   caches          array of num_caches (at most 1024) tensors of 2 to 4 dimensions whose
+ *                   first is the page: K and V caches of every layer, scales, latent
+ *                   caches.  Any element type of pa_dtype; any positive strides that keep
+ *                   elements apart; a page holds at most 256 MiB a tensor.  All have the
+ *                   same number of pages NB (below 2^31 - 64).
+ *   block_tables    int32 [B, max_blocks], B at most 8192; rows contiguous and not
+ *                   overlapping.  Row i holds ceil(seq_lens[i] / 16) pages.
+ *   seq_lens        int32 [B] contiguous: the tokens whose pages a row holds (include pages
+ *                   reserved ahead by passing the reserved length); 0 = an empty row.
+ *   ref_counts      int32 [NB] contiguous: holders of each page (rows, and any the caller
+ *                   counts itself); a page is free while its count is not positive.
+ * Lists are contiguous int32 vectors; a negative entry is padding and does nothing.  All
+ * results are independent of the order in which the device runs.  The tensors of one call
+ * must not overlap one another.  Asynchronous; no workspace; allocate nothing.
+ *
+ * paged_attn_pages_copy - page src_pages[k] of every cache copied to page dst_pages[k].
+ *   An entry outside [0, NB) copies nothing and sets bit 0 of the device status word.  A
+ *   destination must be neither another entry's destination nor its source (else that
+ *   destination's contents are unspecified).
+ *
+ * paged_attn_pages_fork - entry k makes row children[k] a copy of row parents[k]: the
+ *   full pages are shared (their counts grow by 1), a partial last page is copied in every
+ *   cache to the free page new_pages[k] (count 1), which the child holds instead, and the
+ *   child's length becomes its parent's.  new_pages (in and out): an entry whose page was
+ *   not taken (length a multiple of 16, padding, or refused) is set to -1.  A parent may
+ *   have several children.  Refused, with bit 5 of the status word and no effect: rows out
+ *   of range, a child that is not empty or is itself a parent in the call, a child or a
+ *   taken page that an earlier entry names, a page that is not free or out of range when
+ *   one is needed, a parent whose length does not fit its row.  A page id out of range in a
+ *   parent's row is copied as it is and sets bit 0.
+ *
+ * paged_attn_pages_free - every row in `rows` gives its pages back (their counts shrink by
+ *   1) and becomes empty (its length 0; its table entries stay as they were); then
+ *   free_pages (int32 [NB], written) lists the pages whose count is not positive in
+ *   ascending order, followed by -1, and num_free (int32 [1], written) counts them.  A row
+ *   listed twice is freed once.  A row out of range, or a page whose count was not positive
+ *   (it stays as it was), sets bit 5; a page id out of range sets bit 0; a length past the
+ *   row's entries sets bit 1.
+ *
+ * paged_attn_pages_compact - the U pages in use move to ids 0 .. U - 1: the k-th page in
+ *   use with id >= U goes to the k-th free page with id < U, contents (in every cache) and
+ *   count; a page with id below U stays.  page_map (int32 [NB], written) gives every page's
+ *   new id, -1 for a page that was free; num_used (int32 [1], written) is U.  Every entry of
+ *   block_tables in [0, NB) that names a page in use is replaced by its new id (entries
+ *   past a row's length too); other entries stay.  A negative count is taken as free and
+ *   sets bit 5.
+ */
+int paged_attn_pages_copy(const pa_tensor_t* caches, int32_t num_caches, const pa_tensor_t* src_pages,
+                          const pa_tensor_t* dst_pages, pa_stream_t stream);
+int paged_attn_pages_fork(const pa_tensor_t* caches, int32_t num_caches, const pa_tensor_t* block_tables,
+                          const pa_tensor_t* seq_lens, const pa_tensor_t* ref_counts, const pa_tensor_t* parents,
+                          const pa_tensor_t* children, const pa_tensor_t* new_pages, pa_stream_t stream);
+int paged_attn_pages_free(const pa_tensor_t* block_tables, const pa_tensor_t* seq_lens,
+                          const pa_tensor_t* ref_counts, const pa_tensor_t* rows, const pa_tensor_t* free_pages,
+                          const pa_tensor_t* num_free, pa_stream_t stream);
+int paged_attn_pages_compact(const pa_tensor_t* caches, int32_t num_caches, const pa_tensor_t* block_tables,
+                             const pa_tensor_t* ref_counts, const pa_tensor_t* page_map,
+                             const pa_tensor_t* num_used, pa_stream_t stream);
+
 /* Plan for a shape on the current device (kv_dtype: PA_BF16 or PA_FP8_E4M3).
  * opts may be NULL.  Reads device attributes only; enqueues nothing. */
 int paged_attn_plan(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
@@ -370,7 +476,8 @@ int paged_attn_release(void);
 /* Read the device status word of the current device into *flags (bit 0: page id out of
  * range; bit 1: seq_len < query length; bit 2: query length outside [1, max_query_len]
  * or query_start_loc inconsistent; bit 3: a pipeline wait timed out; bit 4: a query value
- * overflowed the f16 range on the fp8 path, or an MLA partial output did).  clear != 0 resets it to 0.  Synchronises
+ * overflowed the f16 range on the fp8 path, or an MLA partial output did; bit 5: a page
+ * operation refused an entry).  clear != 0 resets it to 0.  Synchronises
  * the device: a debugging aid, not for the hot path. */
 int paged_attn_device_status(uint32_t* flags, int32_t clear);
 

@@ -15,10 +15,11 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpagedattn.so")
 
-PA_BF16, PA_FP8_E4M3, PA_F32, PA_I32 = 1, 2, 3, 4
+PA_BF16, PA_FP8_E4M3, PA_F32, PA_I32, PA_FP4_E2M1X2 = 1, 2, 3, 4, 5
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA = 0, 1, 2, 3, 4
 
 STATUS_PAGE_RANGE, STATUS_SEQ_LEN, STATUS_QUERY_LEN, STATUS_TIMEOUT, STATUS_F16_RANGE = 1, 2, 4, 8, 16
+STATUS_PAGE_OP = 32
 
 
 class PaTensor(ctypes.Structure):
@@ -67,6 +68,12 @@ _SIGNATURES = {
                                                         ctypes.c_float, ctypes.c_float, _P, _P, ctypes.c_void_p]),
     "paged_attn_cache_write": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_float, ctypes.c_float, ctypes.c_void_p]),
     "paged_attn_cache_write_per_token": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_void_p]),
+    "paged_attn_cache_write_q4": (ctypes.c_int, [_P] * 7 + [ctypes.c_float, ctypes.c_float, ctypes.c_void_p]),
+    "paged_attn_cache_read_q4": (ctypes.c_int, [_P] * 5 + [ctypes.c_float, ctypes.c_float, _P, _P, ctypes.c_void_p]),
+    "paged_attn_pages_copy": (ctypes.c_int, [_P, ctypes.c_int32, _P, _P, ctypes.c_void_p]),
+    "paged_attn_pages_fork": (ctypes.c_int, [_P, ctypes.c_int32] + [_P] * 6 + [ctypes.c_void_p]),
+    "paged_attn_pages_free": (ctypes.c_int, [_P] * 6 + [ctypes.c_void_p]),
+    "paged_attn_pages_compact": (ctypes.c_int, [_P, ctypes.c_int32] + [_P] * 4 + [ctypes.c_void_p]),
     "paged_attn_mla_decode": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_int32, ctypes.c_float, ctypes.c_float, _P,
                                              _P, ctypes.c_void_p]),
     "paged_attn_mla_decode_ex": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_int32, ctypes.c_float, ctypes.c_float,
@@ -118,29 +125,42 @@ def _dtype_code(t: torch.Tensor) -> int:
     return 0          # not a pa_dtype: the library rejects it with PA_ERR_INVALID_ARG
 
 
+_FLOAT4 = getattr(torch, "float4_e2m1fn_x2", None)
+
+
+def _fp4_code(t: torch.Tensor) -> int:
+    """Packed e2m1 codes: uint8 or torch's packed float4 type."""
+    return PA_FP4_E2M1X2 if t.dtype == torch.uint8 or (_FLOAT4 is not None and t.dtype == _FLOAT4) else 0
+
+
+def _bytes_code(t: torch.Tensor) -> int:
+    """A type of the tensor's element size, for calls that only move bytes."""
+    return {1: PA_FP8_E4M3, 2: PA_BF16, 4: PA_F32}.get(t.element_size(), 0)
+
+
 _DESC_CACHE = {}
 _DESC_CACHE_MAX = 1024
 
 
-def tensor_desc(t: Optional[torch.Tensor]) -> PaTensor:
-    """The pa_tensor_t of a tensor.  Descriptors hold only (pointer, dtype,
+def tensor_desc(t: Optional[torch.Tensor], code=_dtype_code) -> PaTensor:
+    """The pa_tensor_t of a tensor (`code` gives its pa_dtype).  Descriptors hold only (pointer, dtype,
     shape, strides), so one built for a key serves every later tensor with the
     same key: they are cached (a per-call decode then costs a few dictionary
     lookups instead of ctypes field assignments).  Treat the result as
     read-only."""
     if t is None:
         return _new_desc(None)
-    key = (t.data_ptr(), t.dtype, t.shape, t.stride())
+    key = (t.data_ptr(), t.dtype, t.shape, t.stride(), code)
     d = _DESC_CACHE.get(key)
     if d is None:
-        d = _new_desc(t)
+        d = _new_desc(t, code)
         if len(_DESC_CACHE) >= _DESC_CACHE_MAX:
             _DESC_CACHE.clear()
         _DESC_CACHE[key] = d
     return d
 
 
-def _new_desc(t: Optional[torch.Tensor]) -> PaTensor:
+def _new_desc(t: Optional[torch.Tensor], code=_dtype_code) -> PaTensor:
     d = PaTensor()
     if t is None:
         d.data = None
@@ -148,7 +168,7 @@ def _new_desc(t: Optional[torch.Tensor]) -> PaTensor:
     if t.dim() > 4:
         raise ValueError("at most 4 dimensions")
     d.data = t.data_ptr() if t.numel() > 0 else None
-    d.dtype = _dtype_code(t)
+    d.dtype = code(t)
     d.ndim = t.dim()
     for i in range(t.dim()):
         d.shape[i] = t.shape[i]
@@ -288,6 +308,114 @@ def paged_attn_cache_write_per_token(key, value, slot_mapping, k_cache, v_cache,
     lib = load()
     d = [tensor_desc(t) for t in (key, value, slot_mapping, k_cache, v_cache, k_token_scales, v_token_scales)]
     _check(lib, lib.paged_attn_cache_write_per_token(*[ctypes.byref(x) for x in d], _stream_handle(stream)))
+
+
+def _on_current_device(*tensors):
+    """The calls below take device pointers of the current CUDA device: a tensor
+    elsewhere is refused here (the library cannot see where a pointer lives)."""
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"a CUDA tensor is required, got one on {t.device}")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def paged_attn_cache_write_q4(key, value, slot_mapping, k_cache, v_cache, k_group_scales, v_group_scales,
+                              k_scale=1.0, v_scale=1.0, stream=None):
+    """Write new tokens' K/V rows into a 4-bit cache (see include/paged_attn.h).
+    key/value bf16 [T, Hkv, D]; slot_mapping int32 [T]; caches uint8 (or torch's
+    packed float4) [NB, 16, Hkv, D / 2]; group scales uint8 or float8_e4m3fn
+    [NB, Hkv, 16, D / 16]; caches and scales updated in place."""
+    lib = load()
+    _on_current_device(key, value, slot_mapping, k_cache, v_cache, k_group_scales, v_group_scales)
+    d = [tensor_desc(key), tensor_desc(value), tensor_desc(slot_mapping), tensor_desc(k_cache, _fp4_code),
+         tensor_desc(v_cache, _fp4_code), tensor_desc(k_group_scales), tensor_desc(v_group_scales)]
+    _check(lib, lib.paged_attn_cache_write_q4(*[ctypes.byref(x) for x in d], float(k_scale), float(v_scale),
+                                              _stream_handle(stream)))
+
+
+def paged_attn_cache_read_q4(slot_mapping, k_cache, v_cache, k_group_scales, v_group_scales, key=None, value=None,
+                             k_scale=1.0, v_scale=1.0, stream=None):
+    """Rows of a 4-bit cache, dequantised (see include/paged_attn.h): returns
+    (key, value) bf16 [T, Hkv, D].  Rows of negative slots stay as they were in
+    the key / value given (zeros without)."""
+    lib = load()
+    _on_current_device(slot_mapping, k_cache, v_cache, k_group_scales, v_group_scales, key, value)
+    shape = (slot_mapping.shape[0], k_cache.shape[2], k_cache.shape[3] * 2)
+    if key is None:
+        key = torch.zeros(shape, dtype=torch.bfloat16, device=k_cache.device)
+    if value is None:
+        value = torch.zeros(shape, dtype=torch.bfloat16, device=k_cache.device)
+    d = [tensor_desc(slot_mapping), tensor_desc(k_cache, _fp4_code), tensor_desc(v_cache, _fp4_code),
+         tensor_desc(k_group_scales), tensor_desc(v_group_scales)]
+    _check(lib, lib.paged_attn_cache_read_q4(*[ctypes.byref(x) for x in d], float(k_scale), float(v_scale),
+                                             ctypes.byref(tensor_desc(key)), ctypes.byref(tensor_desc(value)),
+                                             _stream_handle(stream)))
+    return key, value
+
+
+def _cache_array(caches):
+    """The pa_tensor_t array of page tensors (only their element size matters)."""
+    caches = [caches] if isinstance(caches, torch.Tensor) else list(caches)
+    _on_current_device(*caches)
+    return (PaTensor * max(1, len(caches)))(*[tensor_desc(c, _bytes_code) for c in caches]), len(caches)
+
+
+def paged_attn_pages_copy(caches, src_pages, dst_pages, stream=None):
+    """Copy page src_pages[k] to page dst_pages[k] in every cache of the list
+    (see include/paged_attn.h).  caches: tensors whose first dimension is the
+    page; src_pages / dst_pages int32 [n], negative entries are padding."""
+    lib = load()
+    arr, n = _cache_array(caches)
+    _on_current_device(src_pages, dst_pages)
+    _check(lib, lib.paged_attn_pages_copy(arr, n, ctypes.byref(tensor_desc(src_pages)),
+                                          ctypes.byref(tensor_desc(dst_pages)), _stream_handle(stream)))
+
+
+def paged_attn_pages_fork(caches, block_tables, seq_lens, ref_counts, parents, children, new_pages, stream=None):
+    """Fork table rows: children[k] shares the full pages of parents[k] and gets
+    a copy of its partial last page in new_pages[k] (see include/paged_attn.h).
+    block_tables, seq_lens, ref_counts and new_pages are updated in place."""
+    lib = load()
+    arr, n = _cache_array(caches)
+    ints = (block_tables, seq_lens, ref_counts, parents, children, new_pages)
+    _on_current_device(*ints)
+    _check(lib, lib.paged_attn_pages_fork(arr, n, *[ctypes.byref(tensor_desc(t)) for t in ints],
+                                          _stream_handle(stream)))
+
+
+def paged_attn_pages_free(block_tables, seq_lens, ref_counts, rows, free_pages=None, num_free=None, stream=None):
+    """Give the pages of table rows back and list the pool's free pages (see
+    include/paged_attn.h).  seq_lens and ref_counts are updated in place;
+    returns (free_pages int32 [NB], num_free int32 [1])."""
+    lib = load()
+    if free_pages is None:
+        free_pages = torch.empty_like(ref_counts)
+    if num_free is None:
+        num_free = torch.empty(1, dtype=torch.int32, device=ref_counts.device)
+    ints = (block_tables, seq_lens, ref_counts, rows, free_pages, num_free)
+    _on_current_device(*ints)
+    _check(lib, lib.paged_attn_pages_free(*[ctypes.byref(tensor_desc(t)) for t in ints], _stream_handle(stream)))
+    return free_pages, num_free
+
+
+def paged_attn_pages_compact(caches, block_tables, ref_counts, page_map=None, num_used=None, stream=None):
+    """Move the pages in use to the lowest ids, contents, counts and table
+    entries (see include/paged_attn.h).  block_tables, ref_counts and the caches
+    are updated in place; returns (page_map int32 [NB], num_used int32 [1])."""
+    lib = load()
+    arr, n = _cache_array(caches)
+    if page_map is None:
+        page_map = torch.empty_like(ref_counts)
+    if num_used is None:
+        num_used = torch.empty(1, dtype=torch.int32, device=ref_counts.device)
+    ints = (block_tables, ref_counts, page_map, num_used)
+    _on_current_device(*ints)
+    _check(lib, lib.paged_attn_pages_compact(arr, n, *[ctypes.byref(tensor_desc(t)) for t in ints],
+                                             _stream_handle(stream)))
+    return page_map, num_used
 
 
 def paged_attn_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, kv_dtype=PA_BF16, max_query_len=1,

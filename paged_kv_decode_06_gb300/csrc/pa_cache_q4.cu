@@ -1,0 +1,273 @@
+// Rows of the 4-bit paged cache: write (quantise) and read back (dequantise).
+//
+// Write, for every token t with slot s >= 0, KV head h and group of 16
+// consecutive features x of its key (or value) row, with ts the tensor's scale:
+//     S     = e4m3fn(amax / (6 ts)),  amax = max |x|        (6 = the largest e2m1)
+//     code  = e2m1(x / (S ts))
+// Products are rounded to fp32, quotients are IEEE fp32 quotients, both
+// encodings round to nearest even and saturate.  S = 0 (or a group that holds
+// a NaN, whose S is the e4m3fn NaN) stores codes 0.  Read is the inverse:
+// code * S (exact) times ts rounded to fp32, then to bf16.
+//
+// Both are bound by memory: 4 bytes of bf16 a (key, value) feature pair against
+// 9/8 bytes of codes and scales.
+#include "pa_device.cuh"
+#include "pa_host.h"
+#include "pa_q4.cuh"
+#include "pa_quant.cuh"
+
+#include <algorithm>
+#include <cmath>
+
+namespace pa {
+
+struct RowsQ4Params {
+  uint16_t* rows[2];           // key, value: bf16 [T, Hkv, D]
+  int64_t row_t[2], row_h[2];  // their token and head strides (elements)
+  const int32_t* slots;
+  uint8_t* codes[2];           // K, V codes [NB, 16, Hkv, D / 2]
+  int64_t code_page[2], code_slot[2], code_head[2];
+  uint8_t* scales[2];          // K, V group scales [NB, Hkv, 16, D / 16]
+  int64_t sc_page[2], sc_head[2], sc_slot[2], sc_group[2];
+  int32_t num_tokens, num_kv_heads, groups, num_pages;
+  float ts[2];                 // tensor scales
+  float six_ts[2];             // fp32(6 ts)
+  uint32_t* err;
+};
+
+struct GroupIndex {
+  int64_t t;
+  int h, g;
+};
+
+// Index of a (token, head, group) triple, groups innermost.
+__device__ __forceinline__ GroupIndex group_index(const RowsQ4Params& p, int64_t i, bool narrow) {
+  GroupIndex x;
+  const int64_t per = static_cast<int64_t>(p.num_kv_heads) * p.groups;
+  x.t = cw_div(i, per, narrow);
+  const int r = static_cast<int>(i - x.t * per);
+  x.h = r / p.groups;
+  x.g = r - x.h * p.groups;
+  return x;
+}
+
+// One thread quantises one group of one tensor (blockIdx.y: 0 = K, 1 = V).
+__global__ void __launch_bounds__(256) pa_cache_write_q4_kernel(const RowsQ4Params p) {
+  const int y = blockIdx.y;
+  const int64_t total = static_cast<int64_t>(p.num_tokens) * p.num_kv_heads * p.groups;
+  const bool narrow = total <= 0xFFFFFFFFll;
+  const int64_t num_slots = static_cast<int64_t>(p.num_pages) * kPage;
+  const float ts = p.ts[y], six = p.six_ts[y];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
+    const GroupIndex x = group_index(p, i, narrow);
+    const int slot = p.slots[x.t];
+    const uint4* src =
+        reinterpret_cast<const uint4*>(p.rows[y] + x.t * p.row_t[y] + x.h * p.row_h[y] + x.g * kQ4Group);
+    const uint4 a = src[0], b = src[1];
+    if (slot < 0) continue;                        // padding token
+    if (slot >= num_slots) {
+      if (x.h == 0 && x.g == 0) atomicOr(p.err, kErrPageRange);
+      continue;
+    }
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t m2 = 0u;                              // magnitudes of bf16 order as their bits
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m2 = max_u16x2(m2, w[e] & 0x7FFF7FFFu);
+    const float amax = __uint_as_float(max(m2 << 16, m2 & 0xFFFF0000u));
+    const uint32_t s8 = e4m3x2_from_f32(__fdiv_rn(amax, six), 0.f) & 0xFFu;
+    const float d = __fmul_rn(f16_lo(e4m3x2_to_f16x2(s8)), ts);
+    uint2 codes = make_uint2(0u, 0u);
+    if (d > 0.f) {                                 // not 0, not NaN
+      const ScaleDiv sd = scale_div(d);
+      float q[16];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (sd.fast) {
+          div_by2(sd, bf16_lo(w[e]), bf16_hi(w[e]), q[2 * e], q[2 * e + 1]);
+        } else {
+          q[2 * e] = __fdiv_rn(bf16_lo(w[e]), d);
+          q[2 * e + 1] = __fdiv_rn(bf16_hi(w[e]), d);
+        }
+      }
+      const float lo[8] = {q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7]};
+      const float hi[8] = {q[8], q[9], q[10], q[11], q[12], q[13], q[14], q[15]};
+      codes = make_uint2(e2m1x8_from_f32(lo), e2m1x8_from_f32(hi));
+    }
+    const int64_t page = slot / kPage, off = slot % kPage;
+    *reinterpret_cast<uint2*>(p.codes[y] + page * p.code_page[y] + off * p.code_slot[y] + x.h * p.code_head[y] +
+                              x.g * (kQ4Group / 2)) = codes;
+    p.scales[y][page * p.sc_page[y] + x.h * p.sc_head[y] + off * p.sc_slot[y] + x.g * p.sc_group[y]] =
+        static_cast<uint8_t>(s8);
+  }
+}
+
+// One thread reads one group of one tensor back.
+__global__ void __launch_bounds__(256) pa_cache_read_q4_kernel(const RowsQ4Params p) {
+  const int y = blockIdx.y;
+  const int64_t total = static_cast<int64_t>(p.num_tokens) * p.num_kv_heads * p.groups;
+  const bool narrow = total <= 0xFFFFFFFFll;
+  const int64_t num_slots = static_cast<int64_t>(p.num_pages) * kPage;
+  const float ts = p.ts[y];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
+    const GroupIndex x = group_index(p, i, narrow);
+    const int slot = p.slots[x.t];
+    if (slot < 0) continue;                        // padding token: its row stays as it was
+    if (slot >= num_slots) {
+      if (x.h == 0 && x.g == 0) atomicOr(p.err, kErrPageRange);
+      continue;
+    }
+    const int64_t page = slot / kPage, off = slot % kPage;
+    const uint2 codes = *reinterpret_cast<const uint2*>(p.codes[y] + page * p.code_page[y] + off * p.code_slot[y] +
+                                                        x.h * p.code_head[y] + x.g * (kQ4Group / 2));
+    const uint32_t s8 =
+        p.scales[y][page * p.sc_page[y] + x.h * p.sc_head[y] + off * p.sc_slot[y] + x.g * p.sc_group[y]];
+    const uint32_t s2 = e4m3x2_to_f16x2(s8 * 0x0101u);
+    uint32_t h[8], o[8];
+    {
+      uint32_t lo[4], hi[4];
+      e2m1x8_to_f16(codes.x, lo);
+      e2m1x8_to_f16(codes.y, hi);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        h[e] = lo[e];
+        h[4 + e] = hi[e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t v = hmul2(h[e], s2);
+      o[e] = pack_bf16(__fmul_rn(f16_lo(v), ts), __fmul_rn(f16_hi(v), ts));
+    }
+    uint4* dst = reinterpret_cast<uint4*>(p.rows[y] + x.t * p.row_t[y] + x.h * p.row_h[y] + x.g * kQ4Group);
+    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+namespace {
+
+// Codes [NB, 16, Hkv, D / 2] and group scales [NB, Hkv, 16, D / 16] of K and V.
+int check_q4_cache(const pa_tensor_t* const* code, const pa_tensor_t* const* scale, int64_t Hkv, int64_t D,
+                   bool written) {
+  const char* cn[2] = {"k_cache", "v_cache"};
+  const char* sn[2] = {"k_group_scales", "v_group_scales"};
+  for (int y = 0; y < 2; ++y) {
+    int st;
+    if ((st = host_check_tensor(code[y], cn[y], 4, false)) != PA_OK) return st;
+    if ((st = host_check_tensor(scale[y], sn[y], 4, false)) != PA_OK) return st;
+    if (code[y]->dtype != PA_FP4_E2M1X2) return host_fail(PA_ERR_INVALID_ARG, "%s must hold packed e2m1 codes", cn[y]);
+    if (scale[y]->dtype != PA_FP8_E4M3) return host_fail(PA_ERR_INVALID_ARG, "%s must be fp8 e4m3", sn[y]);
+    if (code[y]->shape[1] != kPage) return host_fail(PA_ERR_UNSUPPORTED, "page size must be 16");
+    if (code[y]->shape[0] != code[0]->shape[0] || code[y]->shape[2] != Hkv || code[y]->shape[3] * 2 != D)
+      return host_fail(PA_ERR_INVALID_ARG, "%s must be [NB, 16, Hkv, D / 2] with D = %lld, Hkv = %lld", cn[y],
+                       static_cast<long long>(D), static_cast<long long>(Hkv));
+    if (scale[y]->shape[0] != code[0]->shape[0] || scale[y]->shape[1] != Hkv || scale[y]->shape[2] != kPage ||
+        scale[y]->shape[3] * kQ4Group != D)
+      return host_fail(PA_ERR_INVALID_ARG, "%s must be [NB, Hkv, 16, D / 16]", sn[y]);
+    if (code[y]->stride[3] != 1) return host_fail(PA_ERR_INVALID_ARG, "%s last dim must be contiguous", cn[y]);
+    for (int d = 0; d < 3; ++d)
+      if (code[y]->stride[d] % 8 != 0)
+        return host_fail(PA_ERR_INVALID_ARG, "%s strides must be multiples of 8 bytes", cn[y]);
+    if (!host_aligned(code[y]->data, 8)) return host_fail(PA_ERR_INVALID_ARG, "%s must be 8-byte aligned", cn[y]);
+    if (written)
+      for (int d = 0; d < 4; ++d)
+        if ((code[y]->stride[d] == 0 && code[y]->shape[d] > 1) || (scale[y]->stride[d] == 0 && scale[y]->shape[d] > 1))
+          return host_fail(PA_ERR_INVALID_ARG, "%s and %s are written: their strides must not be 0", cn[y], sn[y]);
+  }
+  return PA_OK;
+}
+
+int rows_q4(bool write, const pa_tensor_t* key, const pa_tensor_t* value, const pa_tensor_t* slots,
+            const pa_tensor_t* kc, const pa_tensor_t* vc, const pa_tensor_t* ks, const pa_tensor_t* vs, float k_scale,
+            float v_scale, cudaStream_t stream) {
+  int st;
+  const bool none = key != nullptr && key->ndim == 3 && key->shape[0] == 0;   // no tokens: empty tensors have no memory
+  if ((st = host_check_tensor(key, "key", 3, none)) || (st = host_check_tensor(value, "value", 3, none)) ||
+      (st = host_check_tensor(slots, "slot_mapping", 1, none)))
+    return st;
+  if (key->dtype != PA_BF16 || value->dtype != PA_BF16)
+    return host_fail(PA_ERR_INVALID_ARG, "key and value must be bf16");
+  if (slots->dtype != PA_I32) return host_fail(PA_ERR_INVALID_ARG, "slot_mapping must be int32");
+  const int64_t T = key->shape[0], Hkv = key->shape[1], D = key->shape[2];
+  for (int d = 0; d < 3; ++d)
+    if (value->shape[d] != key->shape[d]) return host_fail(PA_ERR_INVALID_ARG, "value shape differs from key");
+  if (slots->shape[0] != T) return host_fail(PA_ERR_INVALID_ARG, "slot_mapping needs one entry per token");
+  if (T > 1 && slots->stride[0] != 1) return host_fail(PA_ERR_INVALID_ARG, "slot_mapping must be contiguous");
+  if (D < 16 || D % kQ4Group != 0 || D > 512)
+    return host_fail(PA_ERR_UNSUPPORTED, "head_dim must be a multiple of 16 up to 512");
+  if (Hkv < 1) return host_fail(PA_ERR_INVALID_ARG, "num_kv_heads %lld < 1", static_cast<long long>(Hkv));
+  const pa_tensor_t *code[2] = {kc, vc}, *scale[2] = {ks, vs}, *rows[2] = {key, value};
+  if ((st = check_q4_cache(code, scale, Hkv, D, write)) != PA_OK) return st;
+  if (T > (int64_t(1) << 30) || Hkv > 4096 || kc->shape[0] > (int64_t(1) << 31) - 1)
+    return host_fail(PA_ERR_UNSUPPORTED, "tensor extents too large");
+  for (const pa_tensor_t* t : rows) {
+    if (t->stride[2] != 1 || t->stride[1] % 8 != 0 || t->stride[0] % 8 != 0 || !host_aligned(t->data, 16))
+      return host_fail(PA_ERR_INVALID_ARG,
+                       "key/value rows must be contiguous and 16-byte aligned (strides multiple of 8)");
+    if (!write && ((t->stride[0] == 0 && T > 1) || (t->stride[1] == 0 && Hkv > 1)))
+      return host_fail(PA_ERR_INVALID_ARG, "key and value are written: their strides must not be 0");
+  }
+  if (!std::isfinite(k_scale) || !std::isfinite(v_scale) || !(k_scale > 0.f) || !(v_scale > 0.f))
+    return host_fail(PA_ERR_INVALID_ARG, "k_scale and v_scale must be finite and positive");
+  if (T == 0) return PA_OK;
+  auto lock = host_lock();
+  HostDevice dev;
+  if ((st = host_device(&dev)) != PA_OK) return st;
+  RowsQ4Params p = {};
+  for (int y = 0; y < 2; ++y) {
+    p.rows[y] = static_cast<uint16_t*>(rows[y]->data);
+    p.row_t[y] = rows[y]->stride[0];
+    p.row_h[y] = rows[y]->stride[1];
+    p.codes[y] = static_cast<uint8_t*>(code[y]->data);
+    p.code_page[y] = code[y]->stride[0];
+    p.code_slot[y] = code[y]->stride[1];
+    p.code_head[y] = code[y]->stride[2];
+    p.scales[y] = static_cast<uint8_t*>(scale[y]->data);
+    p.sc_page[y] = scale[y]->stride[0];
+    p.sc_head[y] = scale[y]->stride[1];
+    p.sc_slot[y] = scale[y]->stride[2];
+    p.sc_group[y] = scale[y]->stride[3];
+    p.ts[y] = y ? v_scale : k_scale;
+    p.six_ts[y] = 6.f * p.ts[y];
+  }
+  p.slots = static_cast<const int32_t*>(slots->data);
+  p.num_tokens = static_cast<int32_t>(T);
+  p.num_kv_heads = static_cast<int32_t>(Hkv);
+  p.groups = static_cast<int32_t>(D / kQ4Group);
+  p.num_pages = static_cast<int32_t>(kc->shape[0]);
+  p.err = dev.status;
+  const int64_t blocks = (T * Hkv * p.groups + 255) / 256;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, int64_t(dev.num_sms) * 4)), 2, 1);
+  if (write)
+    pa_cache_write_q4_kernel<<<grid, 256, 0, stream>>>(p);
+  else
+    pa_cache_read_q4_kernel<<<grid, 256, 0, stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? PA_OK : host_cuda_fail(e, write ? "4-bit cache write launch" : "4-bit cache read launch");
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" int paged_attn_cache_write_q4(const pa_tensor_t* key, const pa_tensor_t* value,
+                                         const pa_tensor_t* slot_mapping, const pa_tensor_t* k_cache,
+                                         const pa_tensor_t* v_cache, const pa_tensor_t* k_group_scales,
+                                         const pa_tensor_t* v_group_scales, float k_scale, float v_scale,
+                                         pa_stream_t stream) {
+  return pa::host_entry([&] {
+    return pa::rows_q4(true, key, value, slot_mapping, k_cache, v_cache, k_group_scales, v_group_scales, k_scale,
+                       v_scale, reinterpret_cast<cudaStream_t>(stream));
+  });
+}
+
+extern "C" int paged_attn_cache_read_q4(const pa_tensor_t* slot_mapping, const pa_tensor_t* k_cache,
+                                        const pa_tensor_t* v_cache, const pa_tensor_t* k_group_scales,
+                                        const pa_tensor_t* v_group_scales, float k_scale, float v_scale,
+                                        const pa_tensor_t* key, const pa_tensor_t* value, pa_stream_t stream) {
+  return pa::host_entry([&] {
+    return pa::rows_q4(false, key, value, slot_mapping, k_cache, v_cache, k_group_scales, v_group_scales, k_scale,
+                       v_scale, reinterpret_cast<cudaStream_t>(stream));
+  });
+}

@@ -16,6 +16,7 @@
 #include <string>
 
 #include "paged_attn.h"
+#include "pa_host.h"
 #include "pa_kernels.h"
 
 namespace {
@@ -997,6 +998,46 @@ namespace pa {
 // Lets other translation units of the library report a detailed message
 // through paged_attn_last_error_message().
 void set_last_error_message(const std::string& msg) { t_last_error = msg; }
+
+// ---- helpers of the other translation units' entry points (pa_host.h)
+int host_fail(int status, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return fail(status, "%s", buf);
+}
+int host_cuda_fail(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+void host_clear_error() { t_last_error.clear(); }
+int host_check_tensor(const pa_tensor_t* t, const char* name, int ndim, bool allow_null) {
+  return check_tensor(t, name, ndim, allow_null);
+}
+bool host_aligned(const void* ptr, size_t a) { return aligned(ptr, a); }
+std::unique_lock<std::mutex> host_lock() { return std::unique_lock<std::mutex>(g_mu); }
+int host_device(HostDevice* out) {
+  DeviceState* ds = nullptr;
+  const int st = device_state(&ds, nullptr);
+  if (st != PA_OK) return st;
+  out->num_sms = ds->num_sms;
+  out->smem_optin = ds->smem_optin;
+  out->status = ds->status;
+  return PA_OK;
+}
+int host_workspace(const pa_options_t* opts, size_t bytes, cudaStream_t stream, const char* reserve_fn, void** ws) {
+  DeviceState* ds = nullptr;
+  const int st = device_state(&ds, nullptr);
+  return st != PA_OK ? st : acquire_workspace(ds, opts, bytes, stream, reserve_fn, ws);
+}
+int host_reserve(size_t bytes) {
+  DeviceState* ds = nullptr;
+  const int st = device_state(&ds, nullptr);
+  return st != PA_OK ? st : grow_workspace(ds, bytes);
+}
+CUresult host_encode_tiled(CUtensorMap* map, CUtensorMapDataType dtype, int rank, void* ptr, const cuuint64_t* dims,
+                           const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+  return encode_tiled(map, dtype, rank, ptr, dims, strides, box, swizzle);
+}
 }  // namespace pa
 
 extern "C" {

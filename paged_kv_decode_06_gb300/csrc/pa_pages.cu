@@ -1,0 +1,741 @@
+// Operations on whole pages of the paged caches: copy, fork, free, compact.
+//
+// A pool of NB pages is described by ref_counts [NB]: a page is in use while
+// its count is positive.  Block-table rows hold page ids; the page operations
+// move page contents in every tensor whose first dimension is the page (any
+// element type, any layout of the other dimensions), counts and table entries.
+//
+// Copies are bound by memory (twice the page bytes).  The bookkeeping of fork,
+// free and compact is a few passes over small integer arrays in which every
+// step needs the one before (claims before updates, counts before ranks); it
+// runs in one cluster of eight blocks, whose hardware barrier and shared
+// counts take the place of separate launches.
+#include <cooperative_groups.h>
+
+#include "pa_device.cuh"
+#include "pa_host.h"
+
+#include <algorithm>
+
+namespace cg = cooperative_groups;
+
+namespace pa {
+
+constexpr int kMaxPageTensors = 48;      // tensors of one copy launch (kernel parameters of 4 KB)
+constexpr int kMaxCaches = 1024;         // tensors of one call
+constexpr int kItemBytes = 4096;         // one warp's share of a page of one tensor: 8 x 16 bytes a lane
+constexpr int kClusterCtas = 8;
+constexpr int kClusterThreads = 1024;
+constexpr uint32_t kErrPageOp = 32u;
+
+// One tensor's pages: `n2 x n1` runs of `run` contiguous bytes.
+struct PageTensor {
+  uint8_t* base;
+  int64_t page_stride, s1, s2;   // bytes
+  int32_t run, n1, n2;
+  int32_t vec;                   // bytes a lane moves at once (16, 8, 4, 2 or 1)
+  int32_t item0;                 // first item of this tensor within a page's items
+  int32_t pad;
+};
+
+enum PairSource { kPairsListed, kPairsFork, kPairsCompact };
+
+struct CopyParams {
+  PageTensor t[kMaxPageTensors];
+  int32_t num_tensors, items;    // items of one page
+  int64_t pairs;                 // copies to look at
+  int32_t num_pages;
+  const int32_t *src, *dst;      // listed pairs; fork: dst = the new pages; compact: dst = the page map
+  const int32_t *parents, *seq_lens, *tables;   // fork
+  int64_t table_stride;
+  const int32_t* num_used;       // compact
+  uint32_t* err;
+};
+
+// Source and destination page of copy k; false: nothing to do.
+template <PairSource SRC>
+__device__ __forceinline__ bool pair_of(const CopyParams& p, int64_t k, int64_t base, int& src, int& dst, bool report) {
+  if constexpr (SRC == kPairsListed) {
+    src = p.src[k];
+    dst = p.dst[k];
+    if (src < 0 || dst < 0) return false;                  // padding
+    if (src >= p.num_pages || dst >= p.num_pages) {
+      if (report) atomicOr(p.err, kErrPageRange);
+      return false;
+    }
+  } else if constexpr (SRC == kPairsFork) {
+    dst = __ldcg(p.dst + k);                               // -1 where the fork took no page
+    if (dst < 0) return false;
+    const int row = p.parents[k];
+    src = p.tables[static_cast<int64_t>(row) * p.table_stride + p.seq_lens[row] / kPage];
+    if (src < 0 || src >= p.num_pages) return false;       // reported by the fork kernel
+  } else {
+    src = static_cast<int>(base + k);
+    dst = __ldcg(p.dst + src);
+    if (dst < 0) return false;
+  }
+  return src != dst;
+}
+
+// Byte `x` of a page of several runs: its offset from the page's start.
+__device__ __forceinline__ int64_t run_offset(const PageTensor& t, int x) {
+  const int i = x / t.run;
+  const int i2 = i / t.n1;
+  return i2 * t.s2 + (i - i2 * t.n1) * t.s1 + (x - i * t.run);
+}
+
+// `bytes` (at most kItemBytes) starting at byte `off` of a page, one warp:
+// U loads of a lane are issued before any is stored.
+template <typename V>
+__device__ __forceinline__ void copy_item(const PageTensor& t, int64_t src, int64_t dst, int off, int bytes, int lane) {
+  constexpr int W = static_cast<int>(sizeof(V));
+  const uint8_t* a = t.base + src * t.page_stride;
+  uint8_t* b = t.base + dst * t.page_stride;
+  if (t.n1 == 1 && t.n2 == 1) {
+    constexpr int U = 8;
+    for (int o = lane * W; o < bytes; o += U * 32 * W) {
+      V v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (o + u * 32 * W < bytes) v[u] = *reinterpret_cast<const V*>(a + off + o + u * 32 * W);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (o + u * 32 * W < bytes) *reinterpret_cast<V*>(b + off + o + u * 32 * W) = v[u];
+    }
+  } else {
+    constexpr int U = 4;
+    for (int o = lane * W; o < bytes; o += U * 32 * W) {
+      V v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (o + u * 32 * W < bytes) v[u] = *reinterpret_cast<const V*>(a + run_offset(t, off + o + u * 32 * W));
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (o + u * 32 * W < bytes) *reinterpret_cast<V*>(b + run_offset(t, off + o + u * 32 * W)) = v[u];
+    }
+  }
+}
+
+// A warp takes one item (at most 4 KB of one tensor of one page) at a time.
+template <PairSource SRC>
+__global__ void __launch_bounds__(256, 4) pa_page_copy_kernel(const __grid_constant__ CopyParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x / 32);
+  int64_t base = 0, n = p.pairs;
+  if constexpr (SRC == kPairsCompact) {
+    base = __ldcg(p.num_used);           // pages that move have ids from here on
+    n = p.num_pages - base;
+  }
+  const int64_t total = n * p.items;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32; i < total; i += warps) {
+    const int64_t k = i / p.items;
+    const int item = static_cast<int>(i - k * p.items);
+    int src, dst;
+    if (!pair_of<SRC>(p, k, base, src, dst, item == 0 && lane == 0)) continue;
+    int lo = 0, hi = p.num_tensors - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.t[mid].item0 <= item) lo = mid; else hi = mid - 1;
+    }
+    const PageTensor& t = p.t[lo];
+    const int off = (item - t.item0) * kItemBytes;
+    const int bytes = min(kItemBytes, t.run * t.n1 * t.n2 - off);
+    switch (t.vec) {
+      case 16: copy_item<uint4>(t, src, dst, off, bytes, lane); break;
+      case 8: copy_item<uint2>(t, src, dst, off, bytes, lane); break;
+      case 4: copy_item<uint32_t>(t, src, dst, off, bytes, lane); break;
+      case 2: copy_item<uint16_t>(t, src, dst, off, bytes, lane); break;
+      default: copy_item<uint8_t>(t, src, dst, off, bytes, lane); break;
+    }
+  }
+}
+
+// Table entries after a compaction: every entry that names a page in use.
+__global__ void __launch_bounds__(256) pa_table_remap_kernel(int32_t* tables, int64_t stride, int64_t rows,
+                                                             int64_t cols, const int32_t* map, int32_t num_pages) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t total = rows * cols, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
+    const int64_t r = i / cols;
+    int32_t* e = tables + r * stride + (i - r * cols);
+    const int32_t id = *e;
+    if (id < 0 || id >= num_pages) continue;
+    const int32_t to = __ldcg(map + id);
+    if (to >= 0 && to != id) *e = to;
+  }
+}
+
+// ------------------------------------------------------------ bookkeeping
+struct PoolParams {
+  int32_t* tables;
+  int64_t table_stride;
+  int32_t rows, cols;
+  int32_t* seq_lens;
+  int32_t* ref;
+  int32_t num_pages;
+  const int32_t *parents, *children;
+  int32_t* pages;        // fork: new pages; free: the free list; compact: the page map
+  int32_t* count;        // free: entries of the list; compact: pages in use
+  int32_t n;             // entries of the call's lists
+  const int32_t* list;   // free: rows
+  uint32_t* err;
+};
+
+// Fork: a warp decides one entry (every check reads state that no entry's
+// update changes: lengths of the children, counts of the new pages), then,
+// after the cluster's barrier, applies it.
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterThreads, 1)
+    pa_page_fork_kernel(const PoolParams p) {
+  constexpr int W = kClusterThreads / 32;
+  static_assert(kMaxSeqsHost <= 32 * kClusterCtas * W, "a warp's verdicts fit one word");
+  uint32_t accepted = 0u;                         // bit j: this warp's j-th entry
+  grid_dependency_wait();
+  grid_launch_dependents();
+  cg::cluster_group cluster = cg::this_cluster();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w0 = static_cast<int>(cluster.block_rank()) * W + warp;
+  int j = 0;
+  for (int k = w0; k < p.n; k += kClusterCtas * W, ++j) {
+    const int par = p.parents[k], chi = p.children[k], page = p.pages[k];
+    if (par < 0 || chi < 0) continue;             // padding
+    bool ok = par < p.rows && chi < p.rows;
+    if (ok) {
+      const int len = p.seq_lens[par];
+      const int full = len / kPage;
+      const bool part = len % kPage != 0;
+      ok = len >= 0 && full + (part ? 1 : 0) <= p.cols && p.seq_lens[chi] == 0;
+      if (ok && part) ok = page >= 0 && page < p.num_pages && p.ref[page] == 0;
+      bool clash = false;
+      for (int x = lane; x < p.n; x += 32) {
+        const int xp = p.parents[x], xc = p.children[x];
+        if (xp < 0 || xc < 0) continue;
+        clash |= xp == chi;                                     // the child is itself forked from
+        clash |= x < k && (xc == chi || (part && p.pages[x] == page));   // an earlier entry has it
+      }
+      ok = !__any_sync(0xffffffffu, clash) && ok;
+    }
+    if (ok) accepted |= 1u << j;
+    else if (lane == 0) atomicOr(p.err, kErrPageOp);
+  }
+  cluster.sync();
+  j = 0;
+  for (int k = w0; k < p.n; k += kClusterCtas * W, ++j) {
+    if (!((accepted >> j) & 1u)) {
+      if (lane == 0) p.pages[k] = -1;
+      continue;
+    }
+    const int par = p.parents[k], chi = p.children[k];
+    const int len = p.seq_lens[par], full = len / kPage;
+    const int32_t* from = p.tables + static_cast<int64_t>(par) * p.table_stride;
+    int32_t* to = p.tables + static_cast<int64_t>(chi) * p.table_stride;
+    for (int x = lane; x < full; x += 32) {
+      const int id = from[x];
+      to[x] = id;
+      if (id >= 0 && id < p.num_pages) atomicAdd(p.ref + id, 1);
+      else atomicOr(p.err, kErrPageRange);
+    }
+    if (lane == 0) {
+      if (len % kPage != 0) {
+        const int page = p.pages[k];
+        to[full] = page;
+        p.ref[page] = 1;
+        if (from[full] < 0 || from[full] >= p.num_pages) atomicOr(p.err, kErrPageRange);
+      } else {
+        p.pages[k] = -1;
+      }
+      p.seq_lens[chi] = len;
+    }
+  }
+}
+
+// Pages [lo, hi) of a warp: the pool cut into equal runs of 32-page words.
+__device__ __forceinline__ void warp_pages(int num_pages, int w, int warps, int64_t& lo, int64_t& hi) {
+  const int64_t words = (static_cast<int64_t>(num_pages) + 31) / 32;
+  lo = min(static_cast<int64_t>(num_pages), words * w / warps * 32);
+  hi = min(static_cast<int64_t>(num_pages), words * (w + 1) / warps * 32);
+}
+
+// Exclusive prefix of one value per warp over the cluster's warps, in (block,
+// warp) order, and the total.  `s` holds this block's warps' values.
+__device__ __forceinline__ int cluster_prefix(cg::cluster_group& cluster, int v, int* s_warp, int* s_total, int& total) {
+  constexpr int W = kClusterThreads / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) s_warp[warp] = v;
+  __syncthreads();
+  const int wv = s_warp[lane % W];
+  int inc = wv;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (threadIdx.x == 31) *s_total = inc;
+  const int before = __shfl_sync(0xffffffffu, inc - wv, warp);
+  cluster.sync();
+  const int rank = static_cast<int>(cluster.block_rank());
+  int off = 0;
+  total = 0;
+  for (int b = 0; b < kClusterCtas; ++b) {
+    const int c = *cluster.map_shared_rank(s_total, b);
+    if (b < rank) off += c;
+    total += c;
+  }
+  return off + before;
+}
+
+// Free: a warp releases one row at a time; then the pages whose count is 0 are
+// listed in ascending order.
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterThreads, 1)
+    pa_page_free_kernel(const PoolParams p) {
+  constexpr int W = kClusterThreads / 32;
+  __shared__ int s_warp[W];
+  __shared__ int s_total;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  cg::cluster_group cluster = cg::this_cluster();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w = static_cast<int>(cluster.block_rank()) * W + warp;
+  for (int k = w; k < p.n; k += kClusterCtas * W) {
+    const int row = p.list[k];
+    if (row < 0) continue;                        // padding
+    if (row >= p.rows) {
+      if (lane == 0) atomicOr(p.err, kErrPageOp);
+      continue;
+    }
+    // the exchange makes a row listed twice release its pages once
+    int len = 0;
+    if (lane == 0) len = atomicExch(p.seq_lens + row, 0);
+    len = __shfl_sync(0xffffffffu, len, 0);
+    if (len <= 0) continue;
+    int held = (len - 1) / kPage + 1;
+    if (held > p.cols) {
+      if (lane == 0) atomicOr(p.err, kErrSeqLen);
+      held = p.cols;
+    }
+    const int32_t* from = p.tables + static_cast<int64_t>(row) * p.table_stride;
+    for (int x = lane; x < held; x += 32) {
+      const int id = from[x];
+      if (id < 0 || id >= p.num_pages) {
+        atomicOr(p.err, kErrPageRange);
+      } else if (atomicSub(p.ref + id, 1) <= 0) {
+        atomicAdd(p.ref + id, 1);                 // was free already: its count stays
+        atomicOr(p.err, kErrPageOp);
+      }
+    }
+  }
+  cluster.sync();
+  int64_t lo, hi;
+  warp_pages(p.num_pages, w, kClusterCtas * W, lo, hi);
+  int mine = 0;
+  for (int64_t b = lo; b < hi; b += 32) {
+    const bool is_free = b + lane < hi && __ldcg(p.ref + b + lane) <= 0;
+    mine += __popc(__ballot_sync(0xffffffffu, is_free));
+  }
+  int total;
+  int at = cluster_prefix(cluster, mine, s_warp, &s_total, total);
+  for (int64_t b = lo; b < hi; b += 32) {
+    const bool is_free = b + lane < hi && __ldcg(p.ref + b + lane) <= 0;
+    const uint32_t m = __ballot_sync(0xffffffffu, is_free);
+    if (is_free) p.pages[at + __popc(m & ((1u << lane) - 1u))] = static_cast<int32_t>(b + lane);
+    at += __popc(m);
+  }
+  if (w == 0 && lane == 0) *p.count = total;
+  for (int64_t i = total + static_cast<int64_t>(w) * 32 + lane; i < p.num_pages; i += kClusterCtas * W * 32)
+    p.pages[i] = -1;
+  cluster.sync();                                  // no block leaves while its total may still be read
+}
+
+// Compact, the bookkeeping: U pages are in use; the k-th page in use with id
+// >= U ("high") moves to the k-th free page with id < U ("hole").  The holes'
+// list lives in map[U ..] until the high pages have read it (there are at most
+// NB - U holes), a high page's target in its own count, negated, until the map
+// is written.
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterThreads, 1)
+    pa_page_compact_kernel(const PoolParams p) {
+  constexpr int W = kClusterThreads / 32;
+  __shared__ int s_warp[W];
+  __shared__ int s_total[3];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  cg::cluster_group cluster = cg::this_cluster();
+  const int lane = threadIdx.x & 31;
+  const int w = static_cast<int>(cluster.block_rank()) * W + (threadIdx.x >> 5);
+  int64_t lo, hi;
+  warp_pages(p.num_pages, w, kClusterCtas * W, lo, hi);
+  int mine = 0;
+  bool negative = false;
+  for (int64_t b = lo; b < hi; b += 32) {
+    const int r = b + lane < hi ? p.ref[b + lane] : 0;
+    negative |= r < 0;
+    mine += __popc(__ballot_sync(0xffffffffu, r > 0));
+  }
+  if (negative) atomicOr(p.err, kErrPageOp);
+  int U, holes_all, high_all;
+  cluster_prefix(cluster, mine, s_warp, &s_total[0], U);
+  int holes = 0, high = 0;
+  for (int64_t b = lo; b < hi; b += 32) {
+    const bool in = b + lane < hi;
+    const bool used = in && p.ref[b + lane] > 0;
+    holes += __popc(__ballot_sync(0xffffffffu, in && !used && b + lane < U));
+    high += __popc(__ballot_sync(0xffffffffu, used && b + lane >= U));
+  }
+  int at_hole = cluster_prefix(cluster, holes, s_warp, &s_total[1], holes_all);
+  int at_high = cluster_prefix(cluster, high, s_warp, &s_total[2], high_all);
+  for (int64_t b = lo; b < min(hi, static_cast<int64_t>(U)); b += 32) {
+    const int64_t id = b + lane;
+    const bool below = id < hi && id < U;
+    const bool used = below && p.ref[id] > 0;
+    const uint32_t m = __ballot_sync(0xffffffffu, below && !used);
+    if (below) p.pages[id] = used ? static_cast<int32_t>(id) : -1;
+    if (below && !used)
+      p.pages[U + at_hole + __popc(m & ((1u << lane) - 1u))] = static_cast<int32_t>(id);
+    at_hole += __popc(m);
+  }
+  cluster.sync();
+  for (int64_t b = lo; b < hi; b += 32) {
+    const int64_t id = b + lane;
+    const bool above = id < hi && id >= U;
+    const int r = above ? p.ref[id] : 0;
+    const uint32_t m = __ballot_sync(0xffffffffu, r > 0);
+    if (r > 0) {
+      const int to = __ldcg(p.pages + U + at_high + __popc(m & ((1u << lane) - 1u)));
+      p.ref[to] = r;
+      p.ref[id] = -1 - to;
+    } else if (above) {
+      p.ref[id] = 0;
+    }
+    at_high += __popc(m);
+  }
+  cluster.sync();
+  for (int64_t b = lo; b < hi; b += 32) {
+    const int64_t id = b + lane;
+    if (id >= hi || id < U) continue;
+    const int r = p.ref[id];
+    p.pages[id] = r < 0 ? -1 - r : -1;
+    p.ref[id] = 0;
+  }
+  if (w == 0 && lane == 0) *p.count = U;
+}
+
+namespace {
+
+template <typename K, typename... A>
+cudaError_t launch_pdl(K kernel, dim3 grid, int threads, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+int elem_bytes(int dtype) {
+  switch (dtype) {
+    case PA_BF16: return 2;
+    case PA_FP8_E4M3: case PA_FP4_E2M1X2: return 1;
+    case PA_F32: case PA_I32: return 4;
+    default: return 0;
+  }
+}
+
+// Geometry of one cache tensor [NB, ...]: its pages as n2 x n1 contiguous runs.
+int page_tensor(const pa_tensor_t& c, int index, int64_t nb, PageTensor* out, int64_t* page_bytes) {
+  if (c.data == nullptr) return host_fail(PA_ERR_INVALID_ARG, "caches[%d]: data pointer is NULL", index);
+  if (c.ndim < 2 || c.ndim > 4) return host_fail(PA_ERR_INVALID_ARG, "caches[%d]: ndim %d not in 2..4", index, c.ndim);
+  const int64_t es = elem_bytes(c.dtype);
+  if (es == 0) return host_fail(PA_ERR_INVALID_ARG, "caches[%d]: unknown element type", index);
+  if (c.shape[0] != nb)
+    return host_fail(PA_ERR_INVALID_ARG, "caches[%d] has %lld pages, expected %lld", index,
+                     static_cast<long long>(c.shape[0]), static_cast<long long>(nb));
+  int64_t bytes = es;
+  for (int d = 0; d < c.ndim; ++d) {
+    if (c.shape[d] < 1 && d > 0) return host_fail(PA_ERR_INVALID_ARG, "caches[%d]: empty dimension", index);
+    if (c.stride[d] < 0 || (c.stride[d] == 0 && c.shape[d] > 1))
+      return host_fail(PA_ERR_INVALID_ARG, "caches[%d]: strides must be positive", index);
+    if (d > 0) {
+      if (c.shape[d] > (int64_t(1) << 28) || bytes * c.shape[d] > (int64_t(1) << 28))
+        return host_fail(PA_ERR_UNSUPPORTED, "caches[%d]: a page of more than 256 MiB", index);
+      bytes *= c.shape[d];
+    }
+  }
+  if (!host_aligned(c.data, static_cast<size_t>(es)))
+    return host_fail(PA_ERR_INVALID_ARG, "caches[%d]: data not aligned to its element", index);
+  // dimensions inside the page, innermost first, merged where contiguous
+  int64_t run = es, n[3] = {1, 1, 1}, s[3] = {0, 0, 0};
+  int m = 0;
+  for (int d = c.ndim - 1; d >= 1; --d) {
+    if (c.shape[d] == 1) continue;
+    const int64_t sb = c.stride[d] * es;
+    if (m == 0 && sb == run) {
+      run *= c.shape[d];
+    } else if (m > 0 && sb == n[m - 1] * s[m - 1]) {
+      n[m - 1] *= c.shape[d];
+    } else {
+      n[m] = c.shape[d];
+      s[m] = sb;
+      ++m;
+    }
+  }
+  if (m == 3) return host_fail(PA_ERR_UNSUPPORTED, "caches[%d]: a page layout with no contiguous run", index);
+  PageTensor t = {};
+  t.base = static_cast<uint8_t*>(c.data);
+  t.page_stride = c.stride[0] * es;
+  t.run = static_cast<int32_t>(run);
+  t.n1 = static_cast<int32_t>(n[0]);
+  t.s1 = s[0];
+  t.n2 = static_cast<int32_t>(n[1]);
+  t.s2 = s[1];
+  uint64_t bits = reinterpret_cast<uint64_t>(c.data) | static_cast<uint64_t>(t.page_stride) |
+                  static_cast<uint64_t>(run) | static_cast<uint64_t>(t.s1) | static_cast<uint64_t>(t.s2);
+  t.vec = 16;
+  while (bits % static_cast<uint64_t>(t.vec) != 0) t.vec /= 2;
+  *out = t;
+  *page_bytes = bytes;
+  return PA_OK;
+}
+
+struct CacheList {
+  const pa_tensor_t* caches;
+  int32_t count;
+};
+
+int check_caches(const CacheList& c, int64_t nb) {
+  if (c.count < 0 || c.count > kMaxCaches)
+    return host_fail(PA_ERR_UNSUPPORTED, "num_caches %d not in [0, %d]", c.count, kMaxCaches);
+  if (c.count > 0 && c.caches == nullptr) return host_fail(PA_ERR_INVALID_ARG, "caches: pointer is NULL");
+  PageTensor t;
+  int64_t bytes;
+  for (int i = 0; i < c.count; ++i) {
+    const int st = page_tensor(c.caches[i], i, nb, &t, &bytes);
+    if (st != PA_OK) return st;
+  }
+  return PA_OK;
+}
+
+// The copies of `p` (pairs set by the caller) in every tensor, up to
+// kMaxPageTensors a launch.
+template <PairSource SRC>
+int launch_copies(CopyParams& p, const CacheList& c, int64_t nb, int num_sms, cudaStream_t stream) {
+  for (int first = 0; first < c.count; first += kMaxPageTensors) {
+    p.num_tensors = std::min(kMaxPageTensors, c.count - first);
+    int64_t items = 0;
+    for (int i = 0; i < p.num_tensors; ++i) {
+      int64_t bytes;
+      const int st = page_tensor(c.caches[first + i], first + i, nb, &p.t[i], &bytes);
+      if (st != PA_OK) return st;
+      p.t[i].item0 = static_cast<int32_t>(items);
+      items += (bytes + kItemBytes - 1) / kItemBytes;
+    }
+    p.items = static_cast<int32_t>(items);
+    const int64_t blocks = (p.pairs * items + 7) / 8;
+    const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(blocks, int64_t(num_sms) * 8))), 1, 1);
+    const cudaError_t e = launch_pdl(pa_page_copy_kernel<SRC>, grid, 256, stream, p);
+    if (e != cudaSuccess) return host_cuda_fail(e, "page copy launch");
+  }
+  return PA_OK;
+}
+
+// A contiguous int32 vector.
+int check_ints(const pa_tensor_t* t, const char* name, int64_t n) {
+  const int st = host_check_tensor(t, name, 1, n == 0);
+  if (st != PA_OK) return st;
+  if (t->data == nullptr) return PA_OK;
+  if (t->dtype != PA_I32) return host_fail(PA_ERR_INVALID_ARG, "%s must be int32", name);
+  if (t->shape[0] != n)
+    return host_fail(PA_ERR_INVALID_ARG, "%s has %lld entries, expected %lld", name,
+                     static_cast<long long>(t->shape[0]), static_cast<long long>(n));
+  if (n > 1 && t->stride[0] != 1) return host_fail(PA_ERR_INVALID_ARG, "%s must be contiguous", name);
+  if (!host_aligned(t->data, 4)) return host_fail(PA_ERR_INVALID_ARG, "%s must be 4-byte aligned", name);
+  return PA_OK;
+}
+
+int64_t length_of(const pa_tensor_t* t) { return t != nullptr && t->ndim >= 1 ? t->shape[0] : -1; }
+
+// Block tables [B, max_blocks] whose rows do not overlap, and ref_counts [NB].
+int check_pool(const pa_tensor_t* bt, const pa_tensor_t* ref, PoolParams* p) {
+  int st;
+  if ((st = host_check_tensor(bt, "block_tables", 2, false)) != PA_OK) return st;
+  if (bt->dtype != PA_I32) return host_fail(PA_ERR_INVALID_ARG, "block_tables must be int32");
+  if ((bt->shape[1] > 1 && bt->stride[1] != 1) || (bt->shape[0] > 1 && bt->stride[0] < bt->shape[1]))
+    return host_fail(PA_ERR_INVALID_ARG, "block_tables rows must be contiguous and must not overlap");
+  if (!host_aligned(bt->data, 4)) return host_fail(PA_ERR_INVALID_ARG, "block_tables must be 4-byte aligned");
+  if (bt->shape[0] > kMaxSeqsHost || bt->shape[1] > (int64_t(1) << 27))
+    return host_fail(PA_ERR_UNSUPPORTED, "block table too large");
+  const int64_t nb = length_of(ref);
+  if (nb < 0) return host_fail(PA_ERR_INVALID_ARG, "ref_counts must be a vector");
+  if (nb < 1 || nb > (int64_t(1) << 31) - 64)
+    return host_fail(PA_ERR_UNSUPPORTED, "ref_counts: %lld pages", static_cast<long long>(nb));
+  if ((st = check_ints(ref, "ref_counts", nb)) != PA_OK) return st;
+  p->tables = static_cast<int32_t*>(bt->data);
+  p->table_stride = bt->stride[0];
+  p->rows = static_cast<int32_t>(bt->shape[0]);
+  p->cols = static_cast<int32_t>(bt->shape[1]);
+  p->ref = static_cast<int32_t*>(ref->data);
+  p->num_pages = static_cast<int32_t>(nb);
+  return PA_OK;
+}
+
+int pages_copy(const CacheList& c, const pa_tensor_t* src, const pa_tensor_t* dst, cudaStream_t stream) {
+  int st;
+  const int64_t n = length_of(src);
+  if (n < 0 || n > (int64_t(1) << 30)) return host_fail(PA_ERR_INVALID_ARG, "src_pages must be a vector");
+  if ((st = check_ints(src, "src_pages", n)) || (st = check_ints(dst, "dst_pages", n))) return st;
+  if (c.count < 1) return host_fail(PA_ERR_INVALID_ARG, "num_caches %d < 1", c.count);
+  if (c.caches == nullptr) return host_fail(PA_ERR_INVALID_ARG, "caches: pointer is NULL");
+  const int64_t nb = c.caches[0].ndim >= 1 ? c.caches[0].shape[0] : 0;
+  if (nb < 0 || nb > (int64_t(1) << 31) - 64) return host_fail(PA_ERR_UNSUPPORTED, "tensor extents too large");
+  if ((st = check_caches(c, nb)) != PA_OK) return st;
+  if (n == 0) return PA_OK;
+  auto lock = host_lock();
+  HostDevice dev;
+  if ((st = host_device(&dev)) != PA_OK) return st;
+  CopyParams p = {};
+  p.pairs = n;
+  p.num_pages = static_cast<int32_t>(nb);
+  p.src = static_cast<const int32_t*>(src->data);
+  p.dst = static_cast<const int32_t*>(dst->data);
+  p.err = dev.status;
+  return launch_copies<kPairsListed>(p, c, nb, dev.num_sms, stream);
+}
+
+int pages_fork(const CacheList& c, const pa_tensor_t* bt, const pa_tensor_t* sl, const pa_tensor_t* ref,
+               const pa_tensor_t* parents, const pa_tensor_t* children, const pa_tensor_t* pages,
+               cudaStream_t stream) {
+  int st;
+  PoolParams p = {};
+  if ((st = check_pool(bt, ref, &p)) != PA_OK) return st;
+  if ((st = check_ints(sl, "seq_lens", p.rows)) != PA_OK) return st;
+  const int64_t n = length_of(parents);
+  if (n < 0) return host_fail(PA_ERR_INVALID_ARG, "parents must be a vector");
+  if (n > kMaxSeqsHost)
+    return host_fail(PA_ERR_UNSUPPORTED, "parents: %lld entries > %d", static_cast<long long>(n),
+                     kMaxSeqsHost);
+  if ((st = check_ints(parents, "parents", n)) || (st = check_ints(children, "children", n)) ||
+      (st = check_ints(pages, "new_pages", n)) || (st = check_caches(c, p.num_pages)))
+    return st;
+  if (n == 0) return PA_OK;
+  auto lock = host_lock();
+  HostDevice dev;
+  if ((st = host_device(&dev)) != PA_OK) return st;
+  p.seq_lens = static_cast<int32_t*>(sl->data);
+  p.parents = static_cast<const int32_t*>(parents->data);
+  p.children = static_cast<const int32_t*>(children->data);
+  p.pages = static_cast<int32_t*>(pages->data);
+  p.n = static_cast<int32_t>(n);
+  p.err = dev.status;
+  const cudaError_t e = launch_pdl(pa_page_fork_kernel, dim3(kClusterCtas, 1, 1), kClusterThreads, stream, p);
+  if (e != cudaSuccess) return host_cuda_fail(e, "page fork launch");
+  CopyParams cp = {};
+  cp.pairs = n;
+  cp.num_pages = p.num_pages;
+  cp.dst = p.pages;
+  cp.parents = p.parents;
+  cp.seq_lens = p.seq_lens;
+  cp.tables = p.tables;
+  cp.table_stride = p.table_stride;
+  cp.err = dev.status;
+  return launch_copies<kPairsFork>(cp, c, p.num_pages, dev.num_sms, stream);
+}
+
+int pages_free(const pa_tensor_t* bt, const pa_tensor_t* sl, const pa_tensor_t* ref, const pa_tensor_t* rows,
+               const pa_tensor_t* pages, const pa_tensor_t* count, cudaStream_t stream) {
+  int st;
+  PoolParams p = {};
+  if ((st = check_pool(bt, ref, &p)) != PA_OK) return st;
+  if ((st = check_ints(sl, "seq_lens", p.rows)) != PA_OK) return st;
+  const int64_t n = length_of(rows);
+  if (n < 0) return host_fail(PA_ERR_INVALID_ARG, "rows must be a vector");
+  if (n > kMaxSeqsHost)
+    return host_fail(PA_ERR_UNSUPPORTED, "rows: %lld entries > %d", static_cast<long long>(n), kMaxSeqsHost);
+  if ((st = check_ints(rows, "rows", n)) || (st = check_ints(pages, "free_pages", p.num_pages)) ||
+      (st = check_ints(count, "num_free", 1)))
+    return st;
+  auto lock = host_lock();
+  HostDevice dev;
+  if ((st = host_device(&dev)) != PA_OK) return st;
+  p.seq_lens = static_cast<int32_t*>(sl->data);
+  p.list = static_cast<const int32_t*>(rows->data);
+  p.pages = static_cast<int32_t*>(pages->data);
+  p.count = static_cast<int32_t*>(count->data);
+  p.n = static_cast<int32_t>(n);
+  p.err = dev.status;
+  const cudaError_t e = launch_pdl(pa_page_free_kernel, dim3(kClusterCtas, 1, 1), kClusterThreads, stream, p);
+  return e == cudaSuccess ? PA_OK : host_cuda_fail(e, "page free launch");
+}
+
+int pages_compact(const CacheList& c, const pa_tensor_t* bt, const pa_tensor_t* ref, const pa_tensor_t* map,
+                  const pa_tensor_t* count, cudaStream_t stream) {
+  int st;
+  PoolParams p = {};
+  if ((st = check_pool(bt, ref, &p)) != PA_OK) return st;
+  if ((st = check_ints(map, "page_map", p.num_pages)) || (st = check_ints(count, "num_used", 1)) ||
+      (st = check_caches(c, p.num_pages)))
+    return st;
+  auto lock = host_lock();
+  HostDevice dev;
+  if ((st = host_device(&dev)) != PA_OK) return st;
+  p.pages = static_cast<int32_t*>(map->data);
+  p.count = static_cast<int32_t*>(count->data);
+  p.err = dev.status;
+  cudaError_t e = launch_pdl(pa_page_compact_kernel, dim3(kClusterCtas, 1, 1), kClusterThreads, stream, p);
+  if (e != cudaSuccess) return host_cuda_fail(e, "page compaction launch");
+  CopyParams cp = {};
+  cp.pairs = p.num_pages;
+  cp.num_pages = p.num_pages;
+  cp.dst = p.pages;
+  cp.num_used = p.count;
+  cp.err = dev.status;
+  if ((st = launch_copies<kPairsCompact>(cp, c, p.num_pages, dev.num_sms, stream)) != PA_OK) return st;
+  const int64_t entries = static_cast<int64_t>(p.rows) * p.cols;
+  if (entries == 0) return PA_OK;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((entries + 255) / 256, int64_t(dev.num_sms) * 8)), 1, 1);
+  e = launch_pdl(pa_table_remap_kernel, grid, 256, stream, p.tables, p.table_stride, static_cast<int64_t>(p.rows),
+                 static_cast<int64_t>(p.cols), static_cast<const int32_t*>(p.pages), p.num_pages);
+  return e == cudaSuccess ? PA_OK : host_cuda_fail(e, "table remap launch");
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" int paged_attn_pages_copy(const pa_tensor_t* caches, int32_t num_caches, const pa_tensor_t* src_pages,
+                                     const pa_tensor_t* dst_pages, pa_stream_t stream) {
+  return pa::host_entry([&] {
+    return pa::pages_copy({caches, num_caches}, src_pages, dst_pages, reinterpret_cast<cudaStream_t>(stream));
+  });
+}
+
+extern "C" int paged_attn_pages_fork(const pa_tensor_t* caches, int32_t num_caches, const pa_tensor_t* block_tables,
+                                     const pa_tensor_t* seq_lens, const pa_tensor_t* ref_counts,
+                                     const pa_tensor_t* parents, const pa_tensor_t* children,
+                                     const pa_tensor_t* new_pages, pa_stream_t stream) {
+  return pa::host_entry([&] {
+    return pa::pages_fork({caches, num_caches}, block_tables, seq_lens, ref_counts, parents, children, new_pages,
+                          reinterpret_cast<cudaStream_t>(stream));
+  });
+}
+
+extern "C" int paged_attn_pages_free(const pa_tensor_t* block_tables, const pa_tensor_t* seq_lens,
+                                     const pa_tensor_t* ref_counts, const pa_tensor_t* rows,
+                                     const pa_tensor_t* free_pages, const pa_tensor_t* num_free, pa_stream_t stream) {
+  return pa::host_entry([&] {
+    return pa::pages_free(block_tables, seq_lens, ref_counts, rows, free_pages, num_free,
+                          reinterpret_cast<cudaStream_t>(stream));
+  });
+}
+
+extern "C" int paged_attn_pages_compact(const pa_tensor_t* caches, int32_t num_caches,
+                                        const pa_tensor_t* block_tables, const pa_tensor_t* ref_counts,
+                                        const pa_tensor_t* page_map, const pa_tensor_t* num_used,
+                                        pa_stream_t stream) {
+  return pa::host_entry([&] {
+    return pa::pages_compact({caches, num_caches}, block_tables, ref_counts, page_map, num_used,
+                             reinterpret_cast<cudaStream_t>(stream));
+  });
+}
