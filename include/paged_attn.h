@@ -143,7 +143,7 @@ typedef struct pa_plan_t {
   int32_t page_pairing;      /* 1 if consumer warps take two pages of a sequence at once */
   int64_t workspace_bytes;   /* split workspace the call needs                          */
   int32_t variant;           /* 0: mma.sync warps; 1: tcgen05 / tensor-memory kernel; 2: MLA on
-                                mma.sync warps; 3: MLA on tcgen05 / tensor memory           */
+                                mma.sync warps; 3: MLA on tcgen05 / tensor memory; 4: 4-bit */
   int32_t block_pages;       /* pages a consumer step takes (1, 2 paired, 4 tcgen05)    */
 } pa_plan_t;
 
@@ -389,6 +389,43 @@ int paged_attn_cache_write_q4(const pa_tensor_t* key, const pa_tensor_t* value, 
 int paged_attn_cache_read_q4(const pa_tensor_t* slot_mapping, const pa_tensor_t* k_cache, const pa_tensor_t* v_cache,
                              const pa_tensor_t* k_group_scales, const pa_tensor_t* v_group_scales, float k_scale,
                              float v_scale, const pa_tensor_t* key, const pa_tensor_t* value, pa_stream_t stream);
+
+/*
+ * paged_attn_decode_q4 - paged_attn_decode over a 4-bit cache: the same operation on the
+ * values above, except that
+ *   - k_cache, v_cache are codes with strides (but the last, 1) that are multiples of 16
+ *     bytes and 16-byte aligned data; each page's [Hkv, 16, D / 16] block of the group
+ *     scales is contiguous and 16-byte aligned;
+ *   - q may hold any finite values (its rows need 8-byte alignment);
+ *   - with query_start_loc a sequence may have no query tokens (a padded batch): its
+ *     pages are not read.  Rows of `out` and `lse` past the last sequence's stay as they
+ *     were, and T may exceed them;
+ *   - a row that sees no key (L_i = 0, or L_i < q_i) gets out = 0 and lse = -inf (its
+ *     sink's logit with sinks) and sets bit 1 of the status word;
+ *   - what a row does not see cannot reach it: slots past a sequence's end or before its
+ *     window, and scale codes that are NaN, may be anything there.
+ * G * max_query_len <= 64, D in {64, 128}, 1 <= B <= 8192.
+ *   opts   NULL = defaults.  num_ctas (at most 16384), min_pages_per_cta, heads_per_cta,
+ *          disable_pdl, sliding_window, sinks, workspace, the split events and
+ *          wait_limit_us apply; any other option is refused with PA_ERR_UNSUPPORTED.
+ *          Calls without opts->workspace share the library-owned workspace of the device:
+ *          calls that may overlap on the device (two streams, two captured graphs) each
+ *          need a workspace of their own.
+ * paged_attn_q4_plan (variant 4), _workspace_size and _reserve as for paged_attn_plan,
+ * paged_attn_workspace_size and paged_attn_reserve.
+ */
+int paged_attn_decode_q4(const pa_tensor_t* q, const pa_tensor_t* k_cache, const pa_tensor_t* v_cache,
+                         const pa_tensor_t* k_group_scales, const pa_tensor_t* v_group_scales,
+                         const pa_tensor_t* block_tables, const pa_tensor_t* seq_lens,
+                         const pa_tensor_t* query_start_loc, int32_t max_query_len, float scale, float k_scale,
+                         float v_scale, const pa_tensor_t* out, const pa_tensor_t* lse, const pa_options_t* opts,
+                         pa_stream_t stream);
+int paged_attn_q4_plan(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                       int32_t max_query_len, const pa_options_t* opts, pa_plan_t* plan);
+int paged_attn_q4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                 int32_t max_query_len, size_t* bytes);
+int paged_attn_q4_reserve(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                          int32_t max_query_len);
 
 /*
  * Operations on whole pages.  They work on any paged cache of this library.

@@ -6,6 +6,7 @@ fallback implementation.  Function names mirror the C entry points.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -70,6 +71,11 @@ _SIGNATURES = {
     "paged_attn_cache_write_per_token": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_void_p]),
     "paged_attn_cache_write_q4": (ctypes.c_int, [_P] * 7 + [ctypes.c_float, ctypes.c_float, ctypes.c_void_p]),
     "paged_attn_cache_read_q4": (ctypes.c_int, [_P] * 5 + [ctypes.c_float, ctypes.c_float, _P, _P, ctypes.c_void_p]),
+    "paged_attn_decode_q4": (ctypes.c_int, [_P] * 8 + [ctypes.c_int32, ctypes.c_float, ctypes.c_float, ctypes.c_float,
+                                                       _P, _P, ctypes.POINTER(PaOptions), ctypes.c_void_p]),
+    "paged_attn_q4_plan": (ctypes.c_int, [ctypes.c_int32] * 5 + [ctypes.POINTER(PaOptions), ctypes.POINTER(PaPlan)]),
+    "paged_attn_q4_workspace_size": (ctypes.c_int, [ctypes.c_int32] * 5 + [ctypes.POINTER(ctypes.c_size_t)]),
+    "paged_attn_q4_reserve": (ctypes.c_int, [ctypes.c_int32] * 5),
     "paged_attn_pages_copy": (ctypes.c_int, [_P, ctypes.c_int32, _P, _P, ctypes.c_void_p]),
     "paged_attn_pages_fork": (ctypes.c_int, [_P, ctypes.c_int32] + [_P] * 6 + [ctypes.c_void_p]),
     "paged_attn_pages_free": (ctypes.c_int, [_P] * 6 + [ctypes.c_void_p]),
@@ -356,6 +362,106 @@ def paged_attn_cache_read_q4(slot_mapping, k_cache, v_cache, k_group_scales, v_g
     return key, value
 
 
+def paged_attn_q4_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len=1, options=None) -> dict:
+    lib = load()
+    plan = PaPlan()
+    _check(lib, lib.paged_attn_q4_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len,
+                                       ctypes.byref(options) if options is not None else None, ctypes.byref(plan)))
+    return plan.as_dict()
+
+
+def paged_attn_q4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len=1) -> int:
+    lib = load()
+    n = ctypes.c_size_t(0)
+    _check(lib, lib.paged_attn_q4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len,
+                                                 ctypes.byref(n)))
+    return int(n.value)
+
+
+def paged_attn_q4_reserve(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len=1):
+    lib = load()
+    _check(lib, lib.paged_attn_q4_reserve(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len))
+
+
+_Q4_WORKSPACE_BYTES = {}
+
+
+def _with_workspace(options, shape, device):
+    """Options whose workspace is a tensor of torch's allocator (so calls on
+    several streams or in several graphs do not share one); the caller's own
+    workspace is kept."""
+    if options is not None and options.workspace:
+        return options, None
+    o = PaOptions()
+    if options is not None:
+        ctypes.pointer(o)[0] = options
+    key = (device.index, shape, o.num_ctas, o.min_pages_per_cta, o.heads_per_cta)
+    n = _Q4_WORKSPACE_BYTES.get(key)
+    if n is None:
+        n = paged_attn_q4_plan(*shape, options=options)["workspace_bytes"]
+        if len(_Q4_WORKSPACE_BYTES) >= _DESC_CACHE_MAX:
+            _Q4_WORKSPACE_BYTES.clear()
+        _Q4_WORKSPACE_BYTES[key] = n
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    o.workspace, o.workspace_bytes = ws.data_ptr(), n
+    return o, ws
+
+
+def _allocating_on(stream):
+    """The context in which a call's tensors are allocated: the memory then
+    belongs to the stream the call runs on."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream))
+    return torch.cuda.stream(stream)
+
+
+def _decode_q4_call(q, k_cache, v_cache, k_group_scales, v_group_scales, block_tables, seq_lens, query_start_loc,
+                    max_query_len, scale, k_scale, v_scale, out, lse, options, want_lse):
+    """The pieces of a 4-bit decode call: tensors, their descriptors, scalars, options, out, lse."""
+    tensors = (q, k_cache, v_cache, k_group_scales, v_group_scales, block_tables, seq_lens, query_start_loc)
+    _on_current_device(*tensors, out, lse)
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    ws = None
+    if q.dim() == 3 and k_cache.dim() == 4 and block_tables.dim() == 2 and q.shape[0] > 0:
+        options, ws = _with_workspace(options, (block_tables.shape[0], q.shape[1], k_cache.shape[2], q.shape[2],
+                                                int(max_query_len)), q.device)
+    codes = (_dtype_code, _fp4_code, _fp4_code) + (_dtype_code,) * 5
+    scalars = (ctypes.c_int32(int(max_query_len)), ctypes.c_float(float(scale)), ctypes.c_float(float(k_scale)),
+               ctypes.c_float(float(v_scale)))
+    return tensors, codes, scalars, out, lse, options, ws
+
+
+def paged_attn_decode_q4(q, k_cache, v_cache, k_group_scales, v_group_scales, block_tables, seq_lens,
+                         query_start_loc=None, max_query_len=1, scale=None, k_scale=1.0, v_scale=1.0, out=None,
+                         lse=None, stream=None, options=None, want_lse=True):
+    """Decode attention over a 4-bit cache (see include/paged_attn.h).
+
+    q bf16 [T, Hq, D]; k_cache / v_cache uint8 (or torch's packed float4)
+    [NB, 16, Hkv, D / 2]; group scales uint8 or float8_e4m3fn [NB, Hkv, 16,
+    D / 16]; block_tables int32 [B, max_blocks]; seq_lens int32 [B];
+    query_start_loc int32 [B+1] or None.  Returns (out bf16 [T, Hq, D], lse f32
+    [T, Hq] or None).  Without a workspace in `options` the call takes one from
+    torch's allocator."""
+    lib = load()
+    with _allocating_on(stream):
+        tensors, codes, scalars, out, lse, options, ws = _decode_q4_call(
+            q, k_cache, v_cache, k_group_scales, v_group_scales, block_tables, seq_lens, query_start_loc,
+            max_query_len, scale, k_scale, v_scale, out, lse, options, want_lse)
+    refs = [ctypes.byref(tensor_desc(t, c)) for t, c in zip(tensors, codes)]
+    _check(lib, lib.paged_attn_decode_q4(*refs, *scalars, ctypes.byref(tensor_desc(out)),
+                                         ctypes.byref(tensor_desc(lse)),
+                                         ctypes.byref(options) if options is not None else None,
+                                         _stream_handle(stream)))
+    return out, lse
+
+
 def _cache_array(caches):
     """The pa_tensor_t array of page tensors (only their element size matters)."""
     caches = [caches] if isinstance(caches, torch.Tensor) else list(caches)
@@ -527,11 +633,12 @@ class PreparedCall:
     and returns (out, lse).  The tensors are kept referenced by the object;
     their addresses, shapes and strides must not change while it is used."""
 
-    def __init__(self, fn, tensors, scalars, out, lse, options):
+    def __init__(self, fn, tensors, scalars, out, lse, options, codes=None):
         self._lib = load()
         self._fn = fn
         self._keep = (tensors, out, lse, options)
-        self._descs = [_new_desc(t) for t in tensors] + [_new_desc(out), _new_desc(lse)]
+        self._descs = [_new_desc(t, c) for t, c in zip(tensors, codes or (_dtype_code,) * len(tensors))]
+        self._descs += [_new_desc(out), _new_desc(lse)]
         n_in = len(tensors)
         refs = [ctypes.byref(d) for d in self._descs]
         head = refs[:n_in] + list(scalars) + refs[n_in:]
@@ -561,6 +668,22 @@ def prepare_decode(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc=
                ctypes.c_float(float(v_scale)))
     fn = lib.paged_attn_decode if options is None else lib.paged_attn_decode_ex
     return PreparedCall(fn, (q, k_cache, v_cache, block_tables, seq_lens, query_start_loc), scalars, out, lse, options)
+
+
+def prepare_decode_q4(q, k_cache, v_cache, k_group_scales, v_group_scales, block_tables, seq_lens,
+                      query_start_loc=None, max_query_len=1, scale=None, k_scale=1.0, v_scale=1.0, out=None, lse=None,
+                      options=None, want_lse=True) -> PreparedCall:
+    """``paged_attn_decode_q4`` with its arguments marshalled once (see
+    PreparedCall).  The prepared call owns its workspace (unless `options` has
+    one): use one prepared call for each stream that may run at the same time."""
+    lib = load()
+    tensors, codes, scalars, out, lse, options, ws = _decode_q4_call(
+        q, k_cache, v_cache, k_group_scales, v_group_scales, block_tables, seq_lens, query_start_loc, max_query_len,
+        scale, k_scale, v_scale, out, lse, options, want_lse)
+    call = PreparedCall(lib.paged_attn_decode_q4, tensors, scalars, out, lse,
+                        options if options is not None else PaOptions(), codes)
+    call._workspace = ws
+    return call
 
 
 def prepare_mla_decode(q, kv_cache, block_tables, seq_lens, query_start_loc=None, max_query_len=1, scale=None,

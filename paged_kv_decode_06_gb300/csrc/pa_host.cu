@@ -109,6 +109,8 @@ int device_state(DeviceState** out, int* dev_out) {
       return cuda_fail(e, "cudaFuncSetAttribute(MLA)");
     if ((e = pa::set_mla_tc_smem_limits(s.smem_optin)) != cudaSuccess)
       return cuda_fail(e, "cudaFuncSetAttribute(MLA, tcgen05)");
+    if ((e = pa::set_split_smem_limits_q4(s.smem_optin)) != cudaSuccess)
+      return cuda_fail(e, "cudaFuncSetAttribute(split 4-bit)");
     pa::init_cache_write_occupancy();
     void* ptr = nullptr;
     if ((e = cudaGetSymbolAddress(&ptr, g_status_word)) != cudaSuccess)

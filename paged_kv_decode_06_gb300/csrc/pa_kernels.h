@@ -93,6 +93,19 @@ struct MergeParams {
   const float2* ws_ml;
   const float* ws_o;
   uint32_t* err;
+  // sink logits [Hq], for the lse of rows of an empty context (nullptr: -inf)
+  const float* sinks;
+  // a NaN sum gives a NaN lse (4-bit caches; else -inf)
+  bool keep_nan;
+};
+
+// The split kernel over a 4-bit cache (pa_split_q4.cu).
+struct SplitQ4Params : SplitParams {
+  const uint8_t* k_sc;      // group scales [NB, Hkv, 16, D / 16], a page's block contiguous
+  const uint8_t* v_sc;
+  int64_t k_sc_page, v_sc_page;   // bytes between pages
+  int32_t KW;               // warps that share a head's pages (token split), a power of two
+  uint32_t off_v, off_ks, off_vs;   // inside a stage: V codes, K scales, V scales
 };
 
 struct CacheWriteParams {
@@ -157,6 +170,10 @@ cudaError_t launch_mla_tc(bool fp8, int rpad, const CUtensorMap& tm, const CUten
                           int grid, int smem, bool pdl, cudaStream_t stream);
 int mla_tc_threads();
 cudaError_t set_mla_tc_smem_limits(int smem);
+// 4-bit caches: NT 8-row tiles a warp (1, 2 or 4), ctas resident blocks per SM.
+cudaError_t launch_split_q4(int head_dim, int nt, const CUtensorMap& tk, const CUtensorMap& tv, const SplitQ4Params& p,
+                            int grid, int threads, int smem, bool pdl, cudaStream_t stream);
+cudaError_t set_split_smem_limits_q4(int smem);
 // LSE merge of MLA partials (512 value columns; the split kernel writes each
 // piece's normalised output in f16 into ws_o): one warp per (unit, row).
 cudaError_t launch_merge_mla(const MergeParams& p, int units, int rows, bool pdl, cudaStream_t stream);

@@ -59,7 +59,8 @@ __device__ __forceinline__ MergeRow merge_row(const MergeParams& p, int u, int r
     if (lane == 0) {
       if (p.lse)
         p.lse[static_cast<int64_t>(t0 + m.rho / p.G) * p.lse_stride_t +
-              static_cast<int64_t>((c * p.HC + m.hh) * p.G + m.rho % p.G) * p.lse_stride_h] = -INFINITY;
+              static_cast<int64_t>((c * p.HC + m.hh) * p.G + m.rho % p.G) * p.lse_stride_h] =
+            p.sinks != nullptr ? p.sinks[(c * p.HC + m.hh) * p.G + m.rho % p.G] : -INFINITY;
       atomicOr(p.err, kErrSeqLen);
     }
     return m;
@@ -136,7 +137,8 @@ __device__ __forceinline__ void write_merged(const MergeParams& p, const MergeRo
   pk.x = pack_bf16(acc.x * inv, acc.y * inv);
   pk.y = pack_bf16(acc.z * inv, acc.w * inv);
   *reinterpret_cast<uint2*>(m.orow + 4 * dq) = pk;
-  if (write_lse && m.lse_ptr) *m.lse_ptr = l > 0.f ? (mx + fast_log2(l)) * 0.69314718055994530942f : -INFINITY;
+  if (write_lse && m.lse_ptr)
+    *m.lse_ptr = l > 0.f || (p.keep_nan && l != l) ? (mx + fast_log2(l)) * 0.69314718055994530942f : -INFINITY;
 }
 
 // One warp per (unit, row): units cut into a few pieces.

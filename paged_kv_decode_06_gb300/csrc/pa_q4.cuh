@@ -57,4 +57,12 @@ __device__ __forceinline__ float f16_hi(uint32_t x) {
   return r;
 }
 
+// Transpose of an 8x8 matrix of 16-bit elements held one row pair a lane (row
+// lane / 4, columns 2 (lane % 4) and the next).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
 }  // namespace pa

@@ -145,8 +145,10 @@ __device__ __forceinline__ int d_of(int J, int e, int tig) {
 // Prologue shared by the split kernels (all threads of the CTA call it):
 // sequence lengths and query starts copied to shared memory, pages of work per
 // sequence (pages before a sliding window excluded) and their exclusive prefix.
+// rows_only: a sequence without query rows has no pages of work (an invalid
+// query range is reported here instead of where its pages are walked).
 __device__ __forceinline__ void page_prefix(const SplitParams& p, int window, int32_t* s_pre, int32_t* s_len,
-                                            int32_t* s_qsl, int* s_scan, int* s_total) {
+                                            int32_t* s_qsl, int* s_scan, int* s_total, bool rows_only = false) {
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
@@ -167,6 +169,12 @@ __device__ __forceinline__ void page_prefix(const SplitParams& p, int window, in
       }
       const int qn = p.qsl != nullptr ? p.qsl[i + 1] - p.qsl[i] : 1;
       v -= min(v, first_visible_page(L, qn, window));   // pages before the sliding window are skipped
+      if (rows_only) {
+        const int t0 = s_qsl[i];
+        const bool valid = qn >= 0 && qn <= p.max_qlen && t0 >= 0 && t0 <= p.num_tokens - qn;
+        if (!valid && blockIdx.x == 0) atomicOr(p.err, kErrQueryLen);
+        if (!valid || qn == 0) v = 0;
+      }
     }
     int x = v;
 #pragma unroll
