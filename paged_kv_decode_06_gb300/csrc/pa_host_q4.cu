@@ -1,5 +1,8 @@
 // Host side of decode attention over a 4-bit paged cache: validation, launch
 // plan, TMA descriptors, the split and merge launches.
+#ifndef Q4BP
+#define Q4BP 2
+#endif
 #include <algorithm>
 #include <cmath>
 
@@ -12,7 +15,6 @@ namespace {
 constexpr int kPageTokens = 16;
 constexpr int kGroup = 16;             // features that share a scale code
 constexpr int kMaxRows = 64;           // query rows per KV head
-constexpr int kMaxWarps = 8;           // consumer warps a CTA
 constexpr int kMaxRingStages = 32;
 constexpr int kMinPages = 4;
 constexpr int kMaxCtas = 1 << 14;
@@ -21,7 +23,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 struct PlanQ4 {
   int G, R_max, NT, MT, HC, NC, KW, BP, nstage, threads, grid, min_pages;
   uint32_t code_page, scale_page, off_v, off_ks, off_vs, stage_bytes;
-  uint32_t off_xchg, off_bar, off_prefix, smem;
+  uint32_t off_q, off_xchg, off_bar, off_prefix, smem;
   size_t ws_unit, ws_ml, ws_o, ws_bytes;
 };
 
@@ -62,44 +64,48 @@ int make_plan(int B, int Hq, int Hkv, int D, int max_qlen, const pa_options_t* o
   p.R_max = p.G * max_qlen;
   p.NT = p.R_max <= 8 ? 1 : (p.R_max <= 16 ? 2 : 4);
   p.MT = (p.R_max + 8 * p.NT - 1) / (8 * p.NT);
+  const int warps = split_q4_warps(p.NT);
   const int forced = o ? o->heads_per_cta : 0;
-  if (forced * p.MT > kMaxWarps)
-    return host_fail(PA_ERR_UNSUPPORTED, "heads_per_cta %d x %d row tiles exceeds %d warps", forced, p.MT, kMaxWarps);
-  for (p.HC = forced > 0 ? forced : std::min(Hkv, kMaxWarps / p.MT); Hkv % p.HC != 0; --p.HC) {
+  if (forced > warps / p.MT)
+    return host_fail(PA_ERR_UNSUPPORTED, "heads_per_cta %d x %d row tiles exceeds %d warps", forced, p.MT, warps);
+  for (p.HC = forced > 0 ? forced : std::min(Hkv, warps / p.MT); Hkv % p.HC != 0; --p.HC) {
   }
   p.NC = Hkv / p.HC;
-  p.KW = 1;
-  while (2 * p.KW * p.HC * p.MT <= kMaxWarps) p.KW *= 2;
-  // about 18 KB of pages a stage: every warp of a head finds a page (of 64
-  // features: two) in it
-  p.BP = p.KW * (D == 64 ? 2 : 1);
-  p.threads = 32 * (1 + p.HC * p.MT * p.KW);
+  p.threads = 32 * (4 + warps);
+  // pages of a stage: a producer warp's time for a stage (about a microsecond) has to
+  // be less than memory's for the stages of four warps
+  p.BP = 1;
+  while (p.BP < 16 && p.BP * p.HC * D < 1024 * Q4BP) p.BP *= 2;
   p.code_page = static_cast<uint32_t>(p.HC * kPageTokens * D / 2);
   p.scale_page = static_cast<uint32_t>(p.HC * kPageTokens * D / kGroup);
   p.off_v = p.BP * p.code_page;
   p.off_ks = 2 * p.off_v;
   p.off_vs = p.off_ks + p.BP * p.scale_page;
   p.stage_bytes = static_cast<uint32_t>(up(p.off_vs + p.BP * p.scale_page, 1024));
-  const uint32_t xchg = p.KW == 1 ? 0u
-                                  : static_cast<uint32_t>(up(static_cast<size_t>(p.HC * p.MT * p.KW) *
-                                                                 (8 * p.NT * (D + 4) * 4 + 8 * p.NT * 8), 128));
-  const uint32_t bars = 8u * (2 * kMaxRingStages + 2 * kMaxWarps);
+  const uint32_t bars = 8u * (2 * kMaxRingStages + 2 * warps);
   const uint32_t prefix = static_cast<uint32_t>(up(4u * (3 * static_cast<size_t>(B) + 2), 16));
-  // Two CTAs an SM where the registers allow it (8 rows a warp) and a ring of
-  // three stages fits half of the shared memory, else one.
-  const int half = (dev.smem_optin + 1024 + 1024) / 2 - 1024 - 256;
-  int per_sm = p.NT == 1 ? 2 : 1;
-  for (;; --per_sm) {
-    const int64_t room =
-        (per_sm == 2 ? half : dev.smem_optin) - (1024 + static_cast<int64_t>(xchg) + bars + prefix);
-    p.nstage = room > 0 ? static_cast<int>(std::min<int64_t>(kMaxRingStages, room / p.stage_bytes)) : 0;
-    if (per_sm == 1 || p.nstage >= 3) break;
+  // as many warps a head as the CTA has and the ring has stages for: a stage belongs
+  // to the warps of one kw, so the ring is a multiple of KW deep
+  uint32_t xchg = 0;
+  const uint32_t query = warps * split_q4_query_bytes(D, p.NT);
+  p.KW = 1;
+  while (p.KW < 8 && 2 * p.KW * p.HC * p.MT <= warps) p.KW *= 2;
+  for (;; p.KW /= 2) {
+    // partial rows the KW warps of a head exchange (pa_split_q4.cu): the features a
+    // warp does not gather, and each row's maximum and sum
+    const int cols = D - D / p.KW + 4;
+    xchg = p.KW == 1 ? 0u
+                     : static_cast<uint32_t>(up(static_cast<size_t>(p.HC * p.MT * p.KW) * 8 * p.NT * (cols * 4 + 8), 128));
+    const int64_t room = dev.smem_optin - (1024 + static_cast<int64_t>(query) + xchg + bars + prefix);
+    p.nstage = room > 0 ? static_cast<int>(std::min<int64_t>(kMaxRingStages, room / p.stage_bytes)) / p.KW * p.KW : 0;
+    if (p.KW == 1 || p.nstage >= 2 * p.KW) break;
   }
   if (p.nstage < 2)
     return host_fail(PA_ERR_UNSUPPORTED, "no launch configuration fits %d bytes of shared memory", dev.smem_optin);
-  p.grid = (o && o->num_ctas > 0) ? o->num_ctas : per_sm * dev.num_sms;
-  p.min_pages = (o && o->min_pages_per_cta > 0) ? o->min_pages_per_cta : std::max(kMinPages, p.BP);
-  p.off_xchg = p.nstage * p.stage_bytes;
+  p.grid = (o && o->num_ctas > 0) ? o->num_ctas : dev.num_sms;
+  p.min_pages = (o && o->min_pages_per_cta > 0) ? o->min_pages_per_cta : kMinPages;
+  p.off_q = p.nstage * p.stage_bytes;
+  p.off_xchg = p.off_q + query;
   p.off_bar = p.off_xchg + xchg;
   p.off_prefix = p.off_bar + bars;
   p.smem = 1024 + p.off_prefix + prefix;
@@ -111,16 +117,20 @@ int make_plan(int B, int Hq, int Hkv, int D, int max_qlen, const pa_options_t* o
   return PA_OK;
 }
 
-// Codes [NB, 16, Hkv, D / 2] as (byte, slot, head, page): one box is a row's
-// codes x 16 slots x HC heads, landing head-major.
-int encode_codes(CUtensorMap* map, const pa_tensor_t* t, int HC, const char* name) {
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(t->shape[3]), kPageTokens,
-                              static_cast<cuuint64_t>(t->shape[2]), static_cast<cuuint64_t>(t->shape[0])};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(t->stride[1]), static_cast<cuuint64_t>(t->stride[2]),
-                                 static_cast<cuuint64_t>(t->stride[0])};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(t->shape[3]), kPageTokens, static_cast<cuuint32_t>(HC), 1u};
-  const CUresult r = host_encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, t->data, dims, strides, box,
-                                       t->shape[3] == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE);
+// Codes [NB, 16, Hkv, D / 2] as (byte of a box row, box row of a slot, slot, page):
+// one box is the HC heads' box rows x 16 slots, landing slot by slot as in the
+// cache.  Heads that do not follow one another in memory take a row each.
+int encode_codes(CUtensorMap* map, const pa_tensor_t* t, int HC, int box, const char* name) {
+  const cuuint64_t row = static_cast<cuuint64_t>(t->shape[3]);                        // bytes of a head's row
+  const cuuint64_t pitch = box == static_cast<int>(row) ? static_cast<cuuint64_t>(t->stride[2]) : static_cast<cuuint64_t>(box);
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(box), static_cast<cuuint64_t>(t->shape[2]) * row / box,
+                              kPageTokens, static_cast<cuuint64_t>(t->shape[0])};
+  const cuuint64_t strides[3] = {t->shape[2] > 1 ? pitch : static_cast<cuuint64_t>(box),
+                                 static_cast<cuuint64_t>(t->stride[1]), static_cast<cuuint64_t>(t->stride[0])};
+  const cuuint32_t bx[4] = {static_cast<cuuint32_t>(box), static_cast<cuuint32_t>(HC * row / box), kPageTokens, 1u};
+  const CUresult r = host_encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, t->data, dims, strides, bx,
+                                       box == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                  : (box == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE));
   if (r != CUDA_SUCCESS)
     return host_fail(PA_ERR_INVALID_ARG, "cuTensorMapEncodeTiled failed (%d) for %s", static_cast<int>(r), name);
   return PA_OK;
@@ -209,7 +219,14 @@ int decode_q4(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* vc
   void* ws = nullptr;
   if ((st = host_workspace(opts, pl.ws_bytes, stream, "paged_attn_q4_reserve", &ws)) != PA_OK) return st;
   CUtensorMap tk, tv;
-  if ((st = encode_codes(&tk, kc, pl.HC, "k_cache")) != PA_OK || (st = encode_codes(&tv, vc, pl.HC, "v_cache")) != PA_OK)
+  // box rows: the widest that a slot's bytes are made of; one head's row where heads
+  // of either cache are apart
+  const int64_t row = D / 2;
+  int box = static_cast<int>(row);
+  if (kc->stride[2] == row && vc->stride[2] == row)
+    while (box < 128 && pl.HC * row % (2 * box) == 0) box *= 2;
+  if ((st = encode_codes(&tk, kc, pl.HC, box, "k_cache")) != PA_OK ||
+      (st = encode_codes(&tv, vc, pl.HC, box, "v_cache")) != PA_OK)
     return st;
 
   SplitQ4Params sp = {};
@@ -252,6 +269,7 @@ int decode_q4(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* vc
   sp.off_prefix = pl.off_prefix;
   sp.off_bar = pl.off_bar;
   sp.off_stage = 0;
+  sp.off_q = pl.off_q;
   sp.stage_bytes = pl.stage_bytes;
   sp.off_xchg = pl.off_xchg;
   sp.wait_ns = (opts && opts->wait_limit_us > 0) ? static_cast<uint64_t>(opts->wait_limit_us) * 1000ull : kWaitNs;
@@ -261,6 +279,7 @@ int decode_q4(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* vc
   sp.k_sc_page = ks->stride[0];
   sp.v_sc_page = vs->stride[0];
   sp.KW = pl.KW;
+  sp.box_bytes = box;
   sp.off_v = pl.off_v;
   sp.off_ks = pl.off_ks;
   sp.off_vs = pl.off_vs;
@@ -302,13 +321,17 @@ int decode_q4(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* vc
   }
   if (ev0 && (e = cudaEventRecordWithFlags(ev0, stream, rec)) != cudaSuccess)
     return host_cuda_fail(e, "cudaEventRecord(start)");
-  if ((e = launch_split_q4(static_cast<int>(D), pl.NT, tk, tv, sp, pl.grid, pl.threads, static_cast<int>(pl.smem),
+  if ((e = launch_split_q4(static_cast<int>(D), pl.NT, tk, tv, sp, pl.grid, static_cast<int>(pl.smem),
                            pdl && !ev0, stream)) != cudaSuccess)
     return host_cuda_fail(e, "4-bit split kernel launch");
   if (ev1 && (e = cudaEventRecordWithFlags(ev1, stream, rec)) != cudaSuccess)
     return host_cuda_fail(e, "cudaEventRecord(stop)");
   const int units = static_cast<int>(B) * pl.NC;
-  const bool wide = pl.grid >= 4 * units;
+  // The merge that reads a row's partials with a whole block is for few rows cut
+  // into many pieces: about a block an SM (64 rows of one sequence: 4.6 us;
+  // 8192 rows of 32 sequences in 5 pieces each: 118 us, a warp a row: see the
+  // design notes' table).
+  const bool wide = pl.grid >= 4 * units && static_cast<int64_t>(units) * pl.HC * pl.R_max <= 2 * dev.num_sms;
   if ((e = launch_merge(static_cast<int>(D), mp, units, pl.HC * pl.R_max, wide, pdl && !ev1, stream)) != cudaSuccess)
     return host_cuda_fail(e, "merge kernel launch");
   return PA_OK;

@@ -105,6 +105,7 @@ struct SplitQ4Params : SplitParams {
   const uint8_t* v_sc;
   int64_t k_sc_page, v_sc_page;   // bytes between pages
   int32_t KW;               // warps that share a head's pages (token split), a power of two
+  int32_t box_bytes;        // bytes of a TMA box row of codes (128, 64 or 32), and its swizzle span
   uint32_t off_v, off_ks, off_vs;   // inside a stage: V codes, K scales, V scales
 };
 
@@ -170,9 +171,12 @@ cudaError_t launch_mla_tc(bool fp8, int rpad, const CUtensorMap& tm, const CUten
                           int grid, int smem, bool pdl, cudaStream_t stream);
 int mla_tc_threads();
 cudaError_t set_mla_tc_smem_limits(int smem);
-// 4-bit caches: NT 8-row tiles a warp (1, 2 or 4), ctas resident blocks per SM.
+// 4-bit caches: nt 8-row tiles a warp (1, 2 or 4), split_q4_warps(nt) consumer
+// warps a CTA and a warpgroup for the producer.
 cudaError_t launch_split_q4(int head_dim, int nt, const CUtensorMap& tk, const CUtensorMap& tv, const SplitQ4Params& p,
-                            int grid, int threads, int smem, bool pdl, cudaStream_t stream);
+                            int grid, int smem, bool pdl, cudaStream_t stream);
+int split_q4_warps(int nt);
+uint32_t split_q4_query_bytes(int head_dim, int nt);   // shared memory of a warp's query fragments
 cudaError_t set_split_smem_limits_q4(int smem);
 // LSE merge of MLA partials (512 value columns; the split kernel writes each
 // piece's normalised output in f16 into ws_o): one warp per (unit, row).
