@@ -1,8 +1,5 @@
 // Host side of decode attention over a 4-bit paged cache: validation, launch
-// plan, TMA descriptors, the split and merge launches.
-#ifndef Q4BP
-#define Q4BP 2
-#endif
+// plan, the split and merge launches.
 #include <algorithm>
 #include <cmath>
 
@@ -15,15 +12,12 @@ namespace {
 constexpr int kPageTokens = 16;
 constexpr int kGroup = 16;             // features that share a scale code
 constexpr int kMaxRows = 64;           // query rows per KV head
-constexpr int kMaxRingStages = 32;
 constexpr int kMinPages = 4;
 constexpr int kMaxCtas = 1 << 14;
-constexpr uint64_t kWaitNs = 2000000000ull;
 
 struct PlanQ4 {
-  int G, R_max, NT, MT, HC, NC, KW, BP, nstage, threads, grid, min_pages;
-  uint32_t code_page, scale_page, off_v, off_ks, off_vs, stage_bytes;
-  uint32_t off_q, off_xchg, off_bar, off_prefix, smem;
+  int G, R_max, NT, MT, HC, NC, KW, nstage, threads, grid, min_pages;
+  uint32_t off_q, off_xchg, off_state, off_prefix, smem;
   size_t ws_unit, ws_ml, ws_o, ws_bytes;
 };
 
@@ -64,75 +58,51 @@ int make_plan(int B, int Hq, int Hkv, int D, int max_qlen, const pa_options_t* o
   p.R_max = p.G * max_qlen;
   p.NT = p.R_max <= 8 ? 1 : (p.R_max <= 16 ? 2 : 4);
   p.MT = (p.R_max + 8 * p.NT - 1) / (8 * p.NT);
-  const int warps = split_q4_warps(p.NT);
+  const int warps = split_q4_warps();
   const int forced = o ? o->heads_per_cta : 0;
   if (forced > warps / p.MT)
     return host_fail(PA_ERR_UNSUPPORTED, "heads_per_cta %d x %d row tiles exceeds %d warps", forced, p.MT, warps);
   for (p.HC = forced > 0 ? forced : std::min(Hkv, warps / p.MT); Hkv % p.HC != 0; --p.HC) {
   }
   p.NC = Hkv / p.HC;
-  p.threads = 32 * (4 + warps);
-  // pages of a stage: a producer warp's time for a stage (about a microsecond) has to
-  // be less than memory's for the stages of four warps
-  p.BP = 1;
-  while (p.BP < 16 && p.BP * p.HC * D < 1024 * Q4BP) p.BP *= 2;
-  p.code_page = static_cast<uint32_t>(p.HC * kPageTokens * D / 2);
-  p.scale_page = static_cast<uint32_t>(p.HC * kPageTokens * D / kGroup);
-  p.off_v = p.BP * p.code_page;
-  p.off_ks = 2 * p.off_v;
-  p.off_vs = p.off_ks + p.BP * p.scale_page;
-  p.stage_bytes = static_cast<uint32_t>(up(p.off_vs + p.BP * p.scale_page, 1024));
-  const uint32_t bars = 8u * (2 * kMaxRingStages + 2 * warps);
+  p.threads = 32 * warps;
+  const uint32_t state = static_cast<uint32_t>(up(split_q4_state_bytes(), 16));
   const uint32_t prefix = static_cast<uint32_t>(up(4u * (3 * static_cast<size_t>(B) + 2), 16));
-  // as many warps a head as the CTA has and the ring has stages for: a stage belongs
-  // to the warps of one kw, so the ring is a multiple of KW deep
-  uint32_t xchg = 0;
   const uint32_t query = warps * split_q4_query_bytes(D, p.NT);
-  p.KW = 1;
-  while (p.KW < 8 && 2 * p.KW * p.HC * p.MT <= warps) p.KW *= 2;
-  for (;; p.KW /= 2) {
+  // The shared memory of the CTAs that an SM's registers hold, a full ring and as many
+  // warps a head as the CTA has; where the sequences' metadata (12 bytes each) leaves
+  // too little: one CTA an SM, then one warp a head, then a shallow ring.
+  uint32_t ring = 0, xchg = 0;
+  int per_sm = 0;
+  bool fits = false;
+  for (int form = split_q4_ctas_per_sm(p.NT) == 2 ? 0 : 1; form < 4 && !fits; ++form) {
+    per_sm = form == 0 ? 2 : 1;
+    p.KW = 1;
+    while (form < 2 && p.KW < 8 && 2 * p.KW * p.HC * p.MT <= warps) p.KW *= 2;
+    p.nstage = split_q4_stages(D, form == 3);
+    ring = static_cast<uint32_t>(warps * p.nstage * 2 * kPageTokens * (D / 2 + D / kGroup));
     // partial rows the KW warps of a head exchange (pa_split_q4.cu): the features a
     // warp does not gather, and each row's maximum and sum
     const int cols = D - D / p.KW + 4;
     xchg = p.KW == 1 ? 0u
                      : static_cast<uint32_t>(up(static_cast<size_t>(p.HC * p.MT * p.KW) * 8 * p.NT * (cols * 4 + 8), 128));
-    const int64_t room = dev.smem_optin - (1024 + static_cast<int64_t>(query) + xchg + bars + prefix);
-    p.nstage = room > 0 ? static_cast<int>(std::min<int64_t>(kMaxRingStages, room / p.stage_bytes)) / p.KW * p.KW : 0;
-    if (p.KW == 1 || p.nstage >= 2 * p.KW) break;
+    const int64_t budget = per_sm == 2 ? (dev.smem_optin + 2048) / 2 - 1024 - 512 : dev.smem_optin;
+    fits = static_cast<int64_t>(ring) + query + xchg + state + prefix <= budget;
   }
-  if (p.nstage < 2)
+  if (!fits)
     return host_fail(PA_ERR_UNSUPPORTED, "no launch configuration fits %d bytes of shared memory", dev.smem_optin);
-  p.grid = (o && o->num_ctas > 0) ? o->num_ctas : dev.num_sms;
+  p.grid = (o && o->num_ctas > 0) ? o->num_ctas : per_sm * dev.num_sms;
   p.min_pages = (o && o->min_pages_per_cta > 0) ? o->min_pages_per_cta : kMinPages;
-  p.off_q = p.nstage * p.stage_bytes;
+  p.off_q = ring;
   p.off_xchg = p.off_q + query;
-  p.off_bar = p.off_xchg + xchg;
-  p.off_prefix = p.off_bar + bars;
-  p.smem = 1024 + p.off_prefix + prefix;
+  p.off_state = p.off_xchg + xchg;
+  p.off_prefix = p.off_state + state;
+  p.smem = p.off_prefix + prefix;
   const size_t rows = static_cast<size_t>(2) * p.grid * p.HC * p.R_max;
   p.ws_ml = up(static_cast<size_t>(16) * B * p.NC, 256);
   p.ws_o = up(p.ws_ml + rows * 8, 256);
   p.ws_bytes = up(p.ws_o + rows * D * 4, 256);
   *out = p;
-  return PA_OK;
-}
-
-// Codes [NB, 16, Hkv, D / 2] as (byte of a box row, box row of a slot, slot, page):
-// one box is the HC heads' box rows x 16 slots, landing slot by slot as in the
-// cache.  Heads that do not follow one another in memory take a row each.
-int encode_codes(CUtensorMap* map, const pa_tensor_t* t, int HC, int box, const char* name) {
-  const cuuint64_t row = static_cast<cuuint64_t>(t->shape[3]);                        // bytes of a head's row
-  const cuuint64_t pitch = box == static_cast<int>(row) ? static_cast<cuuint64_t>(t->stride[2]) : static_cast<cuuint64_t>(box);
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(box), static_cast<cuuint64_t>(t->shape[2]) * row / box,
-                              kPageTokens, static_cast<cuuint64_t>(t->shape[0])};
-  const cuuint64_t strides[3] = {t->shape[2] > 1 ? pitch : static_cast<cuuint64_t>(box),
-                                 static_cast<cuuint64_t>(t->stride[1]), static_cast<cuuint64_t>(t->stride[0])};
-  const cuuint32_t bx[4] = {static_cast<cuuint32_t>(box), static_cast<cuuint32_t>(HC * row / box), kPageTokens, 1u};
-  const CUresult r = host_encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, t->data, dims, strides, bx,
-                                       box == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
-                                                  : (box == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE));
-  if (r != CUDA_SUCCESS)
-    return host_fail(PA_ERR_INVALID_ARG, "cuTensorMapEncodeTiled failed (%d) for %s", static_cast<int>(r), name);
   return PA_OK;
 }
 
@@ -175,6 +145,8 @@ int decode_q4(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* vc
       return host_fail(PA_ERR_INVALID_ARG,
                        "%s needs a contiguous last dim, strides that are multiples of 16 bytes and 16-byte alignment",
                        cn[y]);
+    if (c->stride[0] >= (int64_t(1) << 32) || s->stride[0] >= (int64_t(1) << 32))
+      return host_fail(PA_ERR_UNSUPPORTED, "%s and %s: pages 4 GiB or more apart", cn[y], sn[y]);
     if (s->shape[0] != NB || s->shape[1] != Hkv || s->shape[2] != kPageTokens || s->shape[3] * kGroup != D)
       return host_fail(PA_ERR_INVALID_ARG, "%s must be [NB, Hkv, 16, D / 16]", sn[y]);
     if (s->stride[3] != 1 || s->stride[2] != D / kGroup || (Hkv > 1 && s->stride[1] != D) ||
@@ -218,17 +190,6 @@ int decode_q4(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* vc
     return st;
   void* ws = nullptr;
   if ((st = host_workspace(opts, pl.ws_bytes, stream, "paged_attn_q4_reserve", &ws)) != PA_OK) return st;
-  CUtensorMap tk, tv;
-  // box rows: the widest that a slot's bytes are made of; one head's row where heads
-  // of either cache are apart
-  const int64_t row = D / 2;
-  int box = static_cast<int>(row);
-  if (kc->stride[2] == row && vc->stride[2] == row)
-    while (box < 128 && pl.HC * row % (2 * box) == 0) box *= 2;
-  if ((st = encode_codes(&tk, kc, pl.HC, box, "k_cache")) != PA_OK ||
-      (st = encode_codes(&tv, vc, pl.HC, box, "v_cache")) != PA_OK)
-    return st;
-
   SplitQ4Params sp = {};
   sp.q = static_cast<const uint16_t*>(q->data);
   sp.q_stride_t = q->stride[0];
@@ -256,7 +217,6 @@ int decode_q4(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* vc
   sp.R_max = pl.R_max;
   sp.nstage = pl.nstage;
   sp.min_pages = pl.min_pages;
-  sp.block_pages = pl.BP;
   sp.window = (opts && opts->sliding_window > 0) ? opts->sliding_window : 0;
   sp.sinks = opts ? static_cast<const float*>(opts->sinks) : nullptr;
   sp.scale_log2 = scale * k_scale * 1.4426950408889634f;
@@ -267,22 +227,23 @@ int decode_q4(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* vc
   sp.ws_o = reinterpret_cast<float*>(wsb + pl.ws_o);
   sp.err = dev.status;
   sp.off_prefix = pl.off_prefix;
-  sp.off_bar = pl.off_bar;
-  sp.off_stage = 0;
   sp.off_q = pl.off_q;
-  sp.stage_bytes = pl.stage_bytes;
   sp.off_xchg = pl.off_xchg;
-  sp.wait_ns = (opts && opts->wait_limit_us > 0) ? static_cast<uint64_t>(opts->wait_limit_us) * 1000ull : kWaitNs;
+  sp.off_state = pl.off_state;
   sp.starve_cta = -1;
+  sp.k_codes = static_cast<const uint8_t*>(kc->data);
+  sp.v_codes = static_cast<const uint8_t*>(vc->data);
+  sp.kc_stride_page = static_cast<uint32_t>(kc->stride[0]);
+  sp.kc_stride_slot = kc->stride[1];
+  sp.kc_stride_head = kc->stride[2];
+  sp.vc_stride_page = static_cast<uint32_t>(vc->stride[0]);
+  sp.vc_stride_slot = vc->stride[1];
+  sp.vc_stride_head = vc->stride[2];
   sp.k_sc = static_cast<const uint8_t*>(ks->data);
   sp.v_sc = static_cast<const uint8_t*>(vs->data);
-  sp.k_sc_page = ks->stride[0];
-  sp.v_sc_page = vs->stride[0];
+  sp.k_sc_page = static_cast<uint32_t>(ks->stride[0]);
+  sp.v_sc_page = static_cast<uint32_t>(vs->stride[0]);
   sp.KW = pl.KW;
-  sp.box_bytes = box;
-  sp.off_v = pl.off_v;
-  sp.off_ks = pl.off_ks;
-  sp.off_vs = pl.off_vs;
 
   MergeParams mp = {};
   mp.out = sp.out;
@@ -321,8 +282,7 @@ int decode_q4(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* vc
   }
   if (ev0 && (e = cudaEventRecordWithFlags(ev0, stream, rec)) != cudaSuccess)
     return host_cuda_fail(e, "cudaEventRecord(start)");
-  if ((e = launch_split_q4(static_cast<int>(D), pl.NT, tk, tv, sp, pl.grid, static_cast<int>(pl.smem),
-                           pdl && !ev0, stream)) != cudaSuccess)
+  if ((e = launch_split_q4(static_cast<int>(D), pl.NT, sp, pl.grid, static_cast<int>(pl.smem), pdl && !ev0, stream)) != cudaSuccess)
     return host_cuda_fail(e, "4-bit split kernel launch");
   if (ev1 && (e = cudaEventRecordWithFlags(ev1, stream, rec)) != cudaSuccess)
     return host_cuda_fail(e, "cudaEventRecord(stop)");
@@ -380,7 +340,7 @@ extern "C" int paged_attn_q4_plan(int32_t num_seqs, int32_t num_q_heads, int32_t
     plan->page_pairing = 0;
     plan->workspace_bytes = static_cast<int64_t>(pl.ws_bytes);
     plan->variant = 4;
-    plan->block_pages = pl.BP;
+    plan->block_pages = 1;
     return static_cast<int>(PA_OK);
   });
 }

@@ -101,12 +101,15 @@ struct MergeParams {
 
 // The split kernel over a 4-bit cache (pa_split_q4.cu).
 struct SplitQ4Params : SplitParams {
+  const uint8_t* k_codes;   // [NB, 16, Hkv, D / 2]; strides in bytes
+  const uint8_t* v_codes;
+  uint32_t kc_stride_page, vc_stride_page;
+  int64_t kc_stride_slot, kc_stride_head, vc_stride_slot, vc_stride_head;
   const uint8_t* k_sc;      // group scales [NB, Hkv, 16, D / 16], a page's block contiguous
   const uint8_t* v_sc;
-  int64_t k_sc_page, v_sc_page;   // bytes between pages
+  uint32_t k_sc_page, v_sc_page;   // bytes between pages
   int32_t KW;               // warps that share a head's pages (token split), a power of two
-  int32_t box_bytes;        // bytes of a TMA box row of codes (128, 64 or 32), and its swizzle span
-  uint32_t off_v, off_ks, off_vs;   // inside a stage: V codes, K scales, V scales
+  uint32_t off_state;       // the warps' fetch states
 };
 
 struct CacheWriteParams {
@@ -171,12 +174,15 @@ cudaError_t launch_mla_tc(bool fp8, int rpad, const CUtensorMap& tm, const CUten
                           int grid, int smem, bool pdl, cudaStream_t stream);
 int mla_tc_threads();
 cudaError_t set_mla_tc_smem_limits(int smem);
-// 4-bit caches: nt 8-row tiles a warp (1, 2 or 4), split_q4_warps(nt) consumer
-// warps a CTA and a warpgroup for the producer.
-cudaError_t launch_split_q4(int head_dim, int nt, const CUtensorMap& tk, const CUtensorMap& tv, const SplitQ4Params& p,
-                            int grid, int smem, bool pdl, cudaStream_t stream);
-int split_q4_warps(int nt);
-uint32_t split_q4_query_bytes(int head_dim, int nt);   // shared memory of a warp's query fragments
+// 4-bit caches: nt 8-row tiles a warp (1, 2 or 4), split_q4_warps() warps a CTA,
+// p.nstage pages in flight a warp (one of the two split_q4_stages).
+cudaError_t launch_split_q4(int head_dim, int nt, const SplitQ4Params& p, int grid, int smem, bool pdl,
+                            cudaStream_t stream);
+int split_q4_warps();
+int split_q4_ctas_per_sm(int nt);
+int split_q4_stages(int head_dim, bool shallow);
+uint32_t split_q4_state_bytes();                       // a CTA's fetch states
+uint32_t split_q4_query_bytes(int head_dim, int nt);   // shared memory of a warp's query elements
 cudaError_t set_split_smem_limits_q4(int smem);
 // LSE merge of MLA partials (512 value columns; the split kernel writes each
 // piece's normalised output in f16 into ws_o): one warp per (unit, row).

@@ -26,30 +26,38 @@
 // Query rows are scaled by a power of two into f16's range (exact except for
 // elements 2^-14 below the row's largest), and the power goes into the row's logit factor.
 //
-// CTA (one an SM): a warpgroup of producers, then CW = 16
-// consumer warps for 8 query rows a warp or 8 for more, with the registers split
-// between the two kinds (setmaxnreg).  KW x MT x HC consumer warps are in use:
-// HC KV heads, MT tiles of 8 NT query rows, and KW warps that take a head's pages
-// (a stage of the ring, BP pages, at a time) in turn and meet in shared memory at
-// the end of a segment (a sequence's pages in this CTA).  All waits are bounded.
+// A CTA is eight warps, two CTAs an SM for at most 8 query rows a KV head (128
+// registers a thread), else one (255).  KW x MT x HC warps are in use: HC KV heads,
+// MT tiles of 8 NT query rows, and KW warps that take a head's pages in turn and meet
+// in shared memory at the end of a segment (a sequence's pages in this CTA).
+//
+// Every warp feeds itself: it copies the 2.3 KB (D = 128) of its head's codes and
+// scales of a page with five 16-byte cp.async a lane into its own ring, S pages
+// ahead, so no warp ever waits for another or polls a barrier.  The form before it,
+// producer warps with bulk tensor copies of whole pages into a ring of the CTA's,
+// ran 151 us on the batch of 256 (673 MB): a third of the issue slots went to the
+// producers, to polling and to register spills (a producer warpgroup's registers
+// are not the consumers'), and a copy instruction held a producer for 280 to 540
+// cycles beside warps that compute.
 #include "pa_q4.cuh"
 #include "pa_split.cuh"
 
 namespace pa {
 
-// Consumer warps of a CTA and the registers of a consumer / producer thread:
-// with 128 producer threads the two shares add up to what the CTA is launched
-// with (96 x 640 and 168 x 384).
-constexpr int q4_warps(int nt) { return nt == 1 ? 16 : 8; }
-// Query fragments in shared memory (D x 8 NT f16 of a warp) or in registers.
+constexpr int kQ4Warps = 8;                                         // of a CTA
+constexpr int q4_ctas_per_sm(int nt) { return nt == 1 ? 2 : 1; }
+// Pages in flight a warp: about 10 KB, 160 KB an SM; a shallow ring where the
+// sequences' metadata takes the shared memory.
+constexpr int q4_stages(int d) { return d == 128 ? 5 : 8; }
+constexpr int kQ4ShallowStages = 2;
+// A warp's query elements in shared memory (D x 8 NT x 2 bytes): the rows of the next
+// segment, copied there while the current one runs (a load that is waited for takes 2
+// to 5 us beside the page stream); for 32 rows the fragments in use instead
+// (registers cannot hold them beside the outputs).
 constexpr bool q4_query_in_smem(int nt) { return nt == 4; }
-constexpr uint32_t q4_query_bytes(int d, int nt) { return q4_query_in_smem(nt) ? static_cast<uint32_t>(d * 8 * nt * 2) : 0u; }
-template <int NT>
-struct RegsQ4 {
-  static constexpr int CONS = NT == 1 ? 112 : 232, PROD = NT == 1 ? 32 : 40;
-  static constexpr int LAUNCH = NT == 1 ? 96 : 168;
-  static_assert(q4_warps(NT) * CONS + 4 * PROD <= (q4_warps(NT) + 4) * LAUNCH, "register split");
-};
+constexpr uint32_t q4_query_bytes(int d, int nt) { return static_cast<uint32_t>(d * 8 * nt * 2); }
+// Pages a warp takes at once where it has two.
+constexpr int q4_pages_at_once(int nt) { return 1; }
 
 template <int D>
 struct GeoQ4 {
@@ -59,40 +67,34 @@ struct GeoQ4 {
   static constexpr int STILE = 16 * SROW;   // scales of one page and head
   static constexpr int KS = D / 16;         // k-steps of K Q^T; also 16-feature tiles of V^T
   static constexpr int LW = D / 32;         // words of codes a lane reads of its key
+  // a page and head in a warp's ring: K codes, V codes, K scales, V scales
+  static constexpr int V = TILE, KSC = 2 * TILE, VSC = 2 * TILE + STILE, PAGE = 2 * (TILE + STILE);
 };
 
-// A page's codes lie in shared memory as in the cache, [16 slots][HC heads][D / 2
-// bytes], in TMA box rows of IB = 128, 64 or 32 bytes (the largest that divides a
-// slot's bytes: the copy engine's time goes by box rows; with a head's 64-byte row
-// a box row it took 3.7 cycles a row, twice the time of 128-byte rows) and the
-// swizzle of that span: address bits [4, 4 + k) XOR bits [7, 7 + k).
-__device__ __forceinline__ uint32_t code_off(int slot, int byte, int slot_bytes, int ib) {
-  const uint32_t off = static_cast<uint32_t>(slot * slot_bytes + byte);
-  const uint32_t mask = ib == 128 ? 7u : ib == 64 ? 3u : 0u;
-  return off ^ (((off >> 7) & mask) << 4);
-}
-
-// Slot of tile row t (bits t2 t1 t0; rows 8 .. 15 add 8).  A warp reads the scores'
-// keys eight lanes (D = 128: rows t0) or sixteen (D = 64: rows t1 t0) at a time and
-// the values' keys by rows t2 t1: the slot bits that reach the bank of a read,
-// directly or through the swizzle, must differ there.  Which bits these are goes
-// by the bytes of a slot (free of conflicts for 32 to 256 bytes; values two-way at
-// 512, more above).
+// Slot of tile row t (0 .. 7; rows 8 .. 15 add 8): a permutation that makes the
+// values' reads (tile rows 2 tig, 2 tig + 1 of four lanes) free of bank conflicts.
 template <int D>
-__device__ __forceinline__ int slot_of(int t, int slot_bytes) {
-  const int t0 = t & 1, t1 = (t >> 1) & 1, t2 = (t >> 2) & 1;
-  if (slot_bytes == 256 || slot_bytes == 32) return t1 | (t0 ^ t2) << 1 | t2 << 2;
-  if (slot_bytes == 128) return t2 | t1 << 1 | (t0 ^ t2) << 2;
-  if (D == 64 && slot_bytes == 64) return t1 | t2 << 1 | (t0 ^ t2) << 2;
-  return t ^ t1;
+__device__ __forceinline__ int slot_of(int t) {
+  return D == 128 ? t ^ ((t >> 1) & 1) : t ^ ((t >> 2) & 1);
 }
 
-// What a lane reads of every page (offsets into a stage) and the slots of its keys.
-struct LaneQ4 {
-  uint32_t ka, va, dva;      // codes: scores' first key; values' first key, from it to the second
-  uint32_t ksa, vsa, dvs;    // scales, likewise
-  uint32_t slots;            // the scores' key | the values' keys << 8, << 16
-};
+// Byte offset of byte b of a slot's codes: 64-byte rows (D = 128) have their four
+// 16-byte chunks permuted by the pair of rows, 32-byte rows lie as they are.
+template <int D>
+__device__ __forceinline__ uint32_t code_off(int slot, int b) {
+  const uint32_t off = static_cast<uint32_t>(slot * (D / 2) + b);
+  return D == 128 ? off ^ (((off >> 7) & 3u) << 4) : off;
+}
+
+// 16 bytes global -> shared, asynchronous.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
@@ -119,6 +121,14 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
   return v;
 }
+
+// What a lane reads of every page (offsets into the page's place in the ring) and
+// the slots of its keys.
+struct LaneQ4 {
+  uint32_t ka, va, dva;      // codes: scores' first key; values' first key, from it to the second
+  uint32_t ksa, vsa, dvs;    // scales, likewise
+  uint32_t slots;            // the scores' key | the values' keys << 8, << 16
+};
 
 // (a & mask) | (b & ~mask)
 __device__ __forceinline__ uint32_t bitsel(uint32_t a, uint32_t b, uint32_t mask) {
@@ -161,14 +171,28 @@ struct StateQ4 {
     }
   }
 
-  // Query row `row` (bf16, D features; nullptr: no such row) of tile n into
-  // fragments: this lane's features are D/4 tig .. D/4 tig + D/4 - 1.
-  __device__ __forceinline__ void load_query(int n, const uint16_t* row, int tig, float scale_log2) {
-    uint2 w[GG::KS];
-    float amax = 0.f;
+  // Query row `row` (bf16, D features; nullptr: no such row) of tile n: this lane's
+  // features D/4 tig .. D/4 tig + D/4 - 1, read now or copied to this lane's places in
+  // shared memory (`at`).
+  static __device__ __forceinline__ void read_query(uint2 (&w)[GG::KS], const uint16_t* row, int tig) {
 #pragma unroll
     for (int ks = 0; ks < GG::KS; ++ks)
       w[ks] = row != nullptr ? *reinterpret_cast<const uint2*>(row + (D / 4) * tig + 4 * ks) : make_uint2(0u, 0u);
+  }
+  static __device__ __forceinline__ void copy_query(uint32_t at, const uint16_t* row, int tig) {
+#pragma unroll
+    for (int ks = 0; ks < GG::KS; ++ks) {
+      if (row != nullptr)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at + 256 * ks), "l"(row + (D / 4) * tig + 4 * ks)
+                     : "memory");
+      else
+        asm volatile("st.shared.v2.b32 [%0], {%1, %1};" ::"r"(at + 256 * ks), "r"(0u) : "memory");
+    }
+  }
+
+  // ... and into fragments of tile n.
+  __device__ __forceinline__ void set_query(int n, const uint2 (&w)[GG::KS], int tig, float scale_log2) {
+    float amax = 0.f;
 #pragma unroll
     for (int ks = 0; ks < GG::KS; ++ks)
       amax = fmaxf(fmaxf(fmaxf(fabsf(bf16_lo(w[ks].x)), fabsf(bf16_hi(w[ks].x))),
@@ -203,59 +227,71 @@ struct StateQ4 {
     fac[n][1] = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
   }
 
-  // One page of this warp's head: its codes at `co`, its scales at `so`, CH bytes
-  // of codes from a key to the one 8 rows on.  EDGE: some row does not see all 16
-  // keys.
-  template <bool EDGE>
-  __device__ __forceinline__ void page(const LaneQ4& ln, uint32_t co, uint32_t so, uint32_t CH, int tb, int L,
-                                       int window) {
-    constexpr int SH = 8 * GG::SROW;
-    const uint32_t ka = co + ln.ka, ksa = so + ln.ksa, va = co + ln.va, vsa = so + ln.vsa;
-    // ---- S^T = K Q^T, in NA independent sums
-    constexpr int NA = NT == 1 ? 2 : 1;
-    float S[NA][NT][4];
+  // NP pages of this warp's head, from ring address `at`.  EDGE (one page): some row
+  // does not see all 16 keys.
+  template <bool EDGE, int NP>
+  __device__ __forceinline__ void page(const LaneQ4& ln, uint32_t at_page, int tb, int L, int window) {
+    static_assert(!EDGE || NP == 1, "edge pages one at a time");
+    constexpr int CH = 8 * GG::ROWB, SH = 8 * GG::SROW;   // from a key to the one 8 rows on
+    // ---- S^T = K Q^T: NP x NA independent sums
+    constexpr int NA = NT == 1 && NP == 1 ? 2 : 1;
+    float S[NP][NA][NT][4];
 #pragma unroll
-    for (int z = 0; z < NA; ++z)
+    for (int g = 0; g < NP; ++g)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) S[z][n][0] = S[z][n][1] = S[z][n][2] = S[z][n][3] = 0.f;
+      for (int z = 0; z < NA; ++z)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) S[g][z][n][0] = S[g][z][n][1] = S[g][z][n][2] = S[g][z][n][3] = 0.f;
     {
-      uint32_t c0[GG::LW], c1[GG::LW], s0, s1;   // codes and scales of the lane's two keys
-      if constexpr (D == 128) {
-        const uint4 a = lds128(ka), b = lds128(ka + CH);
-        c0[0] = a.x; c0[1] = a.y; c0[2] = a.z; c0[3] = a.w;
-        c1[0] = b.x; c1[1] = b.y; c1[2] = b.z; c1[3] = b.w;
-        s0 = e4m3x2_to_f16x2(lds16(ksa));
-        s1 = e4m3x2_to_f16x2(lds16(ksa + SH));
-      } else {
-        const uint2 a = lds64(ka), b = lds64(ka + CH);
-        c0[0] = a.x; c0[1] = a.y;
-        c1[0] = b.x; c1[1] = b.y;
-        s0 = e4m3x2_to_f16x2(lds8(ksa));
-        s1 = e4m3x2_to_f16x2(lds8(ksa + SH));
+      uint32_t c0[NP][GG::LW], c1[NP][GG::LW], s0[NP], s1[NP];   // codes and scales of the lane's two keys
+#pragma unroll
+      for (int g = 0; g < NP; ++g) {
+        const uint32_t ka = at_page + ln.ka + g * GG::PAGE, ksa = at_page + ln.ksa + g * GG::PAGE;
+        if constexpr (D == 128) {
+          const uint4 a = lds128(ka), b = lds128(ka + CH);
+          c0[g][0] = a.x; c0[g][1] = a.y; c0[g][2] = a.z; c0[g][3] = a.w;
+          c1[g][0] = b.x; c1[g][1] = b.y; c1[g][2] = b.z; c1[g][3] = b.w;
+          s0[g] = e4m3x2_to_f16x2(lds16(ksa));
+          s1[g] = e4m3x2_to_f16x2(lds16(ksa + SH));
+        } else {
+          const uint2 a = lds64(ka), b = lds64(ka + CH);
+          c0[g][0] = a.x; c0[g][1] = a.y;
+          c1[g][0] = b.x; c1[g][1] = b.y;
+          s0[g] = e4m3x2_to_f16x2(lds8(ksa));
+          s1[g] = e4m3x2_to_f16x2(lds8(ksa + SH));
+        }
       }
 #pragma unroll
       for (int j = 0; j < GG::LW; ++j) {
-        const uint32_t t0 = j < 2 ? half_lo2(s0) : half_hi2(s0), t1 = j < 2 ? half_lo2(s1) : half_hi2(s1);
-        uint32_t h0[4], h1[4];
-        e2m1x8_to_f16(c0[j], h0);
-        e2m1x8_to_f16(c1[j], h1);
-        const uint32_t a0[4] = {hmul2(h0[0], t0), hmul2(h1[0], t1), hmul2(h0[1], t0), hmul2(h1[1], t1)};
-        const uint32_t a1[4] = {hmul2(h0[2], t0), hmul2(h1[2], t1), hmul2(h0[3], t0), hmul2(h1[3], t1)};
+        uint32_t f[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           if constexpr (QS) {
-            const uint4 f = lds128(qs + (j * NT + n) * 512);
-            mma_f16(S[0][n], a0, f.x, f.y);
-            mma_f16(S[NA - 1][n], a1, f.z, f.w);
+            const uint4 v = lds128(qs + (j * NT + n) * 512);
+            f[n][0] = v.x; f[n][1] = v.y; f[n][2] = v.z; f[n][3] = v.w;
           } else {
-            mma_f16(S[0][n], a0, Qf[2 * j][n][0], Qf[2 * j][n][1]);
-            mma_f16(S[NA - 1][n], a1, Qf[2 * j + 1][n][0], Qf[2 * j + 1][n][1]);
+            f[n][0] = Qf[2 * j][n][0]; f[n][1] = Qf[2 * j][n][1];
+            f[n][2] = Qf[2 * j + 1][n][0]; f[n][3] = Qf[2 * j + 1][n][1];
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < NP; ++g) {
+          const uint32_t t0 = j < 2 ? half_lo2(s0[g]) : half_hi2(s0[g]), t1 = j < 2 ? half_lo2(s1[g]) : half_hi2(s1[g]);
+          uint32_t h0[4], h1[4];
+          e2m1x8_to_f16(c0[g][j], h0);
+          e2m1x8_to_f16(c1[g][j], h1);
+          const uint32_t a0[4] = {hmul2(h0[0], t0), hmul2(h1[0], t1), hmul2(h0[1], t0), hmul2(h1[1], t1)};
+          const uint32_t a1[4] = {hmul2(h0[2], t0), hmul2(h1[2], t1), hmul2(h0[3], t0), hmul2(h1[3], t1)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_f16(S[g][0][n], a0, f[n][0], f[n][1]);
+            mma_f16(S[g][NA - 1][n], a1, f[n][2], f[n][3]);
           }
         }
       }
       if constexpr (NA == 2) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) S[0][0][k] += S[1][0][k];
+        for (int k = 0; k < 4; ++k) S[0][0][0][k] += S[0][1][0][k];
       }
     }
     // ---- softmax weights.  S[n]: (key t0, rows e), (key t0 + 8, rows e).
@@ -264,26 +300,33 @@ struct StateQ4 {
       const int tok = t0 + 8 * (k >> 1), lm = lim[n][k & 1];
       return EDGE && (tok > lm || (window > 0 && tok <= lm - window));
     };
-    float x[NT][4];
+    float x[NP][NT][4];
     float top = -INFINITY;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int g = 0; g < NP; ++g)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[n][k] = fmaf(S[0][n][k], fac[n][k & 1], -m[n][k & 1]);
-        if (hidden(n, k)) x[n][k] = -INFINITY;
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[g][n][k] = fmaf(S[g][0][n][k], fac[n][k & 1], -m[n][k & 1]);
+          if (hidden(n, k)) x[g][n][k] = -INFINITY;
+        }
+        top = fmax3(top, x[g][n][0], x[g][n][1]);
+        top = fmax3(top, x[g][n][2], x[g][n][3]);
       }
-      top = fmax3(top, x[n][0], x[n][1]);
-      top = fmax3(top, x[n][2], x[n][3]);
-    }
     if (__any_sync(0xffffffffu, top > kMoveMax)) {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float a = hidden(n, e) ? -INFINITY : S[0][n][e] * fac[n][e];
-          const float b = hidden(n, 2 + e) ? -INFINITY : S[0][n][2 + e] * fac[n][e];
-          float mn = fmaxf(a, b);
+          float mn = -INFINITY;
+#pragma unroll
+          for (int g = 0; g < NP; ++g)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              x[g][n][2 * h + e] = hidden(n, 2 * h + e) ? -INFINITY : S[g][0][n][2 * h + e] * fac[n][e];
+              mn = fmaxf(mn, x[g][n][2 * h + e]);
+            }
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
           mn = fmaxf(m[n][e], mn);
@@ -295,98 +338,100 @@ struct StateQ4 {
             O[i][n][e] *= al;
             O[i][n][2 + e] *= al;
           }
-          x[n][e] = a - mn;
-          x[n][2 + e] = b - mn;
+#pragma unroll
+          for (int g = 0; g < NP; ++g) {
+            x[g][n][e] -= mn;
+            x[g][n][2 + e] -= mn;
+          }
         }
     }
-    uint32_t Pb[NT][2];               // P^T as B fragments: keys 2 tig, 2 tig + 1 (+ 8) of row gq
+    uint32_t Pb[NP][NT][2];           // P^T as B fragments: keys 2 tig, 2 tig + 1 (+ 8) of row gq
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int g = 0; g < NP; ++g)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[n][k] = fast_exp2(x[n][k]);
-      l[n][0] += x[n][0] + x[n][2];
-      l[n][1] += x[n][1] + x[n][3];
-      Pb[n][0] = transpose8x8(pack_f16(x[n][0], x[n][1]));
-      Pb[n][1] = transpose8x8(pack_f16(x[n][2], x[n][3]));
-    }
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[g][n][k] = fast_exp2(x[g][n][k]);
+        l[n][0] += x[g][n][0] + x[g][n][2];
+        l[n][1] += x[g][n][1] + x[g][n][3];
+        Pb[g][n][0] = transpose8x8(pack_f16(x[g][n][0], x[g][n][1]));
+        Pb[g][n][1] = transpose8x8(pack_f16(x[g][n][2], x[g][n][3]));
+      }
     // ---- O^T += V^T P^T.  This lane's keys: tile rows 2 tig, 2 tig + 1, + 8; its
     // features: D/8 gq .. D/8 gq + D/8 - 1, of one scale group.
-    const uint32_t vsb = vsa + ln.dvs, vb = va + ln.dva;
-    uint32_t sc[4] = {lds8(vsa), lds8(vsb), lds8(vsa + SH), lds8(vsb + SH)};
-    if constexpr (EDGE) {
-      // Keys that no row sees take scale 0, so that nothing they hold meets
-      // P = 0.  A NaN scale of a key that only some rows see is set aside: its
-      // value is 0 here, and the rows that do see it become NaN.
-      const int v0 = static_cast<int>(ln.slots >> 8 & 255u), v1 = static_cast<int>(ln.slots >> 16);
-      const int tok[4] = {tb + v0, tb + v1, tb + v0 + 8, tb + v1 + 8};
-      bool bad = false;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const bool nan = (sc[k] & 0x7Fu) == 0x7Fu;
-        bad |= nan && tok[k] < L;
-        if (nan || tok[k] >= L) sc[k] = 0u;
-      }
-      if (__any_sync(0xffffffffu, bad)) {
-        const uint32_t col = vsa - static_cast<uint32_t>(v0 * GG::SROW);   // slot 0 of the lane's group
-        for (int s = 0; s < kPage && tb + s < L; ++s) {
-          if ((lds8(col + s * GG::SROW) & 0x7Fu) != 0x7Fu) continue;
+    for (int g = 0; g < NP; ++g) {
+      const uint32_t va = at_page + ln.va + g * GG::PAGE, vsa = at_page + ln.vsa + g * GG::PAGE;
+      const uint32_t vsb = vsa + ln.dvs, vb = va + ln.dva;
+      uint32_t sc[4] = {lds8(vsa), lds8(vsb), lds8(vsa + SH), lds8(vsb + SH)};
+      if constexpr (EDGE) {
+        // Keys that no row sees take scale 0, so that nothing they hold meets
+        // P = 0.  A NaN scale of a key that only some rows see is set aside: its
+        // value is 0 here, and the rows that do see it become NaN.
+        const int v0 = static_cast<int>(ln.slots >> 8 & 255u), v1 = static_cast<int>(ln.slots >> 16);
+        const int tok[4] = {tb + v0, tb + v1, tb + v0 + 8, tb + v1 + 8};
+        bool bad = false;
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+        for (int k = 0; k < 4; ++k) {
+          const bool nan = (sc[k] & 0x7Fu) == 0x7Fu;
+          bad |= nan && tok[k] < L;
+          if (nan || tok[k] >= L) sc[k] = 0u;
+        }
+        if (__any_sync(0xffffffffu, bad)) {
+          const uint32_t col = vsa - static_cast<uint32_t>(v0 * GG::SROW);   // slot 0 of the lane's group
+          for (int s = 0; s < kPage && tb + s < L; ++s) {
+            if ((lds8(col + s * GG::SROW) & 0x7Fu) != 0x7Fu) continue;
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (tb + s <= lim[n][e] && !(window > 0 && tb + s <= lim[n][e] - window)) {
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < GG::KS; ++i) {
-                  O[i][n][e] = __uint_as_float(0x7FC00000u);
-                  O[i][n][2 + e] = __uint_as_float(0x7FC00000u);
+              for (int e = 0; e < 2; ++e)
+                if (tb + s <= lim[n][e] && !(window > 0 && tb + s <= lim[n][e] - window)) {
+#pragma unroll
+                  for (int i = 0; i < GG::KS; ++i) {
+                    O[i][n][e] = __uint_as_float(0x7FC00000u);
+                    O[i][n][2 + e] = __uint_as_float(0x7FC00000u);
+                  }
                 }
-              }
+          }
         }
       }
-    }
-    const uint32_t sa = e4m3x2_to_f16x2(prmt(sc[0], sc[1], 0x0040u)), sb = e4m3x2_to_f16x2(prmt(sc[2], sc[3], 0x0040u));
-    constexpr int VW = D / 64;        // words of codes a lane reads of each key
-    uint32_t w[4][VW];
+      const uint32_t sa = e4m3x2_to_f16x2(prmt(sc[0], sc[1], 0x0040u));
+      const uint32_t sb = e4m3x2_to_f16x2(prmt(sc[2], sc[3], 0x0040u));
+      constexpr int VW = D / 64;        // words of codes a lane reads of each key
+      uint32_t w[4][VW];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t at = (k & 1 ? vb : va) + (k >> 1) * CH;
-      if constexpr (D == 128) {
-        const uint2 v = lds64(at);
-        w[k][0] = v.x;
-        w[k][1] = v.y;
-      } else {
-        w[k][0] = lds32(at);
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t at = (k & 1 ? vb : va) + (k >> 1) * CH;
+        if constexpr (D == 128) {
+          const uint2 v = lds64(at);
+          w[k][0] = v.x;
+          w[k][1] = v.y;
+        } else {
+          w[k][0] = lds32(at);
+        }
       }
-    }
 #pragma unroll
-    for (int j = 0; j < VW; ++j) {
-      uint32_t a0[4], a1[4], a2[4], a3[4];
-      // even features of two keys side by side, then odd features
-      e2m1x8_to_f16(bitsel(w[0][j], w[1][j] * 16u, 0x0F0F0F0Fu), a0);
-      e2m1x8_to_f16(bitsel(w[0][j] >> 4, w[1][j], 0x0F0F0F0Fu), a1);
-      e2m1x8_to_f16(bitsel(w[2][j], w[3][j] * 16u, 0x0F0F0F0Fu), a2);
-      e2m1x8_to_f16(bitsel(w[2][j] >> 4, w[3][j], 0x0F0F0F0Fu), a3);
+      for (int j = 0; j < VW; ++j) {
+        uint32_t a0[4], a1[4], a2[4], a3[4];
+        // even features of two keys side by side, then odd features
+        e2m1x8_to_f16(bitsel(w[0][j], w[1][j] * 16u, 0x0F0F0F0Fu), a0);
+        e2m1x8_to_f16(bitsel(w[0][j] >> 4, w[1][j], 0x0F0F0F0Fu), a1);
+        e2m1x8_to_f16(bitsel(w[2][j], w[3][j] * 16u, 0x0F0F0F0Fu), a2);
+        e2m1x8_to_f16(bitsel(w[2][j] >> 4, w[3][j], 0x0F0F0F0Fu), a3);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const uint32_t a[4] = {hmul2(a0[u], sa), hmul2(a1[u], sa), hmul2(a2[u], sb), hmul2(a3[u], sb)};
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t a[4] = {hmul2(a0[u], sa), hmul2(a1[u], sa), hmul2(a2[u], sb), hmul2(a3[u], sb)};
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma_f16(O[4 * j + u][n], a, Pb[n][0], Pb[n][1]);
+          for (int n = 0; n < NT; ++n) mma_f16(O[4 * j + u][n], a, Pb[g][n][0], Pb[g][n][1]);
+        }
       }
     }
   }
 };
 
-// mbar_wait that sleeps about NS nanoseconds between tries: a try takes about 27
-// cycles, and warps that poll without a pause took a third of the CTA's issue slots.
-template <int NS>
-__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  for (;;) {
-    __nanosleep(NS);
-    if (mbar_try_wait(bar, parity)) return true;
-    if (global_timer_ns() - t0 > limit_ns) return false;
-  }
+// Barrier of the KW warps of a team (all of them come by at every segment's end).
+__device__ __forceinline__ void team_sync(int team, int kw_warps) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * kw_warps) : "memory");
 }
 
 // A segment: the pages [j0, j1) of unit (sequence i, head chunk c) in a CTA's range.
@@ -411,46 +456,34 @@ __device__ __forceinline__ void next_unit(Cursor& cu, const int32_t* pre, int B,
   advance(cu, pre, B, NC);
 }
 
-template <int D, int NT, bool WINDOW>
-__global__ void __launch_bounds__(32 * (4 + q4_warps(NT)), 1)
-    pa_split_q4_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                       const __grid_constant__ SplitQ4Params p) {
-  using GG = GeoQ4<D>;
-  constexpr int CW = q4_warps(NT);
-  const int window = WINDOW ? p.window : 0;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ int s_scan[4 + CW];
-  __shared__ int s_total;
+template <bool V>
+struct Bool {
+  static constexpr bool value = V;
+};
 
-  const uint32_t raw = smem_addr(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* const gbase = smem_raw + (base - raw);
-  int32_t* const s_pre = reinterpret_cast<int32_t*>(gbase + p.off_prefix);
+// A warp's fetch state between segments.
+struct FetchQ4 {
+  Cursor cu;             // the unit after the segment
+  int64_t left;          // pages of the CTA's range from there on
+  int n, i, j;           // pages of the segment whose ids are yet to come, its sequence, the first of them
+  int ahead_i, ahead_j;  // sequence and page of the ids loaded ahead (-1: none)
+};
+
+template <int D, int NT, bool WINDOW>
+__global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
+    pa_split_q4_kernel(const __grid_constant__ SplitQ4Params p) {
+  using GG = GeoQ4<D>;
+  constexpr int S = q4_stages(D);
+  const int window = WINDOW ? p.window : 0;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int s_scan[kQ4Warps];
+  __shared__ int s_total;
+  int32_t* const s_pre = reinterpret_cast<int32_t*>(smem + p.off_prefix);
   int32_t* const s_len = s_pre + (p.num_seqs + 1);
   int32_t* const s_qsl = s_len + p.num_seqs;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int B = p.num_seqs, HC = p.HC, NC = p.NC, MT = p.MT, KW = p.KW, BP = p.block_pages;
-  const int nstage = p.nstage, ncw = HC * MT * KW;
-  const uint32_t bar0 = base + p.off_bar;
-  auto full_bar = [&](int s) { return bar0 + 8u * s; };
-  auto empty_bar = [&](int s) { return bar0 + 8u * (nstage + s); };
-  // teams (the KW warps of a head and row tile): partials written / read
-  auto put_bar = [&](int t) { return bar0 + 8u * (2 * nstage + t); };
-  auto got_bar = [&](int t) { return bar0 + 8u * (2 * nstage + CW + t); };
-  if (tid == 0) {
-    prefetch_tensormap(&tmap_k);
-    prefetch_tensormap(&tmap_v);
-    for (int s = 0; s < nstage; ++s) {
-      mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), HC * MT);   // one kw's warps
-    }
-    for (int t = 0; t < HC * MT; ++t) {
-      mbar_init(put_bar(t), KW);
-      mbar_init(got_bar(t), KW);
-    }
-    fence_mbar_init();
-  }
+  const int B = p.num_seqs, HC = p.HC, NC = p.NC, MT = p.MT, KW = p.KW;
   grid_dependency_wait();
   page_prefix(p, window, s_pre, s_len, s_qsl, s_scan, &s_total, true);
   __syncthreads();
@@ -468,179 +501,226 @@ __global__ void __launch_bounds__(32 * (4 + q4_warps(NT)), 1)
   if (g >= NG || X == 0) return;
   const int64_t start = static_cast<int64_t>(g) * X / NG;
   const int64_t end = static_cast<int64_t>(g + 1) * X / NG;
-  int64_t left = end - start;
-  if (left <= 0) return;
-  const uint32_t code_page = static_cast<uint32_t>(HC * GG::TILE), scale_page = static_cast<uint32_t>(HC * GG::STILE);
-
-  if (warp < 4) {
-    // ============================ producers ================================
-    // Four warps share the stages, warp w those with s % 4 == w (issuing one copy
-    // holds a warp for 280 to 540 cycles beside warps that compute: one producer
-    // fed 5.0 TB/s at most).  A stage has one warp for good, so that its waiter has
-    // seen every earlier phase of its barrier: a parity wait cannot tell a phase
-    // that is two behind from one that is complete.  One lane issues a group's
-    // copies.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(RegsQ4<NT>::PROD));
-    if (warp >= nstage) return;
-    const int box_rows = static_cast<int>(code_page) / (kPage * p.box_bytes);
-    Cursor cu = locate(s_pre, B, NC, start);
-    int mine = warp;                   // this warp's next stage, ...
-    uint32_t turn = 0;                 // its turn, ...
-    int next = warp;                   // and the groups until then, from the segment's first
-    while (left > 0) {
-      const SegmentQ4 sg = segment_at(cu, left);
-      left -= sg.j1 - sg.j0;
-      next_unit(cu, s_pre, B, NC);
-      const int pages = sg.j1 - sg.j0, groups = (pages + BP - 1) / BP;
-      const int32_t* row = p.block_tables + static_cast<int64_t>(sg.i) * p.bt_stride + sg.j0 +
-                           first_visible_page(s_len[sg.i], s_qsl[sg.i + 1] - s_qsl[sg.i], window);
-      // page ids of a group, one a lane, loaded a group ahead
-      int ids = lane < BP && next * BP + lane < pages ? row[next * BP + lane] : 0;
-      while (next < groups) {
-        const int now = ids, np = min(BP, pages - next * BP);
-        const int at_stage = mine;
-        const uint32_t at_turn = turn;
-        // the next group of this warp: its next stage, or its first of the next turn
-        mine += 4;
-        next += 4;
-        if (mine >= nstage) {
-          next += nstage - mine + warp;
-          mine = warp;
-          ++turn;
-        }
-        if (lane < BP && next * BP + lane < pages) ids = row[next * BP + lane];
-        if (at_turn > 0 && !mbar_poll<100>(empty_bar(at_stage), (at_turn - 1) & 1u, p.wait_ns)) {
-          if (lane == 0) atomicOr(p.err, kErrTimeout);
-          return;
-        }
-        const uint32_t bar = full_bar(at_stage);
-        uint32_t dst = base + p.off_stage + static_cast<uint32_t>(at_stage) * p.stage_bytes, dst_sc = dst + p.off_ks;
-        if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(np) * 2u * (code_page + scale_page));
-        for (int pg = 0; pg < np; ++pg) {
-          const int phys = __shfl_sync(0xffffffffu, now, pg);
-          if (lane == 0) {
-            // an out-of-range page reads as zero codes (TMA fill) and page 0's scales
-            const bool bad = phys < 0 || phys >= p.num_pages;
-            if (bad) atomicOr(p.err, kErrPageRange);
-            const int64_t id = bad ? 0 : phys, at = static_cast<int64_t>(sg.c) * scale_page;
-            tma_load_4d(dst, &tmap_k, 0, sg.c * box_rows, 0, phys, bar);
-            tma_load_4d(dst + p.off_v, &tmap_v, 0, sg.c * box_rows, 0, phys, bar);
-            bulk_load(dst_sc, p.k_sc + id * p.k_sc_page + at, scale_page, bar);
-            bulk_load(dst_sc + (p.off_vs - p.off_ks), p.v_sc + id * p.v_sc_page + at, scale_page, bar);
-          }
-          dst += code_page;
-          dst_sc += scale_page;
-        }
-      }
-      next -= groups;
-    }
-    return;
-  }
-
-  // ============================== consumers ================================
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(RegsQ4<NT>::CONS));
-  const int cw = warp - 4;
-  if (cw >= ncw) return;
-  Cursor cu = locate(s_pre, B, NC, start);
-  const int team = cw % (HC * MT), kw = cw / (HC * MT);
+  const int teams = HC * MT;
+  if (end <= start || warp >= teams * KW) return;
+  const int team = warp % teams, kw = warp / teams, lg_kw = __ffs(KW) - 1;
   const int hh = team / MT, wt = team - hh * MT;
   const int gq = lane >> 2, tig = lane & 3;
   const int G = p.G, row0 = 8 * NT * wt;
-  const int slot_bytes = HC * GG::ROWB;
-  const uint32_t CH = static_cast<uint32_t>(8 * slot_bytes);
+  const uint32_t ring = smem_addr(smem) + static_cast<uint32_t>(warp * p.nstage * GG::PAGE);
+
+  // ---- the fetch side: this warp's pages (kw, kw + KW, ... of every segment) in
+  // order, p.nstage of them ahead of the computation.  `ids` holds 32 page ids, one a
+  // lane; the 32 that follow are loaded ahead.  What only a new segment or a new 32
+  // ids need waits in shared memory (every lane stores the same values).
+  FetchQ4* const fst = reinterpret_cast<FetchQ4*>(smem + p.off_state) + warp;
+  fst->cu = locate(s_pre, B, NC, start);
+  fst->left = end - start;
+  fst->n = 0;
+  fst->ahead_i = -1;
+  __syncwarp();
+  int ids = 0, nids = 0, flane = 0, fstop = 0;   // the next id's lane, and the lanes that hold one (< 0: no page left)
+  // this lane's part of a page: rows lane / CPR (and RPI on, ...) of the codes, 16 bytes;
+  // the scales' copy takes the first SL lanes for K and the next for V
+  constexpr int CPR = GG::ROWB / 16, RPI = 32 / CPR, SL = GG::STILE / 16;
+  const uint32_t dlane = code_off<D>(lane / CPR, lane % CPR * 16);
+  const uint8_t *kp = nullptr, *vp = nullptr, *sp = nullptr;   // in page 0, of the segment's head
+  auto ids_of = [&](int i, int j) {
+    const int x = j + lane * KW;
+    return x < pages_of(s_pre, i)
+               ? p.block_tables[static_cast<int64_t>(i) * p.bt_stride + x +
+                                first_visible_page(s_len[i], s_qsl[i + 1] - s_qsl[i], window)]
+               : 0;
+  };
+  auto refill = [&]() {             // the next ids of the segment, or those of the next segment with pages for this warp
+    int n = fst->n, i = fst->i, j = fst->j;      // pages of the segment not yet in `ids`, from page j on
+    Cursor c = fst->cu;
+    int64_t rest = fst->left;
+    if (n == 0) {
+      SegmentQ4 s;
+      while (n == 0 && rest > 0) {
+        s = segment_at(c, rest);
+        rest -= s.j1 - s.j0;
+        next_unit(c, s_pre, B, NC);
+        n = (s.j1 - s.j0 - kw + KW - 1) >> lg_kw;
+      }
+      if (n == 0) {
+        fstop = -1;
+        return;
+      }
+      i = s.i;
+      j = s.j0 + kw;
+      const int head = s.c * HC + hh;
+      kp = p.k_codes + lane / CPR * p.kc_stride_slot + lane % CPR * 16 + head * p.kc_stride_head;
+      vp = p.v_codes + lane / CPR * p.vc_stride_slot + lane % CPR * 16 + head * p.vc_stride_head;
+      sp = (lane < SL ? p.k_sc + lane * 16 : p.v_sc + (lane - SL) * 16) + static_cast<int64_t>(head) * GG::STILE;
+    }
+    ids = fst->ahead_i == i && fst->ahead_j == j ? nids : ids_of(i, j);
+    flane = 0;
+    fstop = min(n, 32);
+    if (lane < fstop && static_cast<uint32_t>(ids) >= static_cast<uint32_t>(p.num_pages)) {
+      atomicOr(p.err, kErrPageRange);             // no such page: page 0's contents instead
+      ids = 0;
+    }
+    n -= fstop;
+    j += 32 * KW;
+    const int ni = n > 0 ? i : (rest > 0 ? c.i : -1), nj = n > 0 ? j : kw;
+    if (ni >= 0) nids = ids_of(ni, nj);
+    __syncwarp();
+    fst->cu = c;
+    fst->left = rest;
+    fst->n = n;
+    fst->i = i;
+    fst->j = j;
+    fst->ahead_i = ni;
+    fst->ahead_j = nj;
+    __syncwarp();
+  };
+  const uint32_t s_page = lane < SL ? p.k_sc_page : p.v_sc_page;
+  auto fetch = [&](uint32_t dst) {                // one page (or none: an empty group)
+    if (flane == fstop) refill();
+    if (fstop >= 0) {
+      const uint32_t id = static_cast<uint32_t>(__shfl_sync(0xffffffffu, ids, flane));
+      ++flane;
+      const uint8_t* k = kp + static_cast<uint64_t>(id) * p.kc_stride_page;
+      const uint8_t* v = vp + static_cast<uint64_t>(id) * p.vc_stride_page;
+#pragma unroll
+      for (int r = 0; r < 16; r += RPI) {
+        copy16(dst + dlane + r * GG::ROWB, k + r * p.kc_stride_slot);
+        copy16(dst + dlane + GG::V + r * GG::ROWB, v + r * p.vc_stride_slot);
+      }
+      if (lane < 2 * SL) copy16(dst + GG::KSC + lane * 16, sp + static_cast<uint64_t>(id) * s_page);
+    }
+    copy_commit();
+  };
+
+  // ---- the compute side
   LaneQ4 ln;
   {
-    const int r0 = slot_of<D>(gq, slot_bytes), v0 = slot_of<D>(2 * tig, slot_bytes), v1 = slot_of<D>(2 * tig + 1, slot_bytes);
-    ln.ka = code_off(r0, hh * GG::ROWB + D / 8 * tig, slot_bytes, p.box_bytes);
-    ln.va = p.off_v + code_off(v0, hh * GG::ROWB + D / 16 * gq, slot_bytes, p.box_bytes);
-    ln.dva = p.off_v + code_off(v1, hh * GG::ROWB + D / 16 * gq, slot_bytes, p.box_bytes) - ln.va;
-    ln.ksa = p.off_ks + hh * GG::STILE + r0 * GG::SROW + (D == 128 ? 2 * tig : tig);
-    ln.vsa = p.off_vs + hh * GG::STILE + v0 * GG::SROW + (D == 128 ? gq : gq >> 1);
+    const int r0 = slot_of<D>(gq), v0 = slot_of<D>(2 * tig), v1 = slot_of<D>(2 * tig + 1);
+    ln.ka = code_off<D>(r0, D / 8 * tig);
+    ln.va = GG::V + code_off<D>(v0, D / 16 * gq);
+    ln.dva = GG::V + code_off<D>(v1, D / 16 * gq) - ln.va;
+    ln.ksa = GG::KSC + r0 * GG::SROW + (D == 128 ? 2 * tig : tig);
+    ln.vsa = GG::VSC + v0 * GG::SROW + (D == 128 ? gq : gq >> 1);
     ln.dvs = static_cast<uint32_t>((v1 - v0) * GG::SROW);
     ln.slots = static_cast<uint32_t>(r0 | v0 << 8 | v1 << 16);
   }
   StateQ4<D, NT, q4_query_in_smem(NT)> cs;
-  cs.qs = base + p.off_q + static_cast<uint32_t>(cw) * q4_query_bytes(D, NT) + 16u * lane;
+  const uint32_t q_smem = smem_addr(smem) + p.off_q + static_cast<uint32_t>(warp) * q4_query_bytes(D, NT);
+  cs.qs = q_smem + 16u * lane;
+  // rows of a KV head are numbered (query token, head of the group): row / G by a
+  // product (exact for the at most 128 rows of a head's tiles)
+  const uint32_t g_inv = (65536u + G - 1u) / static_cast<uint32_t>(G);
+  auto token_of = [&](int rho) { return static_cast<int>(static_cast<uint32_t>(rho) * g_inv >> 16); };
+  Cursor cu = fst->cu;
+  int64_t left = fst->left;
+  SegmentQ4 sg = segment_at(cu, left);
+  SeqInfo si = seq_info(p, s_len, s_qsl, sg.i, lane == 0 && warp == 0, window);
+  auto row_at = [&](const SegmentQ4& s, const SeqInfo& q, int n) {
+    const int rho = row0 + 8 * n + gq, t = token_of(rho);
+    return t < q.qn ? p.q + static_cast<int64_t>(q.t0 + t) * p.q_stride_t + ((s.c * HC + hh) * G + rho - t * G) * D
+                    : nullptr;
+  };
+  // the next segment's query rows: copied to shared memory, or only towards L2
+  auto query_ahead = [&](const SegmentQ4& s, const SeqInfo& q) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint16_t* row = row_at(s, q, n);
+      if constexpr (q4_query_in_smem(NT)) {
+        if (row != nullptr) prefetch_l2(row + (D / 4) * tig);
+      } else {
+        cs.copy_query(q_smem + 8u * lane + n * (GG::KS * 256), row, tig);
+      }
+    }
+    copy_commit();
+  };
+  query_ahead(sg, si);
+  const uint32_t ring_end = ring + static_cast<uint32_t>(p.nstage * GG::PAGE);
+  for (uint32_t a = ring; a < ring_end; a += GG::PAGE) fetch(a);
+  uint32_t at = ring;               // the page to compute
+  int since = 0;                    // groups committed since the rows of the next segment were
   bool first = true;
-  int mine = kw, next = kw;     // this warp's next stage, and the groups until then
-  uint32_t turn = 0, seg_no = 0;
-  while (left > 0) {
-    const SegmentQ4 sg = segment_at(cu, left);
+  for (;;) {
     left -= sg.j1 - sg.j0;
-    next_unit(cu, s_pre, B, NC);
-    const SeqInfo si = seq_info(p, s_len, s_qsl, sg.i, lane == 0 && cw == 0, window);
     const int R = G * si.qn, min_lim = si.L - si.qn;
     const bool active = row0 < R;
     const int hq_base = (sg.c * HC + hh) * G;
-    if (sg.j0 == 0 && cw == 0 && lane == 0) {
+    if (sg.j0 == 0 && warp == 0 && lane == 0) {
       // this CTA holds the unit's first page: describe the unit for the merge
       const int64_t a = static_cast<int64_t>(NC) * s_pre[sg.i] + static_cast<int64_t>(sg.c) * sg.n;
       const int last_cta = static_cast<int>(((a + sg.n) * NG - 1) / X);
       p.ws_unit[static_cast<int64_t>(sg.i) * NC + sg.c] =
           make_int4(g, (last_cta - g + 1) | (first ? 0 : (1 << 30)), si.t0, si.qn);
     }
+    if (!q4_query_in_smem(NT)) {
+      if (first && p.nstage == S) copy_wait<S>();  // all but the pages behind them
+      else if (since < p.nstage) copy_wait<0>();  // else the waits for pages have covered them
+    }
     if (active) {
       cs.reset();
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int rho = row0 + 8 * n + gq;
-        const uint16_t* row = nullptr;
-        if (rho < R) row = p.q + static_cast<int64_t>(si.t0 + rho / G) * p.q_stride_t + (hq_base + rho % G) * D;
-        cs.load_query(n, row, tig, p.scale_log2);
+        uint2 w[GG::KS];
+        if constexpr (q4_query_in_smem(NT)) {
+          cs.read_query(w, row_at(sg, si, n), tig);
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < GG::KS; ++ks) w[ks] = lds64(q_smem + 8u * lane + (n * GG::KS + ks) * 256);
+        }
+        cs.set_query(n, w, tig, p.scale_log2);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r2 = row0 + 8 * n + 2 * tig + e;
-          cs.lim[n][e] = min_lim + (r2 < R ? r2 / G : 0);
+          const int r2 = row0 + 8 * n + 2 * tig + e, t = token_of(r2);
+          cs.lim[n][e] = min_lim + (r2 < R ? t : 0);
           if (p.sinks != nullptr && sg.j0 == 0 && kw == 0 && r2 < R) {
             // the sink: a virtual first key with a zero value row
-            const float sk = p.sinks[hq_base + r2 % G] * 1.4426950408889634f;
+            const float sk = p.sinks[hq_base + r2 - t * G] * 1.4426950408889634f;
             cs.m[n][e] = fmaxf(sk, kUnsetMax);
             cs.l[n][e] = gq == 0 && sk != -INFINITY ? 1.f : 0.f;
           }
         }
       }
     }
+    SegmentQ4 ns = sg;
+    SeqInfo ni = si;
+    if (left > 0) {
+      next_unit(cu, s_pre, B, NC);
+      ns = segment_at(cu, left);
+      ni = seq_info(p, s_len, s_qsl, ns.i, lane == 0 && warp == 0, window);
+      query_ahead(ns, ni);
+    }
     {
-      // the segment's pages in groups of BP, a stage each; this warp's groups are
-      // those in the stages s with s % KW == kw (nstage is a multiple of KW), so
-      // that it waits for every phase of their barriers.  edge_lo .. edge_hi: the
-      // pages (by first token) whose keys every row sees
-      const int tb0 = kPage * (si.js + sg.j0), tb_end = kPage * (si.js + sg.j1);
-      const int groups = (sg.j1 - sg.j0 + BP - 1) / BP;
-      const int edge_hi = min_lim - (kPage - 1), edge_lo = WINDOW ? si.L - window : 0;
-      for (; next < groups; next += KW) {
-        if (!mbar_poll<40>(full_bar(mine), turn & 1u, p.wait_ns)) {
-          if (lane == 0) atomicOr(p.err, kErrTimeout);
-          return;
+      // this warp's pages by their first tokens: below `lo` or from `hi` on some row
+      // does not see all keys
+      constexpr int step = kPage;
+      const int t0 = kPage * (si.js + sg.j0 + kw), t_end = kPage * (si.js + sg.j1);
+      const int lo = WINDOW ? min(t_end, si.L - window) : 0, hi = min(t_end, min_lim - (kPage - 2));
+      int t = t0;
+      auto run = [&](auto edge, int stop) {
+        for (; t < stop; t += step * KW) {
+          if (p.nstage == S) copy_wait<S - 1>();
+          else copy_wait<kQ4ShallowStages - 1>();
+          __syncwarp();
+          if (active) cs.template page<decltype(edge)::value, 1>(ln, at, t, si.L, window);
+          __syncwarp();
+          fetch(at);
+          at += GG::PAGE;
+          if (at == ring_end) at = ring;
         }
-        if (active) {
-          uint32_t co = base + p.off_stage + static_cast<uint32_t>(mine) * p.stage_bytes, so = co;
-          int t = tb0 + kPage * BP * next;
-          const int tb_stop = min(t + kPage * BP, tb_end);
-          for (; t < tb_stop; t += kPage) {
-            if (t > edge_hi || (WINDOW && t < edge_lo))
-              cs.template page<true>(ln, co, so, CH, t, si.L, window);
-            else
-              cs.template page<false>(ln, co, so, CH, t, si.L, window);
-            co += code_page;
-            so += scale_page;
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty_bar(mine));
-        mine += KW;
-        if (mine >= nstage) {
-          mine = kw;
-          ++turn;
-        }
-      }
-      next -= groups;
+      };
+      if (WINDOW) run(Bool<true>{}, lo);
+      run(Bool<false>{}, hi);
+      run(Bool<true>{}, t_end);
+      since = t > t0 ? (t - t0) / (step * KW) : 0;
     }
     // ---- end of the segment
     const bool complete = sg.j0 == 0 && sg.j1 == sg.n;
-    const int which = first ? 0 : 1;
+    const int64_t ws_row = (static_cast<int64_t>(2 * g + (first ? 0 : 1)) * HC + hh) * p.R_max + row0;
+    const int t_first = si.t0;
     first = false;
-    const int64_t ws_row = (static_cast<int64_t>(2 * g + which) * HC + hh) * p.R_max + row0;
+    sg = ns;
+    si = ni;
     constexpr int FPL = D / 8;        // features a lane holds of each of its rows
     if (active) {
 #pragma unroll
@@ -653,23 +733,19 @@ __global__ void __launch_bounds__(32 * (4 + q4_warps(NT)), 1)
     // KW warps of a team meet: warp kw gathers the features of the lanes with
     // gq / (8 / KW) == kw, so every warp leaves the other lanes' rows in shared
     // memory: [rows of the tile][features it does not gather].
-    const int per = 8 / (KW > 8 ? 8 : KW);                       // gq values a warp gathers
-    const bool mine = KW == 1 || gq / per == kw;
+    const int per = 8 >> lg_kw;                                  // gq values a warp gathers
+    const bool gathers = gq >> (3 - lg_kw) == kw;
     if (KW > 1) {
       constexpr int WROWS = 8 * NT;
       const int cols = FPL * (8 - per) + 4;                      // floats between rows (16-byte aligned)
       const uint32_t warp_bytes = static_cast<uint32_t>(WROWS * cols * 4 + WROWS * 8);
       auto ml_of = [&](int k) {
-        return reinterpret_cast<float2*>(gbase + p.off_xchg + (team + k * HC * MT) * warp_bytes);
+        return reinterpret_cast<float2*>(smem + p.off_xchg + (team + k * teams) * warp_bytes);
       };
       // features of lane row q in warp k's rows (k does not gather them)
       auto row_of = [&](int k, int rl, int q) {
-        return reinterpret_cast<float*>(ml_of(k) + WROWS) + rl * cols + FPL * (q / per > k ? q - per : q);
+        return reinterpret_cast<float*>(ml_of(k) + WROWS) + rl * cols + FPL * (q >> (3 - lg_kw) > k ? q - per : q);
       };
-      if (seg_no > 0 && !mbar_poll<40>(got_bar(team), (seg_no - 1) & 1u, p.wait_ns)) {
-        if (lane == 0) atomicOr(p.err, kErrTimeout);
-        return;
-      }
       if (active) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -677,7 +753,7 @@ __global__ void __launch_bounds__(32 * (4 + q4_warps(NT)), 1)
           for (int e = 0; e < 2; ++e) {
             const int rl = 8 * n + 2 * tig + e;
             if (gq == 0) ml_of(kw)[rl] = make_float2(cs.m[n][e], cs.l[n][e]);
-            if (mine) continue;
+            if (gathers) continue;
             float* o = row_of(kw, rl, gq);
 #pragma unroll
             for (int i = 0; i < GG::KS; i += 2)
@@ -685,13 +761,8 @@ __global__ void __launch_bounds__(32 * (4 + q4_warps(NT)), 1)
                   make_float4(cs.O[i][n][e], cs.O[i][n][2 + e], cs.O[i + 1][n][e], cs.O[i + 1][n][2 + e]);
           }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(put_bar(team));
-      if (!mbar_poll<40>(put_bar(team), seg_no & 1u, p.wait_ns)) {
-        if (lane == 0) atomicOr(p.err, kErrTimeout);
-        return;
-      }
-      if (active && mine) {
+      team_sync(team, KW);
+      if (active && gathers) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -725,21 +796,18 @@ __global__ void __launch_bounds__(32 * (4 + q4_warps(NT)), 1)
             cs.l[n][e] = lt;
           }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(got_bar(team));
-      ++seg_no;
+      team_sync(team, KW);             // read: the next segment may write
     }
-    if (!active || !mine) continue;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int rl = 8 * n + 2 * tig + e, rho = row0 + rl;
-        if (rho >= R) continue;
+        if (rho >= R || !gathers) continue;
         const float lt = cs.l[n][e], mm = cs.m[n][e];
         if (complete) {
-          const int t = si.t0 + rho / G, hq = hq_base + rho % G;
-          const float inv = lt == 0.f ? 0.f : p.v_scale / lt;
+          const int tk = token_of(rho), t = t_first + tk, hq = hq_base + rho - tk * G;
+          const float inv = lt == 0.f ? 0.f : __fdividef(p.v_scale, lt);
           uint16_t* o = p.out + static_cast<int64_t>(t) * p.out_stride_t + static_cast<int64_t>(hq) * p.out_stride_h +
                         FPL * gq;
 #pragma unroll
@@ -759,24 +827,24 @@ __global__ void __launch_bounds__(32 * (4 + q4_warps(NT)), 1)
           if (gq == 0) p.ws_ml[ws_row + rl] = make_float2(mm, lt);
         }
       }
+    if (left <= 0) return;
   }
 }
 
 namespace {
 
 template <int D, int NT>
-cudaError_t launch_nt(cudaLaunchConfig_t* cfg, const CUtensorMap& tk, const CUtensorMap& tv, const SplitQ4Params& p) {
-  cfg->blockDim = dim3(32 * (4 + q4_warps(NT)), 1, 1);
-  return p.window > 0 ? cudaLaunchKernelEx(cfg, pa_split_q4_kernel<D, NT, true>, tk, tv, p)
-                      : cudaLaunchKernelEx(cfg, pa_split_q4_kernel<D, NT, false>, tk, tv, p);
+cudaError_t launch_nt(cudaLaunchConfig_t* cfg, const SplitQ4Params& p) {
+  cfg->blockDim = dim3(32 * kQ4Warps, 1, 1);
+  return p.window > 0 ? cudaLaunchKernelEx(cfg, pa_split_q4_kernel<D, NT, true>, p)
+                      : cudaLaunchKernelEx(cfg, pa_split_q4_kernel<D, NT, false>, p);
 }
 
 template <int D>
-cudaError_t launch_d(cudaLaunchConfig_t* cfg, int nt, const CUtensorMap& tk, const CUtensorMap& tv,
-                     const SplitQ4Params& p) {
-  if (nt == 1) return launch_nt<D, 1>(cfg, tk, tv, p);
-  if (nt == 2) return launch_nt<D, 2>(cfg, tk, tv, p);
-  if (nt == 4) return launch_nt<D, 4>(cfg, tk, tv, p);
+cudaError_t launch_d(cudaLaunchConfig_t* cfg, int nt, const SplitQ4Params& p) {
+  if (nt == 1) return launch_nt<D, 1>(cfg, p);
+  if (nt == 2) return launch_nt<D, 2>(cfg, p);
+  if (nt == 4) return launch_nt<D, 4>(cfg, p);
   return cudaErrorInvalidValue;
 }
 
@@ -790,11 +858,14 @@ cudaError_t limit_nt(int smem) {
 
 }  // namespace
 
-int split_q4_warps(int nt) { return q4_warps(nt); }
+int split_q4_warps() { return kQ4Warps; }
+int split_q4_ctas_per_sm(int nt) { return q4_ctas_per_sm(nt); }
+int split_q4_stages(int head_dim, bool shallow) { return shallow ? kQ4ShallowStages : q4_stages(head_dim); }
+uint32_t split_q4_state_bytes() { return kQ4Warps * sizeof(FetchQ4); }
 uint32_t split_q4_query_bytes(int head_dim, int nt) { return q4_query_bytes(head_dim, nt); }
 
-cudaError_t launch_split_q4(int head_dim, int nt, const CUtensorMap& tk, const CUtensorMap& tv, const SplitQ4Params& p,
-                            int grid, int smem, bool pdl, cudaStream_t stream) {
+cudaError_t launch_split_q4(int head_dim, int nt, const SplitQ4Params& p, int grid, int smem, bool pdl,
+                            cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
@@ -804,8 +875,8 @@ cudaError_t launch_split_q4(int head_dim, int nt, const CUtensorMap& tk, const C
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  if (head_dim == 128) return launch_d<128>(&cfg, nt, tk, tv, p);
-  if (head_dim == 64) return launch_d<64>(&cfg, nt, tk, tv, p);
+  if (head_dim == 128) return launch_d<128>(&cfg, nt, p);
+  if (head_dim == 64) return launch_d<64>(&cfg, nt, p);
   return cudaErrorInvalidValue;
 }
 
