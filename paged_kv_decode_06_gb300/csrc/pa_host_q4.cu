@@ -68,7 +68,7 @@ int make_plan(int B, int Hq, int Hkv, int D, int max_qlen, const pa_options_t* o
   p.threads = 32 * warps;
   const uint32_t state = static_cast<uint32_t>(up(split_q4_state_bytes(), 16));
   const uint32_t prefix = static_cast<uint32_t>(up(4u * (3 * static_cast<size_t>(B) + 2), 16));
-  const uint32_t query = warps * split_q4_query_bytes(D, p.NT);
+  const uint32_t query = p.HC * p.MT * split_q4_query_bytes(D, p.NT);
   // The shared memory of the CTAs that an SM's registers hold, a full ring and as many
   // warps a head as the CTA has; where the sequences' metadata (12 bytes each) leaves
   // too little: one CTA an SM, then one warp a head, then a shallow ring.

@@ -182,7 +182,7 @@ int split_q4_warps();
 int split_q4_ctas_per_sm(int nt);
 int split_q4_stages(int head_dim, bool shallow);
 uint32_t split_q4_state_bytes();                       // a CTA's fetch states
-uint32_t split_q4_query_bytes(int head_dim, int nt);   // shared memory of a warp's query elements
+uint32_t split_q4_query_bytes(int head_dim, int nt);   // shared memory of a team's query fragments
 cudaError_t set_split_smem_limits_q4(int smem);
 // LSE merge of MLA partials (512 value columns; the split kernel writes each
 // piece's normalised output in f16 into ws_o): one warp per (unit, row).

@@ -46,18 +46,16 @@ namespace pa {
 
 constexpr int kQ4Warps = 8;                                         // of a CTA
 constexpr int q4_ctas_per_sm(int nt) { return nt == 1 ? 2 : 1; }
-// Pages in flight a warp: about 10 KB, 160 KB an SM; a shallow ring where the
+// Pages in flight a warp: about 9 KB, 150 KB an SM; a shallow ring where the
 // sequences' metadata takes the shared memory.
-constexpr int q4_stages(int d) { return d == 128 ? 5 : 8; }
+constexpr int q4_stages(int d) { return d == 128 ? 4 : 8; }
 constexpr int kQ4ShallowStages = 2;
-// A warp's query elements in shared memory (D x 8 NT x 2 bytes): the rows of the next
-// segment, copied there while the current one runs (a load that is waited for takes 2
-// to 5 us beside the page stream); for 32 rows the fragments in use instead
-// (registers cannot hold them beside the outputs).
-constexpr bool q4_query_in_smem(int nt) { return nt == 4; }
+// A team's query fragments (D x 8 NT x 2 bytes) in shared memory.  Its KW warps write
+// the same values; the barriers at a segment's end keep one segment's apart from the
+// next one's.
 constexpr uint32_t q4_query_bytes(int d, int nt) { return static_cast<uint32_t>(d * 8 * nt * 2); }
 // Pages a warp takes at once where it has two.
-constexpr int q4_pages_at_once(int nt) { return 1; }
+constexpr int q4_pages_at_once(int nt) { return nt <= 2 ? 2 : 1; }
 
 template <int D>
 struct GeoQ4 {
@@ -122,6 +120,17 @@ __device__ __forceinline__ uint32_t lds16(uint32_t a) {
   return v;
 }
 
+// The last key that a query row of a segment sees (rows past the segment's: as its first).
+struct RowsQ4 {
+  int min_lim;               // of the first query token
+  int row0, R;               // first row of the warp's tiles, rows of the segment
+  uint32_t g_inv;
+  __device__ __forceinline__ int last(int rl) const {
+    const int rho = row0 + rl;
+    return min_lim + (rho < R ? static_cast<int>(static_cast<uint32_t>(rho) * g_inv >> 16) : 0);
+  }
+};
+
 // What a lane reads of every page (offsets into the page's place in the ring) and
 // the slots of its keys.
 struct LaneQ4 {
@@ -146,17 +155,15 @@ constexpr float kMoveMax = 8.f;
 // One warp's state: 8 NT query rows of one KV head.  Lane (gq = lane / 4, tig =
 // lane % 4) holds the query rows 8 n + 2 tig + e (n < NT, e < 2) of the scores
 // and the outputs.
-// QS: the query fragments stay in shared memory (qs: this lane's, 512 bytes a pair
-// of k-steps and row tile) instead of registers.
-template <int D, int NT, bool QS>
+// The query fragments stay in shared memory (qs: this lane's, 512 bytes a pair of
+// k-steps and row tile): registers do not hold them beside the outputs.
+template <int D, int NT>
 struct StateQ4 {
   using GG = GeoQ4<D>;
   float O[GG::KS][NT][4];      // O^T: [feature tile][row tile]; elements (feature 2 i, rows e), (2 i + 1, rows e)
-  uint32_t Qf[QS ? 1 : GG::KS][NT][2];  // query rows as B fragments
   uint32_t qs;
   float m[NT][2], l[NT][2];    // running maximum (log2 units), this lane's share of the sum
   float fac[NT][2];            // logit factor of the row (log2 units per raw score)
-  int lim[NT][2];              // last key the row sees
 
   __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -172,22 +179,11 @@ struct StateQ4 {
   }
 
   // Query row `row` (bf16, D features; nullptr: no such row) of tile n: this lane's
-  // features D/4 tig .. D/4 tig + D/4 - 1, read now or copied to this lane's places in
-  // shared memory (`at`).
+  // features D/4 tig .. D/4 tig + D/4 - 1.
   static __device__ __forceinline__ void read_query(uint2 (&w)[GG::KS], const uint16_t* row, int tig) {
 #pragma unroll
     for (int ks = 0; ks < GG::KS; ++ks)
       w[ks] = row != nullptr ? *reinterpret_cast<const uint2*>(row + (D / 4) * tig + 4 * ks) : make_uint2(0u, 0u);
-  }
-  static __device__ __forceinline__ void copy_query(uint32_t at, const uint16_t* row, int tig) {
-#pragma unroll
-    for (int ks = 0; ks < GG::KS; ++ks) {
-      if (row != nullptr)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at + 256 * ks), "l"(row + (D / 4) * tig + 4 * ks)
-                     : "memory");
-      else
-        asm volatile("st.shared.v2.b32 [%0], {%1, %1};" ::"r"(at + 256 * ks), "r"(0u) : "memory");
-    }
   }
 
   // ... and into fragments of tile n.
@@ -211,26 +207,20 @@ struct StateQ4 {
         f[2 * u] = pack_f16(bf16_lo(w[ks + u].x) * down, bf16_hi(w[ks + u].x) * down);
         f[2 * u + 1] = pack_f16(bf16_lo(w[ks + u].y) * down, bf16_hi(w[ks + u].y) * down);
       }
-      if constexpr (QS) {
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(qs + (ks / 2 * NT + n) * 512), "r"(f[0]),
-                     "r"(f[1]), "r"(f[2]), "r"(f[3])
-                     : "memory");
-      } else {
-        Qf[ks][n][0] = f[0];
-        Qf[ks][n][1] = f[1];
-        Qf[ks + 1][n][0] = f[2];
-        Qf[ks + 1][n][1] = f[3];
-      }
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(qs + (ks / 2 * NT + n) * 512), "r"(f[0]),
+                   "r"(f[1]), "r"(f[2]), "r"(f[3])
+                   : "memory");
     }
     const float f = scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
     fac[n][0] = __shfl_sync(0xffffffffu, f, 8 * tig);
     fac[n][1] = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
   }
 
-  // NP pages of this warp's head, from ring address `at`.  EDGE (one page): some row
+  // NP pages of this warp's head, at ring addresses `at`.  EDGE (one page): some row
   // does not see all 16 keys.
   template <bool EDGE, int NP>
-  __device__ __forceinline__ void page(const LaneQ4& ln, uint32_t at_page, int tb, int L, int window) {
+  __device__ __forceinline__ void page(const LaneQ4& ln, const uint32_t (&at)[NP], int tb, int L, int window,
+                                       const RowsQ4& rows, int tig) {
     static_assert(!EDGE || NP == 1, "edge pages one at a time");
     constexpr int CH = 8 * GG::ROWB, SH = 8 * GG::SROW;   // from a key to the one 8 rows on
     // ---- S^T = K Q^T: NP x NA independent sums
@@ -246,7 +236,7 @@ struct StateQ4 {
       uint32_t c0[NP][GG::LW], c1[NP][GG::LW], s0[NP], s1[NP];   // codes and scales of the lane's two keys
 #pragma unroll
       for (int g = 0; g < NP; ++g) {
-        const uint32_t ka = at_page + ln.ka + g * GG::PAGE, ksa = at_page + ln.ksa + g * GG::PAGE;
+        const uint32_t ka = at[g] + ln.ka, ksa = at[g] + ln.ksa;
         if constexpr (D == 128) {
           const uint4 a = lds128(ka), b = lds128(ka + CH);
           c0[g][0] = a.x; c0[g][1] = a.y; c0[g][2] = a.z; c0[g][3] = a.w;
@@ -266,13 +256,8 @@ struct StateQ4 {
         uint32_t f[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          if constexpr (QS) {
-            const uint4 v = lds128(qs + (j * NT + n) * 512);
-            f[n][0] = v.x; f[n][1] = v.y; f[n][2] = v.z; f[n][3] = v.w;
-          } else {
-            f[n][0] = Qf[2 * j][n][0]; f[n][1] = Qf[2 * j][n][1];
-            f[n][2] = Qf[2 * j + 1][n][0]; f[n][3] = Qf[2 * j + 1][n][1];
-          }
+          const uint4 v = lds128(qs + (j * NT + n) * 512);
+          f[n][0] = v.x; f[n][1] = v.y; f[n][2] = v.z; f[n][3] = v.w;
         }
 #pragma unroll
         for (int g = 0; g < NP; ++g) {
@@ -297,7 +282,7 @@ struct StateQ4 {
     // ---- softmax weights.  S[n]: (key t0, rows e), (key t0 + 8, rows e).
     const int t0 = EDGE ? tb + static_cast<int>(ln.slots & 255u) : 0;
     auto hidden = [&](int n, int k) {
-      const int tok = t0 + 8 * (k >> 1), lm = lim[n][k & 1];
+      const int tok = t0 + 8 * (k >> 1), lm = EDGE ? rows.last(8 * n + 2 * tig + (k & 1)) : 0;
       return EDGE && (tok > lm || (window > 0 && tok <= lm - window));
     };
     float x[NP][NT][4];
@@ -361,7 +346,7 @@ struct StateQ4 {
     // features: D/8 gq .. D/8 gq + D/8 - 1, of one scale group.
 #pragma unroll
     for (int g = 0; g < NP; ++g) {
-      const uint32_t va = at_page + ln.va + g * GG::PAGE, vsa = at_page + ln.vsa + g * GG::PAGE;
+      const uint32_t va = at[g] + ln.va, vsa = at[g] + ln.vsa;
       const uint32_t vsb = vsa + ln.dvs, vb = va + ln.dva;
       uint32_t sc[4] = {lds8(vsa), lds8(vsb), lds8(vsa + SH), lds8(vsb + SH)};
       if constexpr (EDGE) {
@@ -384,14 +369,16 @@ struct StateQ4 {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (tb + s <= lim[n][e] && !(window > 0 && tb + s <= lim[n][e] - window)) {
+              for (int e = 0; e < 2; ++e) {
+                const int lm = rows.last(8 * n + 2 * tig + e);
+                if (tb + s <= lm && !(window > 0 && tb + s <= lm - window)) {
 #pragma unroll
                   for (int i = 0; i < GG::KS; ++i) {
                     O[i][n][e] = __uint_as_float(0x7FC00000u);
                     O[i][n][2 + e] = __uint_as_float(0x7FC00000u);
                   }
                 }
+              }
           }
         }
       }
@@ -401,13 +388,13 @@ struct StateQ4 {
       uint32_t w[4][VW];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint32_t at = (k & 1 ? vb : va) + (k >> 1) * CH;
+        const uint32_t row = (k & 1 ? vb : va) + (k >> 1) * CH;
         if constexpr (D == 128) {
-          const uint2 v = lds64(at);
+          const uint2 v = lds64(row);
           w[k][0] = v.x;
           w[k][1] = v.y;
         } else {
-          w[k][0] = lds32(at);
+          w[k][0] = lds32(row);
         }
       }
 #pragma unroll
@@ -606,9 +593,8 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
     ln.dvs = static_cast<uint32_t>((v1 - v0) * GG::SROW);
     ln.slots = static_cast<uint32_t>(r0 | v0 << 8 | v1 << 16);
   }
-  StateQ4<D, NT, q4_query_in_smem(NT)> cs;
-  const uint32_t q_smem = smem_addr(smem) + p.off_q + static_cast<uint32_t>(warp) * q4_query_bytes(D, NT);
-  cs.qs = q_smem + 16u * lane;
+  StateQ4<D, NT> cs;
+  cs.qs = smem_addr(smem) + p.off_q + static_cast<uint32_t>(team) * q4_query_bytes(D, NT) + 16u * lane;
   // rows of a KV head are numbered (query token, head of the group): row / G by a
   // product (exact for the at most 128 rows of a head's tiles)
   const uint32_t g_inv = (65536u + G - 1u) / static_cast<uint32_t>(G);
@@ -622,29 +608,25 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
     return t < q.qn ? p.q + static_cast<int64_t>(q.t0 + t) * p.q_stride_t + ((s.c * HC + hh) * G + rho - t * G) * D
                     : nullptr;
   };
-  // the next segment's query rows: copied to shared memory, or only towards L2
+  // the next segment's query rows on their way towards L2 (a load that misses it takes 2
+  // to 5 us beside the page stream)
   auto query_ahead = [&](const SegmentQ4& s, const SeqInfo& q) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const uint16_t* row = row_at(s, q, n);
-      if constexpr (q4_query_in_smem(NT)) {
-        if (row != nullptr) prefetch_l2(row + (D / 4) * tig);
-      } else {
-        cs.copy_query(q_smem + 8u * lane + n * (GG::KS * 256), row, tig);
-      }
+      if (row != nullptr) prefetch_l2(row + (D / 4) * tig);
     }
-    copy_commit();
   };
   query_ahead(sg, si);
   const uint32_t ring_end = ring + static_cast<uint32_t>(p.nstage * GG::PAGE);
   for (uint32_t a = ring; a < ring_end; a += GG::PAGE) fetch(a);
   uint32_t at = ring;               // the page to compute
-  int since = 0;                    // groups committed since the rows of the next segment were
   bool first = true;
   for (;;) {
     left -= sg.j1 - sg.j0;
     const int R = G * si.qn, min_lim = si.L - si.qn;
     const bool active = row0 < R;
+    const RowsQ4 rows = {min_lim, row0, R, g_inv};
     const int hq_base = (sg.c * HC + hh) * G;
     if (sg.j0 == 0 && warp == 0 && lane == 0) {
       // this CTA holds the unit's first page: describe the unit for the merge
@@ -653,26 +635,16 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
       p.ws_unit[static_cast<int64_t>(sg.i) * NC + sg.c] =
           make_int4(g, (last_cta - g + 1) | (first ? 0 : (1 << 30)), si.t0, si.qn);
     }
-    if (!q4_query_in_smem(NT)) {
-      if (first && p.nstage == S) copy_wait<S>();  // all but the pages behind them
-      else if (since < p.nstage) copy_wait<0>();  // else the waits for pages have covered them
-    }
     if (active) {
       cs.reset();
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         uint2 w[GG::KS];
-        if constexpr (q4_query_in_smem(NT)) {
-          cs.read_query(w, row_at(sg, si, n), tig);
-        } else {
-#pragma unroll
-          for (int ks = 0; ks < GG::KS; ++ks) w[ks] = lds64(q_smem + 8u * lane + (n * GG::KS + ks) * 256);
-        }
+        cs.read_query(w, row_at(sg, si, n), tig);
         cs.set_query(n, w, tig, p.scale_log2);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r2 = row0 + 8 * n + 2 * tig + e, t = token_of(r2);
-          cs.lim[n][e] = min_lim + (r2 < R ? t : 0);
           if (p.sinks != nullptr && sg.j0 == 0 && kw == 0 && r2 < R) {
             // the sink: a virtual first key with a zero value row
             const float sk = p.sinks[hq_base + r2 - t * G] * 1.4426950408889634f;
@@ -681,6 +653,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
           }
         }
       }
+      __syncwarp();
     }
     SegmentQ4 ns = sg;
     SeqInfo ni = si;
@@ -693,26 +666,39 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
     {
       // this warp's pages by their first tokens: below `lo` or from `hi` on some row
       // does not see all keys
-      constexpr int step = kPage;
-      const int t0 = kPage * (si.js + sg.j0 + kw), t_end = kPage * (si.js + sg.j1);
+      const int t_end = kPage * (si.js + sg.j1);
       const int lo = WINDOW ? min(t_end, si.L - window) : 0, hi = min(t_end, min_lim - (kPage - 2));
-      int t = t0;
+      int t = kPage * (si.js + sg.j0 + kw);
+      auto after = [&](uint32_t a) { return a + GG::PAGE == ring_end ? ring : a + GG::PAGE; };
       auto run = [&](auto edge, int stop) {
-        for (; t < stop; t += step * KW) {
+        for (; t < stop; t += kPage * KW) {
           if (p.nstage == S) copy_wait<S - 1>();
           else copy_wait<kQ4ShallowStages - 1>();
           __syncwarp();
-          if (active) cs.template page<decltype(edge)::value, 1>(ln, at, t, si.L, window);
+          const uint32_t one[1] = {at};
+          if (active) cs.template page<decltype(edge)::value, 1>(ln, one, t, si.L, window, rows, tig);
           __syncwarp();
           fetch(at);
-          at += GG::PAGE;
-          if (at == ring_end) at = ring;
+          at = after(at);
         }
       };
       if (WINDOW) run(Bool<true>{}, lo);
+      if constexpr (q4_pages_at_once(NT) == 2) {
+        if (p.nstage == S) {
+          for (; t + kPage * KW < hi; t += 2 * kPage * KW) {
+            copy_wait<S - 2>();
+            __syncwarp();
+            const uint32_t two[2] = {at, after(at)};
+            if (active) cs.template page<false, 2>(ln, two, t, si.L, window, rows, tig);
+            __syncwarp();
+            fetch(two[0]);
+            fetch(two[1]);
+            at = after(two[1]);
+          }
+        }
+      }
       run(Bool<false>{}, hi);
       run(Bool<true>{}, t_end);
-      since = t > t0 ? (t - t0) / (step * KW) : 0;
     }
     // ---- end of the segment
     const bool complete = sg.j0 == 0 && sg.j1 == sg.n;
