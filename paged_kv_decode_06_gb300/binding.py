@@ -9,6 +9,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import threading
 from typing import Optional
 
 import torch
@@ -316,16 +317,65 @@ def paged_attn_cache_write_per_token(key, value, slot_mapping, k_cache, v_cache,
     _check(lib, lib.paged_attn_cache_write_per_token(*[ctypes.byref(x) for x in d], _stream_handle(stream)))
 
 
-def _on_current_device(*tensors):
+_GET_DEVICE = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _on_current_device(*tensors) -> int:
     """The calls below take device pointers of the current CUDA device: a tensor
     elsewhere is refused here (the library cannot see where a pointer lives)."""
+    dev = _GET_DEVICE() if torch.cuda.is_initialized() else -1
     for t in tensors:
         if t is None:
             continue
         if not t.is_cuda:
             raise ValueError(f"a CUDA tensor is required, got one on {t.device}")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+        if t.get_device() != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    return dev
+
+
+class _Marshalled(threading.local):
+    """Argument lists of one thread, by the types, shapes and strides of the tensors."""
+
+    def __init__(self):
+        self.by_layout = {}
+
+
+_MARSHALLED = _Marshalled()
+
+
+def _arguments(codes, tensors, num_caches=0):
+    """The ctypes arguments of a call's tensors and the device they are on: the
+    first `num_caches` as one pa_tensor_t array with its length, then a
+    descriptor pointer each (`codes` gives the pa_dtype of those).  A thread keeps
+    the lists by types, shapes and strides and writes the pointers of every call
+    into them, so a repeated call marshals little else."""
+    dev = _on_current_device(*tensors)
+    key = (codes, num_caches, *[(t.dtype, t.shape, t.stride()) for t in tensors])
+    hit = _MARSHALLED.by_layout.get(key)
+    if hit is None:
+        descs = [_new_desc(t, c) for t, c in zip(tensors[num_caches:], codes)]
+        args = [ctypes.byref(d) for d in descs]
+        if codes is _PAGE_CODES:
+            array = (PaTensor * max(1, num_caches))(*[_new_desc(t, _bytes_code) for t in tensors[:num_caches]])
+            descs = list(array)[:num_caches] + descs      # the array's own elements
+            args = [array, num_caches] + args
+        if len(_MARSHALLED.by_layout) >= _DESC_CACHE_MAX:
+            _MARSHALLED.by_layout.clear()
+        _MARSHALLED.by_layout[key] = hit = (tuple(args), descs)
+    for d, t in zip(hit[1], tensors):
+        d.data = t.data_ptr()
+    return hit[0], dev
+
+
+def _handle_on(stream, dev) -> int:
+    return int(_RAW_STREAM(dev)) if stream is None and _RAW_STREAM is not None else _stream_handle(stream)
+
+
+_ROW_CODES = (_dtype_code, _dtype_code, _dtype_code, _fp4_code, _fp4_code, _dtype_code, _dtype_code)
+_READ_CODES = (_dtype_code, _fp4_code, _fp4_code, _dtype_code, _dtype_code, _dtype_code, _dtype_code)
+_INT_CODES = (_dtype_code,) * 6                  # calls without page tensors
+_PAGE_CODES = (_dtype_code,) * 6 + (None,)       # calls whose tensors begin with page tensors
 
 
 def paged_attn_cache_write_q4(key, value, slot_mapping, k_cache, v_cache, k_group_scales, v_group_scales,
@@ -335,11 +385,10 @@ def paged_attn_cache_write_q4(key, value, slot_mapping, k_cache, v_cache, k_grou
     packed float4) [NB, 16, Hkv, D / 2]; group scales uint8 or float8_e4m3fn
     [NB, Hkv, 16, D / 16]; caches and scales updated in place."""
     lib = load()
-    _on_current_device(key, value, slot_mapping, k_cache, v_cache, k_group_scales, v_group_scales)
-    d = [tensor_desc(key), tensor_desc(value), tensor_desc(slot_mapping), tensor_desc(k_cache, _fp4_code),
-         tensor_desc(v_cache, _fp4_code), tensor_desc(k_group_scales), tensor_desc(v_group_scales)]
-    _check(lib, lib.paged_attn_cache_write_q4(*[ctypes.byref(x) for x in d], float(k_scale), float(v_scale),
-                                              _stream_handle(stream)))
+    args, dev = _arguments(_ROW_CODES, (key, value, slot_mapping, k_cache, v_cache, k_group_scales, v_group_scales))
+    st = lib.paged_attn_cache_write_q4(*args, k_scale, v_scale, _handle_on(stream, dev))
+    if st != PA_OK:
+        _check(lib, st)
 
 
 def paged_attn_cache_read_q4(slot_mapping, k_cache, v_cache, k_group_scales, v_group_scales, key=None, value=None,
@@ -348,17 +397,17 @@ def paged_attn_cache_read_q4(slot_mapping, k_cache, v_cache, k_group_scales, v_g
     (key, value) bf16 [T, Hkv, D].  Rows of negative slots stay as they were in
     the key / value given (zeros without)."""
     lib = load()
-    _on_current_device(slot_mapping, k_cache, v_cache, k_group_scales, v_group_scales, key, value)
-    shape = (slot_mapping.shape[0], k_cache.shape[2], k_cache.shape[3] * 2)
-    if key is None:
-        key = torch.zeros(shape, dtype=torch.bfloat16, device=k_cache.device)
-    if value is None:
-        value = torch.zeros(shape, dtype=torch.bfloat16, device=k_cache.device)
-    d = [tensor_desc(slot_mapping), tensor_desc(k_cache, _fp4_code), tensor_desc(v_cache, _fp4_code),
-         tensor_desc(k_group_scales), tensor_desc(v_group_scales)]
-    _check(lib, lib.paged_attn_cache_read_q4(*[ctypes.byref(x) for x in d], float(k_scale), float(v_scale),
-                                             ctypes.byref(tensor_desc(key)), ctypes.byref(tensor_desc(value)),
-                                             _stream_handle(stream)))
+    if key is None or value is None:
+        shape = (slot_mapping.shape[0], k_cache.shape[2], k_cache.shape[3] * 2)
+        with _allocating_on(stream):
+            if key is None:
+                key = torch.zeros(shape, dtype=torch.bfloat16, device=k_cache.device)
+            if value is None:
+                value = torch.zeros(shape, dtype=torch.bfloat16, device=k_cache.device)
+    args, dev = _arguments(_READ_CODES, (slot_mapping, k_cache, v_cache, k_group_scales, v_group_scales, key, value))
+    st = lib.paged_attn_cache_read_q4(*args[:5], k_scale, v_scale, *args[5:], _handle_on(stream, dev))
+    if st != PA_OK:
+        _check(lib, st)
     return key, value
 
 
@@ -462,34 +511,29 @@ def paged_attn_decode_q4(q, k_cache, v_cache, k_group_scales, v_group_scales, bl
     return out, lse
 
 
-def _cache_array(caches):
-    """The pa_tensor_t array of page tensors (only their element size matters)."""
-    caches = [caches] if isinstance(caches, torch.Tensor) else list(caches)
-    _on_current_device(*caches)
-    return (PaTensor * max(1, len(caches)))(*[tensor_desc(c, _bytes_code) for c in caches]), len(caches)
+def _page_call(fn, caches, ints, stream):
+    """A call of page tensors followed by integer tensors."""
+    lib = load()
+    caches = (caches,) if isinstance(caches, torch.Tensor) else tuple(caches)
+    args, dev = _arguments(_PAGE_CODES, caches + ints, len(caches))
+    st = getattr(lib, fn)(*args, _handle_on(stream, dev))
+    if st != PA_OK:
+        _check(lib, st)
 
 
 def paged_attn_pages_copy(caches, src_pages, dst_pages, stream=None):
     """Copy page src_pages[k] to page dst_pages[k] in every cache of the list
     (see include/paged_attn.h).  caches: tensors whose first dimension is the
     page; src_pages / dst_pages int32 [n], negative entries are padding."""
-    lib = load()
-    arr, n = _cache_array(caches)
-    _on_current_device(src_pages, dst_pages)
-    _check(lib, lib.paged_attn_pages_copy(arr, n, ctypes.byref(tensor_desc(src_pages)),
-                                          ctypes.byref(tensor_desc(dst_pages)), _stream_handle(stream)))
+    _page_call("paged_attn_pages_copy", caches, (src_pages, dst_pages), stream)
 
 
 def paged_attn_pages_fork(caches, block_tables, seq_lens, ref_counts, parents, children, new_pages, stream=None):
     """Fork table rows: children[k] shares the full pages of parents[k] and gets
     a copy of its partial last page in new_pages[k] (see include/paged_attn.h).
     block_tables, seq_lens, ref_counts and new_pages are updated in place."""
-    lib = load()
-    arr, n = _cache_array(caches)
-    ints = (block_tables, seq_lens, ref_counts, parents, children, new_pages)
-    _on_current_device(*ints)
-    _check(lib, lib.paged_attn_pages_fork(arr, n, *[ctypes.byref(tensor_desc(t)) for t in ints],
-                                          _stream_handle(stream)))
+    _page_call("paged_attn_pages_fork", caches, (block_tables, seq_lens, ref_counts, parents, children, new_pages),
+               stream)
 
 
 def paged_attn_pages_free(block_tables, seq_lens, ref_counts, rows, free_pages=None, num_free=None, stream=None):
@@ -497,13 +541,16 @@ def paged_attn_pages_free(block_tables, seq_lens, ref_counts, rows, free_pages=N
     include/paged_attn.h).  seq_lens and ref_counts are updated in place;
     returns (free_pages int32 [NB], num_free int32 [1])."""
     lib = load()
-    if free_pages is None:
-        free_pages = torch.empty_like(ref_counts)
-    if num_free is None:
-        num_free = torch.empty(1, dtype=torch.int32, device=ref_counts.device)
-    ints = (block_tables, seq_lens, ref_counts, rows, free_pages, num_free)
-    _on_current_device(*ints)
-    _check(lib, lib.paged_attn_pages_free(*[ctypes.byref(tensor_desc(t)) for t in ints], _stream_handle(stream)))
+    if free_pages is None or num_free is None:
+        with _allocating_on(stream):
+            if free_pages is None:
+                free_pages = torch.empty_like(ref_counts)
+            if num_free is None:
+                num_free = torch.empty(1, dtype=torch.int32, device=ref_counts.device)
+    args, dev = _arguments(_INT_CODES, (block_tables, seq_lens, ref_counts, rows, free_pages, num_free))
+    st = lib.paged_attn_pages_free(*args, _handle_on(stream, dev))
+    if st != PA_OK:
+        _check(lib, st)
     return free_pages, num_free
 
 
@@ -511,16 +558,13 @@ def paged_attn_pages_compact(caches, block_tables, ref_counts, page_map=None, nu
     """Move the pages in use to the lowest ids, contents, counts and table
     entries (see include/paged_attn.h).  block_tables, ref_counts and the caches
     are updated in place; returns (page_map int32 [NB], num_used int32 [1])."""
-    lib = load()
-    arr, n = _cache_array(caches)
-    if page_map is None:
-        page_map = torch.empty_like(ref_counts)
-    if num_used is None:
-        num_used = torch.empty(1, dtype=torch.int32, device=ref_counts.device)
-    ints = (block_tables, ref_counts, page_map, num_used)
-    _on_current_device(*ints)
-    _check(lib, lib.paged_attn_pages_compact(arr, n, *[ctypes.byref(tensor_desc(t)) for t in ints],
-                                             _stream_handle(stream)))
+    if page_map is None or num_used is None:
+        with _allocating_on(stream):
+            if page_map is None:
+                page_map = torch.empty_like(ref_counts)
+            if num_used is None:
+                num_used = torch.empty(1, dtype=torch.int32, device=ref_counts.device)
+    _page_call("paged_attn_pages_compact", caches, (block_tables, ref_counts, page_map, num_used), stream)
     return page_map, num_used
 
 
