@@ -23,7 +23,8 @@ namespace pa {
 
 constexpr int kMaxPageTensors = 48;      // tensors of one copy launch (kernel parameters of 4 KB)
 constexpr int kMaxCaches = 1024;         // tensors of one call
-constexpr int kItemBytes = 4096;         // one warp's share of a page of one tensor: 8 x 16 bytes a lane
+constexpr int kItemBytes = 1024;         // one warp's share of a page of one tensor: 2 x 16 bytes a lane
+constexpr int kWindow = 8;               // pages of the pool a warp looks at together (compaction)
 constexpr int kClusterCtas = 8;
 constexpr int kClusterThreads = 1024;
 constexpr uint32_t kErrPageOp = 32u;
@@ -54,7 +55,7 @@ struct CopyParams {
 
 // Source and destination page of copy k; false: nothing to do.
 template <PairSource SRC>
-__device__ __forceinline__ bool pair_of(const CopyParams& p, int64_t k, int64_t base, int& src, int& dst, bool report) {
+__device__ __forceinline__ bool pair_of(const CopyParams& p, int64_t k, int& src, int& dst, bool report) {
   if constexpr (SRC == kPairsListed) {
     src = p.src[k];
     dst = p.dst[k];
@@ -63,16 +64,12 @@ __device__ __forceinline__ bool pair_of(const CopyParams& p, int64_t k, int64_t 
       if (report) atomicOr(p.err, kErrPageRange);
       return false;
     }
-  } else if constexpr (SRC == kPairsFork) {
+  } else {
     dst = __ldcg(p.dst + k);                               // -1 where the fork took no page
     if (dst < 0) return false;
     const int row = p.parents[k];
     src = p.tables[static_cast<int64_t>(row) * p.table_stride + p.seq_lens[row] / kPage];
     if (src < 0 || src >= p.num_pages) return false;       // reported by the fork kernel
-  } else {
-    src = static_cast<int>(base + k);
-    dst = __ldcg(p.dst + src);
-    if (dst < 0) return false;
   }
   return src != dst;
 }
@@ -92,7 +89,7 @@ __device__ __forceinline__ void copy_item(const PageTensor& t, int64_t src, int6
   const uint8_t* a = t.base + src * t.page_stride;
   uint8_t* b = t.base + dst * t.page_stride;
   if (t.n1 == 1 && t.n2 == 1) {
-    constexpr int U = 8;
+    constexpr int U = 2;
     for (int o = lane * W; o < bytes; o += U * 32 * W) {
       V v[U];
 #pragma unroll
@@ -103,7 +100,7 @@ __device__ __forceinline__ void copy_item(const PageTensor& t, int64_t src, int6
         if (o + u * 32 * W < bytes) *reinterpret_cast<V*>(b + off + o + u * 32 * W) = v[u];
     }
   } else {
-    constexpr int U = 4;
+    constexpr int U = 2;
     for (int o = lane * W; o < bytes; o += U * 32 * W) {
       V v[U];
 #pragma unroll
@@ -116,43 +113,64 @@ __device__ __forceinline__ void copy_item(const PageTensor& t, int64_t src, int6
   }
 }
 
-// A warp takes one item (at most 4 KB of one tensor of one page) at a time.
+// Item `item` of page src to page dst.
+__device__ __forceinline__ void copy_page_item(const CopyParams& p, int item, int64_t src, int64_t dst, int lane) {
+  int lo = 0, hi = p.num_tensors - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.t[mid].item0 <= item) lo = mid; else hi = mid - 1;
+  }
+  const PageTensor& t = p.t[lo];
+  const int off = (item - t.item0) * kItemBytes;
+  const int bytes = min(kItemBytes, t.run * t.n1 * t.n2 - off);
+  switch (t.vec) {
+    case 16: copy_item<uint4>(t, src, dst, off, bytes, lane); break;
+    case 8: copy_item<uint2>(t, src, dst, off, bytes, lane); break;
+    case 4: copy_item<uint32_t>(t, src, dst, off, bytes, lane); break;
+    case 2: copy_item<uint16_t>(t, src, dst, off, bytes, lane); break;
+    default: copy_item<uint8_t>(t, src, dst, off, bytes, lane); break;
+  }
+}
+
+// A warp takes one item (at most 1 KB of one tensor of one page) at a time, the
+// items of a page side by side.  Bound by memory: 604 MB of random 18 KB pages take
+// 96 us, torch's copy of as many consecutive bytes 95.  Small items and a grid of
+// four waves keep the load even: 4 KB items in one wave took 134 us, 1 KB items in
+// one wave 110, a warp an item (a launch of every item's warp) 100.
 template <PairSource SRC>
-__global__ void __launch_bounds__(256, 4) pa_page_copy_kernel(const __grid_constant__ CopyParams p) {
+__global__ void __launch_bounds__(256, 8) pa_page_copy_kernel(const __grid_constant__ CopyParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x / 32);
-  int64_t base = 0, n = p.pairs;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32;
   if constexpr (SRC == kPairsCompact) {
-    base = __ldcg(p.num_used);           // pages that move have ids from here on
-    n = p.num_pages - base;
-  }
-  const int64_t total = n * p.items;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32; i < total; i += warps) {
-    const int64_t k = i / p.items;
-    const int item = static_cast<int>(i - k * p.items);
-    int src, dst;
-    if (!pair_of<SRC>(p, k, base, src, dst, item == 0 && lane == 0)) continue;
-    int lo = 0, hi = p.num_tensors - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.t[mid].item0 <= item) lo = mid; else hi = mid - 1;
+    // (window of kWindow pages, item): the pages that move have ids from num_used on
+    const int64_t base = __ldcg(p.num_used);
+    const int64_t total = (p.num_pages - base + kWindow - 1) / kWindow * p.items;
+    for (int64_t i = first; i < total; i += warps) {
+      const int64_t w = i / p.items;
+      const int64_t page = base + w * kWindow + lane;
+      const int to = lane < kWindow && page < p.num_pages ? __ldcg(p.dst + page) : -1;
+      for (uint32_t m = __ballot_sync(0xffffffffu, to >= 0); m != 0u; m &= m - 1u) {
+        const int b = __ffs(m) - 1;
+        copy_page_item(p, static_cast<int>(i - w * p.items), base + w * kWindow + b, __shfl_sync(0xffffffffu, to, b), lane);
+      }
     }
-    const PageTensor& t = p.t[lo];
-    const int off = (item - t.item0) * kItemBytes;
-    const int bytes = min(kItemBytes, t.run * t.n1 * t.n2 - off);
-    switch (t.vec) {
-      case 16: copy_item<uint4>(t, src, dst, off, bytes, lane); break;
-      case 8: copy_item<uint2>(t, src, dst, off, bytes, lane); break;
-      case 4: copy_item<uint32_t>(t, src, dst, off, bytes, lane); break;
-      case 2: copy_item<uint16_t>(t, src, dst, off, bytes, lane); break;
-      default: copy_item<uint8_t>(t, src, dst, off, bytes, lane); break;
+  } else {
+    const int64_t total = p.pairs * p.items;
+    for (int64_t i = first; i < total; i += warps) {
+      const int64_t k = i / p.items;
+      const int item = static_cast<int>(i - k * p.items);
+      int src, dst;
+      if (pair_of<SRC>(p, k, src, dst, item == 0 && lane == 0)) copy_page_item(p, item, src, dst, lane);
     }
   }
 }
 
-// Table entries after a compaction: every entry that names a page in use.
+// Table entries after a compaction: every entry that names a page in use.  (As a
+// part of the copy kernel it cost that kernel's registers: 126 us against 116 for a
+// compaction that moves 302 MB.)
 __global__ void __launch_bounds__(256) pa_table_remap_kernel(int32_t* tables, int64_t stride, int64_t rows,
                                                              int64_t cols, const int32_t* map, int32_t num_pages) {
   grid_dependency_wait();
@@ -231,11 +249,17 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
     const int len = p.seq_lens[par], full = len / kPage;
     const int32_t* from = p.tables + static_cast<int64_t>(par) * p.table_stride;
     int32_t* to = p.tables + static_cast<int64_t>(chi) * p.table_stride;
-    for (int x = lane; x < full; x += 32) {
-      const int id = from[x];
-      to[x] = id;
-      if (id >= 0 && id < p.num_pages) atomicAdd(p.ref + id, 1);
-      else atomicOr(p.err, kErrPageRange);
+    for (int x0 = lane; x0 < full; x0 += 4 * 32) {
+      int id[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) id[u] = x0 + 32 * u < full ? from[x0 + 32 * u] : 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (x0 + 32 * u >= full) break;
+        to[x0 + 32 * u] = id[u];
+        if (id[u] >= 0 && id[u] < p.num_pages) atomicAdd(p.ref + id[u], 1);
+        else atomicOr(p.err, kErrPageRange);
+      }
     }
     if (lane == 0) {
       if (len % kPage != 0) {
@@ -256,6 +280,46 @@ __device__ __forceinline__ void warp_pages(int num_pages, int w, int warps, int6
   const int64_t words = (static_cast<int64_t>(num_pages) + 31) / 32;
   lo = min(static_cast<int64_t>(num_pages), words * w / warps * 32);
   hi = min(static_cast<int64_t>(num_pages), words * (w + 1) / warps * 32);
+}
+
+// One bit a page: the pages of a warp's run that are in use (count positive), a word
+// of 32 at a time.  The first look at the counts leaves the words in shared memory
+// (eight loads in flight); runs of more than kMaskWords words are read again.
+constexpr int kMaskWords = 256;          // a warp: pools of up to 2 million pages
+
+template <typename F>
+__device__ __forceinline__ void read_words(const int32_t* ref, int64_t lo, int64_t hi, int lane, uint32_t* words, F each) {
+  for (int64_t b0 = lo; b0 < hi; b0 += 8 * 32) {
+    int r[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int64_t id = b0 + 32 * u + lane;
+      r[u] = id < hi ? __ldcg(ref + id) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int64_t b = b0 + 32 * u;
+      if (b >= hi) break;
+      const uint32_t m = __ballot_sync(0xffffffffu, r[u] > 0);
+      const int64_t w = (b - lo) / 32;
+      if (lane == 0 && w < kMaskWords) words[w] = m;
+      each(b, m, r[u]);
+    }
+  }
+  __syncwarp();
+}
+
+// The word of pages b .. b + 31 of a run that starts at lo.
+__device__ __forceinline__ uint32_t word_of(const int32_t* ref, int64_t lo, int64_t hi, int64_t b, int lane,
+                                            const uint32_t* words) {
+  const int64_t w = (b - lo) / 32;
+  if (w < kMaskWords) return words[w];
+  return __ballot_sync(0xffffffffu, b + lane < hi && __ldcg(ref + b + lane) > 0);
+}
+
+// Bits of a word's pages b .. b + 31 with ids below n.
+__device__ __forceinline__ uint32_t below(int64_t b, int64_t n) {
+  return n <= b ? 0u : (n >= b + 32 ? 0xffffffffu : (1u << (n - b)) - 1u);
 }
 
 // Exclusive prefix of one value per warp over the cluster's warps, in (block,
@@ -293,6 +357,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
   constexpr int W = kClusterThreads / 32;
   __shared__ int s_warp[W];
   __shared__ int s_total;
+  __shared__ uint32_t s_words[W][kMaskWords];
   grid_dependency_wait();
   grid_launch_dependents();
   cg::cluster_group cluster = cg::this_cluster();
@@ -316,30 +381,36 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
       held = p.cols;
     }
     const int32_t* from = p.tables + static_cast<int64_t>(row) * p.table_stride;
-    for (int x = lane; x < held; x += 32) {
-      const int id = from[x];
-      if (id < 0 || id >= p.num_pages) {
-        atomicOr(p.err, kErrPageRange);
-      } else if (atomicSub(p.ref + id, 1) <= 0) {
-        atomicAdd(p.ref + id, 1);                 // was free already: its count stays
-        atomicOr(p.err, kErrPageOp);
+    // four pages a lane in flight: ids, then counts
+    for (int x0 = lane; x0 < held; x0 += 4 * 32) {
+      int id[4], old[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) id[u] = x0 + 32 * u < held ? from[x0 + 32 * u] : -2;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool valid = id[u] >= 0 && id[u] < p.num_pages;
+        if (!valid && x0 + 32 * u < held) atomicOr(p.err, kErrPageRange);
+        old[u] = valid ? atomicSub(p.ref + id[u], 1) : 1;
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (old[u] <= 0) {                        // was free already: its count stays
+          atomicAdd(p.ref + id[u], 1);
+          atomicOr(p.err, kErrPageOp);
+        }
     }
   }
   cluster.sync();
   int64_t lo, hi;
   warp_pages(p.num_pages, w, kClusterCtas * W, lo, hi);
   int mine = 0;
-  for (int64_t b = lo; b < hi; b += 32) {
-    const bool is_free = b + lane < hi && __ldcg(p.ref + b + lane) <= 0;
-    mine += __popc(__ballot_sync(0xffffffffu, is_free));
-  }
+  read_words(p.ref, lo, hi, lane, s_words[warp],
+             [&](int64_t b, uint32_t m, int) { mine += __popc(~m & below(b, hi)); });
   int total;
   int at = cluster_prefix(cluster, mine, s_warp, &s_total, total);
   for (int64_t b = lo; b < hi; b += 32) {
-    const bool is_free = b + lane < hi && __ldcg(p.ref + b + lane) <= 0;
-    const uint32_t m = __ballot_sync(0xffffffffu, is_free);
-    if (is_free) p.pages[at + __popc(m & ((1u << lane) - 1u))] = static_cast<int32_t>(b + lane);
+    const uint32_t m = ~word_of(p.ref, lo, hi, b, lane, s_words[warp]) & below(b, hi);
+    if (m >> lane & 1u) p.pages[at + __popc(m & ((1u << lane) - 1u))] = static_cast<int32_t>(b + lane);
     at += __popc(m);
   }
   if (w == 0 && lane == 0) *p.count = total;
@@ -358,58 +429,56 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
   constexpr int W = kClusterThreads / 32;
   __shared__ int s_warp[W];
   __shared__ int s_total[3];
+  __shared__ uint32_t s_words[W][kMaskWords];
   grid_dependency_wait();
   grid_launch_dependents();
   cg::cluster_group cluster = cg::this_cluster();
-  const int lane = threadIdx.x & 31;
-  const int w = static_cast<int>(cluster.block_rank()) * W + (threadIdx.x >> 5);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w = static_cast<int>(cluster.block_rank()) * W + warp;
+  uint32_t* const words = s_words[warp];
   int64_t lo, hi;
   warp_pages(p.num_pages, w, kClusterCtas * W, lo, hi);
   int mine = 0;
   bool negative = false;
-  for (int64_t b = lo; b < hi; b += 32) {
-    const int r = b + lane < hi ? p.ref[b + lane] : 0;
+  read_words(p.ref, lo, hi, lane, words, [&](int64_t, uint32_t m, int r) {
+    mine += __popc(m);
     negative |= r < 0;
-    mine += __popc(__ballot_sync(0xffffffffu, r > 0));
-  }
+  });
   if (negative) atomicOr(p.err, kErrPageOp);
   int U, holes_all, high_all;
   cluster_prefix(cluster, mine, s_warp, &s_total[0], U);
   int holes = 0, high = 0;
   for (int64_t b = lo; b < hi; b += 32) {
-    const bool in = b + lane < hi;
-    const bool used = in && p.ref[b + lane] > 0;
-    holes += __popc(__ballot_sync(0xffffffffu, in && !used && b + lane < U));
-    high += __popc(__ballot_sync(0xffffffffu, used && b + lane >= U));
+    const uint32_t m = word_of(p.ref, lo, hi, b, lane, words);
+    holes += __popc(~m & below(b, min(hi, static_cast<int64_t>(U))));
+    high += __popc(m & ~below(b, U));
   }
   int at_hole = cluster_prefix(cluster, holes, s_warp, &s_total[1], holes_all);
   int at_high = cluster_prefix(cluster, high, s_warp, &s_total[2], high_all);
   for (int64_t b = lo; b < min(hi, static_cast<int64_t>(U)); b += 32) {
+    const uint32_t in = below(b, min(hi, static_cast<int64_t>(U)));
+    const uint32_t m = word_of(p.ref, lo, hi, b, lane, words);
     const int64_t id = b + lane;
-    const bool below = id < hi && id < U;
-    const bool used = below && p.ref[id] > 0;
-    const uint32_t m = __ballot_sync(0xffffffffu, below && !used);
-    if (below) p.pages[id] = used ? static_cast<int32_t>(id) : -1;
-    if (below && !used)
-      p.pages[U + at_hole + __popc(m & ((1u << lane) - 1u))] = static_cast<int32_t>(id);
-    at_hole += __popc(m);
+    if (in >> lane & 1u) p.pages[id] = m >> lane & 1u ? static_cast<int32_t>(id) : -1;
+    if ((in & ~m) >> lane & 1u) p.pages[U + at_hole + __popc(in & ~m & ((1u << lane) - 1u))] = static_cast<int32_t>(id);
+    at_hole += __popc(in & ~m);
   }
   cluster.sync();
   for (int64_t b = lo; b < hi; b += 32) {
     const int64_t id = b + lane;
-    const bool above = id < hi && id >= U;
-    const int r = above ? p.ref[id] : 0;
-    const uint32_t m = __ballot_sync(0xffffffffu, r > 0);
-    if (r > 0) {
+    const uint32_t m = word_of(p.ref, lo, hi, b, lane, words) & ~below(b, U);
+    if (m >> lane & 1u) {
       const int to = __ldcg(p.pages + U + at_high + __popc(m & ((1u << lane) - 1u)));
-      p.ref[to] = r;
+      p.ref[to] = __ldcg(p.ref + id);
       p.ref[id] = -1 - to;
-    } else if (above) {
-      p.ref[id] = 0;
+    } else if (id < hi) {
+      if (id >= U) p.ref[id] = 0;
     }
     at_high += __popc(m);
+    __syncwarp();
   }
   cluster.sync();
+#pragma unroll 4
   for (int64_t b = lo; b < hi; b += 32) {
     const int64_t id = b + lane;
     if (id >= hi || id < U) continue;
@@ -534,8 +603,9 @@ int launch_copies(CopyParams& p, const CacheList& c, int64_t nb, int num_sms, cu
       items += (bytes + kItemBytes - 1) / kItemBytes;
     }
     p.items = static_cast<int32_t>(items);
-    const int64_t blocks = (p.pairs * items + 7) / 8;
-    const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(blocks, int64_t(num_sms) * 8))), 1, 1);
+    const int64_t units = SRC == kPairsCompact ? (p.pairs + kWindow - 1) / kWindow : p.pairs;
+    const int64_t blocks = (units * items + 7) / 8;
+    const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(blocks, int64_t(num_sms) * 32))), 1, 1);
     const cudaError_t e = launch_pdl(pa_page_copy_kernel<SRC>, grid, 256, stream, p);
     if (e != cudaSuccess) return host_cuda_fail(e, "page copy launch");
   }
@@ -693,7 +763,7 @@ int pages_compact(const CacheList& c, const pa_tensor_t* bt, const pa_tensor_t* 
   cp.num_used = p.count;
   cp.err = dev.status;
   if ((st = launch_copies<kPairsCompact>(cp, c, p.num_pages, dev.num_sms, stream)) != PA_OK) return st;
-  const int64_t entries = static_cast<int64_t>(p.rows) * p.cols;
+  const int64_t entries = int64_t(p.rows) * p.cols;
   if (entries == 0) return PA_OK;
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>((entries + 255) / 256, int64_t(dev.num_sms) * 8)), 1, 1);
   e = launch_pdl(pa_table_remap_kernel, grid, 256, stream, p.tables, p.table_stride, static_cast<int64_t>(p.rows),
