@@ -71,11 +71,14 @@ int make_plan(int B, int Hq, int Hkv, int D, int max_qlen, const pa_options_t* o
   const uint32_t query = p.HC * p.MT * split_q4_query_bytes(D, p.NT);
   // The shared memory of the CTAs that an SM's registers hold, a full ring and as many
   // warps a head as the CTA has; where the sequences' metadata (12 bytes each) leaves
-  // too little: one CTA an SM, then one warp a head, then a shallow ring.
+  // too little: one CTA an SM, then one warp a head, then a shallow ring.  Where all
+  // eight warps take one head's pages in turn, one CTA an SM as well: its segments are
+  // twice as long against the cost of their ends (64 sequences, one KV head: 21.5 us
+  // against 25.6; with two heads and four warps each, two CTAs: 18.7 against 20.7).
   uint32_t ring = 0, xchg = 0;
   int per_sm = 0;
   bool fits = false;
-  for (int form = split_q4_ctas_per_sm(p.NT) == 2 ? 0 : 1; form < 4 && !fits; ++form) {
+  for (int form = split_q4_ctas_per_sm(p.NT) == 2 && p.HC * p.MT > 1 ? 0 : 1; form < 4 && !fits; ++form) {
     per_sm = form == 0 ? 2 : 1;
     p.KW = 1;
     while (form < 2 && p.KW < 8 && 2 * p.KW * p.HC * p.MT <= warps) p.KW *= 2;
@@ -133,7 +136,7 @@ int decode_q4(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* vc
   if ((st = check_shape(B, Hq, Hkv, D, max_qlen, opts)) != PA_OK) return st;
   if (kc->shape[1] != kPageTokens)
     return host_fail(PA_ERR_UNSUPPORTED, "page size %lld, only 16 is supported", static_cast<long long>(kc->shape[1]));
-  if (NB < 1 || NB > (int64_t(1) << 31) - 1 || T > (int64_t(1) << 30) || MB > (1 << 28) || B * MB > (int64_t(1) << 31))
+  if (NB < 1 || NB > (int64_t(1) << 31) - 1 || T > (int64_t(1) << 30) || MB > (1 << 27) - 64 || B * MB > (int64_t(1) << 31))
     return host_fail(PA_ERR_UNSUPPORTED, "tensor extents too large");
   const pa_tensor_t *code[2] = {kc, vc}, *sc[2] = {ks, vs};
   const char *cn[2] = {"k_cache", "v_cache"}, *sn[2] = {"k_group_scales", "v_group_scales"};
@@ -230,7 +233,6 @@ int decode_q4(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* vc
   sp.off_q = pl.off_q;
   sp.off_xchg = pl.off_xchg;
   sp.off_state = pl.off_state;
-  sp.starve_cta = -1;
   sp.k_codes = static_cast<const uint8_t*>(kc->data);
   sp.v_codes = static_cast<const uint8_t*>(vc->data);
   sp.kc_stride_page = static_cast<uint32_t>(kc->stride[0]);
@@ -288,9 +290,8 @@ int decode_q4(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* vc
     return host_cuda_fail(e, "cudaEventRecord(stop)");
   const int units = static_cast<int>(B) * pl.NC;
   // The merge that reads a row's partials with a whole block is for few rows cut
-  // into many pieces: about a block an SM (64 rows of one sequence: 4.6 us;
-  // 8192 rows of 32 sequences in 5 pieces each: 118 us, a warp a row: see the
-  // design notes' table).
+  // into many pieces: about a block an SM (64 rows of one sequence: 4.6 us; 8192
+  // rows of 32 sequences in 5 pieces each: 118 us, where a warp a row takes 9).
   const bool wide = pl.grid >= 4 * units && static_cast<int64_t>(units) * pl.HC * pl.R_max <= 2 * dev.num_sms;
   if ((e = launch_merge(static_cast<int>(D), mp, units, pl.HC * pl.R_max, wide, pdl && !ev1, stream)) != cudaSuccess)
     return host_cuda_fail(e, "merge kernel launch");
