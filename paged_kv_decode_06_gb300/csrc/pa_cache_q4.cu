@@ -10,7 +10,11 @@
 // code * S (exact) times ts rounded to fp32, then to bf16.
 //
 // Both are bound by memory: 4 bytes of bf16 a (key, value) feature pair against
-// 9/8 bytes of codes and scales.
+// 9/8 bytes of codes and scales.  A (token, head) row belongs to L lanes, each with
+// every L-th 8-feature chunk of it (up to four in flight): a copy instruction then
+// moves whole sectors, and one address serves four chunks.  (A thread a 16-feature
+// group took 27 us to write and 19 to read 16384 tokens x 8 heads x 128, a thread a
+// chunk 32 and 26: the address arithmetic of every piece cost more than the piece.)
 #include "pa_device.cuh"
 #include "pa_host.h"
 #include "pa_q4.cuh"
@@ -29,120 +33,153 @@ struct RowsQ4Params {
   int64_t code_page[2], code_slot[2], code_head[2];
   uint8_t* scales[2];          // K, V group scales [NB, Hkv, 16, D / 16]
   int64_t sc_page[2], sc_head[2], sc_slot[2], sc_group[2];
-  int32_t num_tokens, num_kv_heads, groups, num_pages;
+  int32_t num_tokens, num_kv_heads, chunks, num_pages;   // chunks: 8 features each, of a row
+  int32_t lg;                  // 2^lg lanes a row
   float ts[2];                 // tensor scales
   float six_ts[2];             // fp32(6 ts)
   uint32_t* err;
 };
 
-struct GroupIndex {
-  int64_t t;
-  int h, g;
-};
+constexpr int kRowChunks = 4;      // chunks of a lane at a time
+constexpr int kRowWaves = 8;       // CTAs an SM and tensor (4: 40 us for both directions, 8: 39, 16: 41)
 
-// Index of a (token, head, group) triple, groups innermost.
-__device__ __forceinline__ GroupIndex group_index(const RowsQ4Params& p, int64_t i, bool narrow) {
-  GroupIndex x;
-  const int64_t per = static_cast<int64_t>(p.num_kv_heads) * p.groups;
-  x.t = cw_div(i, per, narrow);
-  const int r = static_cast<int>(i - x.t * per);
-  x.h = r / p.groups;
-  x.g = r - x.h * p.groups;
-  return x;
+// Where a row's codes and scales lie.
+__device__ __forceinline__ uint8_t* codes_at(const RowsQ4Params& p, int y, int slot, int h) {
+  const int64_t page = slot / kPage;
+  return p.codes[y] + page * p.code_page[y] + (slot % kPage) * p.code_slot[y] + h * p.code_head[y];
+}
+__device__ __forceinline__ uint8_t* scales_at(const RowsQ4Params& p, int y, int slot, int h) {
+  const int64_t page = slot / kPage;
+  return p.scales[y] + page * p.sc_page[y] + (slot % kPage) * p.sc_slot[y] + h * p.sc_head[y];
 }
 
-// One thread quantises one group of one tensor (blockIdx.y: 0 = K, 1 = V).
+// e2m1 codes of eight features over the group's scale d > 0 (amax: the group's
+// largest magnitude).
+__device__ __forceinline__ uint32_t quantise8(const uint4 v, float d, float amax) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const ScaleDiv sd = scale_div(d);
+  float q[8];
+  // Quotients below 1024 need none of div_by2's exceptions but the sign of a zero,
+  // which every quotient takes from its feature here.
+  if (sd.fast && amax < 1000.f * d) {
+    const uint64_t r2 = f2_pack(sd.r, sd.r), ns2 = f2_pack(-d, -d);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float a = bf16_lo(w[e]), b = bf16_hi(w[e]);
+      const uint64_t x = f2_pack(a, b), q0 = fmul2(x, r2);
+      float qa, qb;
+      f2_unpack(ffma2(ffma2(q0, ns2, x), r2, q0), qa, qb);
+      q[2 * e] = copysignf(qa, a);
+      q[2 * e + 1] = copysignf(qb, b);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      q[2 * e] = __fdiv_rn(bf16_lo(w[e]), d);
+      q[2 * e + 1] = __fdiv_rn(bf16_hi(w[e]), d);
+    }
+  }
+  return e2m1x8_from_f32(q);
+}
+
+// One row a group of L = 2^lg lanes at a time, of one tensor (blockIdx.y: 0 = K, 1 = V).
+// Lanes q and q ^ 1 hold the two halves of a 16-feature group.
 __global__ void __launch_bounds__(256) pa_cache_write_q4_kernel(const RowsQ4Params p) {
-  const int y = blockIdx.y;
-  const int64_t total = static_cast<int64_t>(p.num_tokens) * p.num_kv_heads * p.groups;
-  const bool narrow = total <= 0xFFFFFFFFll;
+  const int y = blockIdx.y, q = threadIdx.x & ((1 << p.lg) - 1);
+  const int64_t rows = static_cast<int64_t>(p.num_tokens) * p.num_kv_heads;
+  const bool narrow = rows <= 0xFFFFFFFFll;
   const int64_t num_slots = static_cast<int64_t>(p.num_pages) * kPage;
   const float ts = p.ts[y], six = p.six_ts[y];
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
-    const GroupIndex x = group_index(p, i, narrow);
-    const int slot = p.slots[x.t];
-    const uint4* src =
-        reinterpret_cast<const uint4*>(p.rows[y] + x.t * p.row_t[y] + x.h * p.row_h[y] + x.g * kQ4Group);
-    const uint4 a = src[0], b = src[1];
-    if (slot < 0) continue;                        // padding token
-    if (slot >= num_slots) {
-      if (x.h == 0 && x.g == 0) atomicOr(p.err, kErrPageRange);
-      continue;
+  const int64_t step = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> p.lg;
+  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> p.lg;
+  const int64_t warp_r0 = (static_cast<int64_t>(blockIdx.x) * blockDim.x + (threadIdx.x & ~31)) >> p.lg;
+  // trips go by the warp's first row, so that whole warps meet in the exchanges
+  for (int64_t k = 0; warp_r0 + k < rows; k += step) {
+    const int64_t r = r0 + k;
+    const bool in = r < rows;
+    const int64_t t = in ? cw_div(r, p.num_kv_heads, narrow) : 0;
+    const int h = in ? static_cast<int>(r - t * p.num_kv_heads) : 0;
+    const int slot = in ? p.slots[t] : -1;
+    const uint16_t* src = p.rows[y] + t * p.row_t[y] + h * p.row_h[y];
+    bool live = slot >= 0;                         // not a padding token
+    if (live && slot >= num_slots) {
+      if (h == 0 && q == 0) atomicOr(p.err, kErrPageRange);
+      live = false;
     }
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    uint32_t m2 = 0u;                              // magnitudes of bf16 order as their bits
+    uint8_t* codes = live ? codes_at(p, y, slot, h) : nullptr;
+    uint8_t* scales = live ? scales_at(p, y, slot, h) : nullptr;
+    for (int c0 = 0; c0 < p.chunks; c0 += kRowChunks << p.lg) {
+      uint4 v[kRowChunks];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m2 = max_u16x2(m2, w[e] & 0x7FFF7FFFu);
-    const float amax = __uint_as_float(max(m2 << 16, m2 & 0xFFFF0000u));
-    const uint32_t s8 = e4m3x2_from_f32(__fdiv_rn(amax, six), 0.f) & 0xFFu;
-    const float d = __fmul_rn(f16_lo(e4m3x2_to_f16x2(s8)), ts);
-    uint2 codes = make_uint2(0u, 0u);
-    if (d > 0.f) {                                 // not 0, not NaN
-      const ScaleDiv sd = scale_div(d);
-      float q[16];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (sd.fast) {
-          div_by2(sd, bf16_lo(w[e]), bf16_hi(w[e]), q[2 * e], q[2 * e + 1]);
-        } else {
-          q[2 * e] = __fdiv_rn(bf16_lo(w[e]), d);
-          q[2 * e + 1] = __fdiv_rn(bf16_hi(w[e]), d);
-        }
+      for (int u = 0; u < kRowChunks; ++u) {
+        const int c = c0 + (u << p.lg) + q;
+        v[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (live && c < p.chunks) v[u] = *reinterpret_cast<const uint4*>(src + c * 8);
       }
-      const float lo[8] = {q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7]};
-      const float hi[8] = {q[8], q[9], q[10], q[11], q[12], q[13], q[14], q[15]};
-      codes = make_uint2(e2m1x8_from_f32(lo), e2m1x8_from_f32(hi));
+#pragma unroll
+      for (int u = 0; u < kRowChunks; ++u) {
+        const int c = c0 + (u << p.lg) + q;
+        // magnitudes in bf16 order as their bits
+        uint32_t m2 = max_u16x2(max_u16x2(v[u].x & 0x7FFF7FFFu, v[u].y & 0x7FFF7FFFu),
+                                max_u16x2(v[u].z & 0x7FFF7FFFu, v[u].w & 0x7FFF7FFFu));
+        m2 = max_u16x2(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
+        if (!live || c >= p.chunks) continue;
+        const float amax = __uint_as_float(max(m2 << 16, m2 & 0xFFFF0000u));
+        const uint32_t s8 = e4m3x2_from_f32(__fdiv_rn(amax, six), 0.f) & 0xFFu;
+        const float d = __fmul_rn(f16_lo(e4m3x2_to_f16x2(s8)), ts);
+        *reinterpret_cast<uint32_t*>(codes + c * 4) = d > 0.f ? quantise8(v[u], d, amax) : 0u;   // else 0 or NaN
+        if ((q & 1) == 0) scales[(c >> 1) * p.sc_group[y]] = static_cast<uint8_t>(s8);
+      }
     }
-    const int64_t page = slot / kPage, off = slot % kPage;
-    *reinterpret_cast<uint2*>(p.codes[y] + page * p.code_page[y] + off * p.code_slot[y] + x.h * p.code_head[y] +
-                              x.g * (kQ4Group / 2)) = codes;
-    p.scales[y][page * p.sc_page[y] + x.h * p.sc_head[y] + off * p.sc_slot[y] + x.g * p.sc_group[y]] =
-        static_cast<uint8_t>(s8);
   }
 }
 
-// One thread reads one group of one tensor back.
+// One row a group of L lanes at a time, read back.
 __global__ void __launch_bounds__(256) pa_cache_read_q4_kernel(const RowsQ4Params p) {
-  const int y = blockIdx.y;
-  const int64_t total = static_cast<int64_t>(p.num_tokens) * p.num_kv_heads * p.groups;
-  const bool narrow = total <= 0xFFFFFFFFll;
+  const int y = blockIdx.y, q = threadIdx.x & ((1 << p.lg) - 1);
+  const int64_t rows = static_cast<int64_t>(p.num_tokens) * p.num_kv_heads;
+  const bool narrow = rows <= 0xFFFFFFFFll;
   const int64_t num_slots = static_cast<int64_t>(p.num_pages) * kPage;
   const float ts = p.ts[y];
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
-    const GroupIndex x = group_index(p, i, narrow);
-    const int slot = p.slots[x.t];
+  const int64_t step = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> p.lg;
+  for (int64_t r = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> p.lg; r < rows; r += step) {
+    const int64_t t = cw_div(r, p.num_kv_heads, narrow);
+    const int h = static_cast<int>(r - t * p.num_kv_heads);
+    const int slot = p.slots[t];
     if (slot < 0) continue;                        // padding token: its row stays as it was
     if (slot >= num_slots) {
-      if (x.h == 0 && x.g == 0) atomicOr(p.err, kErrPageRange);
+      if (h == 0 && q == 0) atomicOr(p.err, kErrPageRange);
       continue;
     }
-    const int64_t page = slot / kPage, off = slot % kPage;
-    const uint2 codes = *reinterpret_cast<const uint2*>(p.codes[y] + page * p.code_page[y] + off * p.code_slot[y] +
-                                                        x.h * p.code_head[y] + x.g * (kQ4Group / 2));
-    const uint32_t s8 =
-        p.scales[y][page * p.sc_page[y] + x.h * p.sc_head[y] + off * p.sc_slot[y] + x.g * p.sc_group[y]];
-    const uint32_t s2 = e4m3x2_to_f16x2(s8 * 0x0101u);
-    uint32_t h[8], o[8];
-    {
-      uint32_t lo[4], hi[4];
-      e2m1x8_to_f16(codes.x, lo);
-      e2m1x8_to_f16(codes.y, hi);
+    const uint8_t* codes = codes_at(p, y, slot, h);
+    const uint8_t* scales = scales_at(p, y, slot, h);
+    uint16_t* dst = p.rows[y] + t * p.row_t[y] + h * p.row_h[y];
+    for (int c0 = 0; c0 < p.chunks; c0 += kRowChunks << p.lg) {
+      uint32_t w[kRowChunks], s8[kRowChunks];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        h[e] = lo[e];
-        h[4 + e] = hi[e];
+      for (int u = 0; u < kRowChunks; ++u) {
+        const int c = c0 + (u << p.lg) + q;
+        w[u] = s8[u] = 0u;
+        if (c < p.chunks) {
+          w[u] = *reinterpret_cast<const uint32_t*>(codes + c * 4);
+          s8[u] = scales[(c >> 1) * p.sc_group[y]];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kRowChunks; ++u) {
+        const int c = c0 + (u << p.lg) + q;
+        if (c >= p.chunks) break;
+        const uint32_t s2 = e4m3x2_to_f16x2(s8[u] * 0x0101u);
+        uint32_t x[4], o[4];
+        e2m1x8_to_f16(w[u], x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t f = hmul2(x[e], s2);
+          o[e] = pack_bf16(__fmul_rn(f16_lo(f), ts), __fmul_rn(f16_hi(f), ts));
+        }
+        *reinterpret_cast<uint4*>(dst + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t v = hmul2(h[e], s2);
-      o[e] = pack_bf16(__fmul_rn(f16_lo(v), ts), __fmul_rn(f16_hi(v), ts));
-    }
-    uint4* dst = reinterpret_cast<uint4*>(p.rows[y] + x.t * p.row_t[y] + x.h * p.row_h[y] + x.g * kQ4Group);
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
 
@@ -235,11 +272,16 @@ int rows_q4(bool write, const pa_tensor_t* key, const pa_tensor_t* value, const 
   p.slots = static_cast<const int32_t*>(slots->data);
   p.num_tokens = static_cast<int32_t>(T);
   p.num_kv_heads = static_cast<int32_t>(Hkv);
-  p.groups = static_cast<int32_t>(D / kQ4Group);
+  p.chunks = static_cast<int32_t>(D / 8);
+  // Four chunks a lane; where the rows leave most of the device idle, they lie side by
+  // side instead (write and read of 64 tokens x 8 heads x 128: 4.1 us against 4.9; from
+  // half a CTA an SM on the four in flight win: 1000 tokens 6.4 us against 8.7).
+  for (p.lg = 1; p.lg < 5 && (kRowChunks << p.lg) < p.chunks;) ++p.lg;
+  while (p.lg < 5 && (1 << p.lg) < p.chunks && ((T * Hkv) << p.lg) < int64_t(dev.num_sms) * 128) ++p.lg;
   p.num_pages = static_cast<int32_t>(kc->shape[0]);
   p.err = dev.status;
-  const int64_t blocks = (T * Hkv * p.groups + 255) / 256;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, int64_t(dev.num_sms) * 4)), 2, 1);
+  const int64_t blocks = (((T * Hkv) << p.lg) + 255) / 256;
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(blocks, int64_t(dev.num_sms) * kRowWaves)), 2, 1);
   if (write)
     pa_cache_write_q4_kernel<<<grid, 256, 0, stream>>>(p);
   else
