@@ -364,7 +364,9 @@ int paged_attn_mla_reserve(int32_t num_seqs, int32_t num_q_heads, int32_t kv_dty
  *   key, value      bf16 [T, Hkv, D]; stride[2] == 1, other strides multiples of 8
  *                   elements, data 16-byte aligned.  D a multiple of 16 up to 512,
  *                   Hkv at most 4096, T at most 2^30, NB below 2^31.
- *   slot_mapping    int32 [T] contiguous, as for paged_attn_cache_write.
+ *   slot_mapping    int32 [T] contiguous, as for paged_attn_cache_write, but that two
+ *                   tokens with the same slot leave it unspecified (a group's codes and
+ *                   scale may be different tokens').
  *   k_cache, v_cache  codes (above): stride[3] == 1, other strides multiples of 8
  *                   bytes, data 8-byte aligned.
  *   k_group_scales, v_group_scales  scales (above), any positive strides.
@@ -404,10 +406,12 @@ int paged_attn_cache_read_q4(const pa_tensor_t* slot_mapping, const pa_tensor_t*
  *     sink's logit with sinks) and sets bit 1 of the status word;
  *   - what a row does not see cannot reach it: slots past a sequence's end or before its
  *     window, and scale codes that are NaN, may be anything there.
- * G * max_query_len <= 64, D in {64, 128}, 1 <= B <= 8192.
+ * G * max_query_len <= 64, D in {64, 128}, 1 <= B <= 8192, max_blocks <= 2^27 - 64, pages
+ * less than 4 GiB apart (else PA_ERR_UNSUPPORTED).
  *   opts   NULL = defaults.  num_ctas (at most 16384), min_pages_per_cta, heads_per_cta,
- *          disable_pdl, sliding_window, sinks, workspace, the split events and
- *          wait_limit_us apply; any other option is refused with PA_ERR_UNSUPPORTED.
+ *          disable_pdl, sliding_window, sinks, workspace and the split events apply;
+ *          wait_limit_us has nothing to limit here (a warp waits for its own copies
+ *          alone); any other option is refused with PA_ERR_UNSUPPORTED.
  *          Calls without opts->workspace share the library-owned workspace of the device:
  *          calls that may overlap on the device (two streams, two captured graphs) each
  *          need a workspace of their own.
@@ -457,8 +461,8 @@ int paged_attn_q4_reserve(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_
  *   not taken (length a multiple of 16, padding, or refused) is set to -1.  A parent may
  *   have several children.  Refused, with bit 5 of the status word and no effect: rows out
  *   of range, a child that is not empty or is itself a parent in the call, a child or a
- *   taken page that an earlier entry names, a page that is not free or out of range when
- *   one is needed, a parent whose length does not fit its row.  A page id out of range in a
+ *   taken page that an earlier entry names, a page whose count is not 0 or that is out of
+ *   range when one is needed, a parent whose length does not fit its row.  A page id out of range in a
  *   parent's row is copied as it is and sets bit 0.
  *
  * paged_attn_pages_free - every row in `rows` gives its pages back (their counts shrink by

@@ -265,7 +265,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
       if (len % kPage != 0) {
         const int page = p.pages[k];
         to[full] = page;
-        p.ref[page] = 1;
+        atomicAdd(p.ref + page, 1);     // was 0; a damaged table may share it in the same call
         if (from[full] < 0 || from[full] >= p.num_pages) atomicOr(p.err, kErrPageRange);
       } else {
         p.pages[k] = -1;

@@ -1,6 +1,8 @@
 """paged_attn_cache_write_q4 and _read_q4 against the oracle: codes and scales
 bit for bit (the same fp32 products and IEEE quotients), values read back after
 one fp32 and one bf16 rounding."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -160,3 +162,40 @@ def test_tensors_off_the_device_are_refused():
     cache = _cache(1, 1, 32, 13)
     with pytest.raises(ValueError):
         binding.paged_attn_cache_write_q4(key.cpu(), val, torch.zeros(2, dtype=torch.int32, device="cuda"), *cache)
+
+
+@pytest.mark.parametrize("T,Hkv,D", [(6, 2, 256), (2500, 8, 128), (5000, 3, 48), (20000, 8, 16)])
+def test_rows_by_lane_groups(T, Hkv, D):
+    """Calls that fill the device and calls that do not, rows of 2 to 32 chunks, warps past the last row."""
+    key, val = _rows(T, Hkv, D, T + D)
+    r = np.random.default_rng(T)
+    NB = -(-T // 16) + 2
+    slots = r.permutation(NB * 16)[:T].astype(np.int32)
+    slots[r.random(T) < 0.05] = -1
+    _check(key, val, slots, _cache(NB, Hkv, D, T))
+
+
+def test_two_threads_with_tensors_of_one_layout():
+    """Calls of the same types and shapes from two threads at once, each with its own tensors and stream."""
+    work = []
+    for seed in (1, 2):
+        key, val = _rows(300, 2, 64, seed)
+        cache = _cache(20, 2, 64, seed)
+        slots = torch.randperm(320, device="cuda", dtype=torch.int32)[:300]
+        want = [t.clone() for t in cache]
+        binding.paged_attn_cache_write_q4(key, val, slots, *want, KS, VS)
+        work.append((key, val, slots, cache, want, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def run(key, val, slots, cache, want, stream):
+        for _ in range(200):
+            binding.paged_attn_cache_write_q4(key, val, slots, *cache, KS, VS, stream=stream)
+
+    threads = [threading.Thread(target=run, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for _, _, _, cache, want, _ in work:
+        assert all(torch.equal(a, b) for a, b in zip(cache, want))

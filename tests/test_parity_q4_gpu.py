@@ -401,3 +401,27 @@ def test_tensors_off_the_device_are_refused():
     dev[5] = dev[5].cpu()
     with pytest.raises(ValueError):
         binding.paged_attn_decode_q4(*dev, 1, c.scale)
+
+
+@pytest.mark.parametrize("b,hq,hkv,d,rows,stages", [
+    (3000, 8, 8, 64, 1, 8),          # the metadata leaves room for one CTA an SM
+    (8192, 1, 1, 64, 32, 8),         # ... for one warp a head
+    (8192, 4, 4, 128, 64, 2),        # ... for a ring of two pages
+    (1000, 2, 1, 128, 8, 4), (1000, 2, 2, 64, 20, 8)])
+def test_launch_forms(b, hq, hkv, d, rows, stages):
+    """Batches whose metadata takes the shared memory of the usual launch (rows: the declared query run)."""
+    r = np.random.default_rng(b + rows)
+    lens = np.where(r.random(b) < 0.2, r.integers(1, 40, b), 0)
+    lens[[7, 500]] = 700, 130
+    c = Case(lens, np.ones(b, dtype=np.int64), hq=hq, hkv=hkv, d=d, seed=rows)
+    c.runs = rows
+    assert binding.paged_attn_q4_plan(b, hq, hkv, d, rows)["num_stages"] == stages
+    c.check(*c.run(), status=binding.STATUS_SEQ_LEN)       # sequences of length 0 are reported
+
+
+@pytest.mark.parametrize("hkv,qlens", [(1, [1, 1, 1]), (1, [2, 2, 1]), (2, [4, 1, 3]), (3, [2, 1, 2]), (4, [4, 4, 4])])
+@pytest.mark.parametrize("ctas", [0, 2])
+def test_windows_over_shared_heads(hkv, qlens, ctas):
+    """Several warps a head, 8 to 32 rows, with pages before, inside and after a window; sinks."""
+    c = Case([500, 333, 90], qlens, hq=8 * hkv, hkv=hkv, d=128, window=200, sinks=True, seed=hkv)
+    c.check(*c.run(num_ctas=ctas, min_pages_per_cta=1))

@@ -11,6 +11,14 @@ from paged_kv_decode_06_gb300 import build as builder
 BAD, UNS = binding.PA_ERR_INVALID_ARG, binding.PA_ERR_UNSUPPORTED
 
 
+@pytest.fixture(autouse=True)
+def _no_gpu():
+    """These calls pass host tensors: where a GPU is present a call that the checks let
+    through would run on their memory."""
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+
+
 @pytest.fixture(scope="module")
 def lib():
     builder.build()
@@ -106,6 +114,81 @@ def test_broadcast_destinations_are_refused(lib):
     a["key"] = torch.zeros(4, 1, 64, dtype=torch.bfloat16).expand(4, 2, 64)
     assert _read(lib, a) == BAD
     _passes(_write(lib, a))
+
+
+# ------------------------------------------------------------------- decode
+
+def _decode_args(T=3, B=3, Hq=8, Hkv=2, D=64, NB=5, MB=4):
+    z = lambda *s: torch.zeros(*s, dtype=torch.uint8)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    return dict(q=torch.zeros(T, Hq, D, dtype=torch.bfloat16), kc=z(NB, 16, Hkv, D // 2), vc=z(NB, 16, Hkv, D // 2),
+                ks=z(NB, Hkv, 16, D // 16), vs=z(NB, Hkv, 16, D // 16), bt=i(B, MB), sl=i(B), qsl=None,
+                out=torch.zeros(T, Hq, D, dtype=torch.bfloat16), lse=torch.zeros(T, Hq), runs=1, scale=0.1, ks1=1.0,
+                vs1=1.0, opts=None, fp4=(1, 2))
+
+
+def _decode(lib, a):
+    r = _refs(a["q"], a["kc"], a["vc"], a["ks"], a["vs"], a["bt"], a["sl"], a["qsl"], a["out"], a["lse"], fp4=a["fp4"])
+    o = binding.make_options(**a["opts"]) if a["opts"] else None
+    return lib.paged_attn_decode_q4(*r[:8], a["runs"], a["scale"], a["ks1"], a["vs1"], *r[8:],
+                                    ctypes.byref(o) if o is not None else None, None)
+
+
+def test_valid_decodes_pass(lib):
+    _passes(_decode(lib, _decode_args()))
+    a = _decode_args(T=5, B=2, Hq=16, Hkv=16, D=128)
+    _passes(_decode(lib, dict(a, qsl=torch.zeros(3, dtype=torch.int32), runs=4, lse=None, opts=dict(heads_per_cta=4))))
+
+
+def test_no_query_tokens_is_nothing_to_do(lib):
+    assert _decode(lib, _decode_args(T=0, B=0)) == binding.PA_OK
+
+
+@pytest.mark.parametrize("change,expect", [
+    (dict(q=torch.zeros(3, 8, 64)), BAD),                                              # not bf16
+    (dict(q=torch.zeros(3, 7, 64, dtype=torch.bfloat16)), BAD),                        # heads not a multiple
+    (dict(q=torch.zeros(3, 8, 128, dtype=torch.bfloat16)), BAD),                       # other head size than the codes'
+    (dict(q=torch.zeros(3, 8, 66, dtype=torch.bfloat16)[:, :, :64]), BAD),             # heads apart
+    (dict(q=torch.zeros(3 * 8 * 64 + 1, dtype=torch.bfloat16)[1:].view(3, 8, 64)), BAD),   # 2-byte aligned
+    (dict(fp4=()), BAD),                                                               # bytes, not codes
+    (dict(kc=torch.zeros(5, 32, 2, 32, dtype=torch.uint8)), UNS),                      # page size
+    (dict(vc=torch.zeros(4, 16, 2, 32, dtype=torch.uint8)), BAD),                      # fewer pages
+    (dict(vc=torch.zeros(5, 16, 2, 40, dtype=torch.uint8)[:, :, :, :32]), BAD),        # strides of 40 bytes
+    (dict(kc=torch.zeros(5, 16, 2, 64, dtype=torch.uint8)[:, :, :, ::2]), BAD),
+    (dict(ks=torch.zeros(5, 16, 2, 4, dtype=torch.uint8).transpose(1, 2)), BAD),       # a page's scales not contiguous
+    (dict(vs=torch.zeros(5, 2, 16, 3, dtype=torch.uint8)), BAD),
+    (dict(ks=torch.zeros(5, 2, 16, 4)), BAD),
+    (dict(bt=torch.zeros(3, 4, dtype=torch.int64)), BAD),
+    (dict(bt=torch.zeros(4, 3, dtype=torch.int32).t()), BAD),
+    (dict(bt=torch.zeros(1, dtype=torch.int32).expand(3, (1 << 27) - 63)), UNS),       # 2^31 tokens
+    (dict(sl=torch.zeros(2, dtype=torch.int32)), BAD),
+    (dict(qsl=torch.zeros(3, dtype=torch.int32)), BAD),
+    (dict(runs=2), BAD),                                                               # runs without offsets
+    (dict(runs=0), BAD),
+    (dict(qsl=torch.zeros(4, dtype=torch.int32), runs=17), UNS),                       # 4 x 17 rows
+    (dict(out=torch.zeros(3, 8, 32, dtype=torch.bfloat16)), BAD),
+    (dict(out=torch.zeros(1, 8, 64, dtype=torch.bfloat16).expand(3, 8, 64)), BAD),
+    (dict(lse=torch.zeros(3, 4)), BAD),
+    (dict(lse=torch.zeros(1, 1).expand(3, 8)), BAD),
+    (dict(scale=float("nan")), BAD),
+    (dict(ks1=float("inf")), BAD),
+    (dict(opts=dict(heads_per_cta=3)), BAD),
+    (dict(opts=dict(num_ctas=1 << 15)), BAD),
+    (dict(opts=dict(num_ctas=-1)), BAD),
+    (dict(opts=dict(page_pairing=1)), UNS),
+])
+def test_decodes_refused(lib, change, expect):
+    st = _decode(lib, dict(_decode_args(), **change))
+    assert st == expect, (st, binding.paged_attn_last_error_message())
+
+
+def test_decode_pages_far_apart_are_refused(lib):
+    a = _decode_args(NB=1)
+    d = binding._new_desc(a["kc"], binding._fp4_code)
+    d.stride[0] = 1 << 32
+    r = _refs(a["q"], a["kc"], a["vc"], a["ks"], a["vs"], a["bt"], a["sl"], None, a["out"], a["lse"], fp4=(1, 2))
+    r[1] = ctypes.byref(d)
+    assert lib.paged_attn_decode_q4(*r[:8], 1, 0.1, 1.0, 1.0, *r[8:], None, None) == UNS
 
 
 # -------------------------------------------------------------------- pages
