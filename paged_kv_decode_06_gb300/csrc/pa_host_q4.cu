@@ -56,7 +56,14 @@ int make_plan(int B, int Hq, int Hkv, int D, int max_qlen, const pa_options_t* o
   PlanQ4 p = {};
   p.G = Hq / Hkv;
   p.R_max = p.G * max_qlen;
-  p.NT = p.R_max <= 8 ? 1 : (p.R_max <= 16 ? 2 : 4);
+  // Tiles of 8 NT query rows, a warp each.  Two warps that both convert a page beat one
+  // with 32 rows of 128 features, whose outputs leave no registers for two pages at once
+  // (32 sequences of 4 tokens, 8 heads, 32 rows: 70 us against 81; one head: 28 against
+  // 43).  With 64 features the 32 rows fit, and win where the heads fill the CTA and the
+  // batch the device (32 sequences: 45 us against 51, 64 rows 72 against 90; 16 short
+  // sequences: 21 against 17; one head: 31 against 22).
+  const bool wide = D == 64 && p.R_max > 16 && Hkv * ((p.R_max + 31) / 32) >= 8 && B >= 32;
+  p.NT = p.R_max <= 8 ? 1 : (wide ? 4 : 2);
   p.MT = (p.R_max + 8 * p.NT - 1) / (8 * p.NT);
   const int warps = split_q4_warps();
   const int forced = o ? o->heads_per_cta : 0;
@@ -69,20 +76,20 @@ int make_plan(int B, int Hq, int Hkv, int D, int max_qlen, const pa_options_t* o
   const uint32_t state = static_cast<uint32_t>(up(split_q4_state_bytes(), 16));
   const uint32_t prefix = static_cast<uint32_t>(up(4u * (3 * static_cast<size_t>(B) + 2), 16));
   const uint32_t query = p.HC * p.MT * split_q4_query_bytes(D, p.NT);
-  // The shared memory of the CTAs that an SM's registers hold, a full ring and as many
-  // warps a head as the CTA has; where the sequences' metadata (12 bytes each) leaves
-  // too little: one CTA an SM, then one warp a head, then a shallow ring.  Where all
+  // The shared memory of the CTAs that an SM's registers hold, and as many warps a head
+  // as the CTA has; where the sequences' metadata (12 bytes each) leaves too little: one
+  // CTA an SM, then one warp a head.  Where all
   // eight warps take one head's pages in turn, one CTA an SM as well: its segments are
   // twice as long against the cost of their ends (64 sequences, one KV head: 21.5 us
   // against 25.6; with two heads and four warps each, two CTAs: 18.7 against 20.7).
   uint32_t ring = 0, xchg = 0;
   int per_sm = 0;
   bool fits = false;
-  for (int form = split_q4_ctas_per_sm(p.NT) == 2 && p.HC * p.MT > 1 ? 0 : 1; form < 4 && !fits; ++form) {
+  for (int form = split_q4_ctas_per_sm(p.NT) == 2 && p.HC * p.MT > 1 ? 0 : 1; form < 3 && !fits; ++form) {
     per_sm = form == 0 ? 2 : 1;
     p.KW = 1;
     while (form < 2 && p.KW < 8 && 2 * p.KW * p.HC * p.MT <= warps) p.KW *= 2;
-    p.nstage = split_q4_stages(D, form == 3);
+    p.nstage = split_q4_stages(D);
     ring = static_cast<uint32_t>(warps * p.nstage * 2 * kPageTokens * (D / 2 + D / kGroup));
     // partial rows the KW warps of a head exchange (pa_split_q4.cu): the features a
     // warp does not gather, and each row's maximum and sum
@@ -218,7 +225,6 @@ int decode_q4(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* vc
   sp.NC = pl.NC;
   sp.MT = pl.MT;
   sp.R_max = pl.R_max;
-  sp.nstage = pl.nstage;
   sp.min_pages = pl.min_pages;
   sp.window = (opts && opts->sliding_window > 0) ? opts->sliding_window : 0;
   sp.sinks = opts ? static_cast<const float*>(opts->sinks) : nullptr;

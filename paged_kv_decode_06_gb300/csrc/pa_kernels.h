@@ -180,7 +180,7 @@ cudaError_t launch_split_q4(int head_dim, int nt, const SplitQ4Params& p, int gr
                             cudaStream_t stream);
 int split_q4_warps();
 int split_q4_ctas_per_sm(int nt);
-int split_q4_stages(int head_dim, bool shallow);
+int split_q4_stages(int head_dim);
 uint32_t split_q4_state_bytes();                       // a CTA's fetch states
 uint32_t split_q4_query_bytes(int head_dim, int nt);   // shared memory of a team's query fragments
 cudaError_t set_split_smem_limits_q4(int smem);

@@ -46,16 +46,12 @@ namespace pa {
 
 constexpr int kQ4Warps = 8;                                         // of a CTA
 constexpr int q4_ctas_per_sm(int nt) { return nt == 1 ? 2 : 1; }
-// Pages in flight a warp: about 9 KB, 150 KB an SM; a shallow ring where the
-// sequences' metadata takes the shared memory.
+// Pages in flight a warp: about 9 KB, 150 KB an SM where two CTAs are on it.
 constexpr int q4_stages(int d) { return d == 128 ? 4 : 8; }
-constexpr int kQ4ShallowStages = 2;
 // A team's query fragments (D x 8 NT x 2 bytes) in shared memory.  Its KW warps write
 // the same values; the barriers at a segment's end keep one segment's apart from the
 // next one's.
 constexpr uint32_t q4_query_bytes(int d, int nt) { return static_cast<uint32_t>(d * 8 * nt * 2); }
-// Pages a warp takes at once where it has two.
-constexpr int q4_pages_at_once(int nt) { return nt <= 2 ? 2 : 1; }
 
 template <int D>
 struct GeoQ4 {
@@ -494,10 +490,10 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
   const int hh = team / MT, wt = team - hh * MT;
   const int gq = lane >> 2, tig = lane & 3;
   const int G = p.G, row0 = 8 * NT * wt;
-  const uint32_t ring = smem_addr(smem) + static_cast<uint32_t>(warp * p.nstage * GG::PAGE);
+  const uint32_t ring = smem_addr(smem) + static_cast<uint32_t>(warp * S * GG::PAGE);
 
   // ---- the fetch side: this warp's pages (kw, kw + KW, ... of every segment) in
-  // order, p.nstage of them ahead of the computation.  `ids` holds 32 page ids, one a
+  // order, S of them ahead of the computation.  `ids` holds 32 page ids, one a
   // lane; the 32 that follow are loaded ahead.  What only a new segment or a new 32
   // ids need waits in shared memory (every lane stores the same values).
   FetchQ4* const fst = reinterpret_cast<FetchQ4*>(smem + p.off_state) + warp;
@@ -618,7 +614,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
     }
   };
   query_ahead(sg, si);
-  const uint32_t ring_end = ring + static_cast<uint32_t>(p.nstage * GG::PAGE);
+  const uint32_t ring_end = ring + static_cast<uint32_t>(S * GG::PAGE);
   for (uint32_t a = ring; a < ring_end; a += GG::PAGE) fetch(a);
   uint32_t at = ring;               // the page to compute
   bool first = true;
@@ -672,8 +668,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
       auto after = [&](uint32_t a) { return a + GG::PAGE == ring_end ? ring : a + GG::PAGE; };
       auto run = [&](auto edge, int stop) {
         for (; t < stop; t += kPage * KW) {
-          if (p.nstage == S) copy_wait<S - 1>();
-          else copy_wait<kQ4ShallowStages - 1>();
+          copy_wait<S - 1>();
           __syncwarp();
           const uint32_t one[1] = {at};
           if (active) cs.template page<decltype(edge)::value, 1>(ln, one, t, si.L, window, rows, tig);
@@ -683,19 +678,16 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
         }
       };
       if (WINDOW) run(Bool<true>{}, lo);
-      if constexpr (q4_pages_at_once(NT) == 2) {
-        if (p.nstage == S) {
-          for (; t + kPage * KW < hi; t += 2 * kPage * KW) {
-            copy_wait<S - 2>();
-            __syncwarp();
-            const uint32_t two[2] = {at, after(at)};
-            if (active) cs.template page<false, 2>(ln, two, t, si.L, window, rows, tig);
-            __syncwarp();
-            fetch(two[0]);
-            fetch(two[1]);
-            at = after(two[1]);
-          }
-        }
+      // two at once while there are two: their chains of dependent steps overlap
+      for (; t + kPage * KW < hi; t += 2 * kPage * KW) {
+        copy_wait<S - 2>();
+        __syncwarp();
+        const uint32_t two[2] = {at, after(at)};
+        if (active) cs.template page<false, 2>(ln, two, t, si.L, window, rows, tig);
+        __syncwarp();
+        fetch(two[0]);
+        fetch(two[1]);
+        at = after(two[1]);
       }
       run(Bool<false>{}, hi);
       run(Bool<true>{}, t_end);
@@ -826,14 +818,6 @@ cudaError_t launch_nt(cudaLaunchConfig_t* cfg, const SplitQ4Params& p) {
                       : cudaLaunchKernelEx(cfg, pa_split_q4_kernel<D, NT, false>, p);
 }
 
-template <int D>
-cudaError_t launch_d(cudaLaunchConfig_t* cfg, int nt, const SplitQ4Params& p) {
-  if (nt == 1) return launch_nt<D, 1>(cfg, p);
-  if (nt == 2) return launch_nt<D, 2>(cfg, p);
-  if (nt == 4) return launch_nt<D, 4>(cfg, p);
-  return cudaErrorInvalidValue;
-}
-
 template <int D, int NT>
 cudaError_t limit_nt(int smem) {
   const cudaError_t e = cudaFuncSetAttribute(pa_split_q4_kernel<D, NT, false>,
@@ -846,7 +830,7 @@ cudaError_t limit_nt(int smem) {
 
 int split_q4_warps() { return kQ4Warps; }
 int split_q4_ctas_per_sm(int nt) { return q4_ctas_per_sm(nt); }
-int split_q4_stages(int head_dim, bool shallow) { return shallow ? kQ4ShallowStages : q4_stages(head_dim); }
+int split_q4_stages(int head_dim) { return q4_stages(head_dim); }
 uint32_t split_q4_state_bytes() { return kQ4Warps * sizeof(FetchQ4); }
 uint32_t split_q4_query_bytes(int head_dim, int nt) { return q4_query_bytes(head_dim, nt); }
 
@@ -861,15 +845,18 @@ cudaError_t launch_split_q4(int head_dim, int nt, const SplitQ4Params& p, int gr
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
-  if (head_dim == 128) return launch_d<128>(&cfg, nt, p);
-  if (head_dim == 64) return launch_d<64>(&cfg, nt, p);
+  if (head_dim == 128 && nt == 1) return launch_nt<128, 1>(&cfg, p);
+  if (head_dim == 128 && nt == 2) return launch_nt<128, 2>(&cfg, p);
+  if (head_dim == 64 && nt == 1) return launch_nt<64, 1>(&cfg, p);
+  if (head_dim == 64 && nt == 2) return launch_nt<64, 2>(&cfg, p);
+  if (head_dim == 64 && nt == 4) return launch_nt<64, 4>(&cfg, p);
   return cudaErrorInvalidValue;
 }
 
 cudaError_t set_split_smem_limits_q4(int smem) {
   cudaError_t e;
-  if ((e = limit_nt<128, 1>(smem)) || (e = limit_nt<128, 2>(smem)) || (e = limit_nt<128, 4>(smem)) ||
-      (e = limit_nt<64, 1>(smem)) || (e = limit_nt<64, 2>(smem)) || (e = limit_nt<64, 4>(smem)))
+  if ((e = limit_nt<128, 1>(smem)) || (e = limit_nt<128, 2>(smem)) || (e = limit_nt<64, 1>(smem)) ||
+      (e = limit_nt<64, 2>(smem)) || (e = limit_nt<64, 4>(smem)))
     return e;
   return cudaSuccess;
 }

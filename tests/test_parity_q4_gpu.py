@@ -406,7 +406,7 @@ def test_tensors_off_the_device_are_refused():
 @pytest.mark.parametrize("b,hq,hkv,d,rows,stages", [
     (3000, 8, 8, 64, 1, 8),          # the metadata leaves room for one CTA an SM
     (8192, 1, 1, 64, 32, 8),         # ... for one warp a head
-    (8192, 4, 4, 128, 64, 2),        # ... for a ring of two pages
+    (8192, 4, 4, 128, 64, 4),        # ... the most shared memory
     (1000, 2, 1, 128, 8, 4), (1000, 2, 2, 64, 20, 8)])
 def test_launch_forms(b, hq, hkv, d, rows, stages):
     """Batches whose metadata takes the shared memory of the usual launch (rows: the declared query run)."""
@@ -425,3 +425,14 @@ def test_windows_over_shared_heads(hkv, qlens, ctas):
     """Several warps a head, 8 to 32 rows, with pages before, inside and after a window; sinks."""
     c = Case([500, 333, 90], qlens, hq=8 * hkv, hkv=hkv, d=128, window=200, sinks=True, seed=hkv)
     c.check(*c.run(num_ctas=ctas, min_pages_per_cta=1))
+
+
+@pytest.mark.parametrize("hq,hkv,runs,window", [(32, 8, 5, 0), (32, 8, 8, 40), (64, 8, 8, 0), (16, 4, 16, 0),
+                                                (20, 5, 10, 33), (64, 16, 7, 0)])
+def test_large_batches_of_many_rows(hq, hkv, runs, window):
+    """32 sequences and more with 17 to 64 rows a head of 64 features: the tiles of 32 rows."""
+    r = np.random.default_rng(hq + runs)
+    lens = r.integers(runs, 300, 37)
+    qlens = np.where(r.random(37) < 0.5, runs, r.integers(1, runs, 37))
+    c = Case(lens, qlens, hq=hq, hkv=hkv, d=64, window=window, sinks=window > 0, seed=runs)
+    c.check(*c.run())
