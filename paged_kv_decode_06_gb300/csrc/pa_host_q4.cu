@@ -299,7 +299,8 @@ int decode_q4(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* vc
   // into many pieces: about a block an SM (64 rows of one sequence: 4.6 us; 8192
   // rows of 32 sequences in 5 pieces each: 118 us, where a warp a row takes 9).
   const bool wide = pl.grid >= 4 * units && static_cast<int64_t>(units) * pl.HC * pl.R_max <= 2 * dev.num_sms;
-  if ((e = launch_merge(static_cast<int>(D), mp, units, pl.HC * pl.R_max, wide, pdl && !ev1, stream)) != cudaSuccess)
+  if ((e = launch_merge(static_cast<int>(D), mp, units, pl.HC * pl.R_max, wide, pdl && !ev1, stream,
+                        true)) != cudaSuccess)
     return host_cuda_fail(e, "merge kernel launch");
   return PA_OK;
 }

@@ -149,8 +149,9 @@ cudaError_t launch_split_fp8_tok(int head_dim, const CUtensorMap& tk, const CUte
 cudaError_t set_split_smem_limits_fp8_tok(int smem);
 // wide: one 256-thread block per (unit, row), threads across partials (many
 // partials per unit); otherwise one warp per (unit, row), 8 rows per block.
+// deep: more partials' loads in flight (the same sums in the same order).
 cudaError_t launch_merge(int head_dim, const MergeParams& p, int units, int rows, bool wide, bool pdl,
-                         cudaStream_t stream);
+                         cudaStream_t stream, bool deep = false);
 // Tensor-memory (tcgen05) variant for up to 128 query rows per KV head (bf16
 // caches, one KV head per CTA, 192 threads).
 cudaError_t launch_split_tc(int head_dim, const CUtensorMap& tk, const CUtensorMap& tv, const SplitParams& p,
