@@ -10,11 +10,14 @@
 // code * S (exact) times ts rounded to fp32, then to bf16.
 //
 // Both are bound by memory: 4 bytes of bf16 a (key, value) feature pair against
-// 9/8 bytes of codes and scales.  A (token, head) row belongs to L lanes, each with
-// every L-th 8-feature chunk of it (up to four in flight): a copy instruction then
-// moves whole sectors, and one address serves four chunks.  (A thread a 16-feature
-// group took 27 us to write and 19 to read 16384 tokens x 8 heads x 128, a thread a
-// chunk 32 and 26: the address arithmetic of every piece cost more than the piece.)
+// 9/8 bytes of codes and scales.  A (token, head) row belongs to L lanes, so that the
+// index arithmetic of a row serves several pieces of it.  Writing, a lane takes whole
+// groups (every L-th, two in flight): a group's maximum, scale and reciprocal are
+// computed once and its codes leave as 8 bytes.  Reading, a lane takes 8-feature chunks
+// (every L-th, four in flight), so that a store instruction fills whole sectors.
+// 16384 tokens x 8 heads x 128: 21 us to write (86 MB, 4.0 TB/s; in chunks 26 us, a
+// thread a group 27) and 15 to read (86 MB, 5.6 TB/s; in groups 19, a thread a group 19).
+// Writing spends the rest on the quotients: 40 instructions a chunk.
 #include "pa_device.cuh"
 #include "pa_host.h"
 #include "pa_q4.cuh"
@@ -33,15 +36,16 @@ struct RowsQ4Params {
   int64_t code_page[2], code_slot[2], code_head[2];
   uint8_t* scales[2];          // K, V group scales [NB, Hkv, 16, D / 16]
   int64_t sc_page[2], sc_head[2], sc_slot[2], sc_group[2];
-  int32_t num_tokens, num_kv_heads, chunks, num_pages;   // chunks: 8 features each, of a row
+  int32_t num_tokens, num_kv_heads, groups, num_pages;   // groups of a row
   int32_t lg;                  // 2^lg lanes a row
   float ts[2];                 // tensor scales
   float six_ts[2];             // fp32(6 ts)
   uint32_t* err;
 };
 
-constexpr int kRowChunks = 4;      // chunks of a lane at a time
-constexpr int kRowWaves = 8;       // CTAs an SM and tensor (4: 40 us for both directions, 8: 39, 16: 41)
+constexpr int kRowGroups = 2;      // groups of a lane at a time (write)
+constexpr int kRowChunks = 4;      // 8-feature chunks of a lane at a time (read)
+constexpr int kRowWaves = 8;       // CTAs an SM and tensor (4 or 16: 1 us more)
 
 // Where a row's codes and scales lie.
 __device__ __forceinline__ uint8_t* codes_at(const RowsQ4Params& p, int y, int slot, int h) {
@@ -53,11 +57,11 @@ __device__ __forceinline__ uint8_t* scales_at(const RowsQ4Params& p, int y, int 
   return p.scales[y] + page * p.sc_page[y] + (slot % kPage) * p.sc_slot[y] + h * p.sc_head[y];
 }
 
-// e2m1 codes of eight features over the group's scale d > 0 (amax: the group's
+// e2m1 codes of eight features over the group's scale sd.s > 0 (amax: the group's
 // largest magnitude).
-__device__ __forceinline__ uint32_t quantise8(const uint4 v, float d, float amax) {
+__device__ __forceinline__ uint32_t quantise8(const uint4 v, const ScaleDiv& sd, float amax) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  const ScaleDiv sd = scale_div(d);
+  const float d = sd.s;
   float q[8];
   // Quotients below 1024 need none of div_by2's exceptions but the sign of a zero,
   // which every quotient takes from its feature here.
@@ -83,7 +87,6 @@ __device__ __forceinline__ uint32_t quantise8(const uint4 v, float d, float amax
 }
 
 // One row a group of L = 2^lg lanes at a time, of one tensor (blockIdx.y: 0 = K, 1 = V).
-// Lanes q and q ^ 1 hold the two halves of a 16-feature group.
 __global__ void __launch_bounds__(256) pa_cache_write_q4_kernel(const RowsQ4Params p) {
   const int y = blockIdx.y, q = threadIdx.x & ((1 << p.lg) - 1);
   const int64_t rows = static_cast<int64_t>(p.num_tokens) * p.num_kv_heads;
@@ -91,44 +94,48 @@ __global__ void __launch_bounds__(256) pa_cache_write_q4_kernel(const RowsQ4Para
   const int64_t num_slots = static_cast<int64_t>(p.num_pages) * kPage;
   const float ts = p.ts[y], six = p.six_ts[y];
   const int64_t step = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> p.lg;
-  const int64_t r0 = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> p.lg;
-  const int64_t warp_r0 = (static_cast<int64_t>(blockIdx.x) * blockDim.x + (threadIdx.x & ~31)) >> p.lg;
-  // trips go by the warp's first row, so that whole warps meet in the exchanges
-  for (int64_t k = 0; warp_r0 + k < rows; k += step) {
-    const int64_t r = r0 + k;
-    const bool in = r < rows;
-    const int64_t t = in ? cw_div(r, p.num_kv_heads, narrow) : 0;
-    const int h = in ? static_cast<int>(r - t * p.num_kv_heads) : 0;
-    const int slot = in ? p.slots[t] : -1;
+  for (int64_t r = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> p.lg; r < rows; r += step) {
+    const int64_t t = cw_div(r, p.num_kv_heads, narrow);
+    const int h = static_cast<int>(r - t * p.num_kv_heads);
     const uint16_t* src = p.rows[y] + t * p.row_t[y] + h * p.row_h[y];
-    bool live = slot >= 0;                         // not a padding token
-    if (live && slot >= num_slots) {
+    const int slot = p.slots[t];
+    if (slot < 0) continue;                        // padding token
+    if (slot >= num_slots) {
       if (h == 0 && q == 0) atomicOr(p.err, kErrPageRange);
-      live = false;
+      continue;
     }
-    uint8_t* codes = live ? codes_at(p, y, slot, h) : nullptr;
-    uint8_t* scales = live ? scales_at(p, y, slot, h) : nullptr;
-    for (int c0 = 0; c0 < p.chunks; c0 += kRowChunks << p.lg) {
-      uint4 v[kRowChunks];
+    uint8_t* codes = codes_at(p, y, slot, h);
+    uint8_t* scales = scales_at(p, y, slot, h);
+    for (int g0 = 0; g0 < p.groups; g0 += kRowGroups << p.lg) {
+      uint4 v[kRowGroups][2];
 #pragma unroll
-      for (int u = 0; u < kRowChunks; ++u) {
-        const int c = c0 + (u << p.lg) + q;
-        v[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (live && c < p.chunks) v[u] = *reinterpret_cast<const uint4*>(src + c * 8);
+      for (int u = 0; u < kRowGroups; ++u) {
+        const int g = g0 + (u << p.lg) + q;
+        if (g >= p.groups) break;
+        const uint4* x = reinterpret_cast<const uint4*>(src + g * kQ4Group);
+        v[u][0] = x[0];
+        v[u][1] = x[1];
       }
 #pragma unroll
-      for (int u = 0; u < kRowChunks; ++u) {
-        const int c = c0 + (u << p.lg) + q;
+      for (int u = 0; u < kRowGroups; ++u) {
+        const int g = g0 + (u << p.lg) + q;
+        if (g >= p.groups) break;
         // magnitudes in bf16 order as their bits
-        uint32_t m2 = max_u16x2(max_u16x2(v[u].x & 0x7FFF7FFFu, v[u].y & 0x7FFF7FFFu),
-                                max_u16x2(v[u].z & 0x7FFF7FFFu, v[u].w & 0x7FFF7FFFu));
-        m2 = max_u16x2(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
-        if (!live || c >= p.chunks) continue;
+        uint32_t m2 = 0u;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          m2 = max_u16x2(m2, max_u16x2(max_u16x2(v[u][k].x & 0x7FFF7FFFu, v[u][k].y & 0x7FFF7FFFu),
+                                       max_u16x2(v[u][k].z & 0x7FFF7FFFu, v[u][k].w & 0x7FFF7FFFu)));
         const float amax = __uint_as_float(max(m2 << 16, m2 & 0xFFFF0000u));
         const uint32_t s8 = e4m3x2_from_f32(__fdiv_rn(amax, six), 0.f) & 0xFFu;
         const float d = __fmul_rn(f16_lo(e4m3x2_to_f16x2(s8)), ts);
-        *reinterpret_cast<uint32_t*>(codes + c * 4) = d > 0.f ? quantise8(v[u], d, amax) : 0u;   // else 0 or NaN
-        if ((q & 1) == 0) scales[(c >> 1) * p.sc_group[y]] = static_cast<uint8_t>(s8);
+        uint2 c = make_uint2(0u, 0u);
+        if (d > 0.f) {                             // else 0 or NaN
+          const ScaleDiv sd = scale_div(d);
+          c = make_uint2(quantise8(v[u][0], sd, amax), quantise8(v[u][1], sd, amax));
+        }
+        *reinterpret_cast<uint2*>(codes + g * (kQ4Group / 2)) = c;
+        scales[g * p.sc_group[y]] = static_cast<uint8_t>(s8);
       }
     }
   }
@@ -141,6 +148,7 @@ __global__ void __launch_bounds__(256) pa_cache_read_q4_kernel(const RowsQ4Param
   const bool narrow = rows <= 0xFFFFFFFFll;
   const int64_t num_slots = static_cast<int64_t>(p.num_pages) * kPage;
   const float ts = p.ts[y];
+  const int chunks = 2 * p.groups;                 // of 8 features
   const int64_t step = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> p.lg;
   for (int64_t r = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> p.lg; r < rows; r += step) {
     const int64_t t = cw_div(r, p.num_kv_heads, narrow);
@@ -154,13 +162,13 @@ __global__ void __launch_bounds__(256) pa_cache_read_q4_kernel(const RowsQ4Param
     const uint8_t* codes = codes_at(p, y, slot, h);
     const uint8_t* scales = scales_at(p, y, slot, h);
     uint16_t* dst = p.rows[y] + t * p.row_t[y] + h * p.row_h[y];
-    for (int c0 = 0; c0 < p.chunks; c0 += kRowChunks << p.lg) {
+    for (int c0 = 0; c0 < chunks; c0 += kRowChunks << p.lg) {
       uint32_t w[kRowChunks], s8[kRowChunks];
 #pragma unroll
       for (int u = 0; u < kRowChunks; ++u) {
         const int c = c0 + (u << p.lg) + q;
         w[u] = s8[u] = 0u;
-        if (c < p.chunks) {
+        if (c < chunks) {
           w[u] = *reinterpret_cast<const uint32_t*>(codes + c * 4);
           s8[u] = scales[(c >> 1) * p.sc_group[y]];
         }
@@ -168,7 +176,7 @@ __global__ void __launch_bounds__(256) pa_cache_read_q4_kernel(const RowsQ4Param
 #pragma unroll
       for (int u = 0; u < kRowChunks; ++u) {
         const int c = c0 + (u << p.lg) + q;
-        if (c >= p.chunks) break;
+        if (c >= chunks) break;
         const uint32_t s2 = e4m3x2_to_f16x2(s8[u] * 0x0101u);
         uint32_t x[4], o[4];
         e2m1x8_to_f16(w[u], x);
@@ -272,12 +280,13 @@ int rows_q4(bool write, const pa_tensor_t* key, const pa_tensor_t* value, const 
   p.slots = static_cast<const int32_t*>(slots->data);
   p.num_tokens = static_cast<int32_t>(T);
   p.num_kv_heads = static_cast<int32_t>(Hkv);
-  p.chunks = static_cast<int32_t>(D / 8);
-  // Four chunks a lane; where the rows leave most of the device idle, they lie side by
-  // side instead (write and read of 64 tokens x 8 heads x 128: 4.1 us against 4.9; from
-  // half a CTA an SM on the four in flight win: 1000 tokens 6.4 us against 8.7).
-  for (p.lg = 1; p.lg < 5 && (kRowChunks << p.lg) < p.chunks;) ++p.lg;
-  while (p.lg < 5 && (1 << p.lg) < p.chunks && ((T * Hkv) << p.lg) < int64_t(dev.num_sms) * 128) ++p.lg;
+  p.groups = static_cast<int32_t>(D / kQ4Group);
+  const int pieces = write ? p.groups : 2 * p.groups, at_once = write ? kRowGroups : kRowChunks;
+  // A lane's pieces at a time; where the rows leave most of the device idle, they lie side
+  // by side instead (write and read of 64 tokens x 8 heads x 128: 4.1 us against 4.9; from
+  // half a CTA an SM on the several in flight win: 1000 tokens 6.4 us against 8.7).
+  for (p.lg = 0; p.lg < 5 && (at_once << p.lg) < pieces;) ++p.lg;
+  while (p.lg < 5 && (1 << p.lg) < pieces && ((T * Hkv) << p.lg) < int64_t(dev.num_sms) * 128) ++p.lg;
   p.num_pages = static_cast<int32_t>(kc->shape[0]);
   p.err = dev.status;
   const int64_t blocks = (((T * Hkv) << p.lg) + 255) / 256;
