@@ -923,7 +923,7 @@ def kernel_source_sha256(kernel):
     """Hash of the sources a kernel is compiled from (stamps ncu figures)."""
     import hashlib
     if kernel.startswith("pa_cache_write"):
-        names = ["pa_cache_write.cu", "pa_device.cuh", "pa_pack.cuh"]
+        names = ["pa_cache_write.cu", "pa_quant.cuh", "pa_device.cuh", "pa_pack.cuh"]
     else:
         names = ["pa_split.cuh", "pa_device.cuh", "pa_pack.cuh"] + \
             (["pa_split_tc.cuh"] if kernel == "pa_split_tc_kernel" else []) + \
