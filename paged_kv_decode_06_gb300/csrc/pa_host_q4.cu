@@ -296,8 +296,8 @@ int decode_q4(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* vc
     return host_cuda_fail(e, "cudaEventRecord(stop)");
   const int units = static_cast<int>(B) * pl.NC;
   // The merge that reads a row's partials with a whole block is for few rows cut
-  // into many pieces: about a block an SM (64 rows of one sequence: 4.6 us; 8192
-  // rows of 32 sequences in 5 pieces each: 118 us, where a warp a row takes 9).
+  // into many pieces: up to two blocks an SM (one sequence of 32768 tokens: 15 us a
+  // call against 33 with a warp a row; 512 rows of 19 pieces: 25 us against 21).
   const bool wide = pl.grid >= 4 * units && static_cast<int64_t>(units) * pl.HC * pl.R_max <= 2 * dev.num_sms;
   if ((e = launch_merge(static_cast<int>(D), mp, units, pl.HC * pl.R_max, wide, pdl && !ev1, stream,
                         true)) != cudaSuccess)

@@ -175,8 +175,8 @@ cudaError_t launch_mla_tc(bool fp8, int rpad, const CUtensorMap& tm, const CUten
                           int grid, int smem, bool pdl, cudaStream_t stream);
 int mla_tc_threads();
 cudaError_t set_mla_tc_smem_limits(int smem);
-// 4-bit caches: nt 8-row tiles a warp (1, 2 or 4), split_q4_warps() warps a CTA,
-// p.nstage pages in flight a warp (one of the two split_q4_stages).
+// 4-bit caches: nt 8-row tiles a warp (1 or 2; 4 for head_dim 64), split_q4_warps()
+// warps a CTA, split_q4_stages() pages in flight a warp.
 cudaError_t launch_split_q4(int head_dim, int nt, const SplitQ4Params& p, int grid, int smem, bool pdl,
                             cudaStream_t stream);
 int split_q4_warps();

@@ -29,16 +29,26 @@
 // A CTA is eight warps, two CTAs an SM for at most 8 query rows a KV head (128
 // registers a thread), else one (255).  KW x MT x HC warps are in use: HC KV heads,
 // MT tiles of 8 NT query rows, and KW warps that take a head's pages in turn and meet
-// in shared memory at the end of a segment (a sequence's pages in this CTA).
+// in shared memory at the end of a segment (a sequence's pages in this CTA).  The
+// host's plan has the rules for NT, HC and KW with what each side measured.
 //
 // Every warp feeds itself: it copies the 2.3 KB (D = 128) of its head's codes and
 // scales of a page with five 16-byte cp.async a lane into its own ring, S pages
 // ahead, so no warp ever waits for another or polls a barrier.  The form before it,
 // producer warps with bulk tensor copies of whole pages into a ring of the CTA's,
-// ran 151 us on the batch of 256 (673 MB): a third of the issue slots went to the
+// ran 153 us on the batch of 256 (673 MB): a third of the issue slots went to the
 // producers, to polling and to register spills (a producer warpgroup's registers
 // are not the consumers'), and a copy instruction held a producer for 280 to 540
 // cycles beside warps that compute.
+//
+// Measured: 256 sequences of 128 to 8192 tokens, 32 / 8 heads of 128 (673 MB): 140 us,
+// 4.8 TB/s, 71% of the copy bandwidth.  Issue-bound: 172 instructions a page and head
+// for 2.3 KB, the issue slots 57% full with four warps a scheduler (counters of a batch
+// of 96), and neither more warps (85 registers: spills) nor a wider tile helps.  32
+// sequences of 4 tokens and 64 rows of 8 heads, window 4096 (117 MB): 70 us, bound by
+// the two warps a scheduler that 248 registers leave (issue 42%, tensor pipe 26%).  One
+// sequence of 32768 tokens, 64 features: 15 us, of which the two kernels' start-up and
+// the dependent loads (lengths, page ids, pages; descriptor, partials) are about 12.
 #include "pa_q4.cuh"
 #include "pa_split.cuh"
 
