@@ -1036,10 +1036,6 @@ int host_reserve(size_t bytes) {
   const int st = device_state(&ds, nullptr);
   return st != PA_OK ? st : grow_workspace(ds, bytes);
 }
-CUresult host_encode_tiled(CUtensorMap* map, CUtensorMapDataType dtype, int rank, void* ptr, const cuuint64_t* dims,
-                           const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
-  return encode_tiled(map, dtype, rank, ptr, dims, strides, box, swizzle);
-}
 }  // namespace pa
 
 extern "C" {

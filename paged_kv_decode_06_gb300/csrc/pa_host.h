@@ -1,9 +1,8 @@
 // Host helpers shared by the translation units that implement entry points
-// (defined in pa_host.cu): error details, descriptor checks, per-device state,
-// the split workspace and TMA descriptor encoding.
+// (defined in pa_host.cu): error details, descriptor checks, per-device state
+// and the split workspace.
 #pragma once
 
-#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <exception>
@@ -32,7 +31,7 @@ struct HostDevice {
 };
 
 // Serialises the library's host state.  Hold it across host_device,
-// host_workspace, host_encode_tiled and the launches that use their results.
+// host_workspace and the launches that use their results.
 std::unique_lock<std::mutex> host_lock();
 int host_device(HostDevice* out);
 
@@ -41,9 +40,6 @@ int host_device(HostDevice* out);
 int host_workspace(const pa_options_t* opts, size_t bytes, cudaStream_t stream, const char* reserve_fn, void** ws);
 int host_reserve(size_t bytes);
 
-CUresult host_encode_tiled(CUtensorMap* map, CUtensorMapDataType dtype, int rank, void* ptr, const cuuint64_t* dims,
-                           const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle);
-
 // Runs the body of an entry point: no exception crosses the C boundary.
 template <typename F>
 int host_entry(F body) noexcept {
@@ -51,10 +47,13 @@ int host_entry(F body) noexcept {
     host_clear_error();
     return body();
   } catch (const std::exception& e) {
-    return host_fail(PA_ERR_CUDA, "host error: %s", e.what());
+    try {
+      return host_fail(PA_ERR_CUDA, "host error: %s", e.what());
+    } catch (...) {
+    }
   } catch (...) {
-    return PA_ERR_CUDA;
   }
+  return PA_ERR_CUDA;
 }
 
 }  // namespace pa

@@ -432,7 +432,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
     pa_page_compact_kernel(const PoolParams p) {
   constexpr int W = kClusterThreads / 32;
   __shared__ int s_warp[W];
-  __shared__ int s_total[3];
+  __shared__ int s_total, s_low;                  // s_low: pages in use with ids below U
   __shared__ uint32_t s_words[W][kMaskWords];
   grid_dependency_wait();
   grid_launch_dependents();
@@ -449,16 +449,17 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
     negative |= r < 0;
   });
   if (negative) atomicOr(p.err, kErrPageOp);
-  int U, holes_all, high_all;
-  cluster_prefix(cluster, mine, s_warp, &s_total[0], U);
-  int holes = 0, high = 0;
-  for (int64_t b = lo; b < hi; b += 32) {
-    const uint32_t m = word_of(p.ref, lo, hi, b, lane, words);
-    holes += __popc(~m & below(b, min(hi, static_cast<int64_t>(U))));
-    high += __popc(m & ~below(b, U));
+  int U;
+  const int used = cluster_prefix(cluster, mine, s_warp, &s_total, U);     // pages in use before lo
+  // before a page x there are x - (pages in use before it) free pages, and from U on
+  // (pages in use before x) - (pages in use before U) high ones: the warp whose run
+  // holds U tells every block the latter
+  if (lo <= U && U < hi) {
+    int before = used;
+    for (int64_t b = lo; b < U; b += 32) before += __popc(word_of(p.ref, lo, hi, b, lane, words) & below(b, U));
+    if (lane < kClusterCtas) *cluster.map_shared_rank(&s_low, lane) = before;
   }
-  int at_hole = cluster_prefix(cluster, holes, s_warp, &s_total[1], holes_all);
-  int at_high = cluster_prefix(cluster, high, s_warp, &s_total[2], high_all);
+  int at_hole = static_cast<int>(lo) - used;
   for (int64_t b = lo; b < min(hi, static_cast<int64_t>(U)); b += 32) {
     const uint32_t in = below(b, min(hi, static_cast<int64_t>(U)));
     const uint32_t m = word_of(p.ref, lo, hi, b, lane, words);
@@ -468,6 +469,7 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
     at_hole += __popc(in & ~m);
   }
   cluster.sync();
+  int at_high = lo < U ? 0 : used - s_low;
   for (int64_t b = lo; b < hi; b += 32) {
     const int64_t id = b + lane;
     const uint32_t m = word_of(p.ref, lo, hi, b, lane, words) & ~below(b, U);

@@ -266,3 +266,34 @@ def test_a_chain_in_one_graph_replayed():
         dev[1].copy_(_i32(sl))
         dev[5].copy_(_i32(new))
     binding.paged_attn_device_status()
+
+
+@pytest.mark.parametrize("nb", [2_200_003, 4_500_000])
+def test_pools_past_the_masks_in_shared_memory(nb):
+    """Free list and compaction of pools whose use masks do not fit the kernels' shared memory."""
+    r = np.random.default_rng(nb)
+    ref = (r.random(nb) < 0.7).astype(np.int32) * r.integers(1, 4, nb).astype(np.int32)
+    dref = _i32(ref)
+    ids, num = binding.paged_attn_pages_free(_i32([[0]]), _i32([0]), dref, _i32([-1]))
+    free = np.flatnonzero(ref == 0)
+    assert num.item() == len(free)
+    assert np.array_equal(ids.cpu().numpy(), np.concatenate([free, np.full(nb - len(free), -1)]))
+    cache = torch.arange(nb, dtype=torch.int32, device="cuda")[:, None].repeat(1, 2)
+    bt = r.integers(-1, nb, (3, 1000)).astype(np.int32)
+    dbt = _i32(bt)
+    page_map, used = binding.paged_attn_pages_compact([cache], dbt, dref)
+    U = nb - len(free)
+    high, holes = np.flatnonzero(ref[U:] > 0) + U, np.flatnonzero(ref[:U] == 0)
+    want = np.where(ref > 0, np.arange(nb), -1)
+    want[high] = holes
+    assert used.item() == U and np.array_equal(page_map.cpu().numpy(), want)
+    after = np.zeros(nb, dtype=np.int32)
+    after[:U] = ref[:U]
+    after[holes] = ref[high]
+    assert np.array_equal(dref.cpu().numpy(), after)
+    home = np.arange(U)
+    home[holes] = high
+    assert np.array_equal(cache[:U].cpu().numpy(), np.stack([home, home], 1))
+    moved = np.where(bt >= 0, want[np.maximum(bt, 0)], -1)
+    assert np.array_equal(dbt.cpu().numpy(), np.where(moved >= 0, moved, bt))
+    assert binding.paged_attn_device_status() == 0
