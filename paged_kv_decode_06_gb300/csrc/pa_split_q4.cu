@@ -201,9 +201,11 @@ struct StateQ4 {
                          fmaxf(fabsf(bf16_lo(w[ks].y)), fabsf(bf16_hi(w[ks].y)))), amax);
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    // exponent of the row's largest element, kept where 2^-e and scale * 2^e are normal
+    // exponent of the row's largest element, kept where 2^-e and 2^e are normal (a
+    // subnormal row then lies 2^-7 and less, above f16's subnormals, and elements of
+    // 2^127 at 2^12)
     int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-    ex = max(-100, min(115, ex));
+    ex = max(-126, min(115, ex));
     const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
 #pragma unroll
     for (int ks = 0; ks < GG::KS; ks += 2) {

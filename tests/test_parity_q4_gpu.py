@@ -436,3 +436,10 @@ def test_large_batches_of_many_rows(hq, hkv, runs, window):
     qlens = np.where(r.random(37) < 0.5, runs, r.integers(1, runs, 37))
     c = Case(lens, qlens, hq=hq, hkv=hkv, d=64, window=window, sinks=window > 0, seed=runs)
     c.check(*c.run())
+
+
+@pytest.mark.parametrize("gain,scale,k_scale", [(2e-38, 1e37, 0.02), (1e-39, 1e37, 0.02), (3e37, 1e-20, 6e-21)])
+def test_query_rows_at_the_ends_of_the_range(gain, scale, k_scale):
+    """Rows of subnormal elements, and of the largest, with scales that make up for them."""
+    c = Case([40, 130], [2, 1], q_gain=gain, scale=scale, k_scale=k_scale, seed=33)
+    c.check(*c.run())
