@@ -323,12 +323,17 @@ _GET_DEVICE = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_d
 def _on_current_device(*tensors) -> int:
     """The calls below take device pointers of the current CUDA device: a tensor
     elsewhere is refused here (the library cannot see where a pointer lives)."""
-    dev = _GET_DEVICE() if torch.cuda.is_initialized() else None
+    dev = None
     for t in tensors:
-        if t is not None and t.get_device() != dev:        # -1 for a host tensor
-            if not t.is_cuda:
+        if t is None:
+            continue
+        d = t.get_device()                       # -1 for a host tensor
+        if d != dev:
+            if d < 0:
                 raise ValueError(f"a CUDA tensor is required, got one on {t.device}")
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+            if dev is not None or d != _GET_DEVICE():
+                raise ValueError(f"tensor on {t.device}, but the current device is cuda:{_GET_DEVICE()}")
+            dev = d
     return dev
 
 

@@ -1,8 +1,9 @@
 // Split-KV decode attention over a 4-bit paged cache (pa_q4.cuh has the format).
 //
 // Work decomposition, workspace and merge are those of the bf16 / fp8 split
-// kernel: CTA g takes an equal range of the (sequence, head chunk, page) order;
-// a unit cut by a range boundary leaves fp32 partials for the merge kernel.
+// kernel: CTA g takes a range of the (sequence, head chunk, page) order; a unit cut
+// by a range boundary leaves fp32 partials for the merge kernel.  The ranges are
+// equal in pages plus a few for every unit's start and end.
 //
 // At 4.5 bits a cached feature the walk is bound by what a warp issues per
 // feature, so everything that does not depend on the query rows is done once a
@@ -41,13 +42,13 @@
 // are not the consumers'), and a copy instruction held a producer for 280 to 540
 // cycles beside warps that compute.
 //
-// Measured: 256 sequences of 128 to 8192 tokens, 32 / 8 heads of 128 (673 MB): 140 us,
-// 4.8 TB/s, 71% of the copy bandwidth.  Issue-bound: 172 instructions a page and head
+// Measured: 256 sequences of 128 to 8192 tokens, 32 / 8 heads of 128 (673 MB): 134 us,
+// 5.0 TB/s, 74% of the copy bandwidth (long sequences alone: 5.6 TB/s).  Issue-bound: 172 instructions a page and head
 // for 2.3 KB, the issue slots 57% full with four warps a scheduler (counters of a batch
 // of 96), and neither more warps (85 registers: spills) nor a wider tile helps.  32
-// sequences of 4 tokens and 64 rows of 8 heads, window 4096 (117 MB): 70 us, bound by
+// sequences of 4 tokens and 64 rows of 8 heads, window 4096 (117 MB): 68 us, bound by
 // the two warps a scheduler that 248 registers leave (issue 42%, tensor pipe 26%).  One
-// sequence of 32768 tokens, 64 features: 15 us, of which the two kernels' start-up and
+// sequence of 32768 tokens, 64 features: 15.5 us, of which the two kernels' start-up and
 // the dependent loads (lengths, page ids, pages; descriptor, partials) are about 12.
 #include "pa_q4.cuh"
 #include "pa_split.cuh"
@@ -58,6 +59,11 @@ constexpr int kQ4Warps = 8;                                         // of a CTA
 constexpr int q4_ctas_per_sm(int nt) { return nt == 1 ? 2 : 1; }
 // Pages in flight a warp: about 9 KB, 150 KB an SM where two CTAs are on it.
 constexpr int q4_stages(int d) { return d == 128 ? 4 : 8; }
+// What a segment's start and end cost, in pages of a warp: the CTAs' shares count them
+// (0, 5 and 16 pages: the batch of 256 141, 134 and 142 us; 256 sequences of up to 1000
+// tokens 34, 24 and 31; 64 sequences of up to 3000 tokens, 16 rows: 0, 5 and 8 pages 36,
+// 31 and 30).
+constexpr int q4_segment_pages(int nt) { return nt == 1 ? 5 : 8; }
 // A team's query fragments (D x 8 NT x 2 bytes) in shared memory.  Its KW warps write
 // the same values; the barriers at a segment's end keep one segment's apart from the
 // next one's.
@@ -451,6 +457,20 @@ __device__ __forceinline__ void next_unit(Cursor& cu, const int32_t* pre, int B,
   advance(cu, pre, B, NC);
 }
 
+// The page position at coordinate y of the order in which every unit is W longer than
+// its pages (it starts with the W: a cut there is before the unit's first page).
+__device__ __forceinline__ int64_t cut_at(const int32_t* pre, int B, int NC, int W, int64_t y) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (static_cast<int64_t>(NC) * (pre[mid] + static_cast<int64_t>(W) * mid) <= y) lo = mid; else hi = mid - 1;
+  }
+  const int n = pages_of(pre, lo);
+  const int64_t off = y - static_cast<int64_t>(NC) * (pre[lo] + static_cast<int64_t>(W) * lo);
+  const int64_t c = off / (n + W);
+  return static_cast<int64_t>(NC) * pre[lo] + c * n + max(static_cast<int64_t>(0), off - c * (n + W) - W);
+}
+
 template <bool V>
 struct Bool {
   static constexpr bool value = V;
@@ -494,8 +514,11 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
 
   const int g = blockIdx.x;
   if (g >= NG || X == 0) return;
-  const int64_t start = static_cast<int64_t>(g) * X / NG;
-  const int64_t end = static_cast<int64_t>(g + 1) * X / NG;
+  // CTAs take equal shares of the pages and of the units' starts and ends, W pages each
+  const int W = q4_segment_pages(NT) * p.KW;
+  const int64_t XW = X + static_cast<int64_t>(NC) * B * W;
+  const int64_t start = cut_at(s_pre, B, NC, W, g * XW / NG);
+  const int64_t end = g + 1 == NG ? X : cut_at(s_pre, B, NC, W, (g + 1) * XW / NG);
   const int teams = HC * MT;
   if (end <= start || warp >= teams * KW) return;
   const int team = warp % teams, kw = warp / teams, lg_kw = __ffs(KW) - 1;
@@ -638,8 +661,9 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
     const int hq_base = (sg.c * HC + hh) * G;
     if (sg.j0 == 0 && warp == 0 && lane == 0) {
       // this CTA holds the unit's first page: describe the unit for the merge
-      const int64_t a = static_cast<int64_t>(NC) * s_pre[sg.i] + static_cast<int64_t>(sg.c) * sg.n;
-      const int last_cta = static_cast<int>(((a + sg.n) * NG - 1) / X);
+      const int64_t a = static_cast<int64_t>(NC) * (s_pre[sg.i] + static_cast<int64_t>(W) * sg.i) +
+                        static_cast<int64_t>(sg.c) * (sg.n + W);
+      const int last_cta = static_cast<int>(((a + W + sg.n) * NG - 1) / XW);
       p.ws_unit[static_cast<int64_t>(sg.i) * NC + sg.c] =
           make_int4(g, (last_cta - g + 1) | (first ? 0 : (1 << 30)), si.t0, si.qn);
     }
