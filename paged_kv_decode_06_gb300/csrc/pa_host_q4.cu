@@ -12,7 +12,6 @@ namespace {
 constexpr int kPageTokens = 16;
 constexpr int kGroup = 16;             // features that share a scale code
 constexpr int kMaxRows = 64;           // query rows per KV head
-constexpr int kMinPages = 4;
 constexpr int kMaxCtas = 1 << 14;
 
 struct PlanQ4 {
@@ -102,7 +101,11 @@ int make_plan(int B, int Hq, int Hkv, int D, int max_qlen, const pa_options_t* o
   if (!fits)
     return host_fail(PA_ERR_UNSUPPORTED, "no launch configuration fits %d bytes of shared memory", dev.smem_optin);
   p.grid = (o && o->num_ctas > 0) ? o->num_ctas : per_sm * dev.num_sms;
-  p.min_pages = (o && o->min_pages_per_cta > 0) ? o->min_pages_per_cta : kMinPages;
+  // Short calls gain more from a second CTA than its partials cost the merge (2 pages a
+  // CTA against 4: 3 sequences of up to 100 tokens 8.5 us against 11.5, 64 of up to 300
+  // 15.0 against 17.1, one of 4000 13.1 against 12.5), but for eight warps on one head's
+  // pages (4 sequences of 2000 tokens: 14.4 against 12.5).
+  p.min_pages = (o && o->min_pages_per_cta > 0) ? o->min_pages_per_cta : std::max(2, p.KW / 2);
   p.off_q = ring;
   p.off_xchg = p.off_q + query;
   p.off_state = p.off_xchg + xchg;
