@@ -48,7 +48,7 @@
 // of 96), and neither more warps (85 registers: spills) nor a wider tile helps.  32
 // sequences of 4 tokens and 64 rows of 8 heads, window 4096 (117 MB): 68 us, bound by
 // the two warps a scheduler that 248 registers leave (issue 42%, tensor pipe 26%).  One
-// sequence of 32768 tokens, 64 features: 15.5 us, of which the two kernels' start-up and
+// sequence of 32768 tokens, 64 features: 15.2 us, of which the two kernels' start-up and
 // the dependent loads (lengths, page ids, pages; descriptor, partials) are about 12.
 #include "pa_q4.cuh"
 #include "pa_split.cuh"
