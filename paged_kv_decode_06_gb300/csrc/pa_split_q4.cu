@@ -23,7 +23,7 @@
 //     two words of codes (8 features of each key) are interleaved nibble-wise
 //     with four logical operations, then converted and scaled like K;
 //   * the running maximum moves only when a score exceeds it by 2^8 (one vote a
-//     page); P is then at most 256 and its rounding to f16 is 2^-12 relative.
+//     step); P is then at most 256 and its rounding to f16 is 2^-11 relative.
 // Query rows are scaled by a power of two into f16's range (exact except for
 // elements 2^-14 below the row's largest), and the power goes into the row's logit factor.
 //
@@ -43,9 +43,10 @@
 // cycles beside warps that compute.
 //
 // Measured: 256 sequences of 128 to 8192 tokens, 32 / 8 heads of 128 (673 MB): 134 us,
-// 5.0 TB/s, 74% of the copy bandwidth (long sequences alone: 5.6 TB/s).  Issue-bound: 172 instructions a page and head
-// for 2.3 KB, the issue slots 57% full with four warps a scheduler (counters of a batch
-// of 96), and neither more warps (85 registers: spills) nor a wider tile helps.  32
+// 5.0 TB/s, 74% of the copy bandwidth (long sequences alone: 5.6 TB/s).  Bound by the
+// 172 instructions a page and head for 2.3 KB and the latencies between them: four
+// warps a scheduler fill 57% of the issue slots (counters of a batch of 96), and more
+// warps (85 registers: spills), deeper rings or more independent sums do not help.  32
 // sequences of 4 tokens and 64 rows of 8 heads, window 4096 (117 MB): 68 us, bound by
 // the two warps a scheduler that 248 registers leave (issue 42%, tensor pipe 26%).  One
 // sequence of 32768 tokens, 64 features: 15.2 us, of which the two kernels' start-up and
