@@ -171,7 +171,8 @@ typedef struct pa_plan_t {
  *                   data == NULL (not written).
  *   stream          stream the work is enqueued on.
  *
- * Supported: D in {64, 128}; page size 16; Hq % Hkv == 0; 1 <= B <= 8192.
+ * Supported: D in {64, 128}; page size 16; Hq % Hkv == 0; 1 <= B <= 8192;
+ * B * max_blocks < 2^31 (every decode entry point).
  * Errors: PA_ERR_INVALID_ARG / PA_ERR_UNSUPPORTED are detected on the host before
  * anything is enqueued.  Data errors that only the device can see (a page id
  * outside [0, NB), L_i < q_i, q_i > max_query_len) set bits of the device status

@@ -455,7 +455,7 @@ int decode_impl(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* 
   if (Hq > (1 << 20) || Hkv > (1 << 20) || T > (int64_t(1) << 30) || NB > (int64_t(1) << 31) - 1 || MB > (1 << 28))
     return fail(PA_ERR_UNSUPPORTED, "tensor extents too large");
   if (sl->shape[0] != B) return fail(PA_ERR_INVALID_ARG, "seq_lens has %lld entries, block_tables %lld rows", (long long)sl->shape[0], (long long)B);
-  if (B * MB > (int64_t(1) << 31)) return fail(PA_ERR_UNSUPPORTED, "block table too large");
+  if (B * MB >= (int64_t(1) << 31)) return fail(PA_ERR_UNSUPPORTED, "block table too large");
   if (out->shape[0] != T || out->shape[1] != Hq || out->shape[2] != D) return fail(PA_ERR_INVALID_ARG, "out shape differs from q");
   if (lse->data && (lse->shape[0] != T || lse->shape[1] != Hq)) return fail(PA_ERR_INVALID_ARG, "lse shape must be [T, Hq]");
   if (B == 0 || T == 0) return PA_OK;   // nothing to do
@@ -853,7 +853,7 @@ int mla_decode_impl(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor
   if (Hq > (1 << 20) || T > (int64_t(1) << 30) || NB > (int64_t(1) << 31) - 1 || MB > (1 << 28))
     return fail(PA_ERR_UNSUPPORTED, "tensor extents too large");
   if (sl->shape[0] != B) return fail(PA_ERR_INVALID_ARG, "seq_lens has %lld entries, block_tables %lld rows", (long long)sl->shape[0], (long long)B);
-  if (B * MB > (int64_t(1) << 31)) return fail(PA_ERR_UNSUPPORTED, "block table too large");
+  if (B * MB >= (int64_t(1) << 31)) return fail(PA_ERR_UNSUPPORTED, "block table too large");
   if (lse->data && (lse->shape[0] != T || lse->shape[1] != Hq)) return fail(PA_ERR_INVALID_ARG, "lse shape must be [T, Hq]");
   if (B == 0 || T == 0) return PA_OK;
   if (qsl->data) {

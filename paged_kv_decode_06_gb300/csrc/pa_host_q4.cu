@@ -146,7 +146,7 @@ int decode_q4(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* vc
   if ((st = check_shape(B, Hq, Hkv, D, max_qlen, opts)) != PA_OK) return st;
   if (kc->shape[1] != kPageTokens)
     return host_fail(PA_ERR_UNSUPPORTED, "page size %lld, only 16 is supported", static_cast<long long>(kc->shape[1]));
-  if (NB < 1 || NB > (int64_t(1) << 31) - 1 || T > (int64_t(1) << 30) || MB > (1 << 27) - 64 || B * MB > (int64_t(1) << 31))
+  if (NB < 1 || NB > (int64_t(1) << 31) - 1 || T > (int64_t(1) << 30) || MB > (1 << 27) - 64 || B * MB >= (int64_t(1) << 31))
     return host_fail(PA_ERR_UNSUPPORTED, "tensor extents too large");
   const pa_tensor_t *code[2] = {kc, vc}, *sc[2] = {ks, vs};
   const char *cn[2] = {"k_cache", "v_cache"}, *sn[2] = {"k_group_scales", "v_group_scales"};
