@@ -117,3 +117,49 @@ def decode(q, codes, scales, block_tables, seq_lens, query_start_loc, scale, k_s
                 p /= p.sum()
                 out[t, h] = p[:seen.sum()] @ v[seen, h // G]
     return out, lse
+
+
+def decode_with_bounds(q, codes, scales, block_tables, seq_lens, query_start_loc, scale, k_scale, v_scale, window=0,
+                       sinks=None):
+    """out, lse as ``decode`` and how far an evaluation of the kernel's roundings may be from each.
+
+    Per row of n keys with weights p_j (sink included in the normaliser), A = sum_j p_j |v_j| a feature:
+      * a score is off by ds_j: fp32 sums of D products, (D + 4) 2^-24 of scale sum |q k|; query elements in
+        f16, 2^-25 of the row's largest each; the fp32 factor, product and maximum, 2^-21 (|s_j| + |s_max|);
+      * weights are off by delta = max ds_j + 2^-21 (the exponential) relative, in the sum and in the output;
+      * weights are rounded to f16 for the output: 2^-11 relative, 2^-25 of the row's largest weight where
+        that is more (a warp's largest weight is at least 1 in its own units);
+      * fp32 sums: c = n / 16 + 1000 roundings of 2^-23 (tensor-core sums of 16 keys; pieces, warps, merge),
+        in the sum and in the output;
+      * one bf16 rounding of the output, 2^-8."""
+    out, lse = decode(q, codes, scales, block_tables, seq_lens, query_start_loc, scale, k_scale, v_scale, window, sinks)
+    T, Hq, D = q.shape
+    G = Hq // codes[0].shape[2]
+    tol, tol_lse = np.zeros_like(out), np.zeros_like(lse)
+    for i, L in enumerate(seq_lens):
+        t0, t1 = (query_start_loc[i], query_start_loc[i + 1]) if query_start_loc is not None else (i, i + 1)
+        if t1 <= t0 or L <= 0:
+            continue
+        j = np.arange(L)
+        page, off = block_tables[i][j // PAGE_SIZE], j % PAGE_SIZE
+        k = dequantise_rows(codes[0][page, off], scales[0][page, :, off], k_scale)
+        v = np.abs(dequantise_rows(codes[1][page, off], scales[1][page, :, off], v_scale))
+        for t in range(t0, t1):
+            pos = L - (t1 - t0) + (t - t0)
+            seen = (j <= pos) & ((j > pos - window) if window > 0 else True)
+            n = int(seen.sum())
+            for h in range(Hq):
+                if n == 0:
+                    continue
+                kh, row = k[seen, h // G], q[t, h]
+                s = scale * (kh @ row)
+                p = np.exp(s - lse[t, h])
+                top = max(np.abs(s).max(), abs(float(sinks[h])) if sinks is not None else 0.0)
+                ds = abs(scale) * ((D + 4) * 2.0 ** -24 * (np.abs(kh) @ np.abs(row)) +
+                                   2.0 ** -25 * np.abs(row).max() * np.abs(kh).sum(-1)) + 2.0 ** -20 * top
+                delta, c = ds.max() + 2.0 ** -21, (n / 16 + 1000) * 2.0 ** -23
+                vh = v[seen, h // G]
+                err = (2.0 ** -11 + 2 * delta + 2 * c) * (p @ vh) + 2.0 ** -25 * p.max() * vh.sum(0)
+                tol[t, h] = err + 2.0 ** -8 * (np.abs(out[t, h]) + err)
+                tol_lse[t, h] = delta + c + 2.0 ** -21 + 2.0 ** -22 * abs(lse[t, h])
+    return out, lse, tol, tol_lse

@@ -1,0 +1,66 @@
+"""paged_attn_decode_q4 against the float64 oracle, every output element within the
+bound that its own row's weights and values give (oracle.cache_q4.decode_with_bounds):
+long contexts, whose outputs are far below the values, and sinks above the scores."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_q4
+from paged_kv_decode_06_gb300 import binding
+from test_oracle_q4_bounds import bounds, needle_case
+from test_parity_q4_gpu import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _lib(cuda_lib):
+    binding.paged_attn_device_status(clear=True)
+    yield
+
+
+def inside(out, lse, want):
+    wo, wl, to, tl = want
+    go, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    live = ~np.isnan(wl)
+    inf = np.isinf(wl)
+    assert np.array_equal(gl[inf], wl[inf]) and np.isfinite(gl[live]).sum() == (live & ~inf).sum()
+    ok = live & ~inf
+    assert (np.abs(go - wo)[live] <= to[live]).all(), np.nanmax((np.abs(go - wo) / to)[live])
+    assert (np.abs(gl[ok] - wl[ok]) <= tl[ok]).all(), np.max((np.abs(gl - wl) / tl)[ok])
+
+
+def check(c, status=0, **kw):
+    """A Case of the parity tests, within the bounds of its rows."""
+    out, lse = c.run(**kw)
+    assert binding.paged_attn_device_status(clear=True) == status
+    want = cache_q4.decode_with_bounds(c.q.double().numpy(), c.codes, c.scales, c.bt, c.lens, c.qsl, c.scale, c.k_scale,
+                                       c.v_scale, c.window, c.sinks)
+    inside(out, lse, want)
+    return want
+
+
+def check_needles(c, **kw):
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()
+    q = torch.from_numpy(c["q"].astype(np.float32)).to(torch.bfloat16).cuda()
+    sinks = None if c["sinks"] is None else dev(c["sinks"])
+    out, lse = binding.paged_attn_decode_q4(
+        q, *map(dev, (*c["codes"], *c["scales"], c["bt"], c["lens"])), None, 1, c["scale"], 0.02, 0.03,
+        options=binding.make_options(sliding_window=c["window"], sinks=sinks, **kw))
+    inside(out, lse, bounds(c))
+
+
+@pytest.mark.parametrize("ctas", [0, 1, 7])
+@pytest.mark.parametrize("L,d,hq,hkv,window", [(20000, 64, 64, 1, 0), (20000, 64, 8, 8, 0), (9000, 128, 32, 4, 0),
+                                               (5000, 128, 16, 1, 700), (33, 64, 8, 2, 0)])
+def test_rows_that_look_at_one_token(L, d, hq, hkv, window, ctas):
+    check_needles(needle_case(L, d, hq, hkv, seed=L + hq, window=window), num_ctas=ctas)
+
+
+@pytest.mark.parametrize("lens,qlens,hq,hkv,d,window", [
+    ([20000], None, 8, 1, 64, 0), ([6000, 300, 1], None, 8, 2, 128, 0), ([3000, 2000], [4, 2], 16, 2, 128, 0),
+    ([3000, 900], [3, 4], 8, 2, 64, 1024), ([700] * 40, None, 8, 1, 64, 0)])
+@pytest.mark.parametrize("gain", [0.05, 1.0])
+def test_long_contexts(lens, qlens, hq, hkv, d, window, gain):
+    """Weights alike (gain 0.05) and uneven ones."""
+    check(Case(lens, qlens, hq=hq, hkv=hkv, d=d, window=window, seed=len(lens) + d, q_gain=gain))
