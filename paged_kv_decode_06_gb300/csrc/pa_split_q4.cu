@@ -23,7 +23,9 @@
 //     two words of codes (8 features of each key) are interleaved nibble-wise
 //     with four logical operations, then converted and scaled like K;
 //   * the running maximum moves only when a score exceeds it by 2^8 (one vote a
-//     step); P is then at most 256 and its rounding to f16 is 2^-11 relative.
+//     step); P is then at most 256, a warp's largest P at least 1, and the rounding
+//     to f16 2^-11 relative, or 2^-25 absolute for P below 2^-14 (the sums take P
+//     unrounded).  The maximum is over keys: a sink joins at the end of its piece.
 // Query rows are scaled by a power of two into f16's range (exact except for
 // elements 2^-14 below the row's largest), and the power goes into the row's logit factor.
 //
@@ -675,16 +677,6 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
         uint2 w[GG::KS];
         cs.read_query(w, row_at(sg, si, n), tig);
         cs.set_query(n, w, tig, p.scale_log2);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r2 = row0 + 8 * n + 2 * tig + e, t = token_of(r2);
-          if (p.sinks != nullptr && sg.j0 == 0 && kw == 0 && r2 < R) {
-            // the sink: a virtual first key with a zero value row
-            const float sk = p.sinks[hq_base + r2 - t * G] * 1.4426950408889634f;
-            cs.m[n][e] = fmaxf(sk, kUnsetMax);
-            cs.l[n][e] = gq == 0 && sk != -INFINITY ? 1.f : 0.f;
-          }
-        }
       }
       __syncwarp();
     }
@@ -731,6 +723,15 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
     }
     // ---- end of the segment
     const bool complete = sg.j0 == 0 && sg.j1 == sg.n;
+    const bool sinks_here = p.sinks != nullptr && sg.j0 == 0;
+    float sk[NT][2];                  // this lane's rows' sinks (log2 units)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int rho = row0 + 8 * n + 2 * tig + e;
+        sk[n][e] = sinks_here && rho < R ? p.sinks[hq_base + rho - token_of(rho) * G] * 1.4426950408889634f : 0.f;
+      }
     const int64_t ws_row = (static_cast<int64_t>(2 * g + (first ? 0 : 1)) * HC + hh) * p.R_max + row0;
     const int t_first = si.t0;
     first = false;
@@ -819,9 +820,28 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
       for (int e = 0; e < 2; ++e) {
         const int rl = 8 * n + 2 * tig + e, rho = row0 + rl;
         if (rho >= R || !gathers) continue;
-        const float lt = cs.l[n][e], mm = cs.m[n][e];
+        const int tk = token_of(rho), t = t_first + tk, hq = hq_base + rho - tk * G;
+        float lt = cs.l[n][e], mm = cs.m[n][e];
+        if (sinks_here) {
+          // The sink, a virtual key with a zero value row, joins the sum of the unit's
+          // first piece here, in fp32: the keys' f16 weights stay relative to the keys'
+          // own maximum, however far the sink lies above it.  The maximum moves only
+          // where the sum would leave fp32's range.
+          float mx = mm;
+          if (sk[n][e] - mm > 64.f) {
+            mx = sk[n][e];
+            const float al = fast_exp2(mm - mx);
+            lt *= al;
+#pragma unroll
+            for (int i = 0; i < GG::KS; ++i) {
+              cs.O[i][n][e] *= al;
+              cs.O[i][n][2 + e] *= al;
+            }
+          }
+          lt += fast_exp2(sk[n][e] - mx);
+          mm = mx;
+        }
         if (complete) {
-          const int tk = token_of(rho), t = t_first + tk, hq = hq_base + rho - tk * G;
           const float inv = lt == 0.f ? 0.f : __fdividef(p.v_scale, lt);
           uint16_t* o = p.out + static_cast<int64_t>(t) * p.out_stride_t + static_cast<int64_t>(hq) * p.out_stride_h +
                         FPL * gq;

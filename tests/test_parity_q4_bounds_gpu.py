@@ -64,3 +64,19 @@ def test_rows_that_look_at_one_token(L, d, hq, hkv, window, ctas):
 def test_long_contexts(lens, qlens, hq, hkv, d, window, gain):
     """Weights alike (gain 0.05) and uneven ones."""
     check(Case(lens, qlens, hq=hq, hkv=hkv, d=d, window=window, seed=len(lens) + d, q_gain=gain))
+
+
+@pytest.mark.parametrize("above", [5.0, 10.0, 14.0, 18.0, 25.0, 60.0])
+@pytest.mark.parametrize("lens,qlens,hq,hkv,d,ctas", [
+    ([512], None, 8, 8, 128, 0), ([600, 40], None, 8, 1, 64, 0), ([600, 40], [3, 2], 16, 2, 128, 5),
+    ([1500, 300], [4, 4], 32, 4, 64, 0)])
+def test_sinks_above_the_scores(above, lens, qlens, hq, hkv, d, ctas):
+    """Sinks up to 60 nats above the largest score: the keys' weights keep their relative precision, whatever
+    piece or warp the sink is counted in."""
+    c = Case(lens, qlens, hq=hq, hkv=hkv, d=d, seed=int(above), q_gain=0.2)
+    top = 0.0
+    for h in range(hq):
+        k = cache_q4.dequantise_rows(c.codes[0], c.scales[0].transpose(0, 2, 1, 3), c.k_scale)[:, :, h // (hq // hkv)]
+        top = max(top, c.scale * np.abs(k @ c.q[:, h].double().numpy().T).max())
+    c.sinks = (top + above + np.linspace(0, 1, hq)).astype(np.float32)
+    check(c, num_ctas=ctas)
