@@ -405,6 +405,8 @@ int paged_attn_cache_read_q4(const pa_tensor_t* slot_mapping, const pa_tensor_t*
  *     were, and T may exceed them;
  *   - a row that sees no key (L_i = 0, or L_i < q_i) gets out = 0 and lse = -inf (its
  *     sink's logit with sinks) and sets bit 1 of the status word;
+ *   - a sink of NaN makes its head's rows NaN (out and lse), one of +inf gives them out = 0
+ *     and lse = +inf, one of -inf is no sink;
  *   - what a row does not see cannot reach it: slots past a sequence's end or before its
  *     window, and scale codes that are NaN, may be anything there.
  * G * max_query_len <= 64, D in {64, 128}, 1 <= B <= 8192, max_blocks <= 2^27 - 64, pages

@@ -95,7 +95,7 @@ struct MergeParams {
   uint32_t* err;
   // sink logits [Hq], for the lse of rows of an empty context (nullptr: -inf)
   const float* sinks;
-  // a NaN sum gives a NaN lse (4-bit caches; else -inf)
+  // a NaN sum gives a NaN row and lse (4-bit caches; else 0 and -inf)
   bool keep_nan;
 };
 

@@ -53,14 +53,14 @@ __device__ __forceinline__ MergeRow merge_row(const MergeParams& p, int u, int r
       qn = p.qsl[i + 1] - t0;
     }
     if (qn < 1 || qn > p.max_qlen || t0 < 0 || t0 + qn > p.num_tokens || m.rho >= p.G * qn || lane < 0) return m;
-    uint16_t* orow = p.out + static_cast<int64_t>(t0 + m.rho / p.G) * p.out_stride_t +
-                     static_cast<int64_t>((c * p.HC + m.hh) * p.G + m.rho % p.G) * p.out_stride_h;
-    for (int dd = 2 * lane; dd < D; dd += 64) *reinterpret_cast<uint32_t*>(orow + dd) = 0u;
+    const int t = t0 + m.rho / p.G, hq = (c * p.HC + m.hh) * p.G + m.rho % p.G;
+    const float sink = p.sinks != nullptr ? p.sinks[hq] : -INFINITY;
+    uint16_t* orow = p.out + static_cast<int64_t>(t) * p.out_stride_t + static_cast<int64_t>(hq) * p.out_stride_h;
+    const uint32_t fill = sink != sink ? 0x7FC07FC0u : 0u;
+    for (int dd = 2 * lane; dd < D; dd += 64) *reinterpret_cast<uint32_t*>(orow + dd) = fill;
     if (lane == 0) {
       if (p.lse)
-        p.lse[static_cast<int64_t>(t0 + m.rho / p.G) * p.lse_stride_t +
-              static_cast<int64_t>((c * p.HC + m.hh) * p.G + m.rho % p.G) * p.lse_stride_h] =
-            p.sinks != nullptr ? p.sinks[(c * p.HC + m.hh) * p.G + m.rho % p.G] : -INFINITY;
+        p.lse[static_cast<int64_t>(t) * p.lse_stride_t + static_cast<int64_t>(hq) * p.lse_stride_h] = sink;
       atomicOr(p.err, kErrSeqLen);
     }
     return m;
@@ -155,7 +155,7 @@ __device__ __forceinline__ void gather_rounds(const MergeParams& p, const MergeR
 
 __device__ __forceinline__ void write_merged(const MergeParams& p, const MergeRow& m, int dq, float4 acc, float l,
                                              float mx, bool write_lse) {
-  const float inv = l > 0.f ? p.v_scale / l : 0.f;
+  const float inv = l > 0.f ? p.v_scale / l : (p.keep_nan && l != l ? l : 0.f);
   uint2 pk;
   pk.x = pack_bf16(acc.x * inv, acc.y * inv);
   pk.y = pack_bf16(acc.z * inv, acc.w * inv);

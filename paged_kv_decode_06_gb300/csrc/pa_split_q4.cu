@@ -166,6 +166,8 @@ __device__ __forceinline__ uint32_t bitsel(uint32_t a, uint32_t b, uint32_t mask
 // maximum before it moves.
 constexpr float kUnsetMax = -3e38f;
 constexpr float kMoveMax = 8.f;
+// The largest maximum that a sink sets (differences with it stay finite).
+constexpr float kMaxSink = 3e38f;
 
 // One warp's state: 8 NT query rows of one KV head.  Lane (gq = lane / 4, tig =
 // lane % 4) holds the query rows 8 n + 2 tig + e (n < NT, e < 2) of the scores
@@ -826,10 +828,11 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
           // The sink, a virtual key with a zero value row, joins the sum of the unit's
           // first piece here, in fp32: the keys' f16 weights stay relative to the keys'
           // own maximum, however far the sink lies above it.  The maximum moves only
-          // where the sum would leave fp32's range.
+          // where the sum would leave fp32's range; an infinite sink makes the sum
+          // infinite (output 0), a NaN one NaN.
           float mx = mm;
           if (sk[n][e] - mm > 64.f) {
-            mx = sk[n][e];
+            mx = fminf(sk[n][e], kMaxSink);
             const float al = fast_exp2(mm - mx);
             lt *= al;
 #pragma unroll

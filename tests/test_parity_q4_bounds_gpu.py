@@ -80,3 +80,24 @@ def test_sinks_above_the_scores(above, lens, qlens, hq, hkv, d, ctas):
         top = max(top, c.scale * np.abs(k @ c.q[:, h].double().numpy().T).max())
     c.sinks = (top + above + np.linspace(0, 1, hq)).astype(np.float32)
     check(c, num_ctas=ctas)
+
+
+@pytest.mark.parametrize("lens,qlens,hq,hkv,d,window,ctas", [
+    ([60, 17], None, 8, 8, 128, 0, 1),                 # finished in one warp
+    ([60, 17], None, 8, 8, 128, 0, 0),
+    ([400, 90], None, 8, 1, 64, 0, 1),                 # ... by eight warps
+    ([900, 300], [2, 3], 16, 2, 128, 0, 9),            # cut
+    ([900, 70], None, 32, 8, 64, 0, 300),
+    ([2, 0, 40], [4, 2, 1], 8, 2, 128, 0, 3),          # rows without keys, an empty context
+    ([200, 100], [8, 3], 8, 2, 64, 3, 20)])            # rows whose window starts in a later piece
+def test_sinks_without_a_finite_value(lens, qlens, hq, hkv, d, window, ctas):
+    """A NaN sink makes its head's rows NaN, +inf takes all weight, -inf is no sink."""
+    c = Case(lens, qlens, hq=hq, hkv=hkv, d=d, window=window, seed=hq + ctas)
+    plain = cache_q4.decode_with_bounds(c.q.double().numpy(), c.codes, c.scales, c.bt, c.lens, c.qsl, c.scale,
+                                        c.k_scale, c.v_scale, window, None)
+    c.sinks = np.tile(np.array([np.nan, np.inf, -np.inf, -np.inf], dtype=np.float32), hq // 4)
+    out, lse = c.run(num_ctas=ctas, min_pages_per_cta=1)
+    assert torch.isnan(out[:, 0::4]).all() and torch.isnan(lse[:, 0::4]).all()
+    assert (out[:, 1::4] == 0).all() and (lse[:, 1::4] == np.inf).all()
+    for h in (2, 3):
+        inside(out[:, h::4], lse[:, h::4], [x[:, h::4] for x in plain])
