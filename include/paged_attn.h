@@ -403,8 +403,9 @@ int paged_attn_cache_read_q4(const pa_tensor_t* slot_mapping, const pa_tensor_t*
  *   - with query_start_loc a sequence may have no query tokens (a padded batch): its
  *     pages are not read.  Rows of `out` and `lse` past the last sequence's stay as they
  *     were, and T may exceed them;
- *   - a row that sees no key (L_i = 0, or L_i < q_i) gets out = 0 and lse = -inf (its
- *     sink's logit with sinks) and sets bit 1 of the status word;
+ *   - a row that sees no key (L_i = 0, L_i < q_i, or a window that starts past the last
+ *     entry of its block-table row) gets out = 0 and lse = -inf (its sink's logit with
+ *     sinks) and sets bit 1 of the status word;
  *   - a sink of NaN makes its head's rows NaN (out and lse), one of +inf gives them out = 0
  *     and lse = +inf, one of -inf is no sink;
  *   - what a row does not see cannot reach it: slots past a sequence's end or before its

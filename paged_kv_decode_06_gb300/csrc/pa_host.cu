@@ -596,6 +596,8 @@ int decode_impl(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* 
   mp.qsl = sp.qsl;
   mp.num_seqs = sp.num_seqs;
   mp.num_tokens = sp.num_tokens;
+  mp.max_blocks = sp.max_blocks;
+  mp.window = sp.window;
   mp.G = pl.G;
   mp.HC = pl.HC;
   mp.NC = pl.NC;
@@ -958,6 +960,8 @@ int mla_decode_impl(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor
   mp.qsl = sp.qsl;
   mp.num_seqs = sp.num_seqs;
   mp.num_tokens = sp.num_tokens;
+  mp.max_blocks = sp.max_blocks;
+  mp.window = sp.window;
   mp.G = pl.Gc;
   mp.HC = 1;
   mp.NC = pl.NC;

@@ -267,6 +267,8 @@ int decode_q4(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* vc
   mp.qsl = sp.qsl;
   mp.num_seqs = sp.num_seqs;
   mp.num_tokens = sp.num_tokens;
+  mp.max_blocks = sp.max_blocks;
+  mp.window = sp.window;
   mp.G = pl.G;
   mp.HC = pl.HC;
   mp.NC = pl.NC;

@@ -93,7 +93,8 @@ struct MergeParams {
   const float2* ws_ml;
   const float* ws_o;
   uint32_t* err;
-  // sink logits [Hq], for the lse of rows of an empty context (nullptr: -inf)
+  int32_t max_blocks, window;   // block-table columns, sliding window (0 = off)
+  // sink logits [Hq], for the lse of rows of a sequence without pages (nullptr: -inf)
   const float* sinks;
   // a NaN sum gives a NaN row and lse (4-bit caches; else 0 and -inf)
   bool keep_nan;

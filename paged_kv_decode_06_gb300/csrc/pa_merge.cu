@@ -15,6 +15,7 @@
 
 #include "pa_device.cuh"
 #include "pa_kernels.h"
+#include "pa_split.cuh"
 
 namespace pa {
 
@@ -33,8 +34,8 @@ struct MergeRow {
 // (unit u, row) -> output row and the pieces to merge, from the descriptor the
 // split kernel wrote for the unit (one metadata load).  Rows of a unit that was
 // finished inside one CTA, or that do not exist for the sequence, report
-// work = false.  An empty context (no page ever touched) writes out = 0 and
-// lse = -inf here.
+// work = false.  A sequence without a page to read writes out = 0 and lse = -inf
+// (the sink) here.
 template <int D>
 __device__ __forceinline__ MergeRow merge_row(const MergeParams& p, int u, int row, int lane) {
   MergeRow m;
@@ -46,12 +47,15 @@ __device__ __forceinline__ MergeRow merge_row(const MergeParams& p, int u, int r
   m.rho = row - m.hh * p.R_max;
   const int4 d = p.ws_unit[u];
   const int L = p.seq_lens[i];
-  if (L <= 0) {
-    int t0 = i, qn = 1;
-    if (p.qsl != nullptr) {
-      t0 = p.qsl[i];
-      qn = p.qsl[i + 1] - t0;
-    }
+  int t0 = i, qn = 1;
+  if (p.qsl != nullptr && (L <= 0 || p.window > 0)) {
+    t0 = p.qsl[i];
+    qn = p.qsl[i + 1] - t0;
+  }
+  // No page to read: an empty context, or a window that starts past the end of the
+  // block-table row (as the split kernels' prologue counts pages).
+  if (L <= 0 ||
+      (p.window > 0 && first_visible_page(L, qn, p.window) >= min((L - 1) / kPage + 1, p.max_blocks))) {
     if (qn < 1 || qn > p.max_qlen || t0 < 0 || t0 + qn > p.num_tokens || m.rho >= p.G * qn || lane < 0) return m;
     const int t = t0 + m.rho / p.G, hq = (c * p.HC + m.hh) * p.G + m.rho % p.G;
     const float sink = p.sinks != nullptr ? p.sinks[hq] : -INFINITY;
@@ -68,7 +72,8 @@ __device__ __forceinline__ MergeRow merge_row(const MergeParams& p, int u, int r
   m.gf = d.x;
   m.nparts = d.y & 0x3fffffff;
   m.first_is_tail = (d.y >> 30) & 1;
-  const int t0 = d.z, qn = d.w;
+  t0 = d.z;
+  qn = d.w;
   // A descriptor this call's split kernel did not write (its CTA gave up on a
   // timed-out wait) may hold anything: one that would index outside the
   // workspace or the outputs is skipped, so a failed call stays in bounds.
