@@ -145,19 +145,24 @@ __device__ __forceinline__ int d_of(int J, int e, int tig) {
 // Prologue shared by the split kernels (all threads of the CTA call it):
 // sequence lengths and query starts copied to shared memory, pages of work per
 // sequence (pages before a sliding window excluded) and their exclusive prefix.
-// rows_only: a sequence without query rows has no pages of work (an invalid
-// query range is reported here instead of where its pages are walked).
-__device__ __forceinline__ void page_prefix(const SplitParams& p, int window, int32_t* s_pre, int32_t* s_len,
-                                            int32_t* s_qsl, int* s_scan, int* s_total, bool rows_only = false) {
+// CHARGED: a sequence without query rows has no pages of work (an invalid query
+// range is reported here instead of where its pages are walked), and every
+// sequence with pages counts `charge` more (the prefix is then one of 32 bits
+// without sign); returns how many those are.
+template <bool CHARGED = false>
+__device__ __forceinline__ int page_prefix(const SplitParams& p, int window, int32_t* s_pre, int32_t* s_len,
+                                           int32_t* s_qsl, int* s_scan, int* s_total, int charge = 0) {
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
   const int nwarps = blockDim.x >> 5;
   const int B = p.num_seqs;
-  int carry = 0;
+  uint32_t carry = 0u;
+  int active = 0;
   for (int b0 = 0; b0 < B; b0 += blockDim.x) {
     const int i = b0 + tid;
     int v = 0;
+    bool live = false;
     if (i < B) {
       const int L = p.seq_lens[i];
       s_len[i] = L;
@@ -169,33 +174,35 @@ __device__ __forceinline__ void page_prefix(const SplitParams& p, int window, in
       }
       const int qn = p.qsl != nullptr ? p.qsl[i + 1] - p.qsl[i] : 1;
       v -= min(v, first_visible_page(L, qn, window));   // pages before the sliding window are skipped
-      if (rows_only) {
+      if constexpr (CHARGED) {
         const int t0 = s_qsl[i];
         const bool valid = qn >= 0 && qn <= p.max_qlen && t0 >= 0 && t0 <= p.num_tokens - qn;
         if (!valid && blockIdx.x == 0) atomicOr(p.err, kErrQueryLen);
-        if (!valid || qn == 0) v = 0;
+        live = valid && qn > 0 && v > 0;
+        v = live ? v + charge : 0;
       }
     }
-    int x = v;
+    uint32_t x = static_cast<uint32_t>(v);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
     if (lane == 31) s_scan[warp] = x;
     __syncthreads();
     if (warp == 0) {
-      const int wv = lane < nwarps ? s_scan[lane] : 0;
-      int xs = wv;
+      const uint32_t wv = lane < nwarps ? s_scan[lane] : 0;
+      uint32_t xs = wv;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, xs, o);
+        const uint32_t y = __shfl_up_sync(0xffffffffu, xs, o);
         if (lane >= o) xs += y;
       }
       if (lane < nwarps) s_scan[lane] = xs - wv;
       if (lane == 31) *s_total = xs;
     }
-    __syncthreads();
+    if constexpr (CHARGED) active += __syncthreads_count(live);
+    else __syncthreads();
     if (i < B) s_pre[i] = carry + s_scan[warp] + x - v;
     carry += *s_total;
     __syncthreads();
@@ -204,6 +211,7 @@ __device__ __forceinline__ void page_prefix(const SplitParams& p, int window, in
     s_pre[B] = carry;
     s_qsl[B] = p.qsl != nullptr ? p.qsl[B] : B;
   }
+  return active;
 }
 
 // Block-table entries for the producer warp: 32 at a time (one per lane),

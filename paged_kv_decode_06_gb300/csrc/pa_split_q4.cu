@@ -3,7 +3,7 @@
 // Work decomposition, workspace and merge are those of the bf16 / fp8 split
 // kernel: CTA g takes a range of the (sequence, head chunk, page) order; a unit cut
 // by a range boundary leaves fp32 partials for the merge kernel.  The ranges are
-// equal in pages plus a few for every unit's start and end.
+// equal in pages plus a few for the start and end of every unit that has pages.
 //
 // At 4.5 bits a cached feature the walk is bound by what a warp issues per
 // feature, so everything that does not depend on the query rows is done once a
@@ -440,40 +440,67 @@ __device__ __forceinline__ void team_sync(int team, int kw_warps) {
   asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * kw_warps) : "memory");
 }
 
+// The order in which the CTAs take their shares: a unit with n > 0 pages is W + n long,
+// the W first (its start and end; a cut there is before its first page).  pos[i], the
+// prologue's prefix, is the sum of W + n over the sequences before i that have pages.
+struct OrderQ4 {
+  const int32_t* pos;
+  int B, NC, W;
+  __device__ __forceinline__ uint32_t at(int i) const { return static_cast<uint32_t>(pos[i]); }
+  __device__ __forceinline__ int64_t start(int i) const { return static_cast<int64_t>(NC) * at(i); }
+  __device__ __forceinline__ int pages(int i) const {
+    const uint32_t d = at(i + 1) - at(i);
+    return static_cast<int>(d == 0u ? 0u : d - static_cast<uint32_t>(W));
+  }
+  // The unit at coordinate y < start(B), its page there (j), and the coordinate at which
+  // its pages begin.
+  __device__ __forceinline__ Cursor unit(int64_t y, int64_t& first) const {
+    int lo = 0, hi = B - 1;                        // the last sequence that starts at y or before has pages
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (start(mid) <= y) lo = mid; else hi = mid - 1;
+    }
+    Cursor cu;
+    cu.i = lo;
+    cu.n = pages(lo);
+    cu.c = static_cast<int>((y - start(lo)) / (cu.n + W));
+    first = start(lo) + static_cast<int64_t>(cu.c) * (cu.n + W) + W;
+    cu.j = static_cast<int>(max(static_cast<int64_t>(0), y - first));
+    return cu;
+  }
+  // The unit after cu's, which is not the last.
+  __device__ __forceinline__ void next(Cursor& cu) const {
+    cu.j = 0;
+    if (++cu.c < NC) return;
+    cu.c = 0;
+    const uint32_t here = at(++cu.i);
+    if (at(cu.i + 1) == here) {                    // no pages: to the last sequence that starts here
+      int lo = cu.i + 1, hi = B - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (at(mid) == here) lo = mid; else hi = mid - 1;
+      }
+      cu.i = lo;
+    }
+    cu.n = pages(cu.i);
+  }
+};
+
 // A segment: the pages [j0, j1) of unit (sequence i, head chunk c) in a CTA's range.
 struct SegmentQ4 {
   int i, c, n;      // sequence, head chunk, pages of the sequence
   int j0, j1;
 };
 
+// `left`: the range's end, from the unit's first page on (it may lie behind the unit).
 __device__ __forceinline__ SegmentQ4 segment_at(const Cursor& cu, int64_t left) {
   SegmentQ4 s;
   s.i = cu.i;
   s.c = cu.c;
   s.n = cu.n;
   s.j0 = cu.j;
-  s.j1 = static_cast<int>(min(static_cast<int64_t>(cu.n), cu.j + left));
+  s.j1 = static_cast<int>(min(static_cast<int64_t>(cu.n), left));
   return s;
-}
-
-// The cursor after a segment (its last page was the sequence's, or the range ended).
-__device__ __forceinline__ void next_unit(Cursor& cu, const int32_t* pre, int B, int NC) {
-  cu.j = cu.n - 1;
-  advance(cu, pre, B, NC);
-}
-
-// The page position at coordinate y of the order in which every unit is W longer than
-// its pages (it starts with the W: a cut there is before the unit's first page).
-__device__ __forceinline__ int64_t cut_at(const int32_t* pre, int B, int NC, int W, int64_t y) {
-  int lo = 0, hi = B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<int64_t>(NC) * (pre[mid] + static_cast<int64_t>(W) * mid) <= y) lo = mid; else hi = mid - 1;
-  }
-  const int n = pages_of(pre, lo);
-  const int64_t off = y - static_cast<int64_t>(NC) * (pre[lo] + static_cast<int64_t>(W) * lo);
-  const int64_t c = off / (n + W);
-  return static_cast<int64_t>(NC) * pre[lo] + c * n + max(static_cast<int64_t>(0), off - c * (n + W) - W);
 }
 
 template <bool V>
@@ -484,7 +511,7 @@ struct Bool {
 // A warp's fetch state between segments.
 struct FetchQ4 {
   Cursor cu;             // the unit after the segment
-  int64_t left;          // pages of the CTA's range from there on
+  int64_t left;          // the end of the CTA's range, from that unit's first page on
   int n, i, j;           // pages of the segment whose ids are yet to come, its sequence, the first of them
   int ahead_i, ahead_j;  // sequence and page of the ids loaded ahead (-1: none)
 };
@@ -505,27 +532,29 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = p.num_seqs, HC = p.HC, NC = p.NC, MT = p.MT, KW = p.KW;
   grid_dependency_wait();
-  page_prefix(p, window, s_pre, s_len, s_qsl, s_scan, &s_total, true);
+  const int W = q4_segment_pages(NT) * KW;
+  const int active = page_prefix<true>(p, window, s_pre, s_len, s_qsl, s_scan, &s_total, W);
   __syncthreads();
 
-  const int64_t X = static_cast<int64_t>(NC) * s_pre[B];
+  const OrderQ4 order = {s_pre, B, NC, W};
+  const int64_t XW = order.start(B);
+  const int64_t X = XW - static_cast<int64_t>(NC) * active * W;     // pages
   int64_t ng64 = (X + p.min_pages - 1) / p.min_pages;
   if (ng64 < 1) ng64 = 1;
   const int NG = static_cast<int>(ng64 < gridDim.x ? ng64 : gridDim.x);
   if (blockIdx.x == 0)   // units without pages: nothing for the merge
     for (int64_t u = tid; u < static_cast<int64_t>(B) * NC; u += blockDim.x)
-      if (pages_of(s_pre, static_cast<int>(u / NC)) == 0) p.ws_unit[u] = make_int4(0, 0, 0, 0);
+      if (order.pages(static_cast<int>(u / NC)) == 0) p.ws_unit[u] = make_int4(0, 0, 0, 0);
   grid_launch_dependents();
 
   const int g = blockIdx.x;
   if (g >= NG || X == 0) return;
-  // CTAs take equal shares of the pages and of the units' starts and ends, W pages each
-  const int W = q4_segment_pages(NT) * p.KW;
-  const int64_t XW = X + static_cast<int64_t>(NC) * B * W;
-  const int64_t start = cut_at(s_pre, B, NC, W, g * XW / NG);
-  const int64_t end = g + 1 == NG ? X : cut_at(s_pre, B, NC, W, (g + 1) * XW / NG);
+  // CTAs take equal shares of the order
+  int64_t first_page;
+  Cursor cu = order.unit(g * XW / NG, first_page);
+  int64_t left = (g + 1 == NG ? XW : (g + 1) * XW / NG) - first_page;
   const int teams = HC * MT;
-  if (end <= start || warp >= teams * KW) return;
+  if (left <= cu.j || warp >= teams * KW) return;
   const int team = warp % teams, kw = warp / teams, lg_kw = __ffs(KW) - 1;
   const int hh = team / MT, wt = team - hh * MT;
   const int gq = lane >> 2, tig = lane & 3;
@@ -537,8 +566,8 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
   // lane; the 32 that follow are loaded ahead.  What only a new segment or a new 32
   // ids need waits in shared memory (every lane stores the same values).
   FetchQ4* const fst = reinterpret_cast<FetchQ4*>(smem + p.off_state) + warp;
-  fst->cu = locate(s_pre, B, NC, start);
-  fst->left = end - start;
+  fst->cu = cu;
+  fst->left = left;
   fst->n = 0;
   fst->ahead_i = -1;
   __syncwarp();
@@ -550,7 +579,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
   const uint8_t *kp = nullptr, *vp = nullptr, *sp = nullptr;   // in page 0, of the segment's head
   auto ids_of = [&](int i, int j) {
     const int x = j + lane * KW;
-    return x < pages_of(s_pre, i)
+    return x < order.pages(i)
                ? p.block_tables[static_cast<int64_t>(i) * p.bt_stride + x +
                                 first_visible_page(s_len[i], s_qsl[i + 1] - s_qsl[i], window)]
                : 0;
@@ -563,8 +592,8 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
       SegmentQ4 s;
       while (n == 0 && rest > 0) {
         s = segment_at(c, rest);
-        rest -= s.j1 - s.j0;
-        next_unit(c, s_pre, B, NC);
+        rest -= s.n + W;
+        if (rest > 0) order.next(c);
         n = (s.j1 - s.j0 - kw + KW - 1) >> lg_kw;
       }
       if (n == 0) {
@@ -635,8 +664,6 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
   // product (exact for the at most 128 rows of a head's tiles)
   const uint32_t g_inv = (65536u + G - 1u) / static_cast<uint32_t>(G);
   auto token_of = [&](int rho) { return static_cast<int>(static_cast<uint32_t>(rho) * g_inv >> 16); };
-  Cursor cu = fst->cu;
-  int64_t left = fst->left;
   SegmentQ4 sg = segment_at(cu, left);
   SeqInfo si = seq_info(p, s_len, s_qsl, sg.i, lane == 0 && warp == 0, window);
   auto row_at = [&](const SegmentQ4& s, const SeqInfo& q, int n) {
@@ -659,15 +686,14 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
   uint32_t at = ring;               // the page to compute
   bool first = true;
   for (;;) {
-    left -= sg.j1 - sg.j0;
+    left -= sg.n + W;
     const int R = G * si.qn, min_lim = si.L - si.qn;
     const bool active = row0 < R;
     const RowsQ4 rows = {min_lim, row0, R, g_inv};
     const int hq_base = (sg.c * HC + hh) * G;
     if (sg.j0 == 0 && warp == 0 && lane == 0) {
       // this CTA holds the unit's first page: describe the unit for the merge
-      const int64_t a = static_cast<int64_t>(NC) * (s_pre[sg.i] + static_cast<int64_t>(W) * sg.i) +
-                        static_cast<int64_t>(sg.c) * (sg.n + W);
+      const int64_t a = order.start(sg.i) + static_cast<int64_t>(sg.c) * (sg.n + W);
       const int last_cta = static_cast<int>(((a + W + sg.n) * NG - 1) / XW);
       p.ws_unit[static_cast<int64_t>(sg.i) * NC + sg.c] =
           make_int4(g, (last_cta - g + 1) | (first ? 0 : (1 << 30)), si.t0, si.qn);
@@ -685,7 +711,7 @@ __global__ void __launch_bounds__(32 * kQ4Warps, q4_ctas_per_sm(NT))
     SegmentQ4 ns = sg;
     SeqInfo ni = si;
     if (left > 0) {
-      next_unit(cu, s_pre, B, NC);
+      order.next(cu);
       ns = segment_at(cu, left);
       ni = seq_info(p, s_len, s_qsl, ns.i, lane == 0 && warp == 0, window);
       query_ahead(ns, ni);
