@@ -134,17 +134,19 @@ typedef struct pa_options_t {
 typedef struct pa_plan_t {
   int32_t num_ctas;          /* split-kernel grid size                                  */
   int32_t heads_per_cta;     /* KV heads a CTA processes per page (HC)                  */
-  int32_t row_tiles;         /* 16-row tiles per KV head (ceil(G*max_query_len/16); 8 for tcgen05) */
+  int32_t row_tiles;         /* 16-row tiles per KV head (ceil(G*max_query_len/16); 8 for tcgen05;
+                                4-bit: tiles of 8, 16 or 32 rows)                       */
   int32_t num_stages;        /* depth of the shared-memory page ring                    */
-  int32_t threads_per_cta;   /* 32 * (1 producer + heads_per_cta * row_tiles); tcgen05: 384 */
+  int32_t threads_per_cta;   /* 32 * (1 producer + heads_per_cta * row_tiles); tcgen05: 384; 4-bit: 256 */
   int32_t smem_bytes;        /* dynamic shared memory per CTA                           */
   int32_t min_pages_per_cta; /* work below which fewer CTAs are used                    */
   int32_t merge_rows;        /* rows per merge unit (heads_per_cta * G * max_query_len) */
   int32_t page_pairing;      /* 1 if consumer warps take two pages of a sequence at once */
+  int32_t warps_per_head;    /* 4-bit: warps that take a head's pages in turn (0: other kernels) */
   int64_t workspace_bytes;   /* split workspace the call needs                          */
   int32_t variant;           /* 0: mma.sync warps; 1: tcgen05 / tensor-memory kernel; 2: MLA on
                                 mma.sync warps; 3: MLA on tcgen05 / tensor memory; 4: 4-bit */
-  int32_t block_pages;       /* pages a consumer step takes (1, 2 paired, 4 tcgen05)    */
+  int32_t block_pages;       /* pages a consumer step takes (1, 2 paired and 4-bit, 4 tcgen05) */
 } pa_plan_t;
 
 /*

@@ -46,7 +46,7 @@ class PaPlan(ctypes.Structure):
     _fields_ = [("num_ctas", ctypes.c_int32), ("heads_per_cta", ctypes.c_int32), ("row_tiles", ctypes.c_int32),
                 ("num_stages", ctypes.c_int32), ("threads_per_cta", ctypes.c_int32), ("smem_bytes", ctypes.c_int32),
                 ("min_pages_per_cta", ctypes.c_int32), ("merge_rows", ctypes.c_int32),
-                ("page_pairing", ctypes.c_int32),
+                ("page_pairing", ctypes.c_int32), ("warps_per_head", ctypes.c_int32),
                 ("workspace_bytes", ctypes.c_int64), ("variant", ctypes.c_int32),
                 ("block_pages", ctypes.c_int32)]
 

@@ -1200,6 +1200,7 @@ int paged_attn_plan(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
   plan->min_pages_per_cta = pl.min_pages;
   plan->merge_rows = pl.HC * pl.R_max;
   plan->page_pairing = pl.pair;
+  plan->warps_per_head = 0;
   plan->workspace_bytes = static_cast<int64_t>(pl.ws_bytes);
   plan->variant = pl.tc ? 1 : 0;
   plan->block_pages = pl.tc ? pl.block_pages : (pl.pair ? 2 : 1);
@@ -1269,6 +1270,7 @@ int paged_attn_mla_plan(int32_t num_seqs, int32_t num_q_heads, int32_t kv_dtype,
   plan->min_pages_per_cta = pl.min_pages;
   plan->merge_rows = pl.R_max;
   plan->page_pairing = pl.pair;
+  plan->warps_per_head = 0;
   plan->workspace_bytes = static_cast<int64_t>(pl.ws_bytes);
   plan->variant = pl.tc ? 3 : 2;
   plan->block_pages = pl.tc ? 3 : (pl.pair ? 2 : 1);

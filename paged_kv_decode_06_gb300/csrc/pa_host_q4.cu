@@ -350,10 +350,11 @@ extern "C" int paged_attn_q4_plan(int32_t num_seqs, int32_t num_q_heads, int32_t
     plan->smem_bytes = static_cast<int32_t>(pl.smem);
     plan->min_pages_per_cta = pl.min_pages;
     plan->merge_rows = pl.HC * pl.R_max;
-    plan->page_pairing = 0;
+    plan->page_pairing = 1;
+    plan->warps_per_head = pl.KW;
     plan->workspace_bytes = static_cast<int64_t>(pl.ws_bytes);
     plan->variant = 4;
-    plan->block_pages = 1;
+    plan->block_pages = 2;
     return static_cast<int>(PA_OK);
   });
 }
