@@ -77,29 +77,29 @@ int make_plan(int B, int Hq, int Hkv, int D, int max_qlen, const pa_options_t* o
   const uint32_t query = p.HC * p.MT * split_q4_query_bytes(D, p.NT);
   // The shared memory of the CTAs that an SM's registers hold, and as many warps a head
   // as the CTA has; where the sequences' metadata (12 bytes each) leaves too little: one
-  // CTA an SM, then one warp a head.  Where all
-  // eight warps take one head's pages in turn, one CTA an SM as well: its segments are
-  // twice as long against the cost of their ends (64 sequences, one KV head: 21.5 us
-  // against 25.6; with two heads and four warps each, two CTAs: 18.7 against 20.7).
-  uint32_t ring = 0, xchg = 0;
-  int per_sm = 0;
-  bool fits = false;
-  for (int form = split_q4_ctas_per_sm(p.NT) == 2 && p.HC * p.MT > 1 ? 0 : 1; form < 3 && !fits; ++form) {
-    per_sm = form == 0 ? 2 : 1;
-    p.KW = 1;
-    while (form < 2 && p.KW < 8 && 2 * p.KW * p.HC * p.MT <= warps) p.KW *= 2;
-    p.nstage = split_q4_stages(D);
-    ring = static_cast<uint32_t>(warps * p.nstage * 2 * kPageTokens * (D / 2 + D / kGroup));
+  // CTA an SM, then half as many warps a head until it fits.  (8192 sequences, 16 rows of
+  // one head of 128, four warps a head against one: up to 3000 tokens 959 us against 2431,
+  // up to 400 527 against 565, up to 40, whose three pages leave warps idle, 403 against
+  // 291.)  Where all eight warps take one head's pages in turn, one CTA an SM as well: its
+  // segments are twice as long against the cost of their ends (64 sequences, one KV head:
+  // 21.5 us against 25.6; with two heads and four warps each, two CTAs: 18.7 against 20.7).
+  p.nstage = split_q4_stages(D);
+  const uint32_t ring = static_cast<uint32_t>(warps * p.nstage * 2 * kPageTokens * (D / 2 + D / kGroup));
+  uint32_t xchg = 0;
+  int per_sm = split_q4_ctas_per_sm(p.NT) == 2 && p.HC * p.MT > 1 ? 2 : 1;
+  for (p.KW = 1; p.KW < 8 && 2 * p.KW * p.HC * p.MT <= warps;) p.KW *= 2;
+  for (;;) {
     // partial rows the KW warps of a head exchange (pa_split_q4.cu): the features a
     // warp does not gather, and each row's maximum and sum
     const int cols = D - D / p.KW + 4;
     xchg = p.KW == 1 ? 0u
                      : static_cast<uint32_t>(up(static_cast<size_t>(p.HC * p.MT * p.KW) * 8 * p.NT * (cols * 4 + 8), 128));
     const int64_t budget = per_sm == 2 ? (dev.smem_optin + 2048) / 2 - 1024 - 512 : dev.smem_optin;
-    fits = static_cast<int64_t>(ring) + query + xchg + state + prefix <= budget;
+    if (static_cast<int64_t>(ring) + query + xchg + state + prefix <= budget) break;
+    if (per_sm == 2) per_sm = 1;
+    else if (p.KW > 1) p.KW /= 2;
+    else return host_fail(PA_ERR_UNSUPPORTED, "no launch configuration fits %d bytes of shared memory", dev.smem_optin);
   }
-  if (!fits)
-    return host_fail(PA_ERR_UNSUPPORTED, "no launch configuration fits %d bytes of shared memory", dev.smem_optin);
   p.grid = (o && o->num_ctas > 0) ? o->num_ctas : per_sm * dev.num_sms;
   // Short calls gain more from a second CTA than its partials cost the merge (2 pages a
   // CTA against 4: 3 sequences of up to 100 tokens 8.5 us against 11.5, 64 of up to 300

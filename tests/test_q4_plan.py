@@ -26,7 +26,9 @@ def test_plan_reports_two_pages_a_step(cuda_lib):
 @pytest.mark.gpu
 @pytest.mark.parametrize("b,hq,hkv,d,rows,warps,per_sm", [
     (3000, 8, 8, 64, 1, 1, 1),        # the metadata leaves room for one CTA an SM
-    (100, 8, 8, 64, 1, 1, 2), (100, 8, 4, 128, 1, 2, 2), (100, 8, 1, 128, 1, 8, 1)])
+    (100, 8, 8, 64, 1, 1, 2), (100, 8, 4, 128, 1, 2, 2), (100, 8, 1, 128, 1, 8, 1),
+    (8192, 16, 1, 128, 1, 4, 1),      # ... for four warps a head, not eight
+    (8192, 32, 2, 128, 1, 2, 1)])     # ... for two, not four
 def test_launch_forms_and_their_results(cuda_lib, b, hq, hkv, d, rows, warps, per_sm):
     from test_parity_q4_gpu import Case
     p = binding.paged_attn_q4_plan(b, hq, hkv, d, rows)
