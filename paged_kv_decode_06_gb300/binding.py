@@ -354,7 +354,13 @@ def _arguments(codes, tensors, num_caches=0):
     the lists by types, shapes and strides and writes the pointers of every call
     into them, so a repeated call marshals little else."""
     dev = _on_current_device(*tensors)
-    key = (codes, num_caches, *[(t.dtype, t.shape, t.stride()) for t in tensors])
+    try:
+        key = (codes, num_caches, *[(t.dtype, t.shape, t.stride()) for t in tensors])
+    except AttributeError:
+        missing = [i for i, t in enumerate(tensors) if t is None]
+        if not missing:
+            raise
+        raise PagedAttnError(PA_ERR_INVALID_ARG, f"tensor argument {missing[0]} is None") from None
     hit = _MARSHALLED.by_layout.get(key)
     if hit is None:
         descs = [_new_desc(t, c) for t, c in zip(tensors[num_caches:], codes)]
