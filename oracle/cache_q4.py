@@ -93,8 +93,8 @@ def decode(q, codes, scales, block_tables, seq_lens, query_start_loc, scale, k_s
     G = Hq // Hkv
     out = np.full((T, Hq, D), np.nan)
     lse = np.full((T, Hq), np.nan)
-    for i, L in enumerate(seq_lens):
-        t0, t1 = (query_start_loc[i], query_start_loc[i + 1]) if query_start_loc is not None else (i, i + 1)
+    for i, L in enumerate(map(int, seq_lens)):
+        t0, t1 = map(int, query_start_loc[i:i + 2]) if query_start_loc is not None else (i, i + 1)
         if t1 <= t0:
             continue
         j = np.arange(max(L, 0))
@@ -136,8 +136,8 @@ def decode_with_bounds(q, codes, scales, block_tables, seq_lens, query_start_loc
     T, Hq, D = q.shape
     G = Hq // codes[0].shape[2]
     tol, tol_lse = np.zeros_like(out), np.zeros_like(lse)
-    for i, L in enumerate(seq_lens):
-        t0, t1 = (query_start_loc[i], query_start_loc[i + 1]) if query_start_loc is not None else (i, i + 1)
+    for i, L in enumerate(map(int, seq_lens)):
+        t0, t1 = map(int, query_start_loc[i:i + 2]) if query_start_loc is not None else (i, i + 1)
         if t1 <= t0 or L <= 0:
             continue
         j = np.arange(L)

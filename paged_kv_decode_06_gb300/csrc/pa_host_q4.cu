@@ -229,7 +229,10 @@ int decode_q4(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* vc
   sp.MT = pl.MT;
   sp.R_max = pl.R_max;
   sp.min_pages = pl.min_pages;
-  sp.window = (opts && opts->sliding_window > 0) ? opts->sliding_window : 0;
+  // A window as wide as the longest sequence hides nothing; the kernels' differences of
+  // positions and windows stay within 32 bits below that.
+  constexpr int32_t kWidest = kPageTokens * ((1 << 27) - 64);
+  sp.window = (opts && opts->sliding_window > 0 && opts->sliding_window < kWidest) ? opts->sliding_window : 0;
   sp.sinks = opts ? static_cast<const float*>(opts->sinks) : nullptr;
   sp.scale_log2 = scale * k_scale * 1.4426950408889634f;
   sp.v_scale = v_scale;

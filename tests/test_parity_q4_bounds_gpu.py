@@ -101,3 +101,9 @@ def test_sinks_without_a_finite_value(lens, qlens, hq, hkv, d, window, ctas):
     assert (out[:, 1::4] == 0).all() and (lse[:, 1::4] == np.inf).all()
     for h in (2, 3):
         inside(out[:, h::4], lse[:, h::4], [x[:, h::4] for x in plain])
+
+
+@pytest.mark.parametrize("window", [(1 << 31) - 1, (1 << 31) - 60, (1 << 31) - 2000, 1 << 30])
+def test_windows_of_any_size(window):
+    """A window wider than any context is none, also for runs longer than their contexts."""
+    check(Case([1, 30, 700], [8, 33, 3], hq=8, hkv=8, d=64, window=window, seed=4), status=binding.STATUS_SEQ_LEN)
