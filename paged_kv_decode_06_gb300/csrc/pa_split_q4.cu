@@ -7,7 +7,9 @@
 //
 // At 4.5 bits a cached feature the walk is bound by what a warp issues per
 // feature, so everything that does not depend on the query rows is done once a
-// key, and nothing is done for rows that do not exist:
+// key and row tile (a KV head of up to 16 rows, or 32 of 64 features in a large batch, has one tile;
+// more tiles fetch and convert the pages once each), and nothing is done for rows that
+// do not exist:
 //   * scores are computed transposed, S^T = K Q^T with mma.sync m16n8k16: the
 //     16 keys of a page are the M rows and the N side is 8 query rows (the usual
 //     4 to 8 rows of a KV head fill it; the other orientation pads them to 16);
@@ -45,14 +47,17 @@
 // cycles beside warps that compute.
 //
 // Measured: 256 sequences of 128 to 8192 tokens, 32 / 8 heads of 128 (673 MB): 134 us,
-// 5.0 TB/s, 74% of the copy bandwidth (long sequences alone: 5.6 TB/s).  Bound by the
-// 172 instructions a page and head for 2.3 KB and the latencies between them: four
+// 5.0 TB/s, 74% of the copy bandwidth (long sequences alone: 5.6 TB/s).  Bound by warp
+// instructions, 330 a page and head of 2.3 KB (172 in the compute loop, the rest in the
+// fetch, at the segments' ends and in the prologue), and the latencies between them: four
 // warps a scheduler fill 57% of the issue slots (counters of a batch of 96), and more
 // warps (85 registers: spills), deeper rings or more independent sums do not help.  32
-// sequences of 4 tokens and 64 rows of 8 heads, window 4096 (117 MB): 68 us, bound by
-// the two warps a scheduler that 248 registers leave (issue 42%, tensor pipe 26%).  One
-// sequence of 32768 tokens, 64 features: 15.2 us, of which the two kernels' start-up and
-// the dependent loads (lengths, page ids, pages; descriptor, partials) are about 12.
+// sequences of 4 tokens and 64 rows of 8 heads, window 4096 (117 MB): 70 us, bound by
+// the two warps a scheduler that 246 registers leave (issue 42%, tensor pipe 26%).  One
+// sequence of 32768 tokens, 64 features, its 19 MB in L2: 14.9 us, of which the two
+// kernels' start-up and the dependent loads (lengths, page ids, pages; descriptor,
+// partials) are about 12.  A batch padded with empty sequences (8 of 4096 tokens, 32 / 8
+// heads, in a batch of 256): 25 us, without the padding 21.
 #include "pa_q4.cuh"
 #include "pa_split.cuh"
 
