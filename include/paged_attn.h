@@ -280,6 +280,44 @@ int paged_attn_cache_write_per_token(const pa_tensor_t* key, const pa_tensor_t* 
                                      const pa_tensor_t* v_token_scales, pa_stream_t stream);
 
 /*
+ * paged_attn_rope_cache_write - rotary positions with one to three axes (time, height,
+ * width) applied to a step's query and key rows, and the key and value rows written into
+ * the paged caches (ATOM model-operations guide, "KV cache operations":
+ * fused_qk_rope_reshape_and_cache).
+ *
+ *   query           bf16 [T, Hq, D]; key, value bf16 [T, Hkv, D]: contiguous last dim,
+ *                   other strides multiples of 8 elements, data 16-byte aligned.  D a
+ *                   multiple of 8 up to 512, Hq and Hkv at most 4096, T at most 2^30.
+ *   positions       int32 [axes, T] (rows contiguous), or [T] for one axis.
+ *   cos_sin         f32 [P, R], rows a multiple of 4 elements apart, 16-byte aligned: of
+ *                   position p, the cosines of the R / 2 angles, then their sines.  R is a
+ *                   multiple of 4, at most D; the features R .. D - 1 do not rotate.
+ *   pair_axis       HOST array of R / 2 entries: the axis of each pair (read before the
+ *                   call returns), or NULL: axis 0 throughout.
+ *   neighbours      0: pair i is the features i and i + R / 2; else 2 i and 2 i + 1.
+ *   slot_mapping    int32 [T] contiguous, as for paged_attn_cache_write.
+ *   k_cache, v_cache, k_scale, v_scale  as for paged_attn_cache_write: bf16, or fp8 codes
+ *                   e4m3fn(x / scale), x the rotated key in fp32 (not rounded to bf16
+ *                   before) and the IEEE fp32 quotient.
+ *   query_out       bf16 [T, Hq, D], written: the rotated query.  query itself, or apart
+ *                   from every other tensor of the call.
+ *   key_out         bf16 [T, Hkv, D] or data == NULL: the rotated key.  key itself, or
+ *                   apart from every other tensor of the call.
+ *   A pair (x, y) becomes (x c - y s, y c + x s), each product and sum rounded to fp32, c
+ *   and s of row positions[axis][t].  A negative slot (padding) writes no cache row, but
+ *   the query (and key_out) is rotated; a slot past the pool does the same and sets bit 0
+ *   of the status word.  A token with a position outside [0, P) on any axis writes
+ *   nothing and sets bit 6.
+ *
+ * Errors as for paged_attn_cache_write.  Asynchronous; allocates nothing.
+ */
+int paged_attn_rope_cache_write(const pa_tensor_t* query, const pa_tensor_t* key, const pa_tensor_t* value,
+                                const pa_tensor_t* positions, const pa_tensor_t* cos_sin, const uint8_t* pair_axis,
+                                int32_t neighbours, const pa_tensor_t* slot_mapping, const pa_tensor_t* k_cache,
+                                const pa_tensor_t* v_cache, float k_scale, float v_scale,
+                                const pa_tensor_t* query_out, const pa_tensor_t* key_out, pa_stream_t stream);
+
+/*
  * paged_attn_mla_decode - multi-head latent attention (MLA) decode over a paged
  * latent cache (ATOM model-operations guide, "Multi-head latent attention
  * (attention_mla.py)": MLAModules kv_lora_rank / qk_rope_head_dim, decode flow
@@ -524,7 +562,7 @@ int paged_attn_release(void);
  * range; bit 1: seq_len < query length; bit 2: query length outside [1, max_query_len]
  * or query_start_loc inconsistent; bit 3: a pipeline wait timed out; bit 4: a query value
  * overflowed the f16 range on the fp8 path, or an MLA partial output did; bit 5: a page
- * operation refused an entry).  clear != 0 resets it to 0.  Synchronises
+ * operation refused an entry; bit 6: a rotary position out of range).  clear != 0 resets it to 0.  Synchronises
  * the device: a debugging aid, not for the hot path. */
 int paged_attn_device_status(uint32_t* flags, int32_t clear);
 

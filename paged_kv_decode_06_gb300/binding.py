@@ -21,7 +21,7 @@ PA_BF16, PA_FP8_E4M3, PA_F32, PA_I32, PA_FP4_E2M1X2 = 1, 2, 3, 4, 5
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA = 0, 1, 2, 3, 4
 
 STATUS_PAGE_RANGE, STATUS_SEQ_LEN, STATUS_QUERY_LEN, STATUS_TIMEOUT, STATUS_F16_RANGE = 1, 2, 4, 8, 16
-STATUS_PAGE_OP = 32
+STATUS_PAGE_OP, STATUS_POSITION = 32, 64
 
 
 class PaTensor(ctypes.Structure):
@@ -72,6 +72,8 @@ _SIGNATURES = {
     "paged_attn_cache_write_per_token": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_void_p]),
     "paged_attn_cache_write_q4": (ctypes.c_int, [_P] * 7 + [ctypes.c_float, ctypes.c_float, ctypes.c_void_p]),
     "paged_attn_cache_read_q4": (ctypes.c_int, [_P] * 5 + [ctypes.c_float, ctypes.c_float, _P, _P, ctypes.c_void_p]),
+    "paged_attn_rope_cache_write": (ctypes.c_int, [_P] * 5 + [ctypes.c_char_p, ctypes.c_int32] + [_P] * 3 +
+                                    [ctypes.c_float, ctypes.c_float, _P, _P, ctypes.c_void_p]),
     "paged_attn_decode_q4": (ctypes.c_int, [_P] * 8 + [ctypes.c_int32, ctypes.c_float, ctypes.c_float, ctypes.c_float,
                                                        _P, _P, ctypes.POINTER(PaOptions), ctypes.c_void_p]),
     "paged_attn_q4_plan": (ctypes.c_int, [ctypes.c_int32] * 5 + [ctypes.POINTER(PaOptions), ctypes.POINTER(PaPlan)]),
@@ -377,6 +379,9 @@ def _arguments(codes, tensors, num_caches=0):
     return hit[0], dev
 
 
+_NO_TENSOR = ctypes.byref(PaTensor())
+
+
 def _handle_on(stream, dev) -> int:
     return int(_RAW_STREAM(dev)) if stream is None and _RAW_STREAM is not None else _stream_handle(stream)
 
@@ -418,6 +423,52 @@ def paged_attn_cache_read_q4(slot_mapping, k_cache, v_cache, k_group_scales, v_g
     if st != PA_OK:
         _check(lib, st)
     return key, value
+
+
+def rope_pair_axes(sections, in_turn=False):
+    """The axis of each rotated pair: ``sections[a]`` pairs of axis a, in blocks one
+    after another, or (in_turn) axis i % n for pair i while that axis has pairs left,
+    axis 0 where it has none."""
+    n = sum(sections)
+    if not in_turn:
+        return [a for a, k in enumerate(sections) for _ in range(k)]
+    axes = [i % len(sections) for i in range(n)]
+    return [a if a == 0 or i // len(sections) < sections[a] else 0 for i, a in enumerate(axes)]
+
+
+_ROPE_CODES = (_dtype_code,) * 10
+
+
+def paged_attn_rope_cache_write(query, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, pair_axis=None,
+                                neighbours=False, k_scale=1.0, v_scale=1.0, query_out=None, key_out=None,
+                                stream=None):
+    """Rotate a step's query and key rows by their tokens' positions and write the
+    key and value rows into the paged caches (see include/paged_attn.h).
+
+    query bf16 [T, Hq, D]; key / value bf16 [T, Hkv, D]; positions int32 [axes, T]
+    or [T]; cos_sin float32 [P, R]; pair_axis: the axis of each of the R / 2 pairs
+    (``rope_pair_axes``), None for one axis; slot_mapping int32 [T]; caches bf16 or
+    uint8 (e4m3fn codes) [NB, 16, Hkv, D], updated in place.  Returns query_out
+    (allocated if None; may be query itself).  key_out, where given, receives the
+    rotated key."""
+    lib = load()
+    if query_out is None:
+        with _allocating_on(stream):
+            query_out = torch.empty(query.shape, dtype=query.dtype, device=query.device)
+    tensors = (query, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, query_out)
+    if key_out is not None:
+        tensors += (key_out,)
+    args, dev = _arguments(_ROPE_CODES, tensors)
+    if pair_axis is not None:
+        pair_axis = bytes(pair_axis)
+        if len(pair_axis) != cos_sin.shape[-1] // 2:
+            raise ValueError(f"pair_axis has {len(pair_axis)} entries for {cos_sin.shape[-1] // 2} pairs")
+    st = lib.paged_attn_rope_cache_write(*args[:5], pair_axis, int(bool(neighbours)), *args[5:8], k_scale, v_scale,
+                                         args[8], args[9] if key_out is not None else _NO_TENSOR,
+                                         _handle_on(stream, dev))
+    if st != PA_OK:
+        _check(lib, st)
+    return query_out
 
 
 def paged_attn_q4_plan(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len=1, options=None) -> dict:

@@ -15,6 +15,7 @@ constexpr uint32_t kErrSeqLen = 2u;
 constexpr uint32_t kErrQueryLen = 4u;
 constexpr uint32_t kErrTimeout = 8u;
 constexpr uint32_t kErrF16Range = 16u;
+constexpr uint32_t kErrPosition = 64u;
 
 // A pipeline wait gives up after this long (nanoseconds of %globaltimer)
 // unless the call sets its own limit.
