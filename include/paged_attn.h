@@ -223,6 +223,37 @@ int paged_attn_decode_static_scratch(const pa_tensor_t* q, const pa_tensor_t* k_
                                      const pa_tensor_t* out, const pa_tensor_t* lse, pa_stream_t stream);
 
 /*
+ * paged_attn_decode_window - decode attention over a sliding window and the first tokens
+ * of each sequence, which stay visible: a query token at position p sees the keys j <= p
+ * with j > p - window or j < first_tokens.  Keys keep their positions.  Pages that no
+ * query token of a sequence sees are not read.
+ *
+ * Arguments, layouts and errors as for paged_attn_decode, except that
+ *   - window is at least 1, first_tokens at least 0;
+ *   - G * max_query_len <= 64 for every cache; max_blocks <= 2^27 - 64;
+ *   - with query_start_loc a sequence may have no query tokens (a padded batch): its
+ *     pages are not read.  Rows of `out` and `lse` past the last sequence's stay as they
+ *     were, and T may exceed them;
+ *   - a row that sees no key (L_i = 0 or a position below 0) gets out = 0 and lse = -inf
+ *     (its sink's logit with sinks) and sets bit 1 of the status word;
+ *   - slots that no query token of the sequence sees may hold anything; NaN in a key or a
+ *     value that a row sees makes that row NaN (a value's NaN: every row of its sequence
+ *     and KV head);
+ *   - sinks are finite or -inf (no sink).
+ *   opts   NULL = defaults, as for paged_attn_decode_ex, but that sliding_window,
+ *          use_tcgen05 and segment_cost_pages are refused with PA_ERR_UNSUPPORTED.  Calls
+ *          without opts->workspace share the library-owned workspace of the device: calls
+ *          that may overlap on the device (two streams, two captured graphs) each need a
+ *          workspace of their own.  paged_attn_plan, paged_attn_workspace_size and
+ *          paged_attn_reserve of the same shape serve this call too.
+ */
+int paged_attn_decode_window(const pa_tensor_t* q, const pa_tensor_t* k_cache, const pa_tensor_t* v_cache,
+                             const pa_tensor_t* block_tables, const pa_tensor_t* seq_lens,
+                             const pa_tensor_t* query_start_loc, int32_t max_query_len, int32_t window,
+                             int32_t first_tokens, float scale, float k_scale, float v_scale, const pa_tensor_t* out,
+                             const pa_tensor_t* lse, const pa_options_t* opts, pa_stream_t stream);
+
+/*
  * paged_attn_cache_write - write new tokens' K and V rows into the paged caches
  * (ATOM model-operations guide, "KV cache operations": standard (bf16) and FP8
  * KV cache write; token_layout/slots.py: slot_mapping, "which KV slot a token is

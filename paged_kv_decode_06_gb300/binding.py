@@ -72,6 +72,8 @@ _SIGNATURES = {
     "paged_attn_cache_write_per_token": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_void_p]),
     "paged_attn_cache_write_q4": (ctypes.c_int, [_P] * 7 + [ctypes.c_float, ctypes.c_float, ctypes.c_void_p]),
     "paged_attn_cache_read_q4": (ctypes.c_int, [_P] * 5 + [ctypes.c_float, ctypes.c_float, _P, _P, ctypes.c_void_p]),
+    "paged_attn_decode_window": (ctypes.c_int, [_P] * 6 + [ctypes.c_int32] * 3 + [ctypes.c_float] * 3 +
+                                 [_P, _P, ctypes.POINTER(PaOptions), ctypes.c_void_p]),
     "paged_attn_rope_cache_write": (ctypes.c_int, [_P] * 5 + [ctypes.c_char_p, ctypes.c_int32] + [_P] * 3 +
                                     [ctypes.c_float, ctypes.c_float, _P, _P, ctypes.c_void_p]),
     "paged_attn_decode_q4": (ctypes.c_int, [_P] * 8 + [ctypes.c_int32, ctypes.c_float, ctypes.c_float, ctypes.c_float,
@@ -492,25 +494,25 @@ def paged_attn_q4_reserve(num_seqs, num_q_heads, num_kv_heads, head_dim, max_que
     _check(lib, lib.paged_attn_q4_reserve(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len))
 
 
-_Q4_WORKSPACE_BYTES = {}
+_WORKSPACE_BYTES = {}
 
 
-def _with_workspace(options, shape, device):
+def _with_workspace(options, shape, device, plan=paged_attn_q4_plan):
     """Options whose workspace is a tensor of torch's allocator (so calls on
     several streams or in several graphs do not share one); the caller's own
-    workspace is kept."""
+    workspace is kept.  `plan` gives the bytes of a shape."""
     if options is not None and options.workspace:
         return options, None
     o = PaOptions()
     if options is not None:
         ctypes.pointer(o)[0] = options
-    key = (device.index, shape, o.num_ctas, o.min_pages_per_cta, o.heads_per_cta)
-    n = _Q4_WORKSPACE_BYTES.get(key)
+    key = (plan, device.index, shape, o.num_ctas, o.min_pages_per_cta, o.heads_per_cta)
+    n = _WORKSPACE_BYTES.get(key)
     if n is None:
-        n = paged_attn_q4_plan(*shape, options=options)["workspace_bytes"]
-        if len(_Q4_WORKSPACE_BYTES) >= _DESC_CACHE_MAX:
-            _Q4_WORKSPACE_BYTES.clear()
-        _Q4_WORKSPACE_BYTES[key] = n
+        n = plan(*shape, options=options)["workspace_bytes"]
+        if len(_WORKSPACE_BYTES) >= _DESC_CACHE_MAX:
+            _WORKSPACE_BYTES.clear()
+        _WORKSPACE_BYTES[key] = n
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     o.workspace, o.workspace_bytes = ws.data_ptr(), n
     return o, ws
@@ -569,6 +571,71 @@ def paged_attn_decode_q4(q, k_cache, v_cache, k_group_scales, v_group_scales, bl
                                          ctypes.byref(options) if options is not None else None,
                                          _stream_handle(stream)))
     return out, lse
+
+
+def _decode_hole_call(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, more, scale, out, lse, options,
+                      want_lse, shape, plan):
+    """Tensors, out, lse, scale, options and workspace of a decode call over walks with a hole."""
+    tensors = (q, k_cache, v_cache, block_tables, seq_lens, query_start_loc) + more
+    _on_current_device(*tensors, out, lse)
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    ws = None
+    if q.dim() == 3 and k_cache.dim() == 4 and block_tables.dim() == 2 and q.shape[0] > 0 and k_cache.shape[2] > 0:
+        options, ws = _with_workspace(options, shape(), q.device, plan)
+    return tensors, out, lse, float(scale), options, ws
+
+
+def _window_call(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, max_query_len, window, first_tokens,
+                 scale, k_scale, v_scale, out, lse, options, want_lse):
+    shape = lambda: (block_tables.shape[0], q.shape[1], k_cache.shape[2], q.shape[2], _dtype_code(k_cache),
+                     int(max_query_len))
+    tensors, out, lse, scale, options, ws = _decode_hole_call(
+        q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, (), scale, out, lse, options, want_lse, shape,
+        paged_attn_plan)
+    scalars = (ctypes.c_int32(int(max_query_len)), ctypes.c_int32(int(window)), ctypes.c_int32(int(first_tokens)),
+               ctypes.c_float(scale), ctypes.c_float(float(k_scale)), ctypes.c_float(float(v_scale)))
+    return tensors, scalars, out, lse, options, ws
+
+
+def paged_attn_decode_window(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, max_query_len, window,
+                             first_tokens, scale=None, k_scale=1.0, v_scale=1.0, out=None, lse=None, stream=None,
+                             options=None, want_lse=True):
+    """Decode attention over a sliding window and the first tokens, which stay
+    visible (see include/paged_attn.h): a query at position p sees the keys j <= p
+    with j > p - window or j < first_tokens.  Tensors and results as for
+    ``paged_attn_decode``.  Without a workspace in `options` the call takes one from
+    torch's allocator."""
+    lib = load()
+    with _allocating_on(stream):
+        tensors, scalars, out, lse, options, ws = _window_call(
+            q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, max_query_len, window, first_tokens, scale,
+            k_scale, v_scale, out, lse, options, want_lse)
+    refs = [ctypes.byref(tensor_desc(t)) for t in tensors]
+    _check(lib, lib.paged_attn_decode_window(*refs, *scalars, ctypes.byref(tensor_desc(out)),
+                                             ctypes.byref(tensor_desc(lse)),
+                                             ctypes.byref(options) if options is not None else None,
+                                             _stream_handle(stream)))
+    return out, lse
+
+
+def prepare_decode_window(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, max_query_len, window,
+                          first_tokens, scale=None, k_scale=1.0, v_scale=1.0, out=None, lse=None, options=None,
+                          want_lse=True) -> "PreparedCall":
+    """``paged_attn_decode_window`` with its arguments marshalled once (see
+    PreparedCall).  The prepared call owns its workspace (unless `options` has
+    one): use one prepared call for each stream that may run at the same time."""
+    tensors, scalars, out, lse, options, ws = _window_call(
+        q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, max_query_len, window, first_tokens, scale,
+        k_scale, v_scale, out, lse, options, want_lse)
+    call = PreparedCall(load().paged_attn_decode_window, tensors, scalars, out, lse,
+                        options if options is not None else PaOptions())
+    call._workspace = ws
+    return call
 
 
 def _page_call(fn, caches, ints, stream):

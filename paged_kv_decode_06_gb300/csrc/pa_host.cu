@@ -111,6 +111,9 @@ int device_state(DeviceState** out, int* dev_out) {
       return cuda_fail(e, "cudaFuncSetAttribute(MLA, tcgen05)");
     if ((e = pa::set_split_smem_limits_q4(s.smem_optin)) != cudaSuccess)
       return cuda_fail(e, "cudaFuncSetAttribute(split 4-bit)");
+    if ((e = pa::set_split_smem_limits_first(s.smem_optin)) != cudaSuccess ||
+        (e = pa::set_split_smem_limits_own(s.smem_optin)) != cudaSuccess)
+      return cuda_fail(e, "cudaFuncSetAttribute(split over a walk with a hole)");
     pa::init_cache_write_occupancy();
     void* ptr = nullptr;
     if ((e = cudaGetSymbolAddress(&ptr, g_status_word)) != cudaSuccess)
@@ -142,6 +145,7 @@ struct Plan {
   bool tok;           // per-token fp8 scales staged behind each page's K and V tiles
   uint32_t tok_bytes; // tok: one tensor's scales of one page (HC * 16 * 4)
   int block_pages;    // tc: pages per ring stage
+  int seq_ints;       // mma.sync: int32 a sequence in shared memory
   uint32_t stage_bytes, kv_bytes, q_slot_bytes;
   uint32_t off_stage, off_q, off_bar, off_prefix, off_xchg, smem;
   size_t ws_unit, ws_ml, ws_o, ws_bytes;
@@ -186,7 +190,7 @@ bool has_token_scales(const pa_options_t* opts) {
 // mma.sync kernel: heads per CTA, ring depth and shared-memory layout.
 int plan_mma(Plan& p, int B, int Hkv, int D, int max_qlen, const pa_options_t* opts, int smem_optin) {
   const uint32_t bar_bytes = 8u * (2 * kMaxStages + 4);
-  const uint32_t prefix_bytes = static_cast<uint32_t>(align_up(4u * (3 * B + 2), 16));   // prefix, lengths, starts
+  const uint32_t prefix_bytes = static_cast<uint32_t>(align_up(4u * (p.seq_ints * B + 2), 16));   // prefix, lengths, starts
   const int forced_hc = opts ? opts->heads_per_cta : 0;
   if (forced_hc < 0 || (forced_hc > 0 && Hkv % forced_hc != 0))
     return fail(PA_ERR_INVALID_ARG, "heads_per_cta %d must divide num_kv_heads %d", forced_hc, Hkv);
@@ -243,11 +247,12 @@ int plan_mma(Plan& p, int B, int Hkv, int D, int max_qlen, const pa_options_t* o
 }
 
 int make_plan(int B, int Hq, int Hkv, int D, int kv_dtype, int max_qlen, const pa_options_t* opts, int num_sms,
-              int smem_optin, Plan* pl) {
+              int smem_optin, Plan* pl, int seq_ints = 3) {
   int st = check_shape_args(B, Hq, Hkv, D, kv_dtype, max_qlen);
   if (st != PA_OK) return st;
   Plan p = {};
   p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.D = D; p.max_qlen = max_qlen;
+  p.seq_ints = seq_ints;
   p.esz = (kv_dtype == PA_FP8_E4M3) ? 1 : 2;
   p.G = Hq / Hkv;
   p.R_max = p.G * max_qlen;
@@ -1034,6 +1039,47 @@ int host_workspace(const pa_options_t* opts, size_t bytes, cudaStream_t stream, 
   DeviceState* ds = nullptr;
   const int st = device_state(&ds, nullptr);
   return st != PA_OK ? st : acquire_workspace(ds, opts, bytes, stream, reserve_fn, ws);
+}
+int host_split_plan(int B, int Hq, int Hkv, int D, int kv_dtype, int max_qlen, const pa_options_t* opts, int seq_ints,
+                    const HostDevice& dev, HostSplitPlan* out) {
+  if (static_cast<int64_t>(Hq / std::max(Hkv, 1)) * max_qlen > kMaxRowsMma)
+    return fail(PA_ERR_UNSUPPORTED, "group size %d x max_query_len %d exceeds %d query rows per KV head", Hq / Hkv,
+                max_qlen, kMaxRowsMma);
+  Plan pl{};
+  const int st = make_plan(B, Hq, Hkv, D, kv_dtype, max_qlen, opts, dev.num_sms, dev.smem_optin, &pl, seq_ints);
+  if (st != PA_OK) return st;
+  HostSplitPlan r = {};
+  r.sp.Hq = Hq;
+  r.sp.Hkv = Hkv;
+  r.sp.G = pl.G;
+  r.sp.max_qlen = max_qlen;
+  r.sp.num_seqs = B;
+  r.sp.HC = pl.HC;
+  r.sp.NC = pl.NC;
+  r.sp.MT = pl.MT;
+  r.sp.R_max = pl.R_max;
+  r.sp.nstage = pl.nstage;
+  r.sp.min_pages = pl.min_pages;
+  r.sp.pair_pages = pl.pair;
+  r.sp.off_prefix = pl.off_prefix;
+  r.sp.off_bar = pl.off_bar;
+  r.sp.off_q = pl.off_q;
+  r.sp.q_slot_bytes = pl.q_slot_bytes;
+  r.sp.off_stage = pl.off_stage;
+  r.sp.stage_bytes = pl.stage_bytes;
+  r.sp.kv_bytes = pl.kv_bytes;
+  r.sp.tok_bytes = pl.tok_bytes;
+  r.sp.wait_ns = wait_limit_ns(opts);
+  r.sp.starve_cta = starved_cta(opts);
+  r.threads = pl.threads;
+  r.grid = pl.grid;
+  r.smem = static_cast<int>(pl.smem);
+  r.rows = static_cast<size_t>(2) * pl.grid * pl.HC * pl.R_max;
+  *out = r;
+  return PA_OK;
+}
+int host_cache_map(CUtensorMap* map, const pa_tensor_t* t, int esz, int D, int Hkv, int HC, int64_t NB) {
+  return encode_cache_map(map, t, esz, D, Hkv, HC, NB);
 }
 int host_reserve(size_t bytes) {
   DeviceState* ds = nullptr;

@@ -8,6 +8,7 @@
 #include <exception>
 #include <mutex>
 
+#include "pa_kernels.h"
 #include "paged_attn.h"
 
 namespace pa {
@@ -39,6 +40,19 @@ int host_device(HostDevice* out);
 // device's library-owned one, grown outside stream capture.
 int host_workspace(const pa_options_t* opts, size_t bytes, cudaStream_t stream, const char* reserve_fn, void** ws);
 int host_reserve(size_t bytes);
+
+// Launch plan of the mma.sync split kernel (at most 64 query rows a KV head), `seq_ints`
+// int32 a sequence in its shared memory: sp has the plan's fields, the rest zero; `rows`
+// partial rows are left by cut units.
+struct HostSplitPlan {
+  SplitParams sp;
+  int threads, grid, smem;
+  size_t rows;
+};
+int host_split_plan(int B, int Hq, int Hkv, int D, int kv_dtype, int max_qlen, const pa_options_t* opts, int seq_ints,
+                    const HostDevice& dev, HostSplitPlan* out);
+// TMA map over a cache for boxes of HC heads of a page.
+int host_cache_map(CUtensorMap* map, const pa_tensor_t* t, int esz, int D, int Hkv, int HC, int64_t NB);
 
 // Runs the body of an entry point: no exception crosses the C boundary.
 template <typename F>

@@ -76,6 +76,12 @@ struct SplitParams {
   // charges for every unit a CTA starts (0: an equal page split)
   uint32_t off_qring;
   int32_t seg_cost;
+  // windows with first tokens that stay visible (Walk::kFirst)
+  int32_t first_tokens;
+  // sequences behind a shared prefix (Walk::kOwn): pages each skips (int32 [B]), and the
+  // row of ws_ml / ws_o from which rows of whole units stand by (token, query head)
+  const int32_t* skip;
+  int64_t whole_row0;
 };
 
 struct MergeParams {
@@ -99,6 +105,34 @@ struct MergeParams {
   // a NaN sum gives a NaN row and lse (4-bit caches; else 0 and -inf)
   bool keep_nan;
 };
+
+// Merge of the walks with a hole (pa_merge_rows.cu); what is named as in SplitParams is
+// the same.
+struct SharedGroup;
+struct SharedTotals;
+struct MergeRowsParams : MergeParams {
+  int32_t Hq, first_tokens;
+  const int32_t* skip;
+  int64_t whole_row0;
+  // a shared prefix: the group that each sequence takes part in (-1: none), the groups,
+  // and the prefix kernel's partial rows, grid and least steps a CTA
+  const int32_t* seq_group;
+  const SharedGroup* groups;
+  const SharedTotals* totals;
+  const float2* pre_ml;
+  const float* pre_o;
+  int32_t pre_grid, pre_min_steps;
+};
+cudaError_t launch_merge_rows(int head_dim, bool shared, const MergeRowsParams& p, int units, int rows, bool wide,
+                              bool pdl, cudaStream_t stream);
+// Split kernel over a walk with a hole: windows with first tokens (bf16, fp8, fp8 with
+// per-token scales), sequences behind a shared prefix (bf16, fp8).
+cudaError_t launch_split_first(int head_dim, bool fp8, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const SplitParams& p, int grid, int threads, int smem, bool pdl, cudaStream_t stream);
+cudaError_t launch_split_own(int head_dim, bool fp8, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const SplitParams& p, int grid, int threads, int smem, bool pdl, cudaStream_t stream);
+cudaError_t set_split_smem_limits_first(int smem);
+cudaError_t set_split_smem_limits_own(int smem);
 
 // The split kernel over a 4-bit cache (pa_split_q4.cu).
 struct SplitQ4Params : SplitParams {

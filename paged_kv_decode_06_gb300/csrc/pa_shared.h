@@ -1,0 +1,58 @@
+// Layout of the shared-prefix part of a decode call: what the plan kernel writes, and
+// how the prefix and merge kernels number its work and its partial rows.
+//
+// The rows of one (group, KV head), G query heads of every query token of the group's
+// sequences, are cut into pairs of 128-row tiles, one tile a slot; a last pair of at most
+// 128 rows has one tile, which both slots take, each every other block of keys.  A step
+// is what the two slots do at once: one block of kSharedBlock keys for both tiles, or two
+// blocks for the single tile.  Steps stand end to end in (group, head, pair, block)
+// order, X in all; CTA c of the NG in use takes [c X / NG, (c + 1) X / NG).
+//
+// A CTA leaves partial rows for each piece it holds: piece (pair, CTA c) at rows row0 +
+// 256 c of the pair's row0 = the padded rows of all pairs before it, so that no two pieces
+// meet: a next pair starts at least its predecessor's rows, a next CTA 256 rows further.
+#pragma once
+
+#include <stdint.h>
+
+namespace pa {
+
+constexpr int kSharedTile = 128;
+constexpr int kSharedPair = 2 * kSharedTile;
+constexpr int kSharedBlockPages = 8;
+
+struct SharedGroup {
+  int32_t seq;          // the sequence whose block-table row names the pages
+  int32_t pages;        // shared pages; 0: nothing shared
+  int32_t t0, rows;     // first query token, rows (query tokens x G) a KV head
+  int32_t pairs;        // tile pairs a head
+  int32_t last_rows;    // rows of the last pair
+  int32_t blocks;       // blocks of keys
+  int32_t steps_head;   // steps a head
+  int32_t rows_head;    // padded rows a head
+  int32_t reserved;
+  int64_t step0;        // steps of the groups before
+  int64_t row0;         // padded rows of the groups before
+};
+
+struct SharedTotals {
+  int64_t steps;
+  int64_t rows;
+};
+
+__host__ __device__ inline bool shared_single(const SharedGroup& g, int pair) {
+  return pair == g.pairs - 1 && g.last_rows <= kSharedTile;
+}
+__host__ __device__ inline int shared_steps(const SharedGroup& g, int pair) {
+  return shared_single(g, pair) ? (g.blocks + 1) / 2 : g.blocks;
+}
+// CTAs in use, and the CTA that holds step x.
+__host__ __device__ inline int shared_ctas(int64_t steps, int grid, int min_steps) {
+  const int64_t n = (steps + min_steps - 1) / min_steps;
+  return static_cast<int>(n < 1 ? 1 : (n < grid ? n : grid));
+}
+__host__ __device__ inline int shared_cta_of(int64_t x, int64_t steps, int ng) {
+  return static_cast<int>(((x + 1) * ng - 1) / steps);
+}
+
+}  // namespace pa

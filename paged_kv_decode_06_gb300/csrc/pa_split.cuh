@@ -94,6 +94,33 @@ __device__ __forceinline__ int first_visible_page(int L, int qn, int window) {
   return first_key > 0 ? first_key / kPage : 0;
 }
 
+// Which pages of a sequence a kernel walks.  kAll: those that a sliding window leaves, or
+// all.  kFirst: a window and the first tokens before it.  kOwn: those behind the pages
+// that its group shares (pa_shared.cuh).
+enum class Walk { kAll, kFirst, kOwn };
+
+// kFirst and kOwn: the pages walked are the logical pages 0 .. keep - 1 and keep + skip
+// .. keep + skip + n - keep - 1, none past the sequence's block-table row.
+struct View {
+  int keep, skip, n;
+  __device__ __forceinline__ int page(int j) const { return j < keep ? j : j + skip; }
+};
+
+template <Walk WALK, typename P>
+__device__ __forceinline__ View view_of(const P& p, int L, int qn, int own_skip) {
+  View v;
+  const int pages = L > 0 ? min((L - 1) / kPage + 1, p.max_blocks) : 0;
+  if constexpr (WALK == Walk::kFirst) {
+    v.keep = min((p.first_tokens + kPage - 1) / kPage, pages);
+    v.skip = max(0, min(first_visible_page(L, qn, p.window), pages) - v.keep);
+  } else {
+    v.keep = 0;
+    v.skip = min(own_skip, pages);
+  }
+  v.n = pages - v.skip;
+  return v;
+}
+
 // Sequence metadata from the shared-memory copies made in the prologue.
 __device__ __forceinline__ SeqInfo seq_info(const SplitParams& p, const int32_t* s_len, const int32_t* s_qsl, int i,
                                             bool report, int window) {
@@ -149,7 +176,7 @@ __device__ __forceinline__ int d_of(int J, int e, int tig) {
 // range is reported here instead of where its pages are walked), and every
 // sequence with pages counts `charge` more (the prefix is then one of 32 bits
 // without sign); returns how many those are.
-template <bool CHARGED = false>
+template <bool CHARGED = false, Walk WALK = Walk::kAll>
 __device__ __forceinline__ int page_prefix(const SplitParams& p, int window, int32_t* s_pre, int32_t* s_len,
                                            int32_t* s_qsl, int* s_scan, int* s_total, int charge = 0) {
   const int tid = threadIdx.x;
@@ -173,7 +200,13 @@ __device__ __forceinline__ int page_prefix(const SplitParams& p, int window, int
         v = p.max_blocks;
       }
       const int qn = p.qsl != nullptr ? p.qsl[i + 1] - p.qsl[i] : 1;
-      v -= min(v, first_visible_page(L, qn, window));   // pages before the sliding window are skipped
+      if constexpr (WALK == Walk::kAll) {
+        v -= min(v, first_visible_page(L, qn, window));   // pages before the sliding window are skipped
+      } else {
+        int own = 0;
+        if constexpr (WALK == Walk::kOwn) s_qsl[B + 1 + i] = own = p.skip[i];
+        v = view_of<WALK>(p, L, qn, own).n;
+      }
       if constexpr (CHARGED) {
         const int t0 = s_qsl[i];
         const bool valid = qn >= 0 && qn <= p.max_qlen && t0 >= 0 && t0 <= p.num_tokens - qn;
@@ -221,6 +254,21 @@ struct BlockTableCache {
   int bt_i = -1, bt_j0 = 0, bt_val = 0;   // entries [bt_j0, bt_j0 + 32) of sequence bt_i
   int nx_i = -1, nx_j0 = 0, nx_val = 0;   // the batch after it
 
+  // Entry of visible page j of sequence i.
+  template <Walk WALK>
+  static __device__ __forceinline__ int entry(const SplitParams& p, const int32_t* s_len, const int32_t* s_qsl, int B,
+                                              int i, int j, int n, int window) {
+    const int qn = s_qsl[i + 1] - s_qsl[i];
+    if constexpr (WALK == Walk::kAll) {
+      const int js = first_visible_page(s_len[i], qn, window);
+      return j < n ? p.block_tables[static_cast<int64_t>(i) * p.bt_stride + js + j] : 0;
+    } else {
+      const View v = view_of<WALK>(p, s_len[i], qn, WALK == Walk::kOwn ? s_qsl[B + 1 + i] : 0);
+      return j < n ? p.block_tables[static_cast<int64_t>(i) * p.bt_stride + v.page(j)] : 0;
+    }
+  }
+
+  template <Walk WALK = Walk::kAll>
   __device__ __forceinline__ int lookup(const SplitParams& p, const Cursor& cu, const int32_t* s_pre,
                                         const int32_t* s_len, const int32_t* s_qsl, int B, int NC, int window,
                                         int lane) {
@@ -228,9 +276,7 @@ struct BlockTableCache {
       if (cu.i == nx_i && cu.j == nx_j0) {
         bt_val = nx_val;
       } else {
-        const int jj = cu.j + lane;
-        const int js = first_visible_page(s_len[cu.i], s_qsl[cu.i + 1] - s_qsl[cu.i], window);
-        bt_val = (jj < cu.n) ? p.block_tables[static_cast<int64_t>(cu.i) * p.bt_stride + js + jj] : 0;
+        bt_val = entry<WALK>(p, s_len, s_qsl, B, cu.i, cu.j + lane, cu.n, window);
       }
       bt_i = cu.i;
       bt_j0 = cu.j;
@@ -248,9 +294,7 @@ struct BlockTableCache {
       nx_i = ni;
       nx_j0 = nj;
       if (ni >= 0) {
-        const int jj = nj + lane;
-        const int js = first_visible_page(s_len[ni], s_qsl[ni + 1] - s_qsl[ni], window);
-        nx_val = (jj < pages_of(s_pre, ni)) ? p.block_tables[static_cast<int64_t>(ni) * p.bt_stride + js + jj] : 0;
+        nx_val = entry<WALK>(p, s_len, s_qsl, B, ni, nj + lane, pages_of(s_pre, ni), window);
       }
     }
     return __shfl_sync(0xffffffffu, bt_val, cu.j - bt_j0);
@@ -375,11 +419,12 @@ __device__ __forceinline__ void pv_pages(ConsumerState<D, FP8>& cs, const uint32
 // V follows K at +kv_bytes.  tb = first token of the block; min_lim = L - qn.
 // TOKS: per-token scales; ts[pg] is the shared-memory address of this warp's
 // head's 16 K scales in page pg's stage, its 16 V scales tok_bytes further.
-template <int D, bool FP8, int NP, bool TOKS = false>
+// KEEP: keys below `first` are visible whatever the window.
+template <int D, bool FP8, int NP, bool TOKS = false, bool KEEP = false>
 __device__ __forceinline__ void consume_pages(ConsumerState<D, FP8>& cs, const uint32_t (&hb)[NP], uint32_t kv_bytes,
                                               uint32_t block_stride, int tb, int L, int min_lim, int lim0, int lim1,
                                               int window, float scale_log2, int lane, const uint32_t (&ts)[NP],
-                                              uint32_t tok_bytes) {
+                                              uint32_t tok_bytes, int first = 0) {
   using GG = Geo<D, FP8>;
   const int tig = lane & 3, mi = lane >> 3, rr = lane & 7;
   float S[2 * NP][4];
@@ -445,7 +490,8 @@ __device__ __forceinline__ void consume_pages(ConsumerState<D, FP8>& cs, const u
   const float csc = fold ? scale_log2 : 1.f;   // scale still to apply in the exponent
   // keys allowed for a row: lim - W < token <= lim (causal run end; sliding
   // window start when W > 0, whose largest start is L - W for the last row)
-  if (tb + kPage * NP - 1 > min_lim || (window > 0 && tb < L - window)) {
+  if (tb + kPage * NP - 1 > min_lim ||
+      (window > 0 && tb < L - window && (!KEEP || tb + kPage * NP > first))) {
     const int lo0 = window > 0 ? lim0 - window + 1 : INT_MIN;
     const int lo1 = window > 0 ? lim1 - window + 1 : INT_MIN;
 #pragma unroll
@@ -453,8 +499,9 @@ __device__ __forceinline__ void consume_pages(ConsumerState<D, FP8>& cs, const u
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int tok = tb + 8 * n + 2 * tig + e;
-        if (tok > lim0 || tok < lo0) x[n][e] = -INFINITY;
-        if (tok > lim1 || tok < lo1) x[n][2 + e] = -INFINITY;
+        const bool held = KEEP && tok < first;
+        if (tok > lim0 || (tok < lo0 && !held)) x[n][e] = -INFINITY;
+        if (tok > lim1 || (tok < lo1 && !held)) x[n][2 + e] = -INFINITY;
       }
   }
   float mx0 = fmaxf(x[0][0], x[0][1]);
@@ -536,11 +583,14 @@ __device__ __forceinline__ void consume_pages(ConsumerState<D, FP8>& cs, const u
     }
   }
   }
+  // KEEP: keys from `first` up to here are hidden from every row of the sequence
+  const int near = KEEP ? min_lim - window + 1 : INT_MIN;
+  const bool hole = KEEP && tb < near && tb + kPage * NP > first;
   if constexpr (TOKS) {
     // P V with per-token value scales: each weight takes its value row's scale
     // (the sum l above keeps the unscaled weights).  Slots past the sequence
     // end take 0, so a non-finite scale there cannot reach O.
-    const bool tail = L - tb < kPage * NP;
+    const bool tail = L - tb < kPage * NP || hole;
 #pragma unroll
     for (int pg = 0; pg < NP; ++pg) {
       const int vt = L - tb - kPage * pg;   // value rows of this page inside the sequence
@@ -552,6 +602,11 @@ __device__ __forceinline__ void consume_pages(ConsumerState<D, FP8>& cs, const u
         if (tail) {
           c0 = t0 < vt ? c0 : 0.f;
           c1 = t0 + 1 < vt ? c1 : 0.f;
+          if constexpr (KEEP) {
+            const int tok = tb + kPage * pg + t0;
+            if (tok < near && tok >= first) c0 = 0.f;
+            if (tok + 1 < near && tok + 1 >= first) c1 = 0.f;
+          }
         }
         const uint64_t c2 = f2_pack(c0, c1);
         const int n = 2 * pg + h8;
@@ -580,13 +635,22 @@ __device__ __forceinline__ void consume_pages(ConsumerState<D, FP8>& cs, const u
   for (int pg = 0; pg < NP; ++pg) vb[pg] = hb[pg] + kv_bytes;
   // Value rows at or past the end of the sequence are zeroed so that stale
   // (even non-finite) tail slots cannot leak through P == 0.
-  if (L - tb < kPage * NP) {
+  if (L - tb < kPage * NP || hole) {
     uint32_t mb0[NP], mb1[NP];
 #pragma unroll
     for (int pg = 0; pg < NP; ++pg) {
       const int vt = L - tb - kPage * pg;
       mb0[pg] = (2 * tig < vt ? 0x0000ffffu : 0u) | (2 * tig + 1 < vt ? 0xffff0000u : 0u);
       mb1[pg] = (2 * tig + 8 < vt ? 0x0000ffffu : 0u) | (2 * tig + 9 < vt ? 0xffff0000u : 0u);
+      if constexpr (KEEP) {
+        // rows that no query row sees, between the first tokens and the window
+        const int t0 = tb + kPage * pg + 2 * tig;
+        auto hidden = [&](int tok) { return tok < near && tok >= first; };
+        if (hidden(t0)) mb0[pg] &= 0xffff0000u;
+        if (hidden(t0 + 1)) mb0[pg] &= 0x0000ffffu;
+        if (hidden(t0 + 8)) mb1[pg] &= 0xffff0000u;
+        if (hidden(t0 + 9)) mb1[pg] &= 0x0000ffffu;
+      }
     }
     pv_pages<D, FP8, NP, true>(cs, vb, Pa, block_stride, mb0, mb1, lane);
   } else {
@@ -597,12 +661,15 @@ __device__ __forceinline__ void consume_pages(ConsumerState<D, FP8>& cs, const u
 
 // WINDOW: the sliding-window variant (a separate instantiation, so the
 // windowless kernels carry none of its code).  TOKS: fp8 caches with per-token
-// scales, staged by the producer behind each page's K and V tiles.
-template <int D, bool FP8, bool WINDOW, bool TOKS = false>
+// scales, staged by the producer behind each page's K and V tiles.  WALK: which pages;
+// with kFirst and kOwn a sequence may have no query tokens, NaN stays NaN, and with kOwn
+// every unit leaves partials (one that a CTA holds whole in the row's place of ws_whole).
+template <int D, bool FP8, bool WINDOW, bool TOKS = false, Walk WALK = Walk::kAll>
 __global__ void __launch_bounds__(kSplitMaxThreads, 1)
     pa_split_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                     const SplitParams p) {
   using GG = Geo<D, FP8>;
+  constexpr bool kHole = WALK != Walk::kAll;
   const int window = WINDOW ? p.window : 0;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int s_scan[kSplitMaxThreads / 32 + 1];
@@ -649,7 +716,7 @@ __global__ void __launch_bounds__(kSplitMaxThreads, 1)
   grid_dependency_wait();
 
   // ---- prologue: metadata to shared memory, pages per sequence, prefix -----
-  page_prefix(p, window, s_pre, s_len, s_qsl, s_scan, &s_total);
+  page_prefix<kHole, WALK>(p, window, s_pre, s_len, s_qsl, s_scan, &s_total);
   __syncthreads();   // the prefix totals and the mbarrier initialisation above
 
   const int64_t X = static_cast<int64_t>(p.NC) * s_pre[B];
@@ -703,7 +770,7 @@ __global__ void __launch_bounds__(kSplitMaxThreads, 1)
         }
         ++qseg;
       }
-      const int phys = btc.lookup(p, cu, s_pre, s_len, s_qsl, B, NC, window, lane);
+      const int phys = btc.lookup<WALK>(p, cu, s_pre, s_len, s_qsl, B, NC, window, lane);
       const bool bad_page = phys < 0 || phys >= p.num_pages;
       if (bad_page && lane == 0) atomicOr(p.err, kErrPageRange);
       // An out-of-range page id reads as zeros (TMA fills outside the tensor).
@@ -759,6 +826,7 @@ __global__ void __launch_bounds__(kSplitMaxThreads, 1)
   int64_t seg_k0 = 0;
   int seg_j0 = 0;
   SeqInfo si = {0, 0, 0};
+  View view = {0, 0, 0};
   bool active = false, ok0 = false, ok1 = false;
   int lim0 = 0, lim1 = 0;
   ConsumerState<D, FP8> cs;
@@ -792,6 +860,7 @@ __global__ void __launch_bounds__(kSplitMaxThreads, 1)
         p.ws_unit[static_cast<int64_t>(cu.i) * NC + cu.c] =
             make_int4(g, pieces | (k != 0 ? (1 << 30) : 0), si.t0, si.qn);
       }
+      if constexpr (kHole) view = view_of<WALK>(p, si.L, si.qn, WALK == Walk::kOwn ? s_qsl[B + 1 + cu.i] : 0);
       const int R = G * si.qn;
       active = 16 * w < R;
       ok0 = rho0 < R;
@@ -830,25 +899,27 @@ __global__ void __launch_bounds__(kSplitMaxThreads, 1)
       stage2 = 0;
       ++round2;
     }
-    const bool pair = p.pair_pages && (k + 1 < count) && (cu.j + 1 < cu.n);
+    const bool pair = p.pair_pages && (k + 1 < count) && (cu.j + 1 < cu.n) &&
+                      (WALK != Walk::kFirst || view.skip == 0 || cu.j + 1 != view.keep);
     if (pair && !mbar_wait(full_bar(stage2), round2 & 1u, p.wait_ns)) {
       if (lane == 0) atomicOr(p.err, kErrTimeout);
       break;
     }
-    const int tb = kPage * (si.js + cu.j);
+    const int tb = kPage * (kHole ? view.page(cu.j) : si.js + cu.j);
+    const int first = WALK == Walk::kFirst ? p.first_tokens : 0;
     if (active) {
       if (pair) {
         const uint32_t hb[2] = {head_base + static_cast<uint32_t>(stage) * p.stage_bytes,
                                 head_base + static_cast<uint32_t>(stage2) * p.stage_bytes};
         const uint32_t ts[2] = {tok_base + static_cast<uint32_t>(stage) * p.stage_bytes,
                                 tok_base + static_cast<uint32_t>(stage2) * p.stage_bytes};
-        consume_pages<D, FP8, 2, TOKS>(cs, hb, p.kv_bytes, block_stride, tb, si.L, si.L - si.qn, lim0, lim1, window,
-                                       p.scale_log2, lane, ts, p.tok_bytes);
+        consume_pages<D, FP8, 2, TOKS, WALK == Walk::kFirst>(cs, hb, p.kv_bytes, block_stride, tb, si.L, si.L - si.qn, lim0, lim1, window,
+                                       p.scale_log2, lane, ts, p.tok_bytes, first);
       } else {
         const uint32_t hb[1] = {head_base + static_cast<uint32_t>(stage) * p.stage_bytes};
         const uint32_t ts[1] = {tok_base + static_cast<uint32_t>(stage) * p.stage_bytes};
-        consume_pages<D, FP8, 1, TOKS>(cs, hb, p.kv_bytes, block_stride, tb, si.L, si.L - si.qn, lim0, lim1, window,
-                                       p.scale_log2, lane, ts, p.tok_bytes);
+        consume_pages<D, FP8, 1, TOKS, WALK == Walk::kFirst>(cs, hb, p.kv_bytes, block_stride, tb, si.L, si.L - si.qn, lim0, lim1, window,
+                                       p.scale_log2, lane, ts, p.tok_bytes, first);
       }
     }
     __syncwarp();
@@ -865,10 +936,10 @@ __global__ void __launch_bounds__(kSplitMaxThreads, 1)
       lt0 += __shfl_xor_sync(0xffffffffu, lt0, 2);
       float lt1 = cs.l1 + __shfl_xor_sync(0xffffffffu, cs.l1, 1);
       lt1 += __shfl_xor_sync(0xffffffffu, lt1, 2);
-      if (complete) {
+      if (complete && WALK != Walk::kOwn) {
         const int hq_base = (cu.c * HC + hh) * G;
-        const float inv0 = lt0 > 0.f ? p.v_scale / lt0 : 0.f;
-        const float inv1 = lt1 > 0.f ? p.v_scale / lt1 : 0.f;
+        const float inv0 = lt0 > 0.f ? p.v_scale / lt0 : (kHole && lt0 != lt0 ? lt0 : 0.f);
+        const float inv1 = lt1 > 0.f ? p.v_scale / lt1 : (kHole && lt1 != lt1 ? lt1 : 0.f);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const bool ok = half ? ok1 : ok0;
@@ -892,17 +963,22 @@ __global__ void __launch_bounds__(kSplitMaxThreads, 1)
             const float lt = half ? lt1 : lt0;
             const float mm = half ? cs.m1 : cs.m0;
             p.lse[static_cast<int64_t>(t) * p.lse_stride_t + static_cast<int64_t>(hq) * p.lse_stride_h] =
-                lt > 0.f ? (mm + fast_log2(lt)) * 0.69314718055994530942f : -INFINITY;
+                lt > 0.f || (kHole && lt != lt) ? (mm + fast_log2(lt)) * 0.69314718055994530942f : -INFINITY;
           }
         }
       } else {
         const int which = (seg_k0 == 0) ? 0 : 1;
-        const int64_t rowbase = (static_cast<int64_t>(2 * g + which) * HC + hh) * p.R_max;
+        int64_t rowbase = (static_cast<int64_t>(2 * g + which) * HC + hh) * p.R_max;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const bool ok = half ? ok1 : ok0;
           if (!ok) continue;
           const int rho = half ? rho1 : rho0;
+          if constexpr (WALK == Walk::kOwn) {
+            // a whole unit's row: its own place, behind the cut units' rows
+            if (complete)
+              rowbase = p.whole_row0 + static_cast<int64_t>(si.t0 + rho / G) * p.Hq + (cu.c * HC + hh) * G + rho % G - rho;
+          }
           float* orow = p.ws_o + (rowbase + rho) * D;
 #pragma unroll
           for (int J = 0; J < GG::NT; J += 2) {
