@@ -254,6 +254,43 @@ int paged_attn_decode_window(const pa_tensor_t* q, const pa_tensor_t* k_cache, c
                              const pa_tensor_t* lse, const pa_options_t* opts, pa_stream_t stream);
 
 /*
+ * paged_attn_decode_shared - decode attention for a batch whose sequences share prefixes:
+ * the result of paged_attn_decode on the same tensors, with the keys and values that the
+ * sequences of a group have in common read and attended once for all of the group's query
+ * tokens (ATOM scheduling guide, prefix caching: sequences whose block-table rows begin
+ * with the same pages; paged_attn_pages_fork makes such rows).
+ *
+ *   group_start_loc int32 [groups + 1] contiguous: group g is the sequences
+ *                   group_start_loc[g] .. group_start_loc[g + 1] - 1 (ascending, at most
+ *                   B groups; sequences of no group are attended alone).
+ *   shared_lens     int32 [groups] contiguous: the block-table rows of group g's sequences
+ *                   name the same pages for their first shared_lens[g] tokens.  Whole
+ *                   pages of these are shared; any value is valid as far as the rows agree,
+ *                   also one past a sequence's length.  The pages are read from the row of
+ *                   the group's first sequence that has query tokens.
+ *   The other arguments, layouts and errors as for paged_attn_decode, except that
+ *   - G * max_query_len <= 64 for every cache; max_blocks <= 2^27 - 64; T * Hq < 2^30;
+ *   - padded batches, rows without a key and sinks are as for paged_attn_decode_window;
+ *   - with a group_start_loc or query_start_loc that is not ascending within its range
+ *     nothing is shared, and bit 2 of the status word is set.
+ *   opts   as for paged_attn_decode_window, but that token scales and test_starve_cta are
+ *          refused too; num_ctas is the grid of the prefix's kernel as well.
+ * paged_attn_shared_workspace_size gives the workspace a call with this shape needs
+ * (opts may be NULL); paged_attn_shared_reserve grows the library-owned one to it.
+ */
+int paged_attn_decode_shared(const pa_tensor_t* q, const pa_tensor_t* k_cache, const pa_tensor_t* v_cache,
+                             const pa_tensor_t* block_tables, const pa_tensor_t* seq_lens,
+                             const pa_tensor_t* query_start_loc, int32_t max_query_len,
+                             const pa_tensor_t* group_start_loc, const pa_tensor_t* shared_lens, float scale,
+                             float k_scale, float v_scale, const pa_tensor_t* out, const pa_tensor_t* lse,
+                             const pa_options_t* opts, pa_stream_t stream);
+int paged_attn_shared_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                     int32_t head_dim, int32_t kv_dtype, int32_t max_query_len,
+                                     const pa_options_t* opts, size_t* bytes);
+int paged_attn_shared_reserve(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                              int32_t head_dim, int32_t kv_dtype, int32_t max_query_len);
+
+/*
  * paged_attn_cache_write - write new tokens' K and V rows into the paged caches
  * (ATOM model-operations guide, "KV cache operations": standard (bf16) and FP8
  * KV cache write; token_layout/slots.py: slot_mapping, "which KV slot a token is
@@ -591,7 +628,7 @@ int paged_attn_release(void);
 
 /* Read the device status word of the current device into *flags (bit 0: page id out of
  * range; bit 1: seq_len < query length; bit 2: query length outside [1, max_query_len]
- * or query_start_loc inconsistent; bit 3: a pipeline wait timed out; bit 4: a query value
+ * or query_start_loc (group_start_loc) inconsistent; bit 3: a pipeline wait timed out; bit 4: a query value
  * overflowed the f16 range on the fp8 path, or an MLA partial output did; bit 5: a page
  * operation refused an entry; bit 6: a rotary position out of range).  clear != 0 resets it to 0.  Synchronises
  * the device: a debugging aid, not for the hot path. */

@@ -74,6 +74,11 @@ _SIGNATURES = {
     "paged_attn_cache_read_q4": (ctypes.c_int, [_P] * 5 + [ctypes.c_float, ctypes.c_float, _P, _P, ctypes.c_void_p]),
     "paged_attn_decode_window": (ctypes.c_int, [_P] * 6 + [ctypes.c_int32] * 3 + [ctypes.c_float] * 3 +
                                  [_P, _P, ctypes.POINTER(PaOptions), ctypes.c_void_p]),
+    "paged_attn_decode_shared": (ctypes.c_int, [_P] * 6 + [ctypes.c_int32, _P, _P] + [ctypes.c_float] * 3 +
+                                 [_P, _P, ctypes.POINTER(PaOptions), ctypes.c_void_p]),
+    "paged_attn_shared_workspace_size": (ctypes.c_int, [ctypes.c_int32] * 7 + [ctypes.POINTER(PaOptions),
+                                                                               ctypes.POINTER(ctypes.c_size_t)]),
+    "paged_attn_shared_reserve": (ctypes.c_int, [ctypes.c_int32] * 7),
     "paged_attn_rope_cache_write": (ctypes.c_int, [_P] * 5 + [ctypes.c_char_p, ctypes.c_int32] + [_P] * 3 +
                                     [ctypes.c_float, ctypes.c_float, _P, _P, ctypes.c_void_p]),
     "paged_attn_decode_q4": (ctypes.c_int, [_P] * 8 + [ctypes.c_int32, ctypes.c_float, ctypes.c_float, ctypes.c_float,
@@ -638,6 +643,77 @@ def prepare_decode_window(q, k_cache, v_cache, block_tables, seq_lens, query_sta
     return call
 
 
+def paged_attn_shared_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, kv_dtype=PA_BF16,
+                                     max_query_len=1, options=None) -> int:
+    lib = load()
+    n = ctypes.c_size_t(0)
+    _check(lib, lib.paged_attn_shared_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, kv_dtype,
+                                                     max_query_len,
+                                                     ctypes.byref(options) if options is not None else None,
+                                                     ctypes.byref(n)))
+    return int(n.value)
+
+
+def paged_attn_shared_reserve(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, kv_dtype=PA_BF16,
+                              max_query_len=1):
+    lib = load()
+    _check(lib, lib.paged_attn_shared_reserve(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, kv_dtype,
+                                              max_query_len))
+
+
+def _shared_bytes(*shape, options=None):
+    return {"workspace_bytes": paged_attn_shared_workspace_size(*shape, options=options)}
+
+
+def _shared_call(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, max_query_len, group_start_loc,
+                 shared_lens, scale, k_scale, v_scale, out, lse, options, want_lse):
+    shape = lambda: (q.shape[0], block_tables.shape[0], q.shape[1], k_cache.shape[2], q.shape[2], _dtype_code(k_cache),
+                     int(max_query_len))
+    tensors, out, lse, scale, options, ws = _decode_hole_call(
+        q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, (group_start_loc, shared_lens), scale, out, lse,
+        options, want_lse, shape, _shared_bytes)
+    scalars = (ctypes.c_float(scale), ctypes.c_float(float(k_scale)), ctypes.c_float(float(v_scale)))
+    return tensors, ctypes.c_int32(int(max_query_len)), scalars, out, lse, options, ws
+
+
+def paged_attn_decode_shared(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, max_query_len,
+                             group_start_loc, shared_lens, scale=None, k_scale=1.0, v_scale=1.0, out=None, lse=None,
+                             stream=None, options=None, want_lse=True):
+    """Decode attention for a batch that shares prefixes (see include/paged_attn.h):
+    ``paged_attn_decode`` on the same tensors, with the pages that the sequences
+    group_start_loc[g] .. group_start_loc[g + 1] - 1 hold in common for their first
+    shared_lens[g] tokens attended once for all of them.  group_start_loc int32
+    [groups + 1], shared_lens int32 [groups].  Without a workspace in `options` the
+    call takes one from torch's allocator."""
+    lib = load()
+    with _allocating_on(stream):
+        tensors, runs, scalars, out, lse, options, ws = _shared_call(
+            q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, max_query_len, group_start_loc, shared_lens,
+            scale, k_scale, v_scale, out, lse, options, want_lse)
+    refs = [ctypes.byref(tensor_desc(t)) for t in tensors]
+    _check(lib, lib.paged_attn_decode_shared(*refs[:6], runs, *refs[6:], *scalars, ctypes.byref(tensor_desc(out)),
+                                             ctypes.byref(tensor_desc(lse)),
+                                             ctypes.byref(options) if options is not None else None,
+                                             _stream_handle(stream)))
+    return out, lse
+
+
+def prepare_decode_shared(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, max_query_len,
+                          group_start_loc, shared_lens, scale=None, k_scale=1.0, v_scale=1.0, out=None, lse=None,
+                          options=None, want_lse=True) -> "PreparedCall":
+    """``paged_attn_decode_shared`` with its arguments marshalled once (see
+    PreparedCall).  The prepared call owns its workspace (unless `options` has
+    one): use one prepared call for each stream that may run at the same time."""
+    tensors, runs, scalars, out, lse, options, ws = _shared_call(
+        q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, max_query_len, group_start_loc, shared_lens,
+        scale, k_scale, v_scale, out, lse, options, want_lse)
+    # the library takes max_query_len behind the first six tensors
+    call = PreparedCall(load().paged_attn_decode_shared, tensors, scalars, out, lse,
+                        options if options is not None else PaOptions(), after_six=(runs,))
+    call._workspace = ws
+    return call
+
+
 def _page_call(fn, caches, ints, stream):
     """A call of page tensors followed by integer tensors."""
     lib = load()
@@ -804,7 +880,7 @@ class PreparedCall:
     and returns (out, lse).  The tensors are kept referenced by the object;
     their addresses, shapes and strides must not change while it is used."""
 
-    def __init__(self, fn, tensors, scalars, out, lse, options, codes=None):
+    def __init__(self, fn, tensors, scalars, out, lse, options, codes=None, after_six=()):
         self._lib = load()
         self._fn = fn
         self._keep = (tensors, out, lse, options)
@@ -812,7 +888,8 @@ class PreparedCall:
         self._descs += [_new_desc(out), _new_desc(lse)]
         n_in = len(tensors)
         refs = [ctypes.byref(d) for d in self._descs]
-        head = refs[:n_in] + list(scalars) + refs[n_in:]
+        head = refs[:6] + list(after_six) + refs[6:n_in] if after_six else refs[:n_in]
+        head += list(scalars) + refs[n_in:]
         if options is not None:
             head.append(ctypes.byref(options))
         self._args = tuple(head)

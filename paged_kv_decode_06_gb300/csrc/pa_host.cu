@@ -18,6 +18,7 @@
 #include "paged_attn.h"
 #include "pa_host.h"
 #include "pa_kernels.h"
+#include "pa_shared.h"
 
 namespace {
 
@@ -114,6 +115,7 @@ int device_state(DeviceState** out, int* dev_out) {
     if ((e = pa::set_split_smem_limits_first(s.smem_optin)) != cudaSuccess ||
         (e = pa::set_split_smem_limits_own(s.smem_optin)) != cudaSuccess)
       return cuda_fail(e, "cudaFuncSetAttribute(split over a walk with a hole)");
+    if ((e = pa::set_shared_smem_limits()) != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(shared prefix)");
     pa::init_cache_write_occupancy();
     void* ptr = nullptr;
     if ((e = cudaGetSymbolAddress(&ptr, g_status_word)) != cudaSuccess)

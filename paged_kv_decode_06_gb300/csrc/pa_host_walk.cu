@@ -279,8 +279,208 @@ int decode_window(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
   return PA_OK;
 }
 
+// ------------------------------------------------------------ shared prefixes
+constexpr int kMinSharedPages = 1;
+constexpr int kMinSharedSteps = 1;
+
+struct SharedPlan {
+  HostSplitPlan split;
+  int grid;                      // of the prefix kernel
+  size_t skip, group_of, groups, totals, pre_ml, pre_o, unit, ml, o, bytes;
+};
+
+// Grids and the workspace of a call.
+int plan_shared(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int kv_dtype, int max_qlen,
+                const pa_options_t* opts, const HostDevice& dev, SharedPlan* out) {
+  SharedPlan p = {};
+  const int st = host_split_plan(static_cast<int>(B), static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(D),
+                                 kv_dtype, max_qlen, opts, 4, dev, &p.split);
+  if (st != PA_OK) return st;
+  p.grid = opts && opts->num_ctas > 0 ? opts->num_ctas : dev.num_sms;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at = up(at + bytes, 256);
+    return here;
+  };
+  p.skip = take(4 * static_cast<size_t>(B));
+  p.group_of = take(4 * static_cast<size_t>(B));
+  p.groups = take(sizeof(SharedGroup) * static_cast<size_t>(B));
+  p.totals = take(sizeof(SharedTotals));
+  p.unit = take(static_cast<size_t>(16) * B * p.split.sp.NC);
+  // cut units' rows, then a row for every (token, query head)
+  const size_t rows = p.split.rows + static_cast<size_t>(T) * Hq;
+  p.ml = take(rows * 8);
+  p.o = take(rows * D * 4);
+  // a pair's rows at most twice (a single tile's two slots), and 256 a CTA
+  const size_t pre = 2 * static_cast<size_t>(T) * Hq + static_cast<size_t>(kSharedPair) * p.grid;
+  p.pre_ml = take(pre * 8);
+  p.pre_o = take(pre * D * 4);
+  p.bytes = at;
+  *out = p;
+  return PA_OK;
+}
+
+int decode_shared(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* vc, const pa_tensor_t* bt,
+                  const pa_tensor_t* sl, const pa_tensor_t* qsl, int32_t max_qlen, const pa_tensor_t* gsl,
+                  const pa_tensor_t* lens, float scale, float k_scale, float v_scale, const pa_tensor_t* out,
+                  const pa_tensor_t* lse, const pa_options_t* opts, cudaStream_t stream) {
+  Shape s;
+  bool none;
+  int st = check_call(q, kc, vc, bt, sl, qsl, max_qlen, scale, k_scale, v_scale, out, lse, &s, &none);
+  if (st != PA_OK) return st;
+  const bool no_groups = lens != nullptr && lens->ndim == 1 && lens->shape[0] == 0;
+  if ((st = host_check_tensor(gsl, "group_start_loc", 1, none || no_groups)) ||
+      (st = host_check_tensor(lens, "shared_lens", 1, none || no_groups)))
+    return st;
+  if (none) return PA_OK;
+  const int64_t NG = lens->shape[0];
+  if (!no_groups) {
+    if (gsl->dtype != PA_I32 || lens->dtype != PA_I32)
+      return host_fail(PA_ERR_INVALID_ARG, "group_start_loc and shared_lens must be int32");
+    if (gsl->shape[0] != NG + 1 || gsl->stride[0] != 1 || (NG > 1 && lens->stride[0] != 1))
+      return host_fail(PA_ERR_INVALID_ARG, "group_start_loc needs one entry more than shared_lens, both contiguous");
+  }
+  if (NG > s.B)
+    return host_fail(PA_ERR_UNSUPPORTED, "%lld groups for %lld sequences", ll(NG), ll(s.B));
+  if (s.T * s.Hq >= (int64_t(1) << 30)) return host_fail(PA_ERR_UNSUPPORTED, "tensor extents too large");
+  if ((st = check_options(opts, s.Hkv, false)) != PA_OK) return st;
+
+  auto lock = host_lock();
+  HostDevice dev;
+  if ((st = host_device(&dev)) != PA_OK) return st;
+  SharedPlan pl;
+  if ((st = plan_shared(s.T, s.B, s.Hq, s.Hkv, s.D, kc->dtype, max_qlen, opts, dev, &pl)) != PA_OK) return st;
+  void* ws = nullptr;
+  if ((st = host_workspace(opts, pl.bytes, stream, "paged_attn_shared_reserve", &ws)) != PA_OK) return st;
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  CUtensorMap tk, tv, pk, pv;
+  const int D = static_cast<int>(s.D), Hkv = static_cast<int>(s.Hkv);
+  SplitParams& sp = pl.split.sp;
+  if ((st = host_cache_map(&tk, kc, s.esz, D, Hkv, sp.HC, s.NB)) != PA_OK) return st;
+  if ((st = host_cache_map(&tv, vc, s.esz, D, Hkv, sp.HC, s.NB)) != PA_OK) return st;
+  if ((st = host_cache_map(&pk, kc, s.esz, D, Hkv, 1, s.NB)) != PA_OK) return st;
+  if ((st = host_cache_map(&pv, vc, s.esz, D, Hkv, 1, s.NB)) != PA_OK) return st;
+  fill_split(&sp, s, q, bt, sl, qsl, scale, k_scale, v_scale, out, lse, opts, dev.status);
+  sp.ws_unit = reinterpret_cast<int4*>(wsb + pl.unit);
+  sp.ws_ml = reinterpret_cast<float2*>(wsb + pl.ml);
+  sp.ws_o = reinterpret_cast<float*>(wsb + pl.o);
+  sp.skip = reinterpret_cast<const int32_t*>(wsb + pl.skip);
+  sp.whole_row0 = static_cast<int64_t>(pl.split.rows);
+
+  SharedParams hp = {};
+  hp.q = sp.q;
+  hp.q_stride_t = sp.q_stride_t;
+  hp.block_tables = sp.block_tables;
+  hp.bt_stride = sp.bt_stride;
+  hp.seq_lens = sp.seq_lens;
+  hp.qsl = sp.qsl;
+  hp.group_start = static_cast<const int32_t*>(gsl->data);
+  hp.shared_lens = static_cast<const int32_t*>(lens->data);
+  hp.num_seqs = sp.num_seqs;
+  hp.num_tokens = sp.num_tokens;
+  hp.num_groups = static_cast<int32_t>(NG);
+  hp.max_qlen = max_qlen;
+  hp.max_blocks = sp.max_blocks;
+  hp.num_pages = sp.num_pages;
+  hp.G = sp.G;
+  hp.Hkv = sp.Hkv;
+  hp.min_pages = s.esz == 2 ? kMinSharedPages : INT32_MAX;
+  hp.min_steps = kMinSharedSteps;
+  hp.scale_log2 = sp.scale_log2;
+  hp.wait_ns = sp.wait_ns;
+  hp.err = dev.status;
+  hp.skip = reinterpret_cast<int32_t*>(wsb + pl.skip);
+  hp.seq_group = reinterpret_cast<int32_t*>(wsb + pl.group_of);
+  hp.groups = reinterpret_cast<SharedGroup*>(wsb + pl.groups);
+  hp.totals = reinterpret_cast<SharedTotals*>(wsb + pl.totals);
+  hp.ws_ml = reinterpret_cast<float2*>(wsb + pl.pre_ml);
+  hp.ws_o = reinterpret_cast<float*>(wsb + pl.pre_o);
+
+  MergeRowsParams mp = {};
+  fill_merge(&mp, sp, pl.split.grid);
+  mp.seq_group = hp.seq_group;
+  mp.groups = hp.groups;
+  mp.totals = hp.totals;
+  mp.pre_ml = hp.ws_ml;
+  mp.pre_o = hp.ws_o;
+  mp.pre_grid = pl.grid;
+  mp.pre_min_steps = hp.min_steps;
+
+  Events ev;
+  if ((st = events_of(opts, stream, &ev)) != PA_OK) return st;
+  const bool pdl = !(opts && opts->disable_pdl);
+  cudaError_t e;
+  if ((st = record(ev.start, ev, stream)) != PA_OK) return st;
+  if ((e = launch_shared_plan(hp, pdl && !ev.start, stream)) != cudaSuccess)
+    return host_cuda_fail(e, "shared prefix plan kernel launch");
+  if (s.esz == 2 && (e = launch_shared_prefix(D, pk, pv, hp, pl.grid, pdl, stream)) != cudaSuccess)
+    return host_cuda_fail(e, "shared prefix kernel launch");
+  if ((e = launch_split_own(D, s.esz == 1, tk, tv, sp, pl.split.grid, pl.split.threads, pl.split.smem, pdl, stream)) !=
+      cudaSuccess)
+    return host_cuda_fail(e, "split kernel launch");
+  if ((st = record(ev.stop, ev, stream)) != PA_OK) return st;
+  const int units = static_cast<int>(s.B) * sp.NC;
+  const bool wide = pl.split.grid >= 4 * units;
+  if ((e = launch_merge_rows(D, true, mp, units, sp.HC * sp.R_max, wide, pdl && !ev.stop, stream)) != cudaSuccess)
+    return host_cuda_fail(e, "merge kernel launch");
+  return PA_OK;
+}
+
+int shared_plan_for(int32_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t kv_dtype, int32_t max_qlen,
+                    const pa_options_t* o, SharedPlan* pl) {
+  int st;
+  if (B < 1 || B > kMaxSeqsHost)
+    return host_fail(PA_ERR_UNSUPPORTED, "num_seqs %d outside [1, %d]", B, kMaxSeqsHost);
+  if (T < 0 || static_cast<int64_t>(T) * std::max(Hq, 0) >= (int64_t(1) << 30))
+    return host_fail(PA_ERR_UNSUPPORTED, "num_tokens %d x num_q_heads %d outside [0, 2^30)", T, Hq);
+  if ((st = check_rows(Hq, Hkv, max_qlen)) != PA_OK || (st = check_options(o, Hkv, false)) != PA_OK) return st;
+  HostDevice dev;
+  if ((st = host_device(&dev)) != PA_OK) return st;
+  return plan_shared(T, B, Hq, Hkv, D, kv_dtype, max_qlen, o, dev, pl);
+}
+
 }  // namespace
 }  // namespace pa
+
+extern "C" int paged_attn_decode_shared(const pa_tensor_t* q, const pa_tensor_t* k_cache, const pa_tensor_t* v_cache,
+                                        const pa_tensor_t* block_tables, const pa_tensor_t* seq_lens,
+                                        const pa_tensor_t* query_start_loc, int32_t max_query_len,
+                                        const pa_tensor_t* group_start_loc, const pa_tensor_t* shared_lens, float scale,
+                                        float k_scale, float v_scale, const pa_tensor_t* out, const pa_tensor_t* lse,
+                                        const pa_options_t* opts, pa_stream_t stream) {
+  return pa::host_entry([&] {
+    return pa::decode_shared(q, k_cache, v_cache, block_tables, seq_lens, query_start_loc, max_query_len,
+                             group_start_loc, shared_lens, scale, k_scale, v_scale, out, lse, opts,
+                             reinterpret_cast<cudaStream_t>(stream));
+  });
+}
+
+extern "C" int paged_attn_shared_workspace_size(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                                                int32_t num_kv_heads, int32_t head_dim, int32_t kv_dtype,
+                                                int32_t max_query_len, const pa_options_t* opts, size_t* bytes) {
+  return pa::host_entry([&] {
+    if (bytes == nullptr) return pa::host_fail(PA_ERR_INVALID_ARG, "bytes pointer is NULL");
+    auto lock = pa::host_lock();
+    pa::SharedPlan pl;
+    const int st = pa::shared_plan_for(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, kv_dtype,
+                                       max_query_len, opts, &pl);
+    if (st == PA_OK) *bytes = pl.bytes;
+    return st;
+  });
+}
+
+extern "C" int paged_attn_shared_reserve(int32_t num_tokens, int32_t num_seqs, int32_t num_q_heads,
+                                         int32_t num_kv_heads, int32_t head_dim, int32_t kv_dtype,
+                                         int32_t max_query_len) {
+  return pa::host_entry([&] {
+    auto lock = pa::host_lock();
+    pa::SharedPlan pl;
+    const int st = pa::shared_plan_for(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, kv_dtype,
+                                       max_query_len, nullptr, &pl);
+    return st != PA_OK ? st : pa::host_reserve(pl.bytes);
+  });
+}
 
 extern "C" int paged_attn_decode_window(const pa_tensor_t* q, const pa_tensor_t* k_cache, const pa_tensor_t* v_cache,
                                         const pa_tensor_t* block_tables, const pa_tensor_t* seq_lens,

@@ -13,6 +13,8 @@
 // meet: a next pair starts at least its predecessor's rows, a next CTA 256 rows further.
 #pragma once
 
+#include <cuda.h>
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace pa {
@@ -54,5 +56,35 @@ __host__ __device__ inline int shared_ctas(int64_t steps, int grid, int min_step
 __host__ __device__ inline int shared_cta_of(int64_t x, int64_t steps, int ng) {
   return static_cast<int>(((x + 1) * ng - 1) / steps);
 }
+
+struct SharedParams {
+  const uint16_t* q;          // bf16 [T, Hq, D], head stride D
+  int64_t q_stride_t;
+  const int32_t* block_tables;
+  int64_t bt_stride;
+  const int32_t* seq_lens;
+  const int32_t* qsl;         // [B + 1] or nullptr
+  const int32_t* group_start; // [groups + 1]
+  const int32_t* shared_lens; // [groups]
+  int32_t num_seqs, num_tokens, num_groups, max_qlen, max_blocks, num_pages, G, Hkv;
+  int32_t min_pages;          // fewer shared pages are left to the sequences
+  int32_t min_steps;          // steps a CTA at least
+  float scale_log2;
+  uint64_t wait_ns;
+  uint32_t* err;
+  // workspace: written by the plan kernel ...
+  int32_t* skip;              // [B] pages that the group attends for the sequence
+  int32_t* seq_group;         // [B] its group, -1: none
+  SharedGroup* groups;
+  SharedTotals* totals;
+  // ... and by the prefix kernel: partial rows
+  float2* ws_ml;
+  float* ws_o;
+};
+
+cudaError_t launch_shared_plan(const SharedParams& p, bool pdl, cudaStream_t stream);
+cudaError_t launch_shared_prefix(int head_dim, const CUtensorMap& tk, const CUtensorMap& tv, const SharedParams& p,
+                                 int grid, bool pdl, cudaStream_t stream);
+cudaError_t set_shared_smem_limits();
 
 }  // namespace pa

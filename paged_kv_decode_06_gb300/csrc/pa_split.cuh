@@ -663,7 +663,7 @@ __device__ __forceinline__ void consume_pages(ConsumerState<D, FP8>& cs, const u
 // windowless kernels carry none of its code).  TOKS: fp8 caches with per-token
 // scales, staged by the producer behind each page's K and V tiles.  WALK: which pages;
 // with kFirst and kOwn a sequence may have no query tokens, NaN stays NaN, and with kOwn
-// every unit leaves partials (one that a CTA holds whole in the row's place of ws_whole).
+// every unit leaves partials (one that a CTA holds whole in the rows' own places).
 template <int D, bool FP8, bool WINDOW, bool TOKS = false, Walk WALK = Walk::kAll>
 __global__ void __launch_bounds__(kSplitMaxThreads, 1)
     pa_split_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,

@@ -37,7 +37,15 @@ def _window(lib, a):
                                         ctypes.byref(a["opts"]) if a["opts"] is not None else None, None)
 
 
-CALLS = [_window]
+def _shared(lib, a):
+    gsl, lens = a.get("gsl", torch.tensor([0, 2], dtype=i32)), a.get("shared", torch.tensor([16], dtype=i32))
+    r = [ctypes.byref(binding.tensor_desc(t)) for t in
+         [a[n] for n in ("q", "k", "v", "bt", "sl", "qsl")] + [gsl, lens, a["out"], a["lse"]]]
+    return lib.paged_attn_decode_shared(*r[:6], a["runs"], r[6], r[7], a["scale"], 1.0, 1.0, *r[8:],
+                                        ctypes.byref(a["opts"]) if a["opts"] is not None else None, None)
+
+
+CALLS = [_window, _shared]
 
 
 @pytest.mark.parametrize("call", CALLS)
@@ -104,3 +112,31 @@ def test_window_token_scales(lib):
         assert _window(lib, dict(_args(kv=torch.uint8), opts=o)) == BAD
     o = binding.make_options(k_token_scales=good)
     assert _window(lib, dict(_args(kv=torch.uint8), opts=o)) == BAD
+
+
+@pytest.mark.parametrize("gsl,shared,want", [
+    (torch.tensor([0, 1, 3], dtype=i32), torch.tensor([16], dtype=i32), BAD),
+    (torch.tensor([0, 1]), torch.tensor([16], dtype=i32), BAD), (torch.tensor([0, 1], dtype=i32), torch.tensor([16.0]), BAD),
+    (torch.tensor([0, 9, 1], dtype=i32)[::2], torch.tensor([16], dtype=i32), BAD),
+    (torch.tensor([0, 1, 2], dtype=i32), torch.tensor([16, 0, 16, 0], dtype=i32)[::2], BAD),
+    (torch.zeros(5, dtype=i32), torch.zeros(4, dtype=i32), UNS), (None, torch.tensor([16], dtype=i32), BAD),
+    (torch.tensor([0, 1], dtype=i32), None, BAD),
+    (torch.tensor([0], dtype=i32), torch.zeros(0, dtype=i32), binding.PA_ERR_CUDA)])
+def test_shared_lists(lib, gsl, shared, want):
+    assert _shared(lib, dict(_args(), gsl=gsl, shared=shared)) == want
+
+
+def test_shared_options(lib):
+    z = torch.zeros(10, 2, 16)
+    o = binding.make_options(k_token_scales=z, v_token_scales=z)
+    assert _shared(lib, dict(_args(kv=torch.uint8), opts=o)) == UNS
+    assert _shared(lib, dict(_args(), opts=binding.make_options(test_starve_cta=1))) == UNS
+
+
+def test_shared_workspace_shapes(lib):
+    for shape, want in (((4, 0, 8, 2, 128), UNS), ((1 << 27, 4, 8, 2, 128), UNS), ((-1, 4, 8, 2, 128), UNS),
+                        ((4, 4, 9, 2, 128), BAD), ((4, 4, 8, 2, 128, binding.PA_BF16, 0), BAD),
+                        ((4, 4, 8, 2, 128, binding.PA_BF16, 17), UNS)):
+        with pytest.raises(binding.PagedAttnError) as e:
+            binding.paged_attn_shared_workspace_size(*shape)
+        assert e.value.status == want, shape
