@@ -327,9 +327,9 @@ int check_tensor(const pa_tensor_t* t, const char* name, int ndim, bool allow_nu
 // holds g_mu.
 struct MapKey {
   const void* ptr;
-  uint64_t dims[4];
-  uint64_t strides[3];
-  uint32_t box[4];
+  uint64_t dims[5];
+  uint64_t strides[4];
+  uint32_t box[5];
   int32_t dtype, rank, swizzle;
 };
 struct MapMemo {
@@ -346,7 +346,7 @@ CUresult encode_tiled(CUtensorMap* map, CUtensorMapDataType dtype, int rank, voi
   MapKey k;
   std::memset(&k, 0, sizeof(k));
   k.ptr = ptr;
-  for (int d = 0; d < rank && d < 4; ++d) {
+  for (int d = 0; d < rank && d < 5; ++d) {
     k.dims[d] = dims[d];
     k.box[d] = box[d];
     if (d + 1 < rank) k.strides[d] = strides[d];
@@ -359,11 +359,11 @@ CUresult encode_tiled(CUtensorMap* map, CUtensorMapDataType dtype, int rank, voi
       *map = g_map_memo[i].map;
       return CUDA_SUCCESS;
     }
-  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  const cuuint32_t estr[5] = {1u, 1u, 1u, 1u, 1u};
   const CUresult r = g_encode(map, dtype, static_cast<cuuint32_t>(rank), ptr, dims, strides, box, estr,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r == CUDA_SUCCESS && rank <= 4) {
+  if (r == CUDA_SUCCESS && rank <= 5) {
     MapMemo& m = g_map_memo[g_map_next];
     g_map_next = (g_map_next + 1) % kMapMemo;
     m.used = true;
@@ -388,6 +388,33 @@ int encode_cache_map(CUtensorMap* map, const pa_tensor_t* t, int esz, int D, int
   const CUresult r = encode_tiled(map, esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                                   t->data, dims, strides, box,
                                   rb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+  if (r != CUDA_SUCCESS) return fail(PA_ERR_INVALID_ARG, "cuTensorMapEncodeTiled failed (%d) for a KV cache", r);
+  return PA_OK;
+}
+
+// TMA map of the shared prefix's loads of a page and head.  fp8: rows of D codes, not
+// swizzled.  bf16: rows of 64 features (128-byte swizzle) by eight slots, then feature
+// half, then slot / 8 (dimension order d, slot % 8, 64-feature block of any head, slot / 8,
+// page), so that a page is one box; heads that are not contiguous (*split): (d, slot, head,
+// page) and boxes of 64 features x 8 slots.
+int encode_prefix_map(CUtensorMap* map, const pa_tensor_t* t, int esz, int D, int Hkv, int64_t NB, bool* split) {
+  const cuuint64_t slot = static_cast<cuuint64_t>(t->stride[1]) * esz, page = static_cast<cuuint64_t>(t->stride[0]) * esz;
+  const cuuint64_t head = static_cast<cuuint64_t>(t->stride[2]) * esz;
+  const cuuint64_t nb = static_cast<cuuint64_t>(NB);
+  CUresult r;
+  *split = esz == 2 && D == 128 && Hkv > 1 && t->stride[2] != D;
+  if (esz == 2 && D == 128 && !*split) {
+    cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(2 * Hkv), 2, nb};
+    cuuint64_t strides[4] = {slot, 128, 8 * slot, page};
+    cuuint32_t box[5] = {64, 8, 2, 2, 1};
+    r = encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, t->data, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+  } else {
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(kPageSize), static_cast<cuuint64_t>(Hkv), nb};
+    cuuint64_t strides[3] = {slot, head, page};
+    cuuint32_t box[4] = {esz == 2 ? 64u : static_cast<cuuint32_t>(D), *split ? 8u : static_cast<cuuint32_t>(kPageSize), 1u, 1u};
+    r = encode_tiled(map, esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t->data, dims,
+                     strides, box, esz == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
+  }
   if (r != CUDA_SUCCESS) return fail(PA_ERR_INVALID_ARG, "cuTensorMapEncodeTiled failed (%d) for a KV cache", r);
   return PA_OK;
 }
@@ -1082,6 +1109,9 @@ int host_split_plan(int B, int Hq, int Hkv, int D, int kv_dtype, int max_qlen, c
 }
 int host_cache_map(CUtensorMap* map, const pa_tensor_t* t, int esz, int D, int Hkv, int HC, int64_t NB) {
   return encode_cache_map(map, t, esz, D, Hkv, HC, NB);
+}
+int host_prefix_map(CUtensorMap* map, const pa_tensor_t* t, int esz, int D, int Hkv, int64_t NB, bool* split) {
+  return encode_prefix_map(map, t, esz, D, Hkv, NB, split);
 }
 int host_reserve(size_t bytes) {
   DeviceState* ds = nullptr;

@@ -359,8 +359,11 @@ int decode_shared(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
   SplitParams& sp = pl.split.sp;
   if ((st = host_cache_map(&tk, kc, s.esz, D, Hkv, sp.HC, s.NB)) != PA_OK) return st;
   if ((st = host_cache_map(&tv, vc, s.esz, D, Hkv, sp.HC, s.NB)) != PA_OK) return st;
-  if ((st = host_cache_map(&pk, kc, s.esz, D, Hkv, 1, s.NB)) != PA_OK) return st;
-  if ((st = host_cache_map(&pv, vc, s.esz, D, Hkv, 1, s.NB)) != PA_OK) return st;
+  bool split_k, split_v;
+  if ((st = host_prefix_map(&pk, kc, s.esz, D, Hkv, s.NB, &split_k)) != PA_OK) return st;
+  if ((st = host_prefix_map(&pv, vc, s.esz, D, Hkv, s.NB, &split_v)) != PA_OK) return st;
+  if (split_k != split_v)
+    return host_fail(PA_ERR_UNSUPPORTED, "k_cache and v_cache need heads of the same contiguity");
   fill_split(&sp, s, q, bt, sl, qsl, scale, k_scale, v_scale, out, lse, opts, dev.status);
   sp.ws_unit = reinterpret_cast<int4*>(wsb + pl.unit);
   sp.ws_ml = reinterpret_cast<float2*>(wsb + pl.ml);
@@ -385,7 +388,8 @@ int decode_shared(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
   hp.num_pages = sp.num_pages;
   hp.G = sp.G;
   hp.Hkv = sp.Hkv;
-  hp.min_pages = s.esz == 2 ? kMinSharedPages : INT32_MAX;
+  hp.min_pages = kMinSharedPages;
+  hp.split_boxes = split_k;
   hp.min_steps = kMinSharedSteps;
   hp.scale_log2 = sp.scale_log2;
   hp.wait_ns = sp.wait_ns;
@@ -414,7 +418,7 @@ int decode_shared(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
   if ((st = record(ev.start, ev, stream)) != PA_OK) return st;
   if ((e = launch_shared_plan(hp, pdl && !ev.start, stream)) != cudaSuccess)
     return host_cuda_fail(e, "shared prefix plan kernel launch");
-  if (s.esz == 2 && (e = launch_shared_prefix(D, pk, pv, hp, pl.grid, pdl, stream)) != cudaSuccess)
+  if ((e = launch_shared_prefix(D, s.esz == 1, pk, pv, hp, pl.grid, pdl, stream)) != cudaSuccess)
     return host_cuda_fail(e, "shared prefix kernel launch");
   if ((e = launch_split_own(D, s.esz == 1, tk, tv, sp, pl.split.grid, pl.split.threads, pl.split.smem, pdl, stream)) !=
       cudaSuccess)

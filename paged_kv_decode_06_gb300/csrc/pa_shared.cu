@@ -8,17 +8,16 @@
 //
 // Attention (tcgen05): with R rows a head the products cost 4 R D flops a key against
 // 4 D bytes (bf16), so from about 280 rows on the tensor cores bound it, below that
-// memory does; a softmax thread a row has 128 exponentials a block, half of what the two
-// products of the block take.  A CTA holds two 128-row tiles ("slots") of query rows in
+// memory does.  A CTA holds two 128-row tiles ("slots") of query rows in
 // shared memory and S / P (128 columns) and O (128 columns) of each in tensor memory, all
 // 512 columns; blocks of 128 keys, K and V apart, pass through a ring.  One thread
 // issues P V of slot 0, Q K^T of slot 0's next block, then the same for slot 1, so that
 // one slot's softmax runs while the tensor cores work for the other.
 //
-// Warps: 0 issues the products and owns tensor memory, 1-3 load pages (a warp's TMA issue
-// is serial, about 90 ns a 2 KB box, and a block has 32 boxes), 4-7 and 8-11 are the
-// slots' softmax, thread = query row = tensor-memory lane.  P overwrites its S in
-// 16 bits; O is rescaled only where the running maximum grew by more than 2^8.
+// Warps: 0 issues the products and owns tensor memory; 1 and 2 load pages; of an fp8
+// cache 3 to 6 convert codes to f16 (exact); the last sixteen are the slots' softmax, two
+// threads a row, lane = row of tensor memory.  P overwrites its S in 16 bits (f16 beside
+// an fp8 cache); O is rescaled only where the running maximum grew by more than 2^8.
 //
 // Order in the tensor pipe: one thread issues every product, and they run in that order,
 // so S of a slot's next block may overwrite the P that the slot's P V before it reads.
@@ -30,6 +29,7 @@
 #include "pa_device.cuh"
 #include "pa_kernels.h"
 #include "pa_pack.cuh"
+#include "pa_quant.cuh"
 #include "pa_shared.h"
 #include "pa_split_tc.cuh"
 
@@ -163,21 +163,40 @@ __global__ void __launch_bounds__(kPlanThreads) pa_shared_plan_kernel(const Shar
 }
 
 // ------------------------------------------------------------- prefix kernel
-constexpr int kThreads = 384;
-constexpr int kLoaders = 3;               // warps 1 .. 3
-constexpr int kSoftmaxWarp0 = 4;          // two warpgroups, a slot each
+constexpr int kLoaders = 2;               // warps 1, 2
+constexpr int kConverters = 4;            // fp8 caches: warps 3 .. 6
+constexpr int kSoftmaxWarps = 16;         // a slot's eight: two threads a row, 64 columns of S each
 constexpr int kBlockPages = kSharedBlockPages;
 constexpr int kKeys = 16 * kBlockPages;
-constexpr uint32_t kHalf = kKeys * 128u;  // 64 features (128 bytes) of a block's keys, or of a tile's rows
 constexpr uint32_t kCols = 512;
-constexpr uint32_t kColS = 0;             // + 128 slot: S, its P over the first 64 columns
-constexpr uint32_t kColO = 256;           // + 128 slot
+constexpr uint32_t kColS = 0;             // + 128 slot: S; P of columns 0 .. 63 over the first 32 of them,
+constexpr uint32_t kColO = 256;           //   of 64 .. 127 over the 32 from 64 on.  O: + 128 slot
 
+// Rows of 64 features (128 bytes, 128-byte swizzle) in groups of eight: a block's key rows
+// r = 16 page + slot, or a tile's query rows, at group r / 8, then feature half, then r % 8.
+// A page of a block is then one run of 16 D elements, one TMA box (128 features: of five
+// dimensions), and a product's operand has groups NH KB apart.
 template <int D>
+struct Geo2 {
+  static constexpr int NH = D / 64;
+  static constexpr uint32_t GROUP = NH * 1024u;
+  static constexpr uint32_t PAGE = 2 * GROUP;
+  static constexpr uint32_t TILE = kBlockPages * PAGE;   // bytes of a query tile, a K or a V block
+};
+
+template <int D, bool FP8>
 struct PrefixGeo {
-  static constexpr uint32_t TILE = (D / 64) * kHalf;     // bytes of a query tile, a K or a V block
-  static constexpr int RING = D == 128 ? 5 : 10;
-  static constexpr uint32_t SMEM = 1024 + 2 * TILE + RING * TILE + 1024;
+  static constexpr uint32_t TILE = Geo2<D>::TILE;
+  static constexpr uint32_t RAW = kKeys * D;             // fp8: a block's codes
+  static constexpr int RING = D == 128 ? 4 : 8;
+  static constexpr int RAWS = FP8 ? (D == 128 ? 2 : 6) : 0;
+  static constexpr int SOFT0 = 1 + kLoaders + (FP8 ? kConverters : 0);
+  static constexpr int THREADS = 32 * (SOFT0 + kSoftmaxWarps);
+  static constexpr uint32_t OFF_RING = 2 * TILE;
+  static constexpr uint32_t OFF_RAW = OFF_RING + RING * TILE;
+  static constexpr uint32_t OFF_X = OFF_RAW + RAWS * RAW;           // [slot][half][128] floats
+  static constexpr uint32_t OFF_BAR = OFF_X + 2048;
+  static constexpr uint32_t SMEM = OFF_BAR + 512;
 };
 
 // A piece: consecutive steps of one (group, head, pair) in this CTA.
@@ -244,8 +263,6 @@ __device__ __forceinline__ void after_wait(uint32_t (&r)[N]) {
 #pragma unroll
   for (int e = 0; e < N; ++e) asm volatile("" : "+r"(r[e]));
 }
-__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) { after_wait<16>(r); }
-__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) { after_wait<32>(r); }
 
 // Block of `slot` in step s of a piece, or -1.
 __device__ __forceinline__ int block_of(const Piece& c, const SharedGroup& sg, int s, int slot) {
@@ -253,41 +270,56 @@ __device__ __forceinline__ int block_of(const Piece& c, const SharedGroup& sg, i
   return b < sg.blocks ? b : -1;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+// kind::f16 with f16 A and B and an fp32 accumulator.
+__device__ __forceinline__ uint32_t idesc_f16(int M, int N, bool b_mn_major) {
+  return umma_idesc_bf16(M, N, b_mn_major) & ~((1u << 7) | (1u << 10));
+}
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
     pa_shared_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                             const SharedParams p) {
-  using GG = PrefixGeo<D>;
+  using GG = PrefixGeo<D, FP8>;
   constexpr int NH = D / 64;
-  constexpr int RING = GG::RING;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ uint32_t s_tmem;
-  const uint32_t raw = smem_addr(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* const gbase = smem_raw + (base - raw);
-  const uint32_t ring0 = base + 2 * GG::TILE;
-  const uint32_t bar0 = ring0 + RING * GG::TILE;
-  auto full_bar = [&](int e) { return bar0 + 8u * e; };
+  constexpr int RING = GG::RING, RAWS = GG::RAWS;
+  constexpr uint32_t TILE = GG::TILE, PAGE = Geo2<D>::PAGE, GROUP = Geo2<D>::GROUP;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* const gbase = smem_raw;
+  const uint32_t base = smem_addr(smem_raw);
+  const uint32_t ring0 = base + GG::OFF_RING, raw0 = base + GG::OFF_RAW;
+  float* const xchg = reinterpret_cast<float*>(gbase + GG::OFF_X);
+  const uint32_t bar0 = base + GG::OFF_BAR;
+  auto full_bar = [&](int e) { return bar0 + 8u * e; };             // ring entries: K or V of a block
   auto empty_bar = [&](int e) { return bar0 + 8u * (RING + e); };
   const uint32_t xb = bar0 + 8u * (2 * RING);
   auto sfull_bar = [&](int slot) { return xb + 8u * slot; };
   auto pfull_bar = [&](int slot) { return xb + 8u * (2 + slot); };
   auto qfull_bar = [&](int slot) { return xb + 8u * (4 + slot); };
   auto odone_bar = [&](int slot) { return xb + 8u * (6 + slot); };
-  const uint32_t drain_bar = xb + 8u * 8;
+  auto pair_bar = [&](int slot, int quarter) { return xb + 8u * (8 + 4 * slot + quarter); };
+  const uint32_t drain_bar = xb + 8u * 16;
+  auto rawfull_bar = [&](int e) { return xb + 8u * (17 + e); };     // fp8: code blocks
+  auto rawempty_bar = [&](int e) { return xb + 8u * (17 + RAWS + e); };
+  static_assert(2 * RING + 17 + 2 * RAWS + 1 <= 64, "barriers");
+  uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(gbase + GG::OFF_BAR + 504);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     prefetch_tensormap(&tmap_k);
     prefetch_tensormap(&tmap_v);
     for (int e = 0; e < RING; ++e) {
-      mbar_init(full_bar(e), kLoaders);
+      mbar_init(full_bar(e), FP8 ? kConverters : kLoaders);
       mbar_init(empty_bar(e), 1);
+    }
+    for (int e = 0; e < RAWS; ++e) {
+      mbar_init(rawfull_bar(e), kLoaders);
+      mbar_init(rawempty_bar(e), kConverters);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(sfull_bar(s), 1);
-      mbar_init(pfull_bar(s), 4);
-      mbar_init(qfull_bar(s), 4);
+      mbar_init(pfull_bar(s), kSoftmaxWarps / 2);
+      mbar_init(qfull_bar(s), kSoftmaxWarps / 2);
       mbar_init(odone_bar(s), 1);
+      for (int k = 0; k < 4; ++k) mbar_init(pair_bar(s, k), 2);
     }
     mbar_init(drain_bar, 1);
     fence_mbar_init();
@@ -300,17 +332,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (cta >= ng) return;
   const int64_t from = cta * X / ng, to = (cta + 1) * X / ng;
   if (from >= to) return;
-  if (warp == 0) tmem_alloc(smem_addr(&s_tmem), kCols);
+  if ((base & 1023u) != 0) {              // the swizzle and the operands need the alignment declared above
+    if (tid == 0) atomicOr(p.err, kErrTimeout);
+    return;
+  }
+  if (warp == 0) tmem_alloc(smem_addr(s_tmem), kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = warp_uniform(s_tmem);
+  const uint32_t tbase = warp_uniform(*s_tmem);
   PieceWalker wk;
   wk.start(p, from, to);
 
-  if (warp >= 1 && warp < kSoftmaxWarp0) {
+  if (warp >= 1 && warp <= kLoaders) {
     // =============================== loaders =================================
     const int me = warp - 1;
+    constexpr int SLOTS = FP8 ? RAWS : RING;
     int e = 0;
     uint32_t round = 0;
     bool ok = true;
@@ -325,41 +362,104 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool is_v = k >= nb;
           const int b = b0 + (is_v ? k - nb : k);
           const int np = min(kBlockPages, sg.pages - b * kBlockPages);
-          // box x = (page, half): dealt over the three warps, a lane each
-          const int x = kLoaders * lane + me, pg = x / NH, h = x - pg * NH;
+          // boxes dealt over the warps, a lane each: a page, or (split boxes: heads that
+          // are not contiguous) eight slots and 64 features of one
+          const int per = !FP8 && NH == 2 && p.split_boxes ? 4 : 1;
+          const int x = kLoaders * lane + me, pg = x / per, part = x - pg * per;
           const int page = pg < np ? row[b * kBlockPages + pg] : 0;
-          if (round > 0 && !warp_wait(empty_bar(e), (round - 1) & 1u, p.wait_ns)) {
+          if (round > 0 && !warp_wait(FP8 ? rawempty_bar(e) : empty_bar(e), (round - 1) & 1u, p.wait_ns)) {
             if (lane == 0) atomicOr(p.err, kErrTimeout);
             ok = false;
             break;
           }
-          const int mine = np * NH > me ? (np * NH - me + kLoaders - 1) / kLoaders : 0;
-          if (lane == 0) mbar_arrive_expect_tx(full_bar(e), static_cast<uint32_t>(mine) * kTcBox);
+          const uint32_t bytes = (FP8 ? 16u * D : PAGE) / per;
+          const int mine = np * per > me ? (np * per - me + kLoaders - 1) / kLoaders : 0;
+          const uint32_t full = FP8 ? rawfull_bar(e) : full_bar(e);
+          if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(mine) * bytes);
           __syncwarp();
           if (pg < np) {
-            if ((page < 0 || page >= p.num_pages) && h == 0) atomicOr(p.err, kErrPageRange);
+            if ((page < 0 || page >= p.num_pages) && part == 0) atomicOr(p.err, kErrPageRange);
             // (a page id out of range reads as zeros: TMA fills outside the tensor)
-            tma_load_4d(ring0 + static_cast<uint32_t>(e) * GG::TILE + h * kHalf + static_cast<uint32_t>(pg) * kTcBox,
-                        is_v ? &tmap_v : &tmap_k, h * 64, 0, c.head, page, full_bar(e));
+            const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
+            if constexpr (FP8) {
+              tma_load_4d(raw0 + static_cast<uint32_t>(e) * GG::RAW + static_cast<uint32_t>(pg) * bytes, map, 0, 0,
+                          c.head, page, full);
+            } else {
+              const uint32_t dst = ring0 + static_cast<uint32_t>(e) * TILE + static_cast<uint32_t>(pg) * PAGE;
+              if (NH == 1)
+                tma_load_4d(dst, map, 0, 0, c.head, page, full);
+              else if (per == 1)
+                tma_load_5d(dst, map, 0, 0, NH * c.head, 0, page, full);
+              else                                          // part = 2 (slot / 8) + half
+                tma_load_4d(dst + part * 1024u, map, 64 * (part & 1), 8 * (part >> 1), c.head, page, full);
+            }
           }
-          if (++e == RING) {
+          if (++e == SLOTS) {
             e = 0;
             ++round;
           }
         }
       }
     }
+  } else if (FP8 && warp > kLoaders && warp < GG::SOFT0) {
+    // ============================== converters ===============================
+    // e4m3 codes to f16 (exact), 16 a thread and turn, into the products' layout.  The
+    // two stores of a thread are swapped between the halves of a row: no bank conflict.
+    const int ct = tid - 32 * (1 + kLoaders);
+    constexpr int CPR = D / 16;                              // 16-code chunks a row
+    uint32_t n = 0;
+    bool ok = true;
+    while (ok && wk.more()) {
+      const Piece c = wk.next(p);
+      for (int s = c.s0; ok && s < c.s1; ++s) {
+        const int b0 = block_of(c, wk.sg, s, 0), nb = c.single && block_of(c, wk.sg, s, 1) >= 0 ? 2 : 1;
+        for (int k = 0; k < 2 * nb; ++k, ++n) {
+          const int np = min(kBlockPages, wk.sg.pages - (b0 + (k >= nb ? k - nb : k)) * kBlockPages);
+          constexpr int kRaws = RAWS > 0 ? RAWS : 1;
+          const int er = static_cast<int>(n % kRaws), e = static_cast<int>(n % RING);
+          if (!warp_wait(rawfull_bar(er), (n / kRaws) & 1u, p.wait_ns) ||
+              (n >= RING && !warp_wait(empty_bar(e), (n / RING - 1) & 1u, p.wait_ns))) {
+            if (lane == 0) atomicOr(p.err, kErrTimeout);
+            ok = false;
+            break;
+          }
+          const uint8_t* src = gbase + GG::OFF_RAW + er * GG::RAW;
+          uint8_t* dst = gbase + GG::OFF_RING + e * TILE;
+#pragma unroll 4
+          for (int x = ct; x < 16 * np * CPR; x += 32 * kConverters) {
+            const int r = x / CPR, cc = x % CPR;
+            const uint4 v = *reinterpret_cast<const uint4*>(src + 16 * x);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint4 h[2];
+            h[0] = make_uint4(e4m3x2_to_f16x2(w[0]), e4m3x2_to_f16x2(w[0] >> 16), e4m3x2_to_f16x2(w[1]),
+                              e4m3x2_to_f16x2(w[1] >> 16));
+            h[1] = make_uint4(e4m3x2_to_f16x2(w[2]), e4m3x2_to_f16x2(w[2] >> 16), e4m3x2_to_f16x2(w[3]),
+                              e4m3x2_to_f16x2(w[3] >> 16));
+            uint8_t* g = dst + (r >> 3) * GROUP + (cc >> 2) * 1024u;
+            const int q = 2 * (cc & 3), swap = (cc >> 2) & 1;
+            *reinterpret_cast<uint4*>(g + swz<128>(r & 7, q + swap)) = swap ? h[1] : h[0];
+            *reinterpret_cast<uint4*>(g + swz<128>(r & 7, q + 1 - swap)) = swap ? h[0] : h[1];
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(full_bar(e));
+            mbar_arrive(rawempty_bar(er));
+          }
+        }
+      }
+    }
   } else if (warp == 0) {
     // ============================ product issuer =============================
-    const uint32_t idesc_o = umma_idesc_bf16(128, D, true);
-    const uint32_t idesc_s = umma_idesc_bf16(128, 16, false) & ~(0x3Fu << 17);
+    const uint32_t idesc_o = FP8 ? idesc_f16(128, D, true) : umma_idesc_bf16(128, D, true);
+    const uint32_t idesc_s = (FP8 ? idesc_f16(128, 16, false) : umma_idesc_bf16(128, 16, false)) & ~(0x3Fu << 17);
     struct Cur {
       Piece c;
       int s, blocks, pages;
       uint32_t e;          // ring entry (counted on) of the step's first K block
-      bool has[2];
+      bool has1;           // slot 1 has a block (slot 0 always has)
     };
-    uint32_t pn[2] = {0, 0}, qn[2] = {0, 0};                 // P and Q phases waited for
+    uint32_t pn0 = 0, pn1 = 0, qn0 = 0, qn1 = 0;             // P and Q phases waited for
     uint32_t entries = 0;
     Cur cur = {}, nxt = {};
     auto fetch = [&](Cur& t, const Cur* before) -> bool {
@@ -374,36 +474,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         t.blocks = wk.sg.blocks;
         t.pages = wk.sg.pages;
       }
-      const int b1 = 2 * t.s + 1;
-      t.has[0] = true;
-      t.has[1] = !t.c.single || b1 < t.blocks;
+      t.has1 = !t.c.single || 2 * t.s + 1 < t.blocks;
       t.e = entries;
-      entries += t.c.single && t.has[1] ? 4 : 2;
+      entries += t.c.single && t.has1 ? 4 : 2;
       return true;
     };
     auto np_of = [&](const Cur& t, int slot) {
       const int b = t.c.single ? 2 * t.s + slot : t.s;
       return min(kBlockPages, t.pages - b * kBlockPages);
     };
-    // whether slot has a block in the piece at all / in a later step of it
+    // whether this is the slot's last block of the piece
     auto last_of = [&](const Cur& t, int slot) {
       return t.s + 1 == t.c.s1 || (slot == 1 && t.c.single && 2 * t.s + 3 >= t.blocks);
     };
     auto issue_s = [&](const Cur& t, int slot) -> bool {
-      if (!t.has[slot]) return true;
+      if (slot == 1 && !t.has1) return true;
       const uint32_t e = t.e + (t.c.single ? slot : 0);
       const uint32_t at = e % RING;
-      if (t.s == t.c.s0 && !warp_wait(qfull_bar(slot), qn[slot]++ & 1u, p.wait_ns)) return false;
+      if (t.s == t.c.s0 && !warp_wait(qfull_bar(slot), (slot ? qn1++ : qn0++) & 1u, p.wait_ns)) return false;
       if (!(slot == 1 && !t.c.single) && !warp_wait(full_bar(at), (e / RING) & 1u, p.wait_ns)) return false;
       tc_fence_after();
-      const uint64_t kd = umma_sdesc_sw128(warp_uniform(ring0 + at * GG::TILE), 16u, 1024u);
-      const uint64_t qd = umma_sdesc_sw128(warp_uniform(base + slot * GG::TILE), 16u, 1024u);
+      const uint64_t kd = umma_sdesc_sw128(warp_uniform(ring0 + at * TILE), 16u, GROUP);
+      const uint64_t qd = umma_sdesc_sw128(warp_uniform(base + slot * TILE), 16u, GROUP);
       const uint32_t idesc = warp_uniform(idesc_s | (static_cast<uint32_t>(2 * np_of(t, slot)) << 17));
       const uint32_t tS = warp_uniform(tbase + kColS + 128u * slot);
       if (lane == 0) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32u) >> 4;
+          const uint32_t off = ((k >> 2) * 1024u + (k & 3) * 32u) >> 4;
           umma_ss(tS, qd + off, kd + off, idesc, k > 0);
         }
         umma_commit(sfull_bar(slot));
@@ -413,13 +511,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     auto issue_pv = [&](const Cur& t, int slot) -> bool {
-      if (!t.has[slot]) return true;
-      const uint32_t e = t.e + (t.c.single ? (t.has[1] ? 2 : 1) + slot : 1);
+      if (slot == 1 && !t.has1) return true;
+      const uint32_t e = t.e + (t.c.single ? (t.has1 ? 2 : 1) + slot : 1);
       const uint32_t at = e % RING;
-      if (!warp_wait(pfull_bar(slot), pn[slot]++ & 1u, p.wait_ns)) return false;
+      if (!warp_wait(pfull_bar(slot), (slot ? pn1++ : pn0++) & 1u, p.wait_ns)) return false;
       if (!(slot == 1 && !t.c.single) && !warp_wait(full_bar(at), (e / RING) & 1u, p.wait_ns)) return false;
       tc_fence_after();
-      const uint64_t vd = umma_sdesc_sw128(warp_uniform(ring0 + at * GG::TILE), kHalf, 1024u);
+      const uint64_t vd = umma_sdesc_sw128(warp_uniform(ring0 + at * TILE), 1024u, GROUP);
       const uint32_t tO = warp_uniform(tbase + kColO + 128u * slot), tP = warp_uniform(tbase + kColS + 128u * slot);
       const int np = np_of(t, slot);
       const bool fresh = t.s == t.c.s0;                       // a piece's first block overwrites O
@@ -427,7 +525,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < kBlockPages; ++k)
           if (k < np)
-            umma_ts(tO, tP + 8u * k, vd + static_cast<uint64_t>((k * kTcBox) >> 4), idesc_o, !(fresh && k == 0));
+            umma_ts(tO, tP + 8u * k + (k >= 4 ? 32u : 0u), vd + static_cast<uint64_t>((k * PAGE) >> 4), idesc_o,
+                    !(fresh && k == 0));
         if (t.c.single || slot == 1) umma_commit(empty_bar(at));
         if (last_of(t, slot)) umma_commit(odone_bar(slot));
       }
@@ -448,13 +547,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!warp_wait(drain_bar, 0u, p.wait_ns) && lane == 0) atomicOr(p.err, kErrTimeout);
   } else {
     // ================================ softmax ================================
-    const int slot = (warp - kSoftmaxWarp0) >> 2;
-    const int rho = 32 * (warp & 3) + lane;                   // row of the tile = tensor-memory lane
-    const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t tS = tbase + lane_off + kColS + 128u * slot, tO = tbase + lane_off + kColO + 128u * slot;
-    uint32_t sn = 0, on = 0;
+    const int sw = warp - GG::SOFT0;
+    const int slot = sw >> 3, half = (sw >> 2) & 1;           // columns 64 half .. of the slot's S
+    const int quarter = warp & 3;
+    const int rho = 32 * quarter + lane;                      // row of the tile = tensor-memory lane
+    const uint32_t lane_off = static_cast<uint32_t>(32 * quarter) << 16;
+    const uint32_t tS = tbase + lane_off + kColS + 128u * slot + 64u * half;
+    const uint32_t tO = tbase + lane_off + kColO + 128u * slot + (D / 2) * half;   // this thread's half of O
+    const uint32_t xbar = pair_bar(slot, quarter);
+    float* const x_mine = xchg + (2 * slot + half) * 128 + rho;
+    const float* const x_other = xchg + (2 * slot + (half ^ 1)) * 128 + rho;
+    uint32_t sn = 0, on = 0, xn = 0;
+    float row_scale = 1.f, next_scale = 1.f;                  // fp8: what the staged row was divided by
     bool ok = true;
-    // this thread's query row of a piece into the slot's tile (rows past the pair's are zero)
+    // meets the warp of the rows' other threads
+    auto meet = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(xbar);
+      return warp_wait(xbar, xn++ & 1u, p.wait_ns);
+    };
+    // one value of the row's other thread (read before either writes the next: a block's P,
+    // which all of the slot's warps announce, lies between two of them)
+    auto swap_value = [&](float v, float& other) -> bool {
+      *x_mine = v;
+      if (!meet()) return false;
+      other = *x_other;
+      return true;
+    };
+    // this thread's half of a query row of a piece into the slot's tile (rows past the
+    // pair's are zero).  fp8 caches: in f16, divided by a power of two that leaves the
+    // largest element in [1, 2).
     auto stage_q = [&](const Piece& c, const SharedGroup& sg) {
       const int r = c.pair * kSharedPair + (c.single ? 0 : slot * kSharedTile) + rho;
       const bool have = r < sg.rows;
@@ -462,14 +584,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (have)
         src = reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(sg.t0 + r / p.G) * p.q_stride_t +
                                              static_cast<int64_t>(c.head * p.G + r % p.G) * D);
-      uint8_t* dst = gbase + slot * GG::TILE;
+      float div = 1.f;
+      if constexpr (FP8) {
+        uint32_t mx = 0;
+#pragma unroll 4
+        for (int k = 0; k < D / 8; ++k) {
+          const uint4 v = have ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+          mx = max_u16x2(mx, max_u16x2(max_u16x2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                       max_u16x2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+        }
+        const int ex = static_cast<int>((max(mx & 0xFFFFu, mx >> 16) >> 7) & 0xFFu) - 127;
+        const int e2 = ex == 128 ? 0 : min(126, max(-100, ex));   // (NaN and infinities stay as they are)
+        next_scale = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
+        div = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+      }
+      uint8_t* dst = gbase + slot * TILE + (rho >> 3) * GROUP;
 #pragma unroll
-      for (int h = 0; h < NH; ++h) {
-        uint4 v[8];
+      for (int k = 0; k < D / 16; ++k) {
+        const int ch = (D / 16) * half + k;                   // 8-feature chunk
+        uint4 v = have ? src[ch] : make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (FP8) {
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = have ? src[8 * h + k] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(dst + h * kHalf + swz<128>(rho, k)) = v[k];
+          for (int e = 0; e < 4; ++e) w[e] = pack_f16(bf16_lo(w[e]) * div, bf16_hi(w[e]) * div);
+          v = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        *reinterpret_cast<uint4*>(dst + (ch >> 3) * 1024u + swz<128>(rho & 7, ch & 7)) = v;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -484,67 +624,78 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (blocks_in(c, sg) > 0) stage_q(c, sg);
     for (;;) {
       const int n = blocks_in(c, sg);
-      float m = -INFINITY, l = 0.f, lr = 0.f;                 // running maximum (log2 units), sums of the weights and
-      for (int k = 0; ok && k < n; ++k) {                     // of the weights as rounded into P
+      row_scale = next_scale;
+      // The scale (of either sign, or zero) joins the exponent's FMA where it is positive,
+      // and the maximum is taken over the raw scores.
+      const float cs = p.scale_log2 * row_scale;
+      const bool positive = p.scale_log2 > 0.f;
+      const float mult = positive ? cs : 1.f;
+      const int in_pair = sg.rows - c.pair * kSharedPair;     // rows from the pair's first on
+      const int r = c.single ? rho : slot * kSharedTile + rho;
+      const bool mine = r < in_pair && r < kSharedPair;
+      const bool idle = !__any_sync(0xffffffffu, mine);       // no row of this warp exists
+      float m = -INFINITY, l = 0.f;                           // running maximum (log2 units); this half's sum
+      for (int k = 0; ok && k < n; ++k) {
         const int b = c.single ? 2 * (c.s0 + k) + slot : c.s0 + k;
         const int np = min(kBlockPages, sg.pages - b * kBlockPages);
         if (!warp_wait(sfull_bar(slot), sn++ & 1u, p.wait_ns)) {
           ok = false;
           break;
         }
+        if (idle) {
+          // (what its rows' P and O hold reaches nobody)
+          if (lane == 0) mbar_arrive(pfull_bar(slot));
+          continue;
+        }
         tc_fence_after();
-        // The scale (of either sign, or zero) joins the exponent's FMA where it is positive,
-        // and the maximum is taken over the raw scores.  S is read twice, 32 columns at a
-        // time, rather than held in 128 registers.
-        const float cs = p.scale_log2, mult = cs > 0.f ? cs : 1.f;
-        const bool plain = np == kBlockPages && cs > 0.f;
+        const bool plain = np == kBlockPages && positive;
         auto scores = [&](int k2, float (&sv)[32]) {
-          uint32_t r[32];
-          tmem_ld32(tS + 32u * k2, r);
-          tmem_wait_ld32(r);
+          uint32_t w[32];
+          tmem_ld32(tS + 32u * k2, w);
+          after_wait<32>(w);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) sv[e] = __uint_as_float(r[e]);
+          for (int e = 0; e < 32; ++e) sv[e] = __uint_as_float(w[e]);
           if (!plain) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              if (!(cs > 0.f)) sv[e] *= cs;
-              if (32 * k2 + e >= 16 * np) sv[e] = -INFINITY;
+              if (!positive) sv[e] *= cs;
+              if (64 * half + 32 * k2 + e >= 16 * np) sv[e] = -INFINITY;
             }
           }
         };
-        float mb = -INFINITY;
-#pragma unroll
-        for (int k2 = 0; k2 < kKeys / 32; ++k2) {
-          float sv[32];
-          scores(k2, sv);
-          mb = fmaxf(mb, Max3Tree<32>::run(sv));
+        float mb, mo;
+        {
+          float sv[32], sw2[32];
+          scores(0, sv);
+          mb = Max3Tree<32>::run(sv);
+          scores(1, sw2);
+          mb = fmaxf(mb, Max3Tree<32>::run(sw2)) * mult;
         }
-        mb *= mult;
-        const float m_new = fmaxf(m, mb);
+        if (!swap_value(mb, mo)) {
+          ok = false;
+          break;
+        }
+        const float m_new = fmax3(m, mb, mo);
         const bool grow = m_new > m + 8.f;                    // also from -inf to anything
         if (k > 0 && __any_sync(0xffffffffu, grow)) {
           const float alpha = grow ? fast_exp2(m - m_new) : 1.f;
 #pragma unroll
-          for (int ch = 0; ch < D / 16; ++ch) {
-            uint32_t r[16];
-            tmem_ld16(tO + 16u * ch, r);
-            tmem_wait_ld16(r);
+          for (int ch = 0; ch < D / 32; ++ch) {
+            uint32_t o[16];
+            tmem_ld16(tO + 16u * ch, o);
+            after_wait<16>(o);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-            tmem_st16(tO + 16u * ch, r);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st16(tO + 16u * ch, o);
           }
-          if (grow) {
-            l *= alpha;
-            lr *= alpha;
-          }
+          if (grow) l *= alpha;
         }
         if (grow) m = m_new;
         const float mneg = m == -INFINITY ? 0.f : -m;
         const uint64_t mult2 = f2_pack(mult, mult), mneg2 = f2_pack(mneg, mneg);
-        uint64_t lsum = f2_pack(0.f, 0.f), rsum = lsum;
+        uint64_t lsum = f2_pack(0.f, 0.f), lsum2 = lsum;
 #pragma unroll
-        for (int k2 = 0; k2 < kKeys / 32; ++k2) {
-          // (P's columns 16 k2 .. lie in the 32-column chunks read so far)
+        for (int k2 = 0; k2 < 2; ++k2) {
           uint32_t w[16];
           float sv[32];
           scores(k2, sv);
@@ -553,18 +704,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             float x0, x1;
             f2_unpack(ffma2(f2_pack(sv[2 * e], sv[2 * e + 1]), mult2, mneg2), x0, x1);
             const float a0 = fast_exp2(x0), a1 = fast_exp2(x1);
-            w[e] = pack_bf16(a0, a1);
-            lsum = fadd2(lsum, f2_pack(a0, a1));
-            rsum = fadd2(rsum, f2_pack(bf16_lo(w[e]), bf16_hi(w[e])));
+            w[e] = FP8 ? pack_f16(a0, a1) : pack_bf16(a0, a1);
+            if (e & 1) lsum2 = fadd2(lsum2, f2_pack(a0, a1));
+            else lsum = fadd2(lsum, f2_pack(a0, a1));
           }
-          tmem_st16(tS + 16u * k2, w);
+          tmem_st16(tS + 16u * k2, w);                        // (its S columns have been read)
         }
         {
           float s0, s1;
-          f2_unpack(lsum, s0, s1);
+          f2_unpack(fadd2(lsum, lsum2), s0, s1);
           l += s0 + s1;
-          f2_unpack(rsum, s0, s1);
-          lr += s0 + s1;
         }
         tmem_wait_st();
         tc_fence_before();
@@ -572,49 +721,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(pfull_bar(slot));
       }
       if (!ok) break;
+      const int64_t prow = sg.row0 + static_cast<int64_t>(c.head) * sg.rows_head +
+                           static_cast<int64_t>(c.pair) * kSharedPair + static_cast<int64_t>(cta) * kSharedPair +
+                           (c.single ? slot * sg.last_rows + rho : r);
       // the next piece's rows while this one's last product runs: its Q K^T products are
       // complete (S of the last block was read)
-      const Piece pc = c;
-      const SharedGroup pg = sg;
       const bool more = wk.more();
       if (more) {
         c = wk.next(p);
         sg = wk.sg;
         if (blocks_in(c, sg) > 0) stage_q(c, sg);
       }
-      const int in_pair = pg.rows - pc.pair * kSharedPair;    // rows from the pair's first on
-      const int r = pc.single ? rho : slot * kSharedTile + rho;
-      const bool mine = r < in_pair && (pc.single || r < kSharedPair);
-      const int64_t prow = pg.row0 + static_cast<int64_t>(pc.head) * pg.rows_head +
-                           static_cast<int64_t>(pc.pair) * kSharedPair + static_cast<int64_t>(cta) * kSharedPair +
-                           (pc.single ? slot * pg.last_rows + rho : r);
       if (n == 0) {
-        if (mine) p.ws_ml[prow] = make_float2(-INFINITY, 0.f);
+        if (mine && half == 0) p.ws_ml[prow] = make_float2(-INFINITY, 0.f);
       } else {
         if (!warp_wait(odone_bar(slot), on++ & 1u, p.wait_ns)) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        // O / l is the weighted mean of V rows: O is normalised by the rounded weights' sum
-        const float ps = lr > 0.f ? l / lr : (lr != lr ? lr : 0.f);
-        float* orow = p.ws_o + prow * D;
-#pragma unroll
-        for (int ch = 0; ch < D / 16; ++ch) {
-          uint32_t o[16];
-          tmem_ld16(tO + 16u * ch, o);
-          tmem_wait_ld16(o);
-          if (mine) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<float4*>(orow + 16 * ch + e) =
-                  make_float4(__uint_as_float(o[e]) * ps, __uint_as_float(o[e + 1]) * ps,
-                              __uint_as_float(o[e + 2]) * ps, __uint_as_float(o[e + 3]) * ps);
+        if (!idle) {
+          tc_fence_after();
+          // the row's sum, read before the next piece's first maximum takes its place
+          float lo;
+          if (!swap_value(l, lo) || !meet()) {
+            ok = false;
+            break;
           }
+          float* orow = p.ws_o + prow * D + (D / 2) * half;
+#pragma unroll
+          for (int ch = 0; ch < D / 32; ++ch) {
+            uint32_t o[16];
+            tmem_ld16(tO + 16u * ch, o);
+            after_wait<16>(o);
+            if (mine) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<uint4*>(orow + 16 * ch + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+          }
+          if (mine && half == 0) p.ws_ml[prow] = make_float2(m, l + lo);
+          // (the slot's next P V, which overwrites O, is issued after this thread's next P)
+          tc_fence_before();
         }
-        if (mine) p.ws_ml[prow] = make_float2(m, l);
-        // the slot's next P V, which overwrites O, is issued after this thread's next P
-        tc_fence_before();
       }
       if (!more) break;
     }
@@ -648,27 +796,41 @@ cudaError_t launch_shared_plan(const SharedParams& p, bool pdl, cudaStream_t str
   return cudaLaunchKernelEx(&cfg, pa_shared_plan_kernel, p);
 }
 
-cudaError_t launch_shared_prefix(int head_dim, const CUtensorMap& tk, const CUtensorMap& tv, const SharedParams& p,
-                                 int grid, bool pdl, cudaStream_t stream) {
+namespace {
+
+using PrefixKernel = void (*)(CUtensorMap, CUtensorMap, SharedParams);
+struct PrefixForm {
+  PrefixKernel kernel;
+  int threads;
+  uint32_t smem;
+};
+template <int D, bool FP8>
+PrefixForm prefix_form() {
+  return {pa_shared_prefix_kernel<D, FP8>, PrefixGeo<D, FP8>::THREADS, PrefixGeo<D, FP8>::SMEM};
+}
+PrefixForm prefix_form_of(int head_dim, bool fp8) {
+  if (head_dim == 128) return fp8 ? prefix_form<128, true>() : prefix_form<128, false>();
+  return fp8 ? prefix_form<64, true>() : prefix_form<64, false>();
+}
+
+}  // namespace
+
+cudaError_t launch_shared_prefix(int head_dim, bool fp8, const CUtensorMap& tk, const CUtensorMap& tv,
+                                 const SharedParams& p, int grid, bool pdl, cudaStream_t stream) {
+  const PrefixForm f = prefix_form_of(head_dim, fp8);
   cudaLaunchAttribute attr[1];
-  if (head_dim == 128) {
-    const cudaLaunchConfig_t cfg = config(grid, kThreads, PrefixGeo<128>::SMEM, pdl, stream, attr);
-    return cudaLaunchKernelEx(&cfg, pa_shared_prefix_kernel<128>, tk, tv, p);
-  }
-  if (head_dim == 64) {
-    const cudaLaunchConfig_t cfg = config(grid, kThreads, PrefixGeo<64>::SMEM, pdl, stream, attr);
-    return cudaLaunchKernelEx(&cfg, pa_shared_prefix_kernel<64>, tk, tv, p);
-  }
-  return cudaErrorInvalidValue;
+  const cudaLaunchConfig_t cfg = config(grid, f.threads, f.smem, pdl, stream, attr);
+  return cudaLaunchKernelEx(&cfg, f.kernel, tk, tv, p);
 }
 
 cudaError_t set_shared_smem_limits() {
-  cudaError_t e = cudaFuncSetAttribute(pa_shared_prefix_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(PrefixGeo<128>::SMEM));
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(pa_shared_prefix_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(PrefixGeo<64>::SMEM));
-  return e;
+  for (int form = 0; form < 4; ++form) {
+    const PrefixForm f = prefix_form_of(form & 1 ? 128 : 64, form & 2);
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(f.kernel),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(f.smem));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace pa

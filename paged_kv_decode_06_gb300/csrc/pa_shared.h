@@ -69,6 +69,7 @@ struct SharedParams {
   int32_t num_seqs, num_tokens, num_groups, max_qlen, max_blocks, num_pages, G, Hkv;
   int32_t min_pages;          // fewer shared pages are left to the sequences
   int32_t min_steps;          // steps a CTA at least
+  int32_t split_boxes;        // 128 features, bf16: heads are not contiguous, pages come in four boxes
   float scale_log2;
   uint64_t wait_ns;
   uint32_t* err;
@@ -83,8 +84,8 @@ struct SharedParams {
 };
 
 cudaError_t launch_shared_plan(const SharedParams& p, bool pdl, cudaStream_t stream);
-cudaError_t launch_shared_prefix(int head_dim, const CUtensorMap& tk, const CUtensorMap& tv, const SharedParams& p,
-                                 int grid, bool pdl, cudaStream_t stream);
+cudaError_t launch_shared_prefix(int head_dim, bool fp8, const CUtensorMap& tk, const CUtensorMap& tv,
+                                 const SharedParams& p, int grid, bool pdl, cudaStream_t stream);
 cudaError_t set_shared_smem_limits();
 
 }  // namespace pa

@@ -250,3 +250,17 @@ def test_a_serving_step():
     b.check(out, lse)
     b.check(ref_out, ref_lse)
     assert np.abs(win.double().cpu().numpy() - b.want(100, 4)[0]).max() < 2.0 ** -6
+
+
+@pytest.mark.parametrize("kv,d", [("bf16", 128), ("bf16", 64), ("fp8", 128), ("fp8", 64)])
+def test_heads_that_are_not_contiguous(kv, d):
+    b = Batch([700 + 9 * i for i in range(9)], hq=6, hkv=3, d=d, kv=kv, groups=([0, 9], [690]))
+    dev = b.on_gpu()
+    for x in (1, 2):
+        wide = torch.zeros(dev[x].shape[0], 17, 4, d + 16, dtype=dev[x].dtype, device="cuda")
+        wide[:, :16, :3, :d] = dev[x]
+        dev[x] = wide[:, :16, :3, :d]
+    out, lse = b.buffers()
+    binding.paged_attn_decode_shared(*dev, 1, _i32([0, 9]), _i32([690]), b.scale, b.ks, b.vs, out=out, lse=lse)
+    torch.cuda.synchronize()
+    b.check(out, lse)
