@@ -10,19 +10,20 @@
 // 4 D bytes (bf16), so from about 280 rows on the tensor cores bound it, below that
 // memory does.  A CTA holds two 128-row tiles ("slots") of query rows in
 // shared memory and S / P (128 columns) and O (128 columns) of each in tensor memory, all
-// 512 columns; blocks of 128 keys, K and V apart, pass through a ring.  One thread
-// issues P V of slot 0, Q K^T of slot 0's next block, then the same for slot 1, so that
-// one slot's softmax runs while the tensor cores work for the other.
+// 512 columns; blocks of 128 keys, K and V apart, pass through a ring.  While one slot's
+// softmax runs, the tensor cores work for the other.
 //
-// Warps: 0 issues the products and owns tensor memory; 1 and 2 load pages; of an fp8
-// cache 3 to 6 convert codes to f16 (exact); the last sixteen are the slots' softmax, two
-// threads a row, lane = row of tensor memory.  P overwrites its S in 16 bits (f16 beside
-// an fp8 cache); O is rescaled only where the running maximum grew by more than 2^8.
+// Warps: 0 and 1 issue a slot's products each (one thread needs about 130 cycles a product,
+// twice what the tensor cores take, so one issuer for both would set the pace: 5300 cycles
+// a step) and 0 owns tensor memory; 2 and 3 load pages; of an fp8 cache 4 to 7 convert
+// codes to f16 (exact); the last sixteen are the slots' softmax, two threads a row, lane =
+// row of tensor memory.  P overwrites its S in 16 bits (f16 beside an fp8 cache); O is
+// rescaled only where the running maximum grew by more than 2^8.
 //
-// Order in the tensor pipe: one thread issues every product, and they run in that order,
-// so S of a slot's next block may overwrite the P that the slot's P V before it reads.
-// A commit covers all earlier products: once a softmax warp sees S of block b, P V of the
-// slot's block before it has left O complete, and O may be rescaled.
+// Order in the tensor pipe: one thread issues all of a slot's products, and they run in
+// that order, so S of its next block may overwrite the P that the P V before it reads.  A
+// commit covers all of a thread's earlier products: once a softmax warp sees S of block b,
+// P V of the slot's block before it has left O complete, and O may be rescaled.
 //
 // Waits are bounded, and each is made once a phase in order, so its barrier is never more
 // than one phase behind (mbarrier parities cannot tell further).
@@ -163,8 +164,9 @@ __global__ void __launch_bounds__(kPlanThreads) pa_shared_plan_kernel(const Shar
 }
 
 // ------------------------------------------------------------- prefix kernel
-constexpr int kLoaders = 2;               // warps 1, 2
-constexpr int kConverters = 4;            // fp8 caches: warps 3 .. 6
+constexpr int kIssuers = 2;               // warps 0, 1: a slot's products each
+constexpr int kLoaders = 2;               // warps 2, 3
+constexpr int kConverters = 4;            // fp8 caches: warps 4 .. 7
 constexpr int kSoftmaxWarps = 16;         // a slot's eight: two threads a row, 64 columns of S each
 constexpr int kBlockPages = kSharedBlockPages;
 constexpr int kKeys = 16 * kBlockPages;
@@ -190,7 +192,7 @@ struct PrefixGeo {
   static constexpr uint32_t RAW = kKeys * D;             // fp8: a block's codes
   static constexpr int RING = D == 128 ? 4 : 8;
   static constexpr int RAWS = FP8 ? (D == 128 ? 2 : 6) : 0;
-  static constexpr int SOFT0 = 1 + kLoaders + (FP8 ? kConverters : 0);
+  static constexpr int SOFT0 = kIssuers + kLoaders + (FP8 ? kConverters : 0);
   static constexpr int THREADS = 32 * (SOFT0 + kSoftmaxWarps);
   static constexpr uint32_t OFF_RING = 2 * TILE;
   static constexpr uint32_t OFF_RAW = OFF_RING + RING * TILE;
@@ -270,6 +272,17 @@ __device__ __forceinline__ int block_of(const Piece& c, const SharedGroup& sg, i
   return b < sg.blocks ? b : -1;
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // kind::f16 with f16 A and B and an fp32 accumulator.
 __device__ __forceinline__ uint32_t idesc_f16(int M, int N, bool b_mn_major) {
   return umma_idesc_bf16(M, N, b_mn_major) & ~((1u << 7) | (1u << 10));
@@ -297,10 +310,10 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
   auto qfull_bar = [&](int slot) { return xb + 8u * (4 + slot); };
   auto odone_bar = [&](int slot) { return xb + 8u * (6 + slot); };
   auto pair_bar = [&](int slot, int quarter) { return xb + 8u * (8 + 4 * slot + quarter); };
-  const uint32_t drain_bar = xb + 8u * 16;
-  auto rawfull_bar = [&](int e) { return xb + 8u * (17 + e); };     // fp8: code blocks
-  auto rawempty_bar = [&](int e) { return xb + 8u * (17 + RAWS + e); };
-  static_assert(2 * RING + 17 + 2 * RAWS + 1 <= 64, "barriers");
+  auto drain_bar = [&](int slot) { return xb + 8u * (16 + slot); };
+  auto rawfull_bar = [&](int e) { return xb + 8u * (18 + e); };     // fp8: code blocks
+  auto rawempty_bar = [&](int e) { return xb + 8u * (18 + RAWS + e); };
+  static_assert(2 * RING + 18 + 2 * RAWS + 1 <= 64, "barriers");
   uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(gbase + GG::OFF_BAR + 504);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -308,7 +321,7 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
     prefetch_tensormap(&tmap_v);
     for (int e = 0; e < RING; ++e) {
       mbar_init(full_bar(e), FP8 ? kConverters : kLoaders);
-      mbar_init(empty_bar(e), 1);
+      mbar_init(empty_bar(e), 2);
     }
     for (int e = 0; e < RAWS; ++e) {
       mbar_init(rawfull_bar(e), kLoaders);
@@ -319,9 +332,9 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
       mbar_init(pfull_bar(s), kSoftmaxWarps / 2);
       mbar_init(qfull_bar(s), kSoftmaxWarps / 2);
       mbar_init(odone_bar(s), 1);
+      mbar_init(drain_bar(s), 1);
       for (int k = 0; k < 4; ++k) mbar_init(pair_bar(s, k), 2);
     }
-    mbar_init(drain_bar, 1);
     fence_mbar_init();
   }
   grid_dependency_wait();
@@ -344,9 +357,9 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
   PieceWalker wk;
   wk.start(p, from, to);
 
-  if (warp >= 1 && warp <= kLoaders) {
+  if (warp >= kIssuers && warp < kIssuers + kLoaders) {
     // =============================== loaders =================================
-    const int me = warp - 1;
+    const int me = warp - kIssuers;
     constexpr int SLOTS = FP8 ? RAWS : RING;
     int e = 0;
     uint32_t round = 0;
@@ -355,6 +368,15 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
       const Piece c = wk.next(p);
       const SharedGroup& sg = wk.sg;
       const int32_t* row = p.block_tables + static_cast<int64_t>(sg.seq) * p.bt_stride;
+      // page ids of four blocks, a lane each, and the four after them on their way
+      int batch = -2, ids = 0, ids_next = 0;
+      auto entry = [&](int at) { return at < sg.pages ? row[at] : 0; };
+      auto turn_to = [&](int want) {
+        if (want == batch) return;
+        ids = want == batch + 1 ? ids_next : entry(32 * want + lane);
+        ids_next = entry(32 * (want + 1) + lane);
+        batch = want;
+      };
       for (int s = c.s0; ok && s < c.s1; ++s) {
         // the step's K blocks, then its V blocks
         const int b0 = block_of(c, sg, s, 0), nb = c.single && block_of(c, sg, s, 1) >= 0 ? 2 : 1;
@@ -366,7 +388,8 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
           // are not contiguous) eight slots and 64 features of one
           const int per = !FP8 && NH == 2 && p.split_boxes ? 4 : 1;
           const int x = kLoaders * lane + me, pg = x / per, part = x - pg * per;
-          const int page = pg < np ? row[b * kBlockPages + pg] : 0;
+          turn_to(b >> 2);
+          const int page = __shfl_sync(0xffffffffu, ids, (8 * b + pg) & 31);
           if (round > 0 && !warp_wait(FP8 ? rawempty_bar(e) : empty_bar(e), (round - 1) & 1u, p.wait_ns)) {
             if (lane == 0) atomicOr(p.err, kErrTimeout);
             ok = false;
@@ -401,11 +424,11 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
         }
       }
     }
-  } else if (FP8 && warp > kLoaders && warp < GG::SOFT0) {
+  } else if (FP8 && warp >= kIssuers + kLoaders && warp < GG::SOFT0) {
     // ============================== converters ===============================
     // e4m3 codes to f16 (exact), 16 a thread and turn, into the products' layout.  The
     // two stores of a thread are swapped between the halves of a row: no bank conflict.
-    const int ct = tid - 32 * (1 + kLoaders);
+    const int ct = tid - 32 * (kIssuers + kLoaders);
     constexpr int CPR = D / 16;                              // 16-code chunks a row
     uint32_t n = 0;
     bool ok = true;
@@ -449,102 +472,109 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
         }
       }
     }
-  } else if (warp == 0) {
-    // ============================ product issuer =============================
+  } else if (warp < 2) {
+    // =========================== product issuers =============================
+    const int slot = warp;
     const uint32_t idesc_o = FP8 ? idesc_f16(128, D, true) : umma_idesc_bf16(128, D, true);
     const uint32_t idesc_s = (FP8 ? idesc_f16(128, 16, false) : umma_idesc_bf16(128, 16, false)) & ~(0x3Fu << 17);
-    struct Cur {
-      Piece c;
-      int s, blocks, pages;
-      uint32_t e;          // ring entry (counted on) of the step's first K block
-      bool has1;           // slot 1 has a block (slot 0 always has)
+    const uint64_t qd = umma_sdesc_sw128(warp_uniform(base + slot * TILE), 16u, GROUP);
+    const uint32_t tS = warp_uniform(tbase + kColS + 128u * slot), tO = warp_uniform(tbase + kColO + 128u * slot);
+    // One block of the slot: its K and V entries (counted on), pages, place in the piece.
+    struct Block {
+      uint32_t k, v;
+      int np;
+      bool first, last, both;      // of the piece; both: the other slot uses the entries too
     };
-    uint32_t pn0 = 0, pn1 = 0, qn0 = 0, qn1 = 0;             // P and Q phases waited for
-    uint32_t entries = 0;
-    Cur cur = {}, nxt = {};
-    auto fetch = [&](Cur& t, const Cur* before) -> bool {
-      // the step after `before` (or the first)
-      if (before != nullptr && before->s + 1 < before->c.s1) {
-        t = *before;
-        ++t.s;
-      } else {
-        if (!wk.more()) return false;
-        t.c = wk.next(p);
-        t.s = t.c.s0;
-        t.blocks = wk.sg.blocks;
-        t.pages = wk.sg.pages;
+    uint32_t n = 0, entries = 0;   // blocks issued; ring entries of the steps before
+    uint32_t pieces = 0;
+    Piece c = {};
+    int s = 0, blocks = 0, pages = 0;
+    bool in_piece = false;
+    auto fetch = [&](Block& t) -> bool {
+      for (;;) {
+        if (!in_piece) {
+          if (!wk.more()) return false;
+          c = wk.next(p);
+          s = c.s0;
+          blocks = wk.sg.blocks;
+          pages = wk.sg.pages;
+          in_piece = true;
+        }
+        const bool has1 = !c.single || 2 * s + 1 < blocks;
+        const uint32_t e = entries;
+        const int b = c.single ? 2 * s + slot : s;
+        const bool mine = slot == 0 || has1;
+        t.first = s == c.s0;
+        entries += c.single && has1 ? 4 : 2;
+        if (++s == c.s1) in_piece = false;
+        if (!mine) continue;                                 // (the single tile's last step, slot 1)
+        t.k = e + (c.single ? slot : 0);
+        t.v = e + (c.single ? (has1 ? 2 : 1) + slot : 1);
+        t.np = min(kBlockPages, pages - b * kBlockPages);
+        t.last = !in_piece || (slot == 1 && c.single && 2 * s + 1 >= blocks);
+        t.both = !c.single;
+        return true;
       }
-      t.has1 = !t.c.single || 2 * t.s + 1 < t.blocks;
-      t.e = entries;
-      entries += t.c.single && t.has1 ? 4 : 2;
-      return true;
     };
-    auto np_of = [&](const Cur& t, int slot) {
-      const int b = t.c.single ? 2 * t.s + slot : t.s;
-      return min(kBlockPages, t.pages - b * kBlockPages);
+    // An entry is free once both issuers' products have read it; of a single tile, whose
+    // entries only one uses, that one commits twice.
+    auto release = [&](uint32_t at, bool both) {
+      umma_commit(empty_bar(at));
+      if (!both) umma_commit(empty_bar(at));
     };
-    // whether this is the slot's last block of the piece
-    auto last_of = [&](const Cur& t, int slot) {
-      return t.s + 1 == t.c.s1 || (slot == 1 && t.c.single && 2 * t.s + 3 >= t.blocks);
-    };
-    auto issue_s = [&](const Cur& t, int slot) -> bool {
-      if (slot == 1 && !t.has1) return true;
-      const uint32_t e = t.e + (t.c.single ? slot : 0);
-      const uint32_t at = e % RING;
-      if (t.s == t.c.s0 && !warp_wait(qfull_bar(slot), (slot ? qn1++ : qn0++) & 1u, p.wait_ns)) return false;
-      if (!(slot == 1 && !t.c.single) && !warp_wait(full_bar(at), (e / RING) & 1u, p.wait_ns)) return false;
+    auto issue_s = [&](const Block& t) -> bool {
+      const uint32_t at = t.k % RING;
+      if (t.first && !warp_wait(qfull_bar(slot), pieces++ & 1u, p.wait_ns)) return false;
+      if (!warp_wait(full_bar(at), (t.k / RING) & 1u, p.wait_ns)) return false;
       tc_fence_after();
       const uint64_t kd = umma_sdesc_sw128(warp_uniform(ring0 + at * TILE), 16u, GROUP);
-      const uint64_t qd = umma_sdesc_sw128(warp_uniform(base + slot * TILE), 16u, GROUP);
-      const uint32_t idesc = warp_uniform(idesc_s | (static_cast<uint32_t>(2 * np_of(t, slot)) << 17));
-      const uint32_t tS = warp_uniform(tbase + kColS + 128u * slot);
-      if (lane == 0) {
+      const uint32_t idesc = warp_uniform(idesc_s | (static_cast<uint32_t>(2 * t.np) << 17));
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint32_t off = ((k >> 2) * 1024u + (k & 3) * 32u) >> 4;
           umma_ss(tS, qd + off, kd + off, idesc, k > 0);
         }
         umma_commit(sfull_bar(slot));
-        if (t.c.single || slot == 1) umma_commit(empty_bar(at));
+        release(at, t.both);
       }
       __syncwarp();
       return true;
     };
-    auto issue_pv = [&](const Cur& t, int slot) -> bool {
-      if (slot == 1 && !t.has1) return true;
-      const uint32_t e = t.e + (t.c.single ? (t.has1 ? 2 : 1) + slot : 1);
-      const uint32_t at = e % RING;
-      if (!warp_wait(pfull_bar(slot), (slot ? pn1++ : pn0++) & 1u, p.wait_ns)) return false;
-      if (!(slot == 1 && !t.c.single) && !warp_wait(full_bar(at), (e / RING) & 1u, p.wait_ns)) return false;
+    auto issue_pv = [&](const Block& t) -> bool {
+      const uint32_t at = t.v % RING;
+      if (!warp_wait(full_bar(at), (t.v / RING) & 1u, p.wait_ns) ||
+          !warp_wait(pfull_bar(slot), n++ & 1u, p.wait_ns))
+        return false;
       tc_fence_after();
       const uint64_t vd = umma_sdesc_sw128(warp_uniform(ring0 + at * TILE), 1024u, GROUP);
-      const uint32_t tO = warp_uniform(tbase + kColO + 128u * slot), tP = warp_uniform(tbase + kColS + 128u * slot);
-      const int np = np_of(t, slot);
-      const bool fresh = t.s == t.c.s0;                       // a piece's first block overwrites O
-      if (lane == 0) {
+      const int np = static_cast<int>(warp_uniform(static_cast<uint32_t>(t.np)));
+      const bool acc0 = !t.first;                            // a piece's first block overwrites O
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < kBlockPages; ++k)
           if (k < np)
-            umma_ts(tO, tP + 8u * k + (k >= 4 ? 32u : 0u), vd + static_cast<uint64_t>((k * PAGE) >> 4), idesc_o,
-                    !(fresh && k == 0));
-        if (t.c.single || slot == 1) umma_commit(empty_bar(at));
-        if (last_of(t, slot)) umma_commit(odone_bar(slot));
+            umma_ts(tO, tS + 8u * k + (k >= 4 ? 32u : 0u), vd + static_cast<uint64_t>((k * PAGE) >> 4), idesc_o,
+                    k > 0 || acc0);
+        release(at, t.both);
+        if (t.last) umma_commit(odone_bar(slot));
       }
       __syncwarp();
       return true;
     };
-    bool ok = fetch(cur, nullptr) && issue_s(cur, 0) && issue_s(cur, 1);
-    bool have = true;
+    Block cur, nxt;
+    bool have = fetch(cur);
+    bool ok = !have || issue_s(cur);
     while (ok && have) {
-      have = fetch(nxt, &cur);
-      ok = issue_pv(cur, 0) && (!have || issue_s(nxt, 0)) && issue_pv(cur, 1) && (!have || issue_s(nxt, 1));
+      have = fetch(nxt);
+      ok = issue_pv(cur) && (!have || issue_s(nxt));
       cur = nxt;
     }
     if (!ok && lane == 0) atomicOr(p.err, kErrTimeout);
     // every product must be complete before tensor memory is freed
-    if (lane == 0) umma_commit(drain_bar);
+    if (elect_one()) umma_commit(drain_bar(slot));
     __syncwarp();
-    if (!warp_wait(drain_bar, 0u, p.wait_ns) && lane == 0) atomicOr(p.err, kErrTimeout);
+    if (!warp_wait(drain_bar(slot), 0u, p.wait_ns) && lane == 0) atomicOr(p.err, kErrTimeout);
   } else {
     // ================================ softmax ================================
     const int sw = warp - GG::SOFT0;
