@@ -16,14 +16,15 @@
 // Warps: 0 and 1 issue a slot's products each (one thread needs about 130 cycles a product,
 // twice what the tensor cores take, so one issuer for both would set the pace: 5300 cycles
 // a step) and 0 owns tensor memory; 2 and 3 load pages; of an fp8 cache 4 to 7 convert
-// codes to f16 (exact); the last sixteen are the slots' softmax, two threads a row, lane =
-// row of tensor memory.  P overwrites its S in 16 bits (f16 beside an fp8 cache); O is
-// rescaled only where the running maximum grew by more than 2^8.
+// codes to f16 (exact); the last eight are the slots' softmax, thread = row of tensor
+// memory.  S of 64 keys, twice in each slot, P over it in 16 bits (f16 beside an fp8
+// cache): S of the next 64 keys is there when a softmax ends.  O is rescaled only where
+// the running maximum grew by more than 2^8.
 //
 // Order in the tensor pipe: one thread issues all of a slot's products, and they run in
-// that order, so S of its next block may overwrite the P that the P V before it reads.  A
-// commit covers all of a thread's earlier products: once a softmax warp sees S of block b,
-// P V of the slot's block before it has left O complete, and O may be rescaled.
+// that order, so S may overwrite the P that the P V before it reads, two sub-blocks back.
+// A commit covers all of a thread's earlier products: once a softmax warp sees S of
+// sub-block b, P V of b - 2 has left its part in O.
 //
 // Waits are bounded, and each is made once a phase in order, so its barrier is never more
 // than one phase behind (mbarrier parities cannot tell further).
@@ -167,12 +168,13 @@ __global__ void __launch_bounds__(kPlanThreads) pa_shared_plan_kernel(const Shar
 constexpr int kIssuers = 2;               // warps 0, 1: a slot's products each
 constexpr int kLoaders = 2;               // warps 2, 3
 constexpr int kConverters = 4;            // fp8 caches: warps 4 .. 7
-constexpr int kSoftmaxWarps = 16;         // a slot's eight: two threads a row, 64 columns of S each
-constexpr int kBlockPages = kSharedBlockPages;
+constexpr int kSoftmaxWarps = 8;          // a slot's four: a thread a row
+constexpr int kBlockPages = kSharedBlockPages;   // a ring entry: K or V of 128 keys
 constexpr int kKeys = 16 * kBlockPages;
+constexpr int kSubPages = 4;              // a product and its softmax: 64 keys
 constexpr uint32_t kCols = 512;
-constexpr uint32_t kColS = 0;             // + 128 slot: S; P of columns 0 .. 63 over the first 32 of them,
-constexpr uint32_t kColO = 256;           //   of 64 .. 127 over the 32 from 64 on.  O: + 128 slot
+constexpr uint32_t kColS = 0;             // + 128 slot + 64 (sub-block % 2): S, its P over the first 32 columns
+constexpr uint32_t kColO = 256;           // + 128 slot
 
 // Rows of 64 features (128 bytes, 128-byte swizzle) in groups of eight: a block's key rows
 // r = 16 page + slot, or a tile's query rows, at group r / 8, then feature half, then r % 8.
@@ -196,8 +198,7 @@ struct PrefixGeo {
   static constexpr int THREADS = 32 * (SOFT0 + kSoftmaxWarps);
   static constexpr uint32_t OFF_RING = 2 * TILE;
   static constexpr uint32_t OFF_RAW = OFF_RING + RING * TILE;
-  static constexpr uint32_t OFF_X = OFF_RAW + RAWS * RAW;           // [slot][half][128] floats
-  static constexpr uint32_t OFF_BAR = OFF_X + 2048;
+  static constexpr uint32_t OFF_BAR = OFF_RAW + RAWS * RAW;
   static constexpr uint32_t SMEM = OFF_BAR + 512;
 };
 
@@ -272,6 +273,16 @@ __device__ __forceinline__ int block_of(const Piece& c, const SharedGroup& sg, i
   return b < sg.blocks ? b : -1;
 }
 
+// Sub-blocks of a slot in a piece, and the pages of the last one.
+__device__ __forceinline__ int subs_in(const Piece& c, const SharedGroup& sg, int slot, int& last) {
+  const int b1 = c.single ? min(2 * (c.s1 - 1) + slot, sg.blocks - 1 - ((sg.blocks - 1 - slot) & 1)) : c.s1 - 1;
+  const int b0 = c.single ? 2 * c.s0 + slot : c.s0;
+  if (b1 < b0) return 0;
+  const int np = min(kBlockPages, sg.pages - b1 * kBlockPages);
+  last = np > kSubPages ? np - kSubPages : np;
+  return ((b1 - b0) >> (c.single ? 1 : 0)) * 2 + (np > kSubPages ? 2 : 1);
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -300,20 +311,20 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
   uint8_t* const gbase = smem_raw;
   const uint32_t base = smem_addr(smem_raw);
   const uint32_t ring0 = base + GG::OFF_RING, raw0 = base + GG::OFF_RAW;
-  float* const xchg = reinterpret_cast<float*>(gbase + GG::OFF_X);
   const uint32_t bar0 = base + GG::OFF_BAR;
   auto full_bar = [&](int e) { return bar0 + 8u * e; };             // ring entries: K or V of a block
   auto empty_bar = [&](int e) { return bar0 + 8u * (RING + e); };
   const uint32_t xb = bar0 + 8u * (2 * RING);
-  auto sfull_bar = [&](int slot) { return xb + 8u * slot; };
-  auto pfull_bar = [&](int slot) { return xb + 8u * (2 + slot); };
-  auto qfull_bar = [&](int slot) { return xb + 8u * (4 + slot); };
-  auto odone_bar = [&](int slot) { return xb + 8u * (6 + slot); };
-  auto pair_bar = [&](int slot, int quarter) { return xb + 8u * (8 + 4 * slot + quarter); };
-  auto drain_bar = [&](int slot) { return xb + 8u * (16 + slot); };
-  auto rawfull_bar = [&](int e) { return xb + 8u * (18 + e); };     // fp8: code blocks
-  auto rawempty_bar = [&](int e) { return xb + 8u * (18 + RAWS + e); };
-  static_assert(2 * RING + 18 + 2 * RAWS + 1 <= 64, "barriers");
+  // of a slot: S of a sub-block (by its parity), its P, its P V done; query rows staged; all drained
+  auto sfull_bar = [&](int slot, uint32_t n) { return xb + 8u * (2 * slot + (n & 1)); };
+  auto pfull_bar = [&](int slot, uint32_t n) { return xb + 8u * (4 + 2 * slot + (n & 1)); };
+  auto odone_bar = [&](int slot, uint32_t n) { return xb + 8u * (8 + 2 * slot + (n & 1)); };
+  auto qfull_bar = [&](int slot) { return xb + 8u * (12 + slot); };
+  auto drain_bar = [&](int slot) { return xb + 8u * (14 + slot); };
+  const uint32_t meet_bar = xb + 8u * 16;                           // the issuers, after each piece
+  auto rawfull_bar = [&](int e) { return xb + 8u * (17 + e); };     // fp8: code blocks
+  auto rawempty_bar = [&](int e) { return xb + 8u * (17 + RAWS + e); };
+  static_assert(2 * RING + 17 + 2 * RAWS + 1 <= 64, "barriers");
   uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(gbase + GG::OFF_BAR + 504);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -327,13 +338,15 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
       mbar_init(rawfull_bar(e), kLoaders);
       mbar_init(rawempty_bar(e), kConverters);
     }
+    mbar_init(meet_bar, 2);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(sfull_bar(s), 1);
-      mbar_init(pfull_bar(s), kSoftmaxWarps / 2);
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(sfull_bar(s, k), 1);
+        mbar_init(pfull_bar(s, k), kSoftmaxWarps / 2);
+        mbar_init(odone_bar(s, k), 1);
+      }
       mbar_init(qfull_bar(s), kSoftmaxWarps / 2);
-      mbar_init(odone_bar(s), 1);
       mbar_init(drain_bar(s), 1);
-      for (int k = 0; k < 4; ++k) mbar_init(pair_bar(s, k), 2);
     }
     fence_mbar_init();
   }
@@ -378,17 +391,18 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
         batch = want;
       };
       for (int s = c.s0; ok && s < c.s1; ++s) {
-        // the step's K blocks, then its V blocks
-        const int b0 = block_of(c, sg, s, 0), nb = c.single && block_of(c, sg, s, 1) >= 0 ? 2 : 1;
+        // the step's entries: K blocks, then V blocks; one without a block is empty
+        const int nb = c.single ? 2 : 1;
         for (int k = 0; k < 2 * nb; ++k) {
           const bool is_v = k >= nb;
-          const int b = b0 + (is_v ? k - nb : k);
-          const int np = min(kBlockPages, sg.pages - b * kBlockPages);
+          const int b = block_of(c, sg, s, is_v ? k - nb : k);
+          if (FP8 && b < 0) continue;
+          const int np = b < 0 ? 0 : min(kBlockPages, sg.pages - b * kBlockPages);
           // boxes dealt over the warps, a lane each: a page, or (split boxes: heads that
           // are not contiguous) eight slots and 64 features of one
           const int per = !FP8 && NH == 2 && p.split_boxes ? 4 : 1;
           const int x = kLoaders * lane + me, pg = x / per, part = x - pg * per;
-          turn_to(b >> 2);
+          if (b >= 0) turn_to(b >> 2);
           const int page = __shfl_sync(0xffffffffu, ids, (8 * b + pg) & 31);
           if (round > 0 && !warp_wait(FP8 ? rawempty_bar(e) : empty_bar(e), (round - 1) & 1u, p.wait_ns)) {
             if (lane == 0) atomicOr(p.err, kErrTimeout);
@@ -430,17 +444,18 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
     // two stores of a thread are swapped between the halves of a row: no bank conflict.
     const int ct = tid - 32 * (kIssuers + kLoaders);
     constexpr int CPR = D / 16;                              // 16-code chunks a row
-    uint32_t n = 0;
+    uint32_t n = 0, nraw = 0;
     bool ok = true;
     while (ok && wk.more()) {
       const Piece c = wk.next(p);
       for (int s = c.s0; ok && s < c.s1; ++s) {
-        const int b0 = block_of(c, wk.sg, s, 0), nb = c.single && block_of(c, wk.sg, s, 1) >= 0 ? 2 : 1;
+        const int nb = c.single ? 2 : 1;
         for (int k = 0; k < 2 * nb; ++k, ++n) {
-          const int np = min(kBlockPages, wk.sg.pages - (b0 + (k >= nb ? k - nb : k)) * kBlockPages);
+          const int b = block_of(c, wk.sg, s, k >= nb ? k - nb : k);
+          const int np = b < 0 ? 0 : min(kBlockPages, wk.sg.pages - b * kBlockPages);
           constexpr int kRaws = RAWS > 0 ? RAWS : 1;
-          const int er = static_cast<int>(n % kRaws), e = static_cast<int>(n % RING);
-          if (!warp_wait(rawfull_bar(er), (n / kRaws) & 1u, p.wait_ns) ||
+          const int er = static_cast<int>(nraw % kRaws), e = static_cast<int>(n % RING);
+          if ((b >= 0 && !warp_wait(rawfull_bar(er), (nraw / kRaws) & 1u, p.wait_ns)) ||
               (n >= RING && !warp_wait(empty_bar(e), (n / RING - 1) & 1u, p.wait_ns))) {
             if (lane == 0) atomicOr(p.err, kErrTimeout);
             ok = false;
@@ -467,8 +482,9 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(full_bar(e));
-            mbar_arrive(rawempty_bar(er));
+            if (b >= 0) mbar_arrive(rawempty_bar(er));
           }
+          if (b >= 0) ++nraw;
         }
       }
     }
@@ -479,96 +495,90 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
     const uint32_t idesc_s = (FP8 ? idesc_f16(128, 16, false) : umma_idesc_bf16(128, 16, false)) & ~(0x3Fu << 17);
     const uint64_t qd = umma_sdesc_sw128(warp_uniform(base + slot * TILE), 16u, GROUP);
     const uint32_t tS = warp_uniform(tbase + kColS + 128u * slot), tO = warp_uniform(tbase + kColO + 128u * slot);
-    // One block of the slot: its K and V entries (counted on), pages, place in the piece.
-    struct Block {
-      uint32_t k, v;
-      int np;
-      bool first, last, both;      // of the piece; both: the other slot uses the entries too
-    };
-    uint32_t n = 0, entries = 0;   // blocks issued; ring entries of the steps before
-    uint32_t pieces = 0;
-    Piece c = {};
-    int s = 0, blocks = 0, pages = 0;
-    bool in_piece = false;
-    auto fetch = [&](Block& t) -> bool {
-      for (;;) {
-        if (!in_piece) {
-          if (!wk.more()) return false;
-          c = wk.next(p);
-          s = c.s0;
-          blocks = wk.sg.blocks;
-          pages = wk.sg.pages;
-          in_piece = true;
+    uint32_t entries = 0;          // ring entries of the pieces before
+    uint32_t tiles = 0, ns = 0, npv = 0, pieces = 0;   // query tiles seen, S and P V products, pieces
+    bool ok = true;
+    while (ok && wk.more()) {
+      const Piece c = wk.next(p);
+      int last = 0;
+      const int subs = subs_in(c, wk.sg, slot, last);
+      // An entry is free once both issuers' products have read it; of a single tile, whose
+      // entries only one uses, that one commits twice.
+      auto release = [&](uint32_t at) {
+        umma_commit(empty_bar(at));
+        if (c.single) umma_commit(empty_bar(at));
+      };
+      // ring entry of sub-block i's K or V
+      auto entry = [&](int i, int v) {
+        return entries + (c.single ? 4u * (i >> 1) + 2u * v + slot : 2u * (i >> 1) + v);
+      };
+      auto issue_s = [&](int i) -> bool {
+        const uint32_t e = entry(i, 0), at = e % RING;
+        const int part = i & 1;
+        if (i == 0 && !warp_wait(qfull_bar(slot), tiles++ & 1u, p.wait_ns)) return false;
+        if (part == 0 && !warp_wait(full_bar(at), (e / RING) & 1u, p.wait_ns)) return false;
+        tc_fence_after();
+        const uint64_t kd = umma_sdesc_sw128(warp_uniform(ring0 + at * TILE + part * (kSubPages * PAGE)), 16u, GROUP);
+        const int np = i == subs - 1 ? last : kSubPages;
+        const uint32_t idesc = warp_uniform(idesc_s | (static_cast<uint32_t>(2 * np) << 17));
+        const uint32_t d = warp_uniform(tS + 64u * (ns & 1u));
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * 1024u + (k & 3) * 32u) >> 4;
+            umma_ss(d, qd + off, kd + off, idesc, k > 0);
+          }
+          umma_commit(sfull_bar(slot, ns));
+          if (part == 1 || i == subs - 1) release(at);
         }
-        const bool has1 = !c.single || 2 * s + 1 < blocks;
-        const uint32_t e = entries;
-        const int b = c.single ? 2 * s + slot : s;
-        const bool mine = slot == 0 || has1;
-        t.first = s == c.s0;
-        entries += c.single && has1 ? 4 : 2;
-        if (++s == c.s1) in_piece = false;
-        if (!mine) continue;                                 // (the single tile's last step, slot 1)
-        t.k = e + (c.single ? slot : 0);
-        t.v = e + (c.single ? (has1 ? 2 : 1) + slot : 1);
-        t.np = min(kBlockPages, pages - b * kBlockPages);
-        t.last = !in_piece || (slot == 1 && c.single && 2 * s + 1 >= blocks);
-        t.both = !c.single;
+        __syncwarp();
+        ++ns;
         return true;
-      }
-    };
-    // An entry is free once both issuers' products have read it; of a single tile, whose
-    // entries only one uses, that one commits twice.
-    auto release = [&](uint32_t at, bool both) {
-      umma_commit(empty_bar(at));
-      if (!both) umma_commit(empty_bar(at));
-    };
-    auto issue_s = [&](const Block& t) -> bool {
-      const uint32_t at = t.k % RING;
-      if (t.first && !warp_wait(qfull_bar(slot), pieces++ & 1u, p.wait_ns)) return false;
-      if (!warp_wait(full_bar(at), (t.k / RING) & 1u, p.wait_ns)) return false;
-      tc_fence_after();
-      const uint64_t kd = umma_sdesc_sw128(warp_uniform(ring0 + at * TILE), 16u, GROUP);
-      const uint32_t idesc = warp_uniform(idesc_s | (static_cast<uint32_t>(2 * t.np) << 17));
-      if (elect_one()) {
+      };
+      auto issue_pv = [&](int i) -> bool {
+        const uint32_t e = entry(i, 1), at = e % RING;
+        const int part = i & 1;
+        if ((part == 0 && !warp_wait(full_bar(at), (e / RING) & 1u, p.wait_ns)) ||
+            !warp_wait(pfull_bar(slot, npv), (npv >> 1) & 1u, p.wait_ns))
+          return false;
+        tc_fence_after();
+        const uint64_t vd = umma_sdesc_sw128(warp_uniform(ring0 + at * TILE + part * (kSubPages * PAGE)), 1024u, GROUP);
+        const int np = static_cast<int>(warp_uniform(static_cast<uint32_t>(i == subs - 1 ? last : kSubPages)));
+        const uint32_t a = warp_uniform(tS + 64u * (npv & 1u));
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = ((k >> 2) * 1024u + (k & 3) * 32u) >> 4;
-          umma_ss(tS, qd + off, kd + off, idesc, k > 0);
+          for (int k = 0; k < kSubPages; ++k)                // (a piece's first overwrites O)
+            if (k < np) umma_ts(tO, a + 8u * k, vd + static_cast<uint64_t>((k * PAGE) >> 4), idesc_o, k > 0 || i > 0);
+          umma_commit(odone_bar(slot, npv));
+          if (part == 1 || i == subs - 1) release(at);
         }
-        umma_commit(sfull_bar(slot));
-        release(at, t.both);
+        __syncwarp();
+        ++npv;
+        return true;
+      };
+      // S runs two sub-blocks ahead of P V: the softmax of one runs beside S of the next.
+      // (Not into the next piece: its K may come into the ring only once this V has left.)
+      ok = (subs < 1 || issue_s(0)) && (subs < 2 || issue_s(1));
+      for (int i = 0; ok && i < subs; ++i) ok = issue_pv(i) && (i + 2 >= subs || issue_s(i + 2));
+      if (ok && c.single && slot == 1 && block_of(c, wk.sg, c.s1 - 1, 1) < 0) {
+        // the single tile's last step has no block for this slot: its entries are empty
+        for (int v = 0; ok && v < 2; ++v) {
+          const uint32_t e = entries + 4u * (c.s1 - 1 - c.s0) + 2u * v + 1u, at = e % RING;
+          ok = warp_wait(full_bar(at), (e / RING) & 1u, p.wait_ns);
+          if (ok && lane == 0) {
+            mbar_arrive(empty_bar(at));
+            mbar_arrive(empty_bar(at));
+          }
+        }
       }
-      __syncwarp();
-      return true;
-    };
-    auto issue_pv = [&](const Block& t) -> bool {
-      const uint32_t at = t.v % RING;
-      if (!warp_wait(full_bar(at), (t.v / RING) & 1u, p.wait_ns) ||
-          !warp_wait(pfull_bar(slot), n++ & 1u, p.wait_ns))
-        return false;
-      tc_fence_after();
-      const uint64_t vd = umma_sdesc_sw128(warp_uniform(ring0 + at * TILE), 1024u, GROUP);
-      const int np = static_cast<int>(warp_uniform(static_cast<uint32_t>(t.np)));
-      const bool acc0 = !t.first;                            // a piece's first block overwrites O
-      if (elect_one()) {
-#pragma unroll
-        for (int k = 0; k < kBlockPages; ++k)
-          if (k < np)
-            umma_ts(tO, tS + 8u * k + (k >= 4 ? 32u : 0u), vd + static_cast<uint64_t>((k * PAGE) >> 4), idesc_o,
-                    k > 0 || acc0);
-        release(at, t.both);
-        if (t.last) umma_commit(odone_bar(slot));
+      entries += (c.single ? 4u : 2u) * static_cast<uint32_t>(c.s1 - c.s0);
+      // Both issuers have seen all of the piece's entries before either waits for the
+      // next's: a full barrier's earlier phase is known to be complete.
+      if (ok) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(meet_bar);
+        ok = warp_wait(meet_bar, pieces++ & 1u, p.wait_ns);
       }
-      __syncwarp();
-      return true;
-    };
-    Block cur, nxt;
-    bool have = fetch(cur);
-    bool ok = !have || issue_s(cur);
-    while (ok && have) {
-      have = fetch(nxt);
-      ok = issue_pv(cur) && (!have || issue_s(nxt));
-      cur = nxt;
     }
     if (!ok && lane == 0) atomicOr(p.err, kErrTimeout);
     // every product must be complete before tensor memory is freed
@@ -577,35 +587,15 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
     if (!warp_wait(drain_bar(slot), 0u, p.wait_ns) && lane == 0) atomicOr(p.err, kErrTimeout);
   } else {
     // ================================ softmax ================================
-    const int sw = warp - GG::SOFT0;
-    const int slot = sw >> 3, half = (sw >> 2) & 1;           // columns 64 half .. of the slot's S
+    const int slot = (warp - GG::SOFT0) >> 2;
     const int quarter = warp & 3;
     const int rho = 32 * quarter + lane;                      // row of the tile = tensor-memory lane
     const uint32_t lane_off = static_cast<uint32_t>(32 * quarter) << 16;
-    const uint32_t tS = tbase + lane_off + kColS + 128u * slot + 64u * half;
-    const uint32_t tO = tbase + lane_off + kColO + 128u * slot + (D / 2) * half;   // this thread's half of O
-    const uint32_t xbar = pair_bar(slot, quarter);
-    float* const x_mine = xchg + (2 * slot + half) * 128 + rho;
-    const float* const x_other = xchg + (2 * slot + (half ^ 1)) * 128 + rho;
-    uint32_t sn = 0, on = 0, xn = 0;
-    float row_scale = 1.f, next_scale = 1.f;                  // fp8: what the staged row was divided by
+    const uint32_t tS0 = tbase + lane_off + kColS + 128u * slot, tO = tbase + lane_off + kColO + 128u * slot;
+    uint32_t n = 0;                                           // sub-blocks of the pieces before
+    float next_scale = 1.f;                                   // fp8: what the staged row was divided by
     bool ok = true;
-    // meets the warp of the rows' other threads
-    auto meet = [&]() -> bool {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(xbar);
-      return warp_wait(xbar, xn++ & 1u, p.wait_ns);
-    };
-    // one value of the row's other thread (read before either writes the next: a block's P,
-    // which all of the slot's warps announce, lies between two of them)
-    auto swap_value = [&](float v, float& other) -> bool {
-      *x_mine = v;
-      if (!meet()) return false;
-      other = *x_other;
-      return true;
-    };
-    // this thread's half of a query row of a piece into the slot's tile (rows past the
-    // pair's are zero).  fp8 caches: in f16, divided by a power of two that leaves the
+    // this thread's query row of a piece into the slot's tile (rows past the pair's are zero).  fp8 caches: in f16, divided by a power of two that leaves the
     // largest element in [1, 2).
     auto stage_q = [&](const Piece& c, const SharedGroup& sg) {
       const int r = c.pair * kSharedPair + (c.single ? 0 : slot * kSharedTile) + rho;
@@ -630,8 +620,7 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
       }
       uint8_t* dst = gbase + slot * TILE + (rho >> 3) * GROUP;
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const int ch = (D / 16) * half + k;                   // 8-feature chunk
+      for (int ch = 0; ch < D / 8; ++ch) {                    // 8-feature chunks
         uint4 v = have ? src[ch] : make_uint4(0u, 0u, 0u, 0u);
         if constexpr (FP8) {
           uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -645,72 +634,63 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(qfull_bar(slot));
     };
-    // blocks of this slot in a piece
-    auto blocks_in = [&](const Piece& c, const SharedGroup& sg) {
-      return c.single ? max(0, min(c.s1, (sg.blocks - slot + 1) / 2) - c.s0) : c.s1 - c.s0;
-    };
     Piece c = wk.next(p);
     SharedGroup sg = wk.sg;
-    if (blocks_in(c, sg) > 0) stage_q(c, sg);
+    int last = 0, subs = subs_in(c, sg, slot, last);
+    if (subs > 0) stage_q(c, sg);
     for (;;) {
-      const int n = blocks_in(c, sg);
-      row_scale = next_scale;
       // The scale (of either sign, or zero) joins the exponent's FMA where it is positive,
       // and the maximum is taken over the raw scores.
-      const float cs = p.scale_log2 * row_scale;
+      const float cs = p.scale_log2 * next_scale;
       const bool positive = p.scale_log2 > 0.f;
       const float mult = positive ? cs : 1.f;
       const int in_pair = sg.rows - c.pair * kSharedPair;     // rows from the pair's first on
       const int r = c.single ? rho : slot * kSharedTile + rho;
       const bool mine = r < in_pair && r < kSharedPair;
       const bool idle = !__any_sync(0xffffffffu, mine);       // no row of this warp exists
-      float m = -INFINITY, l = 0.f;                           // running maximum (log2 units); this half's sum
-      for (int k = 0; ok && k < n; ++k) {
-        const int b = c.single ? 2 * (c.s0 + k) + slot : c.s0 + k;
-        const int np = min(kBlockPages, sg.pages - b * kBlockPages);
-        if (!warp_wait(sfull_bar(slot), sn++ & 1u, p.wait_ns)) {
+      float m = -INFINITY, l = 0.f;                           // running maximum (log2 units), sum
+      for (int k = 0; ok && k < subs; ++k) {
+        const uint32_t nk = n + k;
+        if (!warp_wait(sfull_bar(slot, nk), (nk >> 1) & 1u, p.wait_ns)) {
           ok = false;
           break;
         }
         if (idle) {
           // (what its rows' P and O hold reaches nobody)
-          if (lane == 0) mbar_arrive(pfull_bar(slot));
+          if (lane == 0) mbar_arrive(pfull_bar(slot, nk));
           continue;
         }
         tc_fence_after();
-        const bool plain = np == kBlockPages && positive;
-        auto scores = [&](int k2, float (&sv)[32]) {
-          uint32_t w[32];
-          tmem_ld32(tS + 32u * k2, w);
-          after_wait<32>(w);
+        const uint32_t tS = tS0 + 64u * (nk & 1u);
+        const int np = k == subs - 1 ? last : kSubPages;
+        uint32_t w[64];
+        tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&w[0]));
+        tmem_ld32(tS + 32u, *reinterpret_cast<uint32_t(*)[32]>(&w[32]));
+        after_wait<64>(w);
+        if (np < kSubPages || !positive) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) sv[e] = __uint_as_float(w[e]);
-          if (!plain) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if (!positive) sv[e] *= cs;
-              if (64 * half + 32 * k2 + e >= 16 * np) sv[e] = -INFINITY;
-            }
+          for (int e = 0; e < 64; ++e) {
+            float x = __uint_as_float(w[e]);
+            if (!positive) x *= cs;
+            w[e] = __float_as_uint(e < 16 * np ? x : -INFINITY);
           }
-        };
-        float mb, mo;
-        {
-          float sv[32], sw2[32];
-          scores(0, sv);
-          mb = Max3Tree<32>::run(sv);
-          scores(1, sw2);
-          mb = fmaxf(mb, Max3Tree<32>::run(sw2)) * mult;
         }
-        if (!swap_value(mb, mo)) {
-          ok = false;
-          break;
-        }
-        const float m_new = fmax3(m, mb, mo);
+        float mx[64];
+#pragma unroll
+        for (int e = 0; e < 64; ++e) mx[e] = __uint_as_float(w[e]);
+        const float m_new = fmaxf(m, Max3Tree<64>::run(mx) * mult);
         const bool grow = m_new > m + 8.f;                    // also from -inf to anything
         if (k > 0 && __any_sync(0xffffffffu, grow)) {
+          // O must hold P V of the sub-block before (the one before that is complete: S of
+          // this one was issued behind it)
+          if (!warp_wait(odone_bar(slot, nk - 1), ((nk - 1) >> 1) & 1u, p.wait_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
           const float alpha = grow ? fast_exp2(m - m_new) : 1.f;
 #pragma unroll
-          for (int ch = 0; ch < D / 32; ++ch) {
+          for (int ch = 0; ch < D / 16; ++ch) {
             uint32_t o[16];
             tmem_ld16(tO + 16u * ch, o);
             after_wait<16>(o);
@@ -726,60 +706,54 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
         uint64_t lsum = f2_pack(0.f, 0.f), lsum2 = lsum;
 #pragma unroll
         for (int k2 = 0; k2 < 2; ++k2) {
-          uint32_t w[16];
-          float sv[32];
-          scores(k2, sv);
+          uint32_t pw[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             float x0, x1;
-            f2_unpack(ffma2(f2_pack(sv[2 * e], sv[2 * e + 1]), mult2, mneg2), x0, x1);
+            f2_unpack(ffma2(f2_pack(__uint_as_float(w[32 * k2 + 2 * e]), __uint_as_float(w[32 * k2 + 2 * e + 1])), mult2,
+                            mneg2), x0, x1);
             const float a0 = fast_exp2(x0), a1 = fast_exp2(x1);
-            w[e] = FP8 ? pack_f16(a0, a1) : pack_bf16(a0, a1);
+            pw[e] = FP8 ? pack_f16(a0, a1) : pack_bf16(a0, a1);
             if (e & 1) lsum2 = fadd2(lsum2, f2_pack(a0, a1));
             else lsum = fadd2(lsum, f2_pack(a0, a1));
           }
-          tmem_st16(tS + 16u * k2, w);                        // (its S columns have been read)
-        }
-        {
-          float s0, s1;
-          f2_unpack(fadd2(lsum, lsum2), s0, s1);
-          l += s0 + s1;
+          tmem_st16(tS + 16u * k2, pw);
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(pfull_bar(slot));
+        if (lane == 0) mbar_arrive(pfull_bar(slot, nk));
+        float s0, s1;
+        f2_unpack(fadd2(lsum, lsum2), s0, s1);
+        l += s0 + s1;
       }
       if (!ok) break;
+      n += subs;
+      const int done = subs;
       const int64_t prow = sg.row0 + static_cast<int64_t>(c.head) * sg.rows_head +
                            static_cast<int64_t>(c.pair) * kSharedPair + static_cast<int64_t>(cta) * kSharedPair +
                            (c.single ? slot * sg.last_rows + rho : r);
-      // the next piece's rows while this one's last product runs: its Q K^T products are
-      // complete (S of the last block was read)
+      // the next piece's rows while this one's last products run: its Q K^T products are
+      // complete (S of the last sub-block was read)
       const bool more = wk.more();
       if (more) {
         c = wk.next(p);
         sg = wk.sg;
-        if (blocks_in(c, sg) > 0) stage_q(c, sg);
+        subs = subs_in(c, sg, slot, last);
+        if (subs > 0) stage_q(c, sg);
       }
-      if (n == 0) {
-        if (mine && half == 0) p.ws_ml[prow] = make_float2(-INFINITY, 0.f);
+      if (done == 0) {
+        if (mine) p.ws_ml[prow] = make_float2(-INFINITY, 0.f);
       } else {
-        if (!warp_wait(odone_bar(slot), on++ & 1u, p.wait_ns)) {
+        if (!warp_wait(odone_bar(slot, n - 1), ((n - 1) >> 1) & 1u, p.wait_ns)) {
           ok = false;
           break;
         }
         if (!idle) {
           tc_fence_after();
-          // the row's sum, read before the next piece's first maximum takes its place
-          float lo;
-          if (!swap_value(l, lo) || !meet()) {
-            ok = false;
-            break;
-          }
-          float* orow = p.ws_o + prow * D + (D / 2) * half;
+          float* orow = p.ws_o + prow * D;
 #pragma unroll
-          for (int ch = 0; ch < D / 32; ++ch) {
+          for (int ch = 0; ch < D / 16; ++ch) {
             uint32_t o[16];
             tmem_ld16(tO + 16u * ch, o);
             after_wait<16>(o);
@@ -789,7 +763,7 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
                 *reinterpret_cast<uint4*>(orow + 16 * ch + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
           }
-          if (mine && half == 0) p.ws_ml[prow] = make_float2(m, l + lo);
+          if (mine) p.ws_ml[prow] = make_float2(m, l);
           // (the slot's next P V, which overwrites O, is issued after this thread's next P)
           tc_fence_before();
         }

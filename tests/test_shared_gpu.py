@@ -264,3 +264,14 @@ def test_heads_that_are_not_contiguous(kv, d):
     binding.paged_attn_decode_shared(*dev, 1, _i32([0, 9]), _i32([690]), b.scale, b.ks, b.vs, out=out, lse=lse)
     torch.cuda.synchronize()
     b.check(out, lse)
+
+
+@pytest.mark.parametrize("kv,d", [("fp8", 128), ("bf16", 128), ("fp8", 64), ("bf16", 64)])
+@pytest.mark.parametrize("ctas", [1, 5, 152])
+def test_many_pieces_a_cta(kv, d, ctas):
+    """Pieces of every form one after another in a CTA: single tiles, pairs, odd blocks, short last blocks."""
+    r = np.random.default_rng(d + ctas)
+    sizes, shared = [2, 3, 34, 20, 9, 2, 40, 5], [130, 16, 700, 1040, 2000, 129 * 16, 64, 1500]
+    lens = np.concatenate([s + r.integers(1, 30, n) for n, s in zip(sizes, shared)])
+    b = Batch(lens, hq=16, hkv=2, d=d, kv=kv, groups=(np.concatenate([[0], np.cumsum(sizes)]).tolist(), shared), seed=1)
+    b.check(*_run(b, num_ctas=ctas))
