@@ -395,8 +395,8 @@ int encode_cache_map(CUtensorMap* map, const pa_tensor_t* t, int esz, int D, int
 // TMA map of the shared prefix's loads of a page and head.  fp8: rows of D codes, not
 // swizzled.  bf16: rows of 64 features (128-byte swizzle) by eight slots, then feature
 // half, then slot / 8 (dimension order d, slot % 8, 64-feature block of any head, slot / 8,
-// page), so that a page is one box; heads that are not contiguous (*split): (d, slot, head,
-// page) and boxes of 64 features x 8 slots.
+// page), so that a page is one box; 64 features: (d, slot, head, page); heads of 128 that
+// are not contiguous (*split): the same, in boxes of 64 features x 8 slots.
 int encode_prefix_map(CUtensorMap* map, const pa_tensor_t* t, int esz, int D, int Hkv, int64_t NB, bool* split) {
   const cuuint64_t slot = static_cast<cuuint64_t>(t->stride[1]) * esz, page = static_cast<cuuint64_t>(t->stride[0]) * esz;
   const cuuint64_t head = static_cast<cuuint64_t>(t->stride[2]) * esz;

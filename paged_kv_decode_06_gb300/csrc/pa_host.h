@@ -53,7 +53,7 @@ int host_split_plan(int B, int Hq, int Hkv, int D, int kv_dtype, int max_qlen, c
                     const HostDevice& dev, HostSplitPlan* out);
 // TMA map over a cache for boxes of HC heads of a page.
 int host_cache_map(CUtensorMap* map, const pa_tensor_t* t, int esz, int D, int Hkv, int HC, int64_t NB);
-// TMA map for the shared prefix's loads; *split: a page comes in four boxes.
+// TMA map for a shared prefix's loads; *split: a page comes in four boxes.
 int host_prefix_map(CUtensorMap* map, const pa_tensor_t* t, int esz, int D, int Hkv, int64_t NB, bool* split);
 
 // Runs the body of an entry point: no exception crosses the C boundary.

@@ -359,7 +359,7 @@ int decode_shared(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
   SplitParams& sp = pl.split.sp;
   if ((st = host_cache_map(&tk, kc, s.esz, D, Hkv, sp.HC, s.NB)) != PA_OK) return st;
   if ((st = host_cache_map(&tv, vc, s.esz, D, Hkv, sp.HC, s.NB)) != PA_OK) return st;
-  bool split_k, split_v;
+  bool split_k = false, split_v = false;
   if ((st = host_prefix_map(&pk, kc, s.esz, D, Hkv, s.NB, &split_k)) != PA_OK) return st;
   if ((st = host_prefix_map(&pv, vc, s.esz, D, Hkv, s.NB, &split_v)) != PA_OK) return st;
   if (split_k != split_v)

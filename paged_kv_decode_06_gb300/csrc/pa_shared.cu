@@ -13,13 +13,12 @@
 // 512 columns; blocks of 128 keys, K and V apart, pass through a ring.  While one slot's
 // softmax runs, the tensor cores work for the other.
 //
-// Warps: 0 and 1 issue a slot's products each (one thread needs about 130 cycles a product,
-// twice what the tensor cores take, so one issuer for both would set the pace: 5300 cycles
-// a step) and 0 owns tensor memory; 2 and 3 load pages; of an fp8 cache 4 to 7 convert
-// codes to f16 (exact); the last eight are the slots' softmax, thread = row of tensor
-// memory.  S of 64 keys, twice in each slot, P over it in 16 bits (f16 beside an fp8
-// cache): S of the next 64 keys is there when a softmax ends.  O is rescaled only where
-// the running maximum grew by more than 2^8.
+// Warps: 0 and 1 issue a slot's products each (one issuer for both: 5300 cycles a step) and
+// 0 owns tensor memory; 2 and 3 load pages; of an fp8 cache 4 to 7 convert codes to f16
+// (exact); the last eight are the slots' softmax, thread = row of tensor memory.  S of 64
+// keys, twice in each slot, P over it in 16 bits (f16 beside an fp8 cache): S of the next
+// 64 keys is there when a softmax ends.  O is rescaled only where the running maximum grew
+// by more than 2^8.
 //
 // Order in the tensor pipe: one thread issues all of a slot's products, and they run in
 // that order, so S may overwrite the P that the P V before it reads, two sub-blocks back.
@@ -191,12 +190,12 @@ struct Geo2 {
 template <int D, bool FP8>
 struct PrefixGeo {
   static constexpr uint32_t TILE = Geo2<D>::TILE;
-  static constexpr uint32_t RAW = kKeys * D;             // fp8: a block's codes
-  static constexpr int RING = D == 128 ? 4 : 8;
-  static constexpr int RAWS = FP8 ? (D == 128 ? 2 : 6) : 0;
+  static constexpr int RING = D == 128 ? 4 : 8;          // even: a slot's entries of single tiles keep their places
   static constexpr int SOFT0 = kIssuers + kLoaders + (FP8 ? kConverters : 0);
   static constexpr int THREADS = 32 * (SOFT0 + kSoftmaxWarps);
   static constexpr uint32_t OFF_RING = 2 * TILE;
+  static constexpr uint32_t RAW = kKeys * D;             // fp8: codes of an entry
+  static constexpr int RAWS = FP8 ? (D == 128 ? 2 : 4) : 0;
   static constexpr uint32_t OFF_RAW = OFF_RING + RING * TILE;
   static constexpr uint32_t OFF_BAR = OFF_RAW + RAWS * RAW;
   static constexpr uint32_t SMEM = OFF_BAR + 512;
@@ -273,6 +272,28 @@ __device__ __forceinline__ int block_of(const Piece& c, const SharedGroup& sg, i
   return b < sg.blocks ? b : -1;
 }
 
+// Page ids of a group's blocks for a warp: those of four blocks, a lane each, and the four
+// after them on their way.
+struct PageIds {
+  const int32_t* row;
+  int pages, batch, ids, next;
+  __device__ __forceinline__ int entry(int at) const { return at < pages ? row[at] : 0; }
+  __device__ __forceinline__ void start(const SharedParams& p, const SharedGroup& sg) {
+    row = p.block_tables + static_cast<int64_t>(sg.seq) * p.bt_stride;
+    pages = sg.pages;
+    batch = -2;
+  }
+  __device__ __forceinline__ void turn_to(int want) {
+    if (want == batch) return;
+    const int lane = threadIdx.x & 31;
+    ids = want == batch + 1 ? next : entry(32 * want + lane);
+    next = entry(32 * (want + 1) + lane);
+    batch = want;
+  }
+  // page pg of block b (of the batch turned to); every lane calls it
+  __device__ __forceinline__ int of(int b, int pg) const { return __shfl_sync(0xffffffffu, ids, (8 * b + pg) & 31); }
+};
+
 // Sub-blocks of a slot in a piece, and the pages of the last one.
 __device__ __forceinline__ int subs_in(const Piece& c, const SharedGroup& sg, int slot, int& last) {
   const int b1 = c.single ? min(2 * (c.s1 - 1) + slot, sg.blocks - 1 - ((sg.blocks - 1 - slot) & 1)) : c.s1 - 1;
@@ -310,7 +331,7 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const gbase = smem_raw;
   const uint32_t base = smem_addr(smem_raw);
-  const uint32_t ring0 = base + GG::OFF_RING, raw0 = base + GG::OFF_RAW;
+  const uint32_t ring0 = base + GG::OFF_RING;
   const uint32_t bar0 = base + GG::OFF_BAR;
   auto full_bar = [&](int e) { return bar0 + 8u * e; };             // ring entries: K or V of a block
   auto empty_bar = [&](int e) { return bar0 + 8u * (RING + e); };
@@ -322,9 +343,9 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
   auto qfull_bar = [&](int slot) { return xb + 8u * (12 + slot); };
   auto drain_bar = [&](int slot) { return xb + 8u * (14 + slot); };
   const uint32_t meet_bar = xb + 8u * 16;                           // the issuers, after each piece
-  auto rawfull_bar = [&](int e) { return xb + 8u * (17 + e); };     // fp8: code blocks
+  auto rawfull_bar = [&](int e) { return xb + 8u * (17 + e); };     // fp8: codes of an entry
   auto rawempty_bar = [&](int e) { return xb + 8u * (17 + RAWS + e); };
-  static_assert(2 * RING + 17 + 2 * RAWS + 1 <= 64, "barriers");
+  static_assert(2 * RING + 17 + 2 * RAWS <= 63, "barriers");
   uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(gbase + GG::OFF_BAR + 504);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -377,41 +398,32 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
     int e = 0;
     uint32_t round = 0;
     bool ok = true;
+    PageIds ids;
     while (ok && wk.more()) {
       const Piece c = wk.next(p);
-      const SharedGroup& sg = wk.sg;
-      const int32_t* row = p.block_tables + static_cast<int64_t>(sg.seq) * p.bt_stride;
-      // page ids of four blocks, a lane each, and the four after them on their way
-      int batch = -2, ids = 0, ids_next = 0;
-      auto entry = [&](int at) { return at < sg.pages ? row[at] : 0; };
-      auto turn_to = [&](int want) {
-        if (want == batch) return;
-        ids = want == batch + 1 ? ids_next : entry(32 * want + lane);
-        ids_next = entry(32 * (want + 1) + lane);
-        batch = want;
-      };
+      ids.start(p, wk.sg);
       for (int s = c.s0; ok && s < c.s1; ++s) {
         // the step's entries: K blocks, then V blocks; one without a block is empty
         const int nb = c.single ? 2 : 1;
         for (int k = 0; k < 2 * nb; ++k) {
           const bool is_v = k >= nb;
-          const int b = block_of(c, sg, s, is_v ? k - nb : k);
+          const int b = block_of(c, wk.sg, s, is_v ? k - nb : k);
           if (FP8 && b < 0) continue;
-          const int np = b < 0 ? 0 : min(kBlockPages, sg.pages - b * kBlockPages);
+          const int np = b < 0 ? 0 : min(kBlockPages, wk.sg.pages - b * kBlockPages);
           // boxes dealt over the warps, a lane each: a page, or (split boxes: heads that
           // are not contiguous) eight slots and 64 features of one
           const int per = !FP8 && NH == 2 && p.split_boxes ? 4 : 1;
           const int x = kLoaders * lane + me, pg = x / per, part = x - pg * per;
-          if (b >= 0) turn_to(b >> 2);
-          const int page = __shfl_sync(0xffffffffu, ids, (8 * b + pg) & 31);
+          if (b >= 0) ids.turn_to(b >> 2);
+          const int page = ids.of(b, pg);
           if (round > 0 && !warp_wait(FP8 ? rawempty_bar(e) : empty_bar(e), (round - 1) & 1u, p.wait_ns)) {
             if (lane == 0) atomicOr(p.err, kErrTimeout);
             ok = false;
             break;
           }
           const uint32_t bytes = (FP8 ? 16u * D : PAGE) / per;
-          const int mine = np * per > me ? (np * per - me + kLoaders - 1) / kLoaders : 0;
           const uint32_t full = FP8 ? rawfull_bar(e) : full_bar(e);
+          const int mine = np * per > me ? (np * per - me + kLoaders - 1) / kLoaders : 0;
           if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(mine) * bytes);
           __syncwarp();
           if (pg < np) {
@@ -419,8 +431,8 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
             // (a page id out of range reads as zeros: TMA fills outside the tensor)
             const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
             if constexpr (FP8) {
-              tma_load_4d(raw0 + static_cast<uint32_t>(e) * GG::RAW + static_cast<uint32_t>(pg) * bytes, map, 0, 0,
-                          c.head, page, full);
+              tma_load_4d(base + GG::OFF_RAW + static_cast<uint32_t>(e) * GG::RAW + static_cast<uint32_t>(pg) * bytes,
+                          map, 0, 0, c.head, page, full);
             } else {
               const uint32_t dst = ring0 + static_cast<uint32_t>(e) * TILE + static_cast<uint32_t>(pg) * PAGE;
               if (NH == 1)
@@ -440,53 +452,66 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
     }
   } else if (FP8 && warp >= kIssuers + kLoaders && warp < GG::SOFT0) {
     // ============================== converters ===============================
-    // e4m3 codes to f16 (exact), 16 a thread and turn, into the products' layout.  The
-    // two stores of a thread are swapped between the halves of a row: no bank conflict.
+    // e4m3 codes to f16 (exact), into the products' layout: a thread takes 16 codes of a
+    // row of each page (two pages at a time for 64 features), all into registers before it
+    // waits for a free entry.  Its two stores are swapped between the halves of a row: no
+    // bank conflict.  The codes' place is given back after the proxy fence: the copy that
+    // fills it next is not ordered behind plain loads without one (given back right after
+    // the loads, 127 against 126 us for the five groups below, with a fence of its own).
     const int ct = tid - 32 * (kIssuers + kLoaders);
     constexpr int CPR = D / 16;                              // 16-code chunks a row
+    constexpr int ITER = kKeys * CPR / (32 * kConverters);
+    constexpr int PPI = kBlockPages / ITER;                  // pages an iteration
+    constexpr int kRaws = RAWS > 0 ? RAWS : 1;
+    const int cc = ct % CPR, slot16 = (ct / CPR) % 16, pg0 = ct / (16 * CPR);
+    const int q = 2 * (cc & 3), swap = (cc >> 2) & 1;
+    const uint32_t to = static_cast<uint32_t>(pg0) * PAGE + (slot16 >> 3) * GROUP + (cc >> 2) * 1024u;
+    const uint32_t to0 = to + swz<128>(slot16 & 7, q + swap), to1 = to + swz<128>(slot16 & 7, q + 1 - swap);
     uint32_t n = 0, nraw = 0;
     bool ok = true;
     while (ok && wk.more()) {
       const Piece c = wk.next(p);
-      for (int s = c.s0; ok && s < c.s1; ++s) {
-        const int nb = c.single ? 2 : 1;
+      const int blocks = wk.sg.blocks, pages = wk.sg.pages, nb = c.single ? 2 : 1;
+      for (int s = c.s0; ok && s < c.s1; ++s)
         for (int k = 0; k < 2 * nb; ++k, ++n) {
-          const int b = block_of(c, wk.sg, s, k >= nb ? k - nb : k);
-          const int np = b < 0 ? 0 : min(kBlockPages, wk.sg.pages - b * kBlockPages);
-          constexpr int kRaws = RAWS > 0 ? RAWS : 1;
+          const int b = c.single ? 2 * s + (k & 1) : s;
+          const bool empty = b >= blocks;
+          const int np = min(kBlockPages, pages - b * kBlockPages);
           const int er = static_cast<int>(nraw % kRaws), e = static_cast<int>(n % RING);
-          if ((b >= 0 && !warp_wait(rawfull_bar(er), (nraw / kRaws) & 1u, p.wait_ns)) ||
-              (n >= RING && !warp_wait(empty_bar(e), (n / RING - 1) & 1u, p.wait_ns))) {
+          if (!empty) ok = warp_wait(rawfull_bar(er), (nraw / kRaws) & 1u, p.wait_ns);
+          uint4 v[ITER];
+          if (ok && !empty) {
+#pragma unroll
+            for (int i = 0; i < ITER; ++i)
+              v[i] = *reinterpret_cast<const uint4*>(gbase + GG::OFF_RAW + er * GG::RAW + 16 * ct + 2048 * i);
+            ++nraw;
+          }
+          if (ok && n >= RING) ok = warp_wait(empty_bar(e), (n / RING - 1) & 1u, p.wait_ns);
+          if (!ok) {
             if (lane == 0) atomicOr(p.err, kErrTimeout);
-            ok = false;
             break;
           }
-          const uint8_t* src = gbase + GG::OFF_RAW + er * GG::RAW;
-          uint8_t* dst = gbase + GG::OFF_RING + e * TILE;
-#pragma unroll 4
-          for (int x = ct; x < 16 * np * CPR; x += 32 * kConverters) {
-            const int r = x / CPR, cc = x % CPR;
-            const uint4 v = *reinterpret_cast<const uint4*>(src + 16 * x);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint4 h[2];
-            h[0] = make_uint4(e4m3x2_to_f16x2(w[0]), e4m3x2_to_f16x2(w[0] >> 16), e4m3x2_to_f16x2(w[1]),
-                              e4m3x2_to_f16x2(w[1] >> 16));
-            h[1] = make_uint4(e4m3x2_to_f16x2(w[2]), e4m3x2_to_f16x2(w[2] >> 16), e4m3x2_to_f16x2(w[3]),
-                              e4m3x2_to_f16x2(w[3] >> 16));
-            uint8_t* g = dst + (r >> 3) * GROUP + (cc >> 2) * 1024u;
-            const int q = 2 * (cc & 3), swap = (cc >> 2) & 1;
-            *reinterpret_cast<uint4*>(g + swz<128>(r & 7, q + swap)) = swap ? h[1] : h[0];
-            *reinterpret_cast<uint4*>(g + swz<128>(r & 7, q + 1 - swap)) = swap ? h[0] : h[1];
+          if (!empty) {
+            uint8_t* dst = gbase + GG::OFF_RING + e * TILE;
+#pragma unroll
+            for (int i = 0; i < ITER; ++i) {
+              if (PPI * i + pg0 >= np) continue;
+              const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+              const uint4 h0 = make_uint4(e4m3x2_to_f16x2(w[0]), e4m3x2_to_f16x2(w[0] >> 16), e4m3x2_to_f16x2(w[1]),
+                                          e4m3x2_to_f16x2(w[1] >> 16));
+              const uint4 h1 = make_uint4(e4m3x2_to_f16x2(w[2]), e4m3x2_to_f16x2(w[2] >> 16), e4m3x2_to_f16x2(w[3]),
+                                          e4m3x2_to_f16x2(w[3] >> 16));
+              *reinterpret_cast<uint4*>(dst + to0 + PPI * i * PAGE) = swap ? h1 : h0;
+              *reinterpret_cast<uint4*>(dst + to1 + PPI * i * PAGE) = swap ? h0 : h1;
+            }
+            fence_proxy_async_smem();
           }
-          fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(full_bar(e));
-            if (b >= 0) mbar_arrive(rawempty_bar(er));
+            if (!empty) mbar_arrive(rawempty_bar(er));
           }
-          if (b >= 0) ++nraw;
         }
-      }
     }
   } else if (warp < 2) {
     // =========================== product issuers =============================
