@@ -281,7 +281,7 @@ int decode_window(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
 
 // ------------------------------------------------------------ shared prefixes
 constexpr int kMinSharedPages = 1;
-constexpr int kMinSharedSteps = 1;
+constexpr int kStepCost = 1900, kPageCost = 270;   // ns
 
 struct SharedPlan {
   HostSplitPlan split;
@@ -371,6 +371,7 @@ int decode_shared(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
   sp.skip = reinterpret_cast<const int32_t*>(wsb + pl.skip);
   sp.whole_row0 = static_cast<int64_t>(pl.split.rows);
 
+  const bool pdl = !(opts && opts->disable_pdl);
   SharedParams hp = {};
   hp.q = sp.q;
   hp.q_stride_t = sp.q_stride_t;
@@ -390,7 +391,13 @@ int decode_shared(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
   hp.Hkv = sp.Hkv;
   hp.min_pages = kMinSharedPages;
   hp.split_boxes = split_k;
-  hp.min_steps = kMinSharedSteps;
+  hp.ctas = pl.grid;
+  hp.own_ctas = pl.split.grid;
+  // Both grids are then one CTA an SM at most, the plan's shares add up to the SMs, and the
+  // split kernel may start when the plan is made.
+  hp.beside = pdl && pl.grid == dev.num_sms && pl.split.grid == dev.num_sms;
+  hp.step_cost = kStepCost;
+  hp.page_cost = kPageCost;
   hp.scale_log2 = sp.scale_log2;
   hp.wait_ns = sp.wait_ns;
   hp.err = dev.status;
@@ -408,12 +415,10 @@ int decode_shared(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
   mp.totals = hp.totals;
   mp.pre_ml = hp.ws_ml;
   mp.pre_o = hp.ws_o;
-  mp.pre_grid = pl.grid;
-  mp.pre_min_steps = hp.min_steps;
+  sp.own_ctas = &hp.totals->own_ctas;
 
   Events ev;
   if ((st = events_of(opts, stream, &ev)) != PA_OK) return st;
-  const bool pdl = !(opts && opts->disable_pdl);
   cudaError_t e;
   if ((st = record(ev.start, ev, stream)) != PA_OK) return st;
   if ((e = launch_shared_plan(hp, pdl && !ev.start, stream)) != cudaSuccess)

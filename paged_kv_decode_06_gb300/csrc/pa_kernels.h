@@ -78,10 +78,12 @@ struct SplitParams {
   int32_t seg_cost;
   // windows with first tokens that stay visible (Walk::kFirst)
   int32_t first_tokens;
-  // sequences behind a shared prefix (Walk::kOwn): pages each skips (int32 [B]), and the
-  // row of ws_ml / ws_o from which rows of whole units stand by (token, query head)
+  // sequences behind a shared prefix (Walk::kOwn): pages each skips (int32 [B]), the row of
+  // ws_ml / ws_o from which rows of whole units stand by (token, query head), and the number
+  // of CTAs that take part (on the device)
   const int32_t* skip;
   int64_t whole_row0;
+  const int32_t* own_ctas;
 };
 
 struct MergeParams {
@@ -115,13 +117,12 @@ struct MergeRowsParams : MergeParams {
   const int32_t* skip;
   int64_t whole_row0;
   // a shared prefix: the group that each sequence takes part in (-1: none), the groups,
-  // and the prefix kernel's partial rows, grid and least steps a CTA
+  // and the prefix kernel's partial rows
   const int32_t* seq_group;
   const SharedGroup* groups;
   const SharedTotals* totals;
   const float2* pre_ml;
   const float* pre_o;
-  int32_t pre_grid, pre_min_steps;
 };
 cudaError_t launch_merge_rows(int head_dim, bool shared, const MergeRowsParams& p, int units, int rows, bool wide,
                               bool pdl, cudaStream_t stream);

@@ -43,19 +43,20 @@ __global__ void __launch_bounds__(kRowThreads) pa_merge_rows_kernel(const MergeR
   const int u = blockIdx.x;
   const int i = u / p.NC, c = u - i * p.NC;
   const int hh = row / p.R_max, rho = row - hh * p.R_max;
-  // (row-uniform branches: a row is a warp or the block)
-  int t0 = i, qn = 1;
-  if (p.qsl != nullptr) {
-    t0 = p.qsl[i];
-    qn = p.qsl[i + 1] - t0;
-  }
-  if (row >= p.HC * p.R_max || qn < 1 || qn > p.max_qlen || t0 < 0 || t0 > p.num_tokens - qn || rho >= p.G * qn) return;
+  if (row >= p.HC * p.R_max) return;
+  // (row-uniform branches: a row is a group of warps or the block)
+  // what does not depend on another load, in one go
+  const int t0 = p.qsl != nullptr ? p.qsl[i] : i, qn = p.qsl != nullptr ? p.qsl[i + 1] - t0 : 1;
+  const int L = p.seq_lens[i], skip = kShared ? p.skip[i] : 0, g = kShared ? p.seq_group[i] : -1;
+  const int4 d = p.ws_unit[u];
+  SharedTotals totals = {};
+  if constexpr (kShared) totals = *p.totals;
+  if (qn < 1 || qn > p.max_qlen || t0 < 0 || t0 > p.num_tokens - qn || rho >= p.G * qn) return;
   const int t = t0 + rho / p.G, h = c * p.HC + hh, hq = h * p.G + rho % p.G;
-  const View view = view_of<WALK>(p, p.seq_lens[i], qn, kShared ? p.skip[i] : 0);
+  const View view = view_of<WALK>(p, L, qn, skip);
   int gf = 0, nparts = 0, tail = 0, npre = 0, single = 0;
   int64_t pre0 = 0, pre_slot = 0;
   if (view.n > 0) {
-    const int4 d = p.ws_unit[u];
     gf = d.x;
     nparts = d.y & 0x3fffffff;
     tail = (d.y >> 30) & 1;
@@ -65,11 +66,10 @@ __global__ void __launch_bounds__(kRowThreads) pa_merge_rows_kernel(const MergeR
     if (!kShared && nparts == 1) return;             // finished by its CTA
   }
   if constexpr (kShared) {
-    const int g = p.seq_group[i];
     if (g >= 0) {
       const SharedGroup sg = p.groups[g];
-      const int64_t steps = p.totals->steps;
-      const int ng = shared_ctas(steps, p.pre_grid, p.pre_min_steps);
+      const int64_t steps = totals.steps;
+      const int ng = totals.ctas;
       const int rg = (t - sg.t0) * p.G + rho % p.G;
       const int pair = rg / kSharedPair;
       const int64_t a = sg.step0 + static_cast<int64_t>(h) * sg.steps_head + static_cast<int64_t>(pair) * sg.blocks;

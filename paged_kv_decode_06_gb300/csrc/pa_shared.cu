@@ -157,7 +157,25 @@ __global__ void __launch_bounds__(kPlanThreads) pa_shared_plan_kernel(const Shar
     step0 += all_steps;
     row0 += all_rows;
   }
+  // The SMs for each part, in proportion to its work.
+  int64_t own = 0, all_own;
+  if (p.beside)
+    for (int i = tid; i < p.num_seqs; i += kPlanThreads) {
+      const int L = p.seq_lens[i];
+      own += max(0, (L > 0 ? min((L - 1) / kPage + 1, p.max_blocks) : 0) - p.skip[i]);
+    }
+  block_scan(own, s_warp, &all_own);
   if (tid == 0) {
+    int64_t n = p.ctas;
+    p.totals->own_ctas = p.own_ctas;
+    if (p.beside) {
+      const double a = static_cast<double>(step0) * p.step_cost;
+      const double b = static_cast<double>(all_own) * p.Hkv * p.page_cost;
+      if (all_own > 0 && step0 > 0) n = min(p.ctas - 1, max(1, static_cast<int>(p.ctas * (a / (a + b)) + 0.5)));
+      if (n > step0) n = step0;
+      p.totals->own_ctas = max(1, min(p.own_ctas, p.ctas - static_cast<int>(n)));
+    }
+    p.totals->ctas = static_cast<int32_t>(n < step0 ? n : step0);
     p.totals->steps = step0;
     p.totals->rows = row0;
   }
@@ -374,7 +392,7 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
   grid_dependency_wait();
   grid_launch_dependents();
   const int64_t X = p.totals->steps;
-  const int ng = X > 0 ? shared_ctas(X, gridDim.x, p.min_steps) : 0;
+  const int ng = p.totals->ctas;
   const int cta = blockIdx.x;
   if (cta >= ng) return;
   const int64_t from = cta * X / ng, to = (cta + 1) * X / ng;

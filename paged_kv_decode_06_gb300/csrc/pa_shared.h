@@ -8,6 +8,9 @@
 // blocks for the single tile.  Steps stand end to end in (group, head, pair, block)
 // order, X in all; CTA c of the NG in use takes [c X / NG, (c + 1) X / NG).
 //
+// The sequences' own pages are attended beside the shared ones, by the split kernel on the
+// SMs that the prefix kernel leaves: the plan cuts the SMs in two by the work of each.
+//
 // A CTA leaves partial rows for each piece it holds: piece (pair, CTA c) at rows row0 +
 // 256 c of the pair's row0 = the padded rows of all pairs before it, so that no two pieces
 // meet: a next pair starts at least its predecessor's rows, a next CTA 256 rows further.
@@ -40,6 +43,8 @@ struct SharedGroup {
 struct SharedTotals {
   int64_t steps;
   int64_t rows;
+  int32_t ctas;         // CTAs that take the steps
+  int32_t own_ctas;     // CTAs that take the sequences' own pages
 };
 
 __host__ __device__ inline bool shared_single(const SharedGroup& g, int pair) {
@@ -48,13 +53,12 @@ __host__ __device__ inline bool shared_single(const SharedGroup& g, int pair) {
 __host__ __device__ inline int shared_steps(const SharedGroup& g, int pair) {
   return shared_single(g, pair) ? (g.blocks + 1) / 2 : g.blocks;
 }
-// CTAs in use, and the CTA that holds step x.
-__host__ __device__ inline int shared_ctas(int64_t steps, int grid, int min_steps) {
-  const int64_t n = (steps + min_steps - 1) / min_steps;
-  return static_cast<int>(n < 1 ? 1 : (n < grid ? n : grid));
-}
+// The CTA of ng that holds step x (64-bit divisions only where they are needed).
 __host__ __device__ inline int shared_cta_of(int64_t x, int64_t steps, int ng) {
-  return static_cast<int>(((x + 1) * ng - 1) / steps);
+  const int64_t y = (x + 1) * ng - 1;
+  if (y < (int64_t(1) << 32) && steps < (int64_t(1) << 32))
+    return static_cast<int>(static_cast<uint32_t>(y) / static_cast<uint32_t>(steps));
+  return static_cast<int>(y / steps);
 }
 
 struct SharedParams {
@@ -68,7 +72,10 @@ struct SharedParams {
   const int32_t* shared_lens; // [groups]
   int32_t num_seqs, num_tokens, num_groups, max_qlen, max_blocks, num_pages, G, Hkv;
   int32_t min_pages;          // fewer shared pages are left to the sequences
-  int32_t min_steps;          // steps a CTA at least
+  int32_t ctas;               // CTAs of the prefix kernel
+  int32_t own_ctas;           // CTAs of the split kernel
+  int32_t beside;             // they run side by side on `ctas` SMs
+  int32_t step_cost, page_cost;   // time of a step, and of a sequence's page for one head, on one SM
   int32_t split_boxes;        // 128 features, bf16: heads are not contiguous, pages come in four boxes
   float scale_log2;
   uint64_t wait_ns;

@@ -686,6 +686,15 @@ __global__ void __launch_bounds__(kSplitMaxThreads, 1)
   const int warp = tid >> 5;
   const int lane = tid & 31;
   const int B = p.num_seqs;
+  int most = gridDim.x;
+  if constexpr (WALK == Walk::kOwn) {
+    // Runs beside the kernel of the shared part: that kernel lets this one start once it has
+    // seen the plan's kernel complete, and everything read here was there before.  (The fence
+    // drops what this SM may still hold of it from before.)  CTA 0 waits for it at the end.
+    __threadfence();
+    most = min(most, __ldcg(p.own_ctas));
+    if (static_cast<int>(blockIdx.x) >= most) return;
+  }
   if (tid == 0) {
     prefetch_tensormap(&tmap_k);
     prefetch_tensormap(&tmap_v);
@@ -713,7 +722,7 @@ __global__ void __launch_bounds__(kSplitMaxThreads, 1)
     fence_mbar_init();
   }
 
-  grid_dependency_wait();
+  if constexpr (WALK != Walk::kOwn) grid_dependency_wait();
 
   // ---- prologue: metadata to shared memory, pages per sequence, prefix -----
   page_prefix<kHole, WALK>(p, window, s_pre, s_len, s_qsl, s_scan, &s_total);
@@ -722,10 +731,11 @@ __global__ void __launch_bounds__(kSplitMaxThreads, 1)
   const int64_t X = static_cast<int64_t>(p.NC) * s_pre[B];
   int64_t ng64 = (X + p.min_pages - 1) / p.min_pages;
   if (ng64 < 1) ng64 = 1;
-  const int NG = static_cast<int>(ng64 < gridDim.x ? ng64 : gridDim.x);
+  const int NG = static_cast<int>(ng64 < most ? ng64 : most);
   grid_launch_dependents();
 
   const int g = blockIdx.x;
+  if (WALK == Walk::kOwn && g == 0 && X == 0) grid_dependency_wait();
   if (g >= NG || X == 0) return;
   const int64_t start = static_cast<int64_t>(g) * X / NG;
   const int64_t end = static_cast<int64_t>(g + 1) * X / NG;
@@ -804,6 +814,8 @@ __global__ void __launch_bounds__(kSplitMaxThreads, 1)
         ++round;
       }
     }
+    // (the merge, which waits for this grid, reads what the shared part's kernel leaves)
+    if (WALK == Walk::kOwn && g == 0) grid_dependency_wait();
     return;
   }
 
