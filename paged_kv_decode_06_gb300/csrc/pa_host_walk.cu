@@ -281,7 +281,12 @@ int decode_window(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
 
 // ------------------------------------------------------------ shared prefixes
 constexpr int kMinSharedPages = 1;
-constexpr int kStepCost = 1900, kPageCost = 270;   // ns
+// The time of a sequence's page for one head, in thousandths of a step's (pa_shared.h) on the
+// same SM.  Measured by a sweep: 64 sequences with 16 to 512 tokens of their own behind 8192,
+// 90 to 150 is best (52 us; 60: 52, 30: 65, 260: 58), 256 behind 32768, 120 (284 us; 90: 331,
+// 150: 288); 64 features, 60 (36 us; 30 and 90: 40); fp8, 90 (288 us; 60: 292, 120: 319).
+int page_cost(int64_t D, bool fp8) { return D == 64 ? 60 : fp8 ? 90 : 115; }
+constexpr int kStepCost = 1000;
 
 struct SharedPlan {
   HostSplitPlan split;
@@ -397,7 +402,7 @@ int decode_shared(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
   // split kernel may start when the plan is made.
   hp.beside = pdl && pl.grid == dev.num_sms && pl.split.grid == dev.num_sms;
   hp.step_cost = kStepCost;
-  hp.page_cost = kPageCost;
+  hp.page_cost = page_cost(s.D, s.esz == 1);
   hp.scale_log2 = sp.scale_log2;
   hp.wait_ns = sp.wait_ns;
   hp.err = dev.status;
