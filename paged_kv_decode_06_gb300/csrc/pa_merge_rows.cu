@@ -56,6 +56,7 @@ __global__ void __launch_bounds__(kRowThreads) pa_merge_rows_kernel(const MergeR
   const View view = view_of<WALK>(p, L, qn, skip);
   int gf = 0, nparts = 0, tail = 0, npre = 0, single = 0;
   int64_t pre0 = 0, pre_slot = 0;
+  int pre_rho = 0, pre_rows = 0;
   if (view.n > 0) {
     gf = d.x;
     nparts = d.y & 0x3fffffff;
@@ -77,9 +78,12 @@ __global__ void __launch_bounds__(kRowThreads) pa_merge_rows_kernel(const MergeR
       const int c1 = shared_cta_of(a + shared_steps(sg, pair) - 1, steps, ng);
       single = shared_single(sg, pair);
       npre = (c1 - c0 + 1) << single;
+      const int slot = single ? 0 : rg % kSharedPair / kSharedTile;
       pre0 = sg.row0 + static_cast<int64_t>(h) * sg.rows_head + static_cast<int64_t>(pair) * kSharedPair +
-             static_cast<int64_t>(c0) * kSharedPair + rg % kSharedPair;
+             static_cast<int64_t>(c0) * kSharedPair + slot * kSharedTile;
       pre_slot = single ? sg.last_rows : 0;
+      pre_rho = rg % kSharedTile;
+      pre_rows = shared_tile_rows(sg, pair, slot);
     }
   }
   const int total = nparts + npre;
@@ -95,20 +99,18 @@ __global__ void __launch_bounds__(kRowThreads) pa_merge_rows_kernel(const MergeR
       ml[k] = make_float2(-INFINITY, 0.f);
       o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (s >= total) continue;
-      const float2* mls = p.ws_ml;
-      const float* os = p.ws_o;
-      int64_t at;
       if (s < nparts) {
-        at = (static_cast<int64_t>(2 * (gf + s) + (s == 0 && tail ? 1 : 0)) * p.HC + hh) * p.R_max + rho;
+        int64_t at = (static_cast<int64_t>(2 * (gf + s) + (s == 0 && tail ? 1 : 0)) * p.HC + hh) * p.R_max + rho;
         if (kShared && nparts == 1) at = p.whole_row0 + static_cast<int64_t>(t) * p.Hq + hq;
+        ml[k] = p.ws_ml[at];
+        o[k] = *reinterpret_cast<const float4*>(p.ws_o + at * D + 4 * dq);
       } else {
+        // (a tile of partial rows holds chunk dq of all its rows side by side)
         const int k2 = s - nparts;
-        mls = p.pre_ml;
-        os = p.pre_o;
-        at = pre0 + static_cast<int64_t>(k2 >> single) * kSharedPair + ((k2 & single) ? pre_slot : 0);
+        const int64_t tile = pre0 + static_cast<int64_t>(k2 >> single) * kSharedPair + ((k2 & single) ? pre_slot : 0);
+        ml[k] = p.pre_ml[tile + pre_rho];
+        o[k] = *reinterpret_cast<const float4*>(p.pre_o + tile * D + 4 * (static_cast<int64_t>(dq) * pre_rows + pre_rho));
       }
-      ml[k] = mls[at];
-      o[k] = *reinterpret_cast<const float4*>(os + at * D + 4 * dq);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc_piece(mx, l, acc, ml[k], o[k]);

@@ -208,12 +208,12 @@ struct Geo2 {
 template <int D, bool FP8>
 struct PrefixGeo {
   static constexpr uint32_t TILE = Geo2<D>::TILE;
-  static constexpr int RING = D == 128 ? 4 : 8;          // even: a slot's entries of single tiles keep their places
+  static constexpr int RING = D == 128 ? (FP8 ? 3 : 4) : 8;
   static constexpr int SOFT0 = kIssuers + kLoaders + (FP8 ? kConverters : 0);
   static constexpr int THREADS = 32 * (SOFT0 + kSoftmaxWarps);
   static constexpr uint32_t OFF_RING = 2 * TILE;
   static constexpr uint32_t RAW = kKeys * D;             // fp8: codes of an entry
-  static constexpr int RAWS = FP8 ? (D == 128 ? 2 : 4) : 0;
+  static constexpr int RAWS = FP8 ? (D == 128 ? 4 : 8) : 0;
   static constexpr uint32_t OFF_RAW = OFF_RING + RING * TILE;
   static constexpr uint32_t OFF_BAR = OFF_RAW + RAWS * RAW;
   static constexpr uint32_t SMEM = OFF_BAR + 512;
@@ -284,10 +284,10 @@ __device__ __forceinline__ void after_wait(uint32_t (&r)[N]) {
   for (int e = 0; e < N; ++e) asm volatile("" : "+r"(r[e]));
 }
 
-// Block of `slot` in step s of a piece, or -1.
-__device__ __forceinline__ int block_of(const Piece& c, const SharedGroup& sg, int s, int slot) {
-  const int b = c.single ? 2 * s + slot : s;
-  return b < sg.blocks ? b : -1;
+// Blocks of a piece, [b0, b1).
+__device__ __forceinline__ int first_block(const Piece& c) { return c.single ? 2 * c.s0 : c.s0; }
+__device__ __forceinline__ int end_block(const Piece& c, const SharedGroup& sg) {
+  return c.single ? min(2 * c.s1, sg.blocks) : c.s1;
 }
 
 // Page ids of a group's blocks for a warp: those of four blocks, a lane each, and the four
@@ -312,14 +312,19 @@ struct PageIds {
   __device__ __forceinline__ int of(int b, int pg) const { return __shfl_sync(0xffffffffu, ids, (8 * b + pg) & 31); }
 };
 
-// Sub-blocks of a slot in a piece, and the pages of the last one.
+// Sub-blocks of a slot in a piece, and the pages of the last one.  A single tile's slots
+// take a half of each block's pages.
 __device__ __forceinline__ int subs_in(const Piece& c, const SharedGroup& sg, int slot, int& last) {
-  const int b1 = c.single ? min(2 * (c.s1 - 1) + slot, sg.blocks - 1 - ((sg.blocks - 1 - slot) & 1)) : c.s1 - 1;
-  const int b0 = c.single ? 2 * c.s0 + slot : c.s0;
-  if (b1 < b0) return 0;
-  const int np = min(kBlockPages, sg.pages - b1 * kBlockPages);
-  last = np > kSubPages ? np - kSubPages : np;
-  return ((b1 - b0) >> (c.single ? 1 : 0)) * 2 + (np > kSubPages ? 2 : 1);
+  const int b1 = end_block(c, sg), n = b1 - first_block(c);
+  const int np = min(kBlockPages, sg.pages - (b1 - 1) * kBlockPages);
+  if (!c.single) {
+    last = np > kSubPages ? np - kSubPages : np;
+    return 2 * n - (np > kSubPages ? 0 : 1);
+  }
+  last = kSubPages;
+  if (slot == 0) last = min(np, kSubPages);
+  else if (np > kSubPages) last = np - kSubPages;
+  return slot == 1 && np <= kSubPages ? n - 1 : n;
 }
 
 // One lane of a converged warp.
@@ -360,10 +365,9 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
   auto odone_bar = [&](int slot, uint32_t n) { return xb + 8u * (8 + 2 * slot + (n & 1)); };
   auto qfull_bar = [&](int slot) { return xb + 8u * (12 + slot); };
   auto drain_bar = [&](int slot) { return xb + 8u * (14 + slot); };
-  const uint32_t meet_bar = xb + 8u * 16;                           // the issuers, after each piece
-  auto rawfull_bar = [&](int e) { return xb + 8u * (17 + e); };     // fp8: codes of an entry
-  auto rawempty_bar = [&](int e) { return xb + 8u * (17 + RAWS + e); };
-  static_assert(2 * RING + 17 + 2 * RAWS <= 63, "barriers");
+  auto rawfull_bar = [&](int e) { return xb + 8u * (16 + e); };     // fp8: codes of an entry
+  auto rawempty_bar = [&](int e) { return xb + 8u * (16 + RAWS + e); };
+  static_assert(2 * RING + 16 + 2 * RAWS <= 63, "barriers");
   uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(gbase + GG::OFF_BAR + 504);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -377,7 +381,6 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
       mbar_init(rawfull_bar(e), kLoaders);
       mbar_init(rawempty_bar(e), kConverters);
     }
-    mbar_init(meet_bar, 2);
     for (int s = 0; s < 2; ++s) {
       for (int k = 0; k < 2; ++k) {
         mbar_init(sfull_bar(s, k), 1);
@@ -420,19 +423,15 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
     while (ok && wk.more()) {
       const Piece c = wk.next(p);
       ids.start(p, wk.sg);
-      for (int s = c.s0; ok && s < c.s1; ++s) {
-        // the step's entries: K blocks, then V blocks; one without a block is empty
-        const int nb = c.single ? 2 : 1;
-        for (int k = 0; k < 2 * nb; ++k) {
-          const bool is_v = k >= nb;
-          const int b = block_of(c, wk.sg, s, is_v ? k - nb : k);
-          if (FP8 && b < 0) continue;
-          const int np = b < 0 ? 0 : min(kBlockPages, wk.sg.pages - b * kBlockPages);
+      const int b1 = end_block(c, wk.sg);
+      for (int b = first_block(c); ok && b < b1; ++b) {
+        const int np = min(kBlockPages, wk.sg.pages - b * kBlockPages);
+        for (int is_v = 0; is_v < 2; ++is_v) {
           // boxes dealt over the warps, a lane each: a page, or (split boxes: heads that
           // are not contiguous) eight slots and 64 features of one
           const int per = !FP8 && NH == 2 && p.split_boxes ? 4 : 1;
           const int x = kLoaders * lane + me, pg = x / per, part = x - pg * per;
-          if (b >= 0) ids.turn_to(b >> 2);
+          ids.turn_to(b >> 2);
           const int page = ids.of(b, pg);
           if (round > 0 && !warp_wait(FP8 ? rawempty_bar(e) : empty_bar(e), (round - 1) & 1u, p.wait_ns)) {
             if (lane == 0) atomicOr(p.err, kErrTimeout);
@@ -485,49 +484,44 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
     const int q = 2 * (cc & 3), swap = (cc >> 2) & 1;
     const uint32_t to = static_cast<uint32_t>(pg0) * PAGE + (slot16 >> 3) * GROUP + (cc >> 2) * 1024u;
     const uint32_t to0 = to + swz<128>(slot16 & 7, q + swap), to1 = to + swz<128>(slot16 & 7, q + 1 - swap);
-    uint32_t n = 0, nraw = 0;
+    uint32_t n = 0;                                          // entries before
     bool ok = true;
     while (ok && wk.more()) {
       const Piece c = wk.next(p);
-      const int blocks = wk.sg.blocks, pages = wk.sg.pages, nb = c.single ? 2 : 1;
-      for (int s = c.s0; ok && s < c.s1; ++s)
-        for (int k = 0; k < 2 * nb; ++k, ++n) {
-          const int b = c.single ? 2 * s + (k & 1) : s;
-          const bool empty = b >= blocks;
+      const int pages = wk.sg.pages, b1 = end_block(c, wk.sg);
+      for (int b = first_block(c); ok && b < b1; ++b)
+        for (int k = 0; k < 2; ++k, ++n) {
           const int np = min(kBlockPages, pages - b * kBlockPages);
-          const int er = static_cast<int>(nraw % kRaws), e = static_cast<int>(n % RING);
-          if (!empty) ok = warp_wait(rawfull_bar(er), (nraw / kRaws) & 1u, p.wait_ns);
+          const int er = static_cast<int>(n % kRaws), e = static_cast<int>(n % RING);
+          ok = warp_wait(rawfull_bar(er), (n / kRaws) & 1u, p.wait_ns);
           uint4 v[ITER];
-          if (ok && !empty) {
+          if (ok) {
 #pragma unroll
             for (int i = 0; i < ITER; ++i)
               v[i] = *reinterpret_cast<const uint4*>(gbase + GG::OFF_RAW + er * GG::RAW + 16 * ct + 2048 * i);
-            ++nraw;
+            if (n >= RING) ok = warp_wait(empty_bar(e), (n / RING - 1) & 1u, p.wait_ns);
           }
-          if (ok && n >= RING) ok = warp_wait(empty_bar(e), (n / RING - 1) & 1u, p.wait_ns);
           if (!ok) {
             if (lane == 0) atomicOr(p.err, kErrTimeout);
             break;
           }
-          if (!empty) {
-            uint8_t* dst = gbase + GG::OFF_RING + e * TILE;
+          uint8_t* dst = gbase + GG::OFF_RING + e * TILE;
 #pragma unroll
-            for (int i = 0; i < ITER; ++i) {
-              if (PPI * i + pg0 >= np) continue;
-              const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-              const uint4 h0 = make_uint4(e4m3x2_to_f16x2(w[0]), e4m3x2_to_f16x2(w[0] >> 16), e4m3x2_to_f16x2(w[1]),
-                                          e4m3x2_to_f16x2(w[1] >> 16));
-              const uint4 h1 = make_uint4(e4m3x2_to_f16x2(w[2]), e4m3x2_to_f16x2(w[2] >> 16), e4m3x2_to_f16x2(w[3]),
-                                          e4m3x2_to_f16x2(w[3] >> 16));
-              *reinterpret_cast<uint4*>(dst + to0 + PPI * i * PAGE) = swap ? h1 : h0;
-              *reinterpret_cast<uint4*>(dst + to1 + PPI * i * PAGE) = swap ? h0 : h1;
-            }
-            fence_proxy_async_smem();
+          for (int i = 0; i < ITER; ++i) {
+            if (PPI * i + pg0 >= np) continue;
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            const uint4 h0 = make_uint4(e4m3x2_to_f16x2(w[0]), e4m3x2_to_f16x2(w[0] >> 16), e4m3x2_to_f16x2(w[1]),
+                                        e4m3x2_to_f16x2(w[1] >> 16));
+            const uint4 h1 = make_uint4(e4m3x2_to_f16x2(w[2]), e4m3x2_to_f16x2(w[2] >> 16), e4m3x2_to_f16x2(w[3]),
+                                        e4m3x2_to_f16x2(w[3] >> 16));
+            *reinterpret_cast<uint4*>(dst + to0 + PPI * i * PAGE) = swap ? h1 : h0;
+            *reinterpret_cast<uint4*>(dst + to1 + PPI * i * PAGE) = swap ? h0 : h1;
           }
+          fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(full_bar(e));
-            if (!empty) mbar_arrive(rawempty_bar(er));
+            mbar_arrive(rawempty_bar(er));
           }
         }
     }
@@ -539,27 +533,23 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
     const uint64_t qd = umma_sdesc_sw128(warp_uniform(base + slot * TILE), 16u, GROUP);
     const uint32_t tS = warp_uniform(tbase + kColS + 128u * slot), tO = warp_uniform(tbase + kColO + 128u * slot);
     uint32_t entries = 0;          // ring entries of the pieces before
-    uint32_t tiles = 0, ns = 0, npv = 0, pieces = 0;   // query tiles seen, S and P V products, pieces
+    uint32_t tiles = 0, ns = 0, npv = 0;   // query tiles seen, S and P V products
     bool ok = true;
     while (ok && wk.more()) {
       const Piece c = wk.next(p);
       int last = 0;
       const int subs = subs_in(c, wk.sg, slot, last);
-      // An entry is free once both issuers' products have read it; of a single tile, whose
-      // entries only one uses, that one commits twice.
-      auto release = [&](uint32_t at) {
-        umma_commit(empty_bar(at));
-        if (c.single) umma_commit(empty_bar(at));
-      };
-      // ring entry of sub-block i's K or V
-      auto entry = [&](int i, int v) {
-        return entries + (c.single ? 4u * (i >> 1) + 2u * v + slot : 2u * (i >> 1) + v);
-      };
+      // Ring entry of sub-block i's K or V.  It is free once both issuers' products have
+      // read it: each commits at its last sub-block of the entry.
+      auto entry = [&](int i, int v) { return entries + 2u * (c.single ? i : i >> 1) + v; };
+      auto half_of = [&](int i) { return c.single ? slot : i & 1; };
+      auto opens = [&](int i) { return c.single || (i & 1) == 0; };
+      auto closes = [&](int i) { return c.single || (i & 1) == 1 || i == subs - 1; };
       auto issue_s = [&](int i) -> bool {
         const uint32_t e = entry(i, 0), at = e % RING;
-        const int part = i & 1;
+        const int part = half_of(i);
         if (i == 0 && !warp_wait(qfull_bar(slot), tiles++ & 1u, p.wait_ns)) return false;
-        if (part == 0 && !warp_wait(full_bar(at), (e / RING) & 1u, p.wait_ns)) return false;
+        if (opens(i) && !warp_wait(full_bar(at), (e / RING) & 1u, p.wait_ns)) return false;
         tc_fence_after();
         const uint64_t kd = umma_sdesc_sw128(warp_uniform(ring0 + at * TILE + part * (kSubPages * PAGE)), 16u, GROUP);
         const int np = i == subs - 1 ? last : kSubPages;
@@ -572,7 +562,7 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
             umma_ss(d, qd + off, kd + off, idesc, k > 0);
           }
           umma_commit(sfull_bar(slot, ns));
-          if (part == 1 || i == subs - 1) release(at);
+          if (closes(i)) umma_commit(empty_bar(at));
         }
         __syncwarp();
         ++ns;
@@ -580,8 +570,8 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
       };
       auto issue_pv = [&](int i) -> bool {
         const uint32_t e = entry(i, 1), at = e % RING;
-        const int part = i & 1;
-        if ((part == 0 && !warp_wait(full_bar(at), (e / RING) & 1u, p.wait_ns)) ||
+        const int part = half_of(i);
+        if ((opens(i) && !warp_wait(full_bar(at), (e / RING) & 1u, p.wait_ns)) ||
             !warp_wait(pfull_bar(slot, npv), (npv >> 1) & 1u, p.wait_ns))
           return false;
         tc_fence_after();
@@ -593,7 +583,7 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
           for (int k = 0; k < kSubPages; ++k)                // (a piece's first overwrites O)
             if (k < np) umma_ts(tO, a + 8u * k, vd + static_cast<uint64_t>((k * PAGE) >> 4), idesc_o, k > 0 || i > 0);
           umma_commit(odone_bar(slot, npv));
-          if (part == 1 || i == subs - 1) release(at);
+          if (closes(i)) umma_commit(empty_bar(at));
         }
         __syncwarp();
         ++npv;
@@ -603,25 +593,16 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
       // (Not into the next piece: its K may come into the ring only once this V has left.)
       ok = (subs < 1 || issue_s(0)) && (subs < 2 || issue_s(1));
       for (int i = 0; ok && i < subs; ++i) ok = issue_pv(i) && (i + 2 >= subs || issue_s(i + 2));
-      if (ok && c.single && slot == 1 && block_of(c, wk.sg, c.s1 - 1, 1) < 0) {
-        // the single tile's last step has no block for this slot: its entries are empty
+      const uint32_t blocks = end_block(c, wk.sg) - first_block(c);
+      if (ok && c.single && static_cast<uint32_t>(subs) < blocks) {
+        // a last block without pages for this slot
         for (int v = 0; ok && v < 2; ++v) {
-          const uint32_t e = entries + 4u * (c.s1 - 1 - c.s0) + 2u * v + 1u, at = e % RING;
+          const uint32_t e = entry(subs, v), at = e % RING;
           ok = warp_wait(full_bar(at), (e / RING) & 1u, p.wait_ns);
-          if (ok && lane == 0) {
-            mbar_arrive(empty_bar(at));
-            mbar_arrive(empty_bar(at));
-          }
+          if (ok && lane == 0) mbar_arrive(empty_bar(at));
         }
       }
-      entries += (c.single ? 4u : 2u) * static_cast<uint32_t>(c.s1 - c.s0);
-      // Both issuers have seen all of the piece's entries before either waits for the
-      // next's: a full barrier's earlier phase is known to be complete.
-      if (ok) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(meet_bar);
-        ok = warp_wait(meet_bar, pieces++ & 1u, p.wait_ns);
-      }
+      entries += 2 * blocks;
     }
     if (!ok && lane == 0) atomicOr(p.err, kErrTimeout);
     // every product must be complete before tensor memory is freed
@@ -638,8 +619,9 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
     uint32_t n = 0;                                           // sub-blocks of the pieces before
     float next_scale = 1.f;                                   // fp8: what the staged row was divided by
     bool ok = true;
-    // this thread's query row of a piece into the slot's tile (rows past the pair's are zero).  fp8 caches: in f16, divided by a power of two that leaves the
-    // largest element in [1, 2).
+    // this thread's query row of a piece into the slot's tile (rows past the pair's are
+    // zero).  fp8 caches: in f16, divided by a power of two that leaves the largest element
+    // in [1, 2).
     auto stage_q = [&](const Piece& c, const SharedGroup& sg) {
       const int r = c.pair * kSharedPair + (c.single ? 0 : slot * kSharedTile) + rho;
       const bool have = r < sg.rows;
@@ -647,32 +629,30 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
       if (have)
         src = reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(sg.t0 + r / p.G) * p.q_stride_t +
                                              static_cast<int64_t>(c.head * p.G + r % p.G) * D);
-      float div = 1.f;
+      uint4 v[D / 8];
+#pragma unroll
+      for (int ch = 0; ch < D / 8; ++ch) v[ch] = have ? src[ch] : make_uint4(0u, 0u, 0u, 0u);   // 8 features
       if constexpr (FP8) {
         uint32_t mx = 0;
-#pragma unroll 4
-        for (int k = 0; k < D / 8; ++k) {
-          const uint4 v = have ? src[k] : make_uint4(0u, 0u, 0u, 0u);
-          mx = max_u16x2(mx, max_u16x2(max_u16x2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                       max_u16x2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-        }
+#pragma unroll
+        for (int ch = 0; ch < D / 8; ++ch)
+          mx = max_u16x2(mx, max_u16x2(max_u16x2(v[ch].x & 0x7FFF7FFFu, v[ch].y & 0x7FFF7FFFu),
+                                       max_u16x2(v[ch].z & 0x7FFF7FFFu, v[ch].w & 0x7FFF7FFFu)));
         const int ex = static_cast<int>((max(mx & 0xFFFFu, mx >> 16) >> 7) & 0xFFu) - 127;
         const int e2 = ex == 128 ? 0 : min(126, max(-100, ex));   // (NaN and infinities stay as they are)
         next_scale = __uint_as_float(static_cast<uint32_t>(e2 + 127) << 23);
-        div = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+        const float div = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+#pragma unroll
+        for (int ch = 0; ch < D / 8; ++ch)
+          v[ch] = make_uint4(pack_f16(bf16_lo(v[ch].x) * div, bf16_hi(v[ch].x) * div),
+                             pack_f16(bf16_lo(v[ch].y) * div, bf16_hi(v[ch].y) * div),
+                             pack_f16(bf16_lo(v[ch].z) * div, bf16_hi(v[ch].z) * div),
+                             pack_f16(bf16_lo(v[ch].w) * div, bf16_hi(v[ch].w) * div));
       }
       uint8_t* dst = gbase + slot * TILE + (rho >> 3) * GROUP;
 #pragma unroll
-      for (int ch = 0; ch < D / 8; ++ch) {                    // 8-feature chunks
-        uint4 v = have ? src[ch] : make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (FP8) {
-          uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = pack_f16(bf16_lo(w[e]) * div, bf16_hi(w[e]) * div);
-          v = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        *reinterpret_cast<uint4*>(dst + (ch >> 3) * 1024u + swz<128>(rho & 7, ch & 7)) = v;
-      }
+      for (int ch = 0; ch < D / 8; ++ch)
+        *reinterpret_cast<uint4*>(dst + (ch >> 3) * 1024u + swz<128>(rho & 7, ch & 7)) = v[ch];
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(qfull_bar(slot));
@@ -773,9 +753,12 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
       if (!ok) break;
       n += subs;
       const int done = subs;
-      const int64_t prow = sg.row0 + static_cast<int64_t>(c.head) * sg.rows_head +
-                           static_cast<int64_t>(c.pair) * kSharedPair + static_cast<int64_t>(cta) * kSharedPair +
-                           (c.single ? slot * sg.last_rows + rho : r);
+      // the slot's tile of partial rows: chunk d / 4 of all its rows, then the next chunk (a
+      // warp's stores are whole lines)
+      const int64_t tile0 = sg.row0 + static_cast<int64_t>(c.head) * sg.rows_head +
+                            static_cast<int64_t>(c.pair) * kSharedPair + static_cast<int64_t>(cta) * kSharedPair +
+                            slot * (c.single ? sg.last_rows : kSharedTile);
+      const int tile_rows = shared_tile_rows(sg, c.pair, slot);
       // the next piece's rows while this one's last products run: its Q K^T products are
       // complete (S of the last sub-block was read)
       const bool more = wk.more();
@@ -786,7 +769,7 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
         if (subs > 0) stage_q(c, sg);
       }
       if (done == 0) {
-        if (mine) p.ws_ml[prow] = make_float2(-INFINITY, 0.f);
+        if (mine) p.ws_ml[tile0 + rho] = make_float2(-INFINITY, 0.f);
       } else {
         if (!warp_wait(odone_bar(slot, n - 1), ((n - 1) >> 1) & 1u, p.wait_ns)) {
           ok = false;
@@ -794,7 +777,7 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
         }
         if (!idle) {
           tc_fence_after();
-          float* orow = p.ws_o + prow * D;
+          float* orow = p.ws_o + tile0 * D + 4 * rho;
 #pragma unroll
           for (int ch = 0; ch < D / 16; ++ch) {
             uint32_t o[16];
@@ -803,10 +786,11 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
             if (mine) {
 #pragma unroll
               for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<uint4*>(orow + 16 * ch + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                *reinterpret_cast<uint4*>(orow + (16 * ch + e) * tile_rows) =
+                    make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
           }
-          if (mine) p.ws_ml[prow] = make_float2(m, l);
+          if (mine) p.ws_ml[tile0 + rho] = make_float2(m, l);
           // (the slot's next P V, which overwrites O, is issued after this thread's next P)
           tc_fence_before();
         }

@@ -3,9 +3,8 @@
 //
 // The rows of one (group, KV head), G query heads of every query token of the group's
 // sequences, are cut into pairs of 128-row tiles, one tile a slot; a last pair of at most
-// 128 rows has one tile, which both slots take, each every other block of keys.  A step
-// is what the two slots do at once: one block of kSharedBlock keys for both tiles, or two
-// blocks for the single tile.  Steps stand end to end in (group, head, pair, block)
+// 128 rows has one tile, which both slots take, each a half of every block of keys.  A step
+// is one block of 128 keys for both tiles, or two blocks for the single tile.  Steps stand end to end in (group, head, pair, block)
 // order, X in all; CTA c of the NG in use takes [c X / NG, (c + 1) X / NG).
 //
 // The sequences' own pages are attended beside the shared ones, by the split kernel on the
@@ -13,7 +12,8 @@
 //
 // A CTA leaves partial rows for each piece it holds: piece (pair, CTA c) at rows row0 +
 // 256 c of the pair's row0 = the padded rows of all pairs before it, so that no two pieces
-// meet: a next pair starts at least its predecessor's rows, a next CTA 256 rows further.
+// meet: a next pair starts at least its predecessor's rows, a next CTA 256 rows further.  A
+// slot's tile of R rows holds chunk d / 4 of all R rows, then the next chunk.
 #pragma once
 
 #include <cuda.h>
@@ -52,6 +52,12 @@ __host__ __device__ inline bool shared_single(const SharedGroup& g, int pair) {
 }
 __host__ __device__ inline int shared_steps(const SharedGroup& g, int pair) {
   return shared_single(g, pair) ? (g.blocks + 1) / 2 : g.blocks;
+}
+// Rows of a slot's tile.
+__host__ __device__ inline int shared_tile_rows(const SharedGroup& g, int pair, int slot) {
+  const int rows = pair == g.pairs - 1 ? g.last_rows : kSharedPair;
+  if (rows <= kSharedTile) return rows;
+  return slot == 0 ? kSharedTile : rows - kSharedTile;
 }
 // The CTA of ng that holds step x (64-bit divisions only where they are needed).
 __host__ __device__ inline int shared_cta_of(int64_t x, int64_t steps, int ng) {
