@@ -281,12 +281,17 @@ int decode_window(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
 
 // ------------------------------------------------------------ shared prefixes
 constexpr int kMinSharedPages = 1;
-// The time of a sequence's page for one head, in thousandths of a step's (pa_shared.h) on the
-// same SM.  Measured by a sweep: 64 sequences with 16 to 512 tokens of their own behind 8192,
-// 90 to 150 is best (52 us; 60: 52, 30: 65, 260: 58), 256 behind 32768, 120 (284 us; 90: 331,
-// 150: 288); 64 features, 60 (36 us; 30 and 90: 40); fp8, 90 (288 us; 60: 292, 120: 319).
-int page_cost(int64_t D, bool fp8) { return D == 64 ? 60 : fp8 ? 90 : 115; }
-constexpr int kStepCost = 1000;
+// What the plan cuts the SMs by (nanoseconds on one SM).  Measured with 4 and 128 of 152 SMs
+// for one part: a step (pa_shared.h) takes 1.6 us (fp8 codes 2.3, of 64 features 1.75), a
+// page for one head and 16 query rows 0.165 us (64 features 0.06, fp8 0.064; 128, fp8,
+// 0.094), and a sequence about what three of its pages do.
+struct Costs {
+  int step, page;
+};
+Costs costs_of(int64_t D, bool fp8) {
+  if (D == 128) return fp8 ? Costs{2300, 94} : Costs{1600, 165};
+  return fp8 ? Costs{1750, 64} : Costs{1600, 59};
+}
 
 struct SharedPlan {
   HostSplitPlan split;
@@ -401,8 +406,10 @@ int decode_shared(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
   // Both grids are then one CTA an SM at most, the plan's shares add up to the SMs, and the
   // split kernel may start when the plan is made.
   hp.beside = pdl && pl.grid == dev.num_sms && pl.split.grid == dev.num_sms;
-  hp.step_cost = kStepCost;
-  hp.page_cost = page_cost(s.D, s.esz == 1);
+  const Costs cost = costs_of(s.D, s.esz == 1);
+  hp.step_cost = cost.step;
+  hp.page_cost = cost.page * ((sp.R_max + 15) / 16);
+  hp.unit_cost = 3 * hp.page_cost;
   hp.scale_log2 = sp.scale_log2;
   hp.wait_ns = sp.wait_ns;
   hp.err = dev.status;

@@ -30,6 +30,31 @@ __device__ __forceinline__ void acc_piece(float& mx, float& l, float4& acc, floa
   mx = nm;
 }
 
+// A row's pieces of a shared prefix: its tile's in every CTA that has some (both slots' of a
+// single tile).
+struct PrePieces {
+  int64_t row0;             // padded rows before the tile in the first CTA
+  int count, single, second;
+  int rho, rows;            // the row in its tile, the tile's rows
+  __device__ __forceinline__ void start(const SharedGroup& sg, const SharedTotals& all, int h, int rg) {
+    const int pair = rg / kSharedPair;
+    single = shared_single(sg, pair);
+    const int slot = single ? 0 : rg % kSharedPair / kSharedTile;
+    second = single ? sg.last_rows : slot * kSharedTile;      // (rows of the first slot's tile)
+    rho = rg % kSharedTile;
+    rows = shared_tile_rows(sg, pair, slot);
+    const int64_t a = sg.step0 + static_cast<int64_t>(h) * sg.steps_head + static_cast<int64_t>(pair) * sg.blocks;
+    const int c0 = shared_cta_of(a, all.steps, all.ctas);
+    const int c1 = shared_cta_of(a + shared_steps(sg, pair) - 1, all.steps, all.ctas);
+    count = (c1 - c0 + 1) << single;
+    row0 = sg.row0 + static_cast<int64_t>(h) * sg.rows_head + static_cast<int64_t>(pair + c0) * kSharedPair;
+  }
+  // The tile of partial rows of piece k.
+  __device__ __forceinline__ int64_t tile(int k) const {
+    return row0 + static_cast<int64_t>(k >> single) * kSharedPair + (!single || (k & 1) ? second : 0);
+  }
+};
+
 // TPR threads a row (32: a warp; else the block).
 template <int D, Walk WALK, int TPR>
 __global__ void __launch_bounds__(kRowThreads) pa_merge_rows_kernel(const MergeRowsParams p) {
@@ -54,9 +79,7 @@ __global__ void __launch_bounds__(kRowThreads) pa_merge_rows_kernel(const MergeR
   if (qn < 1 || qn > p.max_qlen || t0 < 0 || t0 > p.num_tokens - qn || rho >= p.G * qn) return;
   const int t = t0 + rho / p.G, h = c * p.HC + hh, hq = h * p.G + rho % p.G;
   const View view = view_of<WALK>(p, L, qn, skip);
-  int gf = 0, nparts = 0, tail = 0, npre = 0, single = 0;
-  int64_t pre0 = 0, pre_slot = 0;
-  int pre_rho = 0, pre_rows = 0;
+  int gf = 0, nparts = 0, tail = 0;
   if (view.n > 0) {
     gf = d.x;
     nparts = d.y & 0x3fffffff;
@@ -66,30 +89,17 @@ __global__ void __launch_bounds__(kRowThreads) pa_merge_rows_kernel(const MergeR
     if (gf < 0 || nparts < 1 || nparts > p.split_grid - gf) return;
     if (!kShared && nparts == 1) return;             // finished by its CTA
   }
+  const int dq = lane % LPD, pg = lane / LPD;
+  PrePieces pre = {};
   if constexpr (kShared) {
     if (g >= 0) {
       const SharedGroup sg = p.groups[g];
-      const int64_t steps = totals.steps;
-      const int ng = totals.ctas;
-      const int rg = (t - sg.t0) * p.G + rho % p.G;
-      const int pair = rg / kSharedPair;
-      const int64_t a = sg.step0 + static_cast<int64_t>(h) * sg.steps_head + static_cast<int64_t>(pair) * sg.blocks;
-      const int c0 = shared_cta_of(a, steps, ng);
-      const int c1 = shared_cta_of(a + shared_steps(sg, pair) - 1, steps, ng);
-      single = shared_single(sg, pair);
-      npre = (c1 - c0 + 1) << single;
-      const int slot = single ? 0 : rg % kSharedPair / kSharedTile;
-      pre0 = sg.row0 + static_cast<int64_t>(h) * sg.rows_head + static_cast<int64_t>(pair) * kSharedPair +
-             static_cast<int64_t>(c0) * kSharedPair + slot * kSharedTile;
-      pre_slot = single ? sg.last_rows : 0;
-      pre_rho = rg % kSharedTile;
-      pre_rows = shared_tile_rows(sg, pair, slot);
+      pre.start(sg, totals, h, (t - sg.t0) * p.G + rho % p.G);
     }
   }
-  const int total = nparts + npre;
-  const int dq = lane % LPD, pg = lane / LPD;
   float mx = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int total = nparts + (kShared ? pre.count : 0);
   for (int s0 = pg; s0 < total; s0 += 4 * PG) {
     float2 ml[4];
     float4 o[4];
@@ -106,10 +116,9 @@ __global__ void __launch_bounds__(kRowThreads) pa_merge_rows_kernel(const MergeR
         o[k] = *reinterpret_cast<const float4*>(p.ws_o + at * D + 4 * dq);
       } else {
         // (a tile of partial rows holds chunk dq of all its rows side by side)
-        const int k2 = s - nparts;
-        const int64_t tile = pre0 + static_cast<int64_t>(k2 >> single) * kSharedPair + ((k2 & single) ? pre_slot : 0);
-        ml[k] = p.pre_ml[tile + pre_rho];
-        o[k] = *reinterpret_cast<const float4*>(p.pre_o + tile * D + 4 * (static_cast<int64_t>(dq) * pre_rows + pre_rho));
+        const int64_t tile = pre.tile(s - nparts);
+        ml[k] = p.pre_ml[tile + pre.rho];
+        o[k] = *reinterpret_cast<const float4*>(p.pre_o + tile * D + 4 * (static_cast<int64_t>(dq) * pre.rows + pre.rho));
       }
     }
 #pragma unroll

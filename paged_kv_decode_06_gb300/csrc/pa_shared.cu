@@ -20,10 +20,8 @@
 // 64 keys is there when a softmax ends.  O is rescaled only where the running maximum grew
 // by more than 2^8.
 //
-// Order in the tensor pipe: one thread issues all of a slot's products, and they run in
-// that order, so S may overwrite the P that the P V before it reads, two sub-blocks back.
-// A commit covers all of a thread's earlier products: once a softmax warp sees S of
-// sub-block b, P V of b - 2 has left its part in O.
+// S of a sub-block overwrites the P of two before once P V has read it; so a softmax warp
+// that sees S of sub-block b knows P V of b - 2 in O.
 //
 // Waits are bounded, and each is made once a phase in order, so its barrier is never more
 // than one phase behind (mbarrier parities cannot tell further).
@@ -157,36 +155,39 @@ __global__ void __launch_bounds__(kPlanThreads) pa_shared_plan_kernel(const Shar
     step0 += all_steps;
     row0 += all_rows;
   }
-  // The SMs for each part, in proportion to its work.
+  // The SMs for each part, in proportion to its work; some more for the sequences' own pages,
+  // whose many short walks pay more for memory the longer the other part runs, and four at
+  // least (8 sequences of 500 tokens behind 65536: 57 us with one, 46 with four, 48 with 28).
   int64_t own = 0, all_own;
   if (p.beside)
     for (int i = tid; i < p.num_seqs; i += kPlanThreads) {
       const int L = p.seq_lens[i];
-      own += max(0, (L > 0 ? min((L - 1) / kPage + 1, p.max_blocks) : 0) - p.skip[i]);
+      const int n = (L > 0 ? min((L - 1) / kPage + 1, p.max_blocks) : 0) - p.skip[i];
+      if (n > 0) own += static_cast<int64_t>(n) * p.page_cost + p.unit_cost;
     }
   block_scan(own, s_warp, &all_own);
+  int n = p.ctas;
+  if (p.beside && all_own > 0 && step0 > 0) {
+    const float a = static_cast<float>(step0) * p.step_cost, b = static_cast<float>(all_own) * p.Hkv;
+    const float each = (a + b) / p.ctas;                     // ns
+    const float more = 0.2f * a / (a + b) * fmaxf(0.f, each - 20000.f);
+    n = min(max(1, p.ctas - 4), max(1, p.ctas - static_cast<int>(b / (each - more) + 0.5f)));
+  }
+  if (n > step0) n = static_cast<int>(step0);
   if (tid == 0) {
-    int64_t n = p.ctas;
-    p.totals->own_ctas = p.own_ctas;
-    if (p.beside) {
-      const double a = static_cast<double>(step0) * p.step_cost;
-      const double b = static_cast<double>(all_own) * p.Hkv * p.page_cost;
-      if (all_own > 0 && step0 > 0) n = min(p.ctas - 1, max(1, static_cast<int>(p.ctas * (a / (a + b)) + 0.5)));
-      if (n > step0) n = step0;
-      p.totals->own_ctas = max(1, min(p.own_ctas, p.ctas - static_cast<int>(n)));
-    }
-    p.totals->ctas = static_cast<int32_t>(n < step0 ? n : step0);
     p.totals->steps = step0;
     p.totals->rows = row0;
+    p.totals->ctas = n;
+    p.totals->own_ctas = p.beside ? max(1, min(p.own_ctas, p.ctas - n)) : p.own_ctas;
   }
 }
 
 // ------------------------------------------------------------- prefix kernel
-constexpr int kIssuers = 2;               // warps 0, 1: a slot's products each
-constexpr int kLoaders = 2;               // warps 2, 3
-constexpr int kConverters = 4;            // fp8 caches: warps 4 .. 7
-constexpr int kSoftmaxWarps = 8;          // a slot's four: a thread a row
-constexpr int kBlockPages = kSharedBlockPages;   // a ring entry: K or V of 128 keys
+constexpr int kIssuers = 4;               // warps 0, 1: a slot's S = Q K^T each, 2, 3: its P V
+constexpr int kLoaders = 2;               // warps 4, 5 (6, 7: none)
+constexpr int kConverter0 = 8, kConverters = 8;   // fp8 caches: warps 8 .. 11 for K, 12 .. 15 for V
+constexpr int kSoftmaxWarps = 8;          // the last: a slot's four, a thread a row
+constexpr int kBlockPages = kSharedBlockPages;   // K or V of 128 keys in a place of its ring
 constexpr int kKeys = 16 * kBlockPages;
 constexpr int kSubPages = 4;              // a product and its softmax: 64 keys
 constexpr uint32_t kCols = 512;
@@ -208,22 +209,28 @@ struct Geo2 {
 template <int D, bool FP8>
 struct PrefixGeo {
   static constexpr uint32_t TILE = Geo2<D>::TILE;
-  static constexpr int RING = D == 128 ? (FP8 ? 3 : 4) : 8;
-  static constexpr int SOFT0 = kIssuers + kLoaders + (FP8 ? kConverters : 0);
+  static constexpr int KR = D == 128 ? (FP8 ? 1 : 2) : 4, VR = D == 128 ? 2 : 4;   // blocks of K, of V
+  static constexpr int SOFT0 = FP8 ? kConverter0 + kConverters : kConverter0;
   static constexpr int THREADS = 32 * (SOFT0 + kSoftmaxWarps);
+  // Registers a thread of each role's warps; together what the launch has (4 x 128 and 6 x 80
+  // of 128 threads: an increase beyond that would wait for ever)
+  static constexpr int R_ISSUE = FP8 ? 64 : 80, R_LOAD = FP8 ? 48 : 80, R_CONVERT = 56, R_SOFT = FP8 ? 128 : 176;
+  static_assert(FP8 ? R_ISSUE + R_LOAD + 2 * R_CONVERT + 2 * R_SOFT == 6 * 80 : R_ISSUE + R_LOAD + 2 * R_SOFT == 4 * 128,
+                "register shares");
   static constexpr uint32_t OFF_RING = 2 * TILE;
-  static constexpr uint32_t RAW = kKeys * D;             // fp8: codes of an entry
-  static constexpr int RAWS = FP8 ? (D == 128 ? 4 : 8) : 0;
-  static constexpr uint32_t OFF_RAW = OFF_RING + RING * TILE;
-  static constexpr uint32_t OFF_BAR = OFF_RAW + RAWS * RAW;
+  static constexpr uint32_t RAW = kKeys * D;             // fp8: codes of a block
+  static constexpr int RAWS = FP8 ? (D == 128 ? 2 : 4) : 0;   // code blocks of K, as many of V
+  static constexpr uint32_t OFF_RAW = OFF_RING + (KR + VR) * TILE;
+  static constexpr uint32_t OFF_BAR = OFF_RAW + 2 * RAWS * RAW;
   static constexpr uint32_t SMEM = OFF_BAR + 512;
 };
 
-// A piece: consecutive steps of one (group, head, pair) in this CTA.
+// A piece: consecutive blocks of one (group, head, pair) in this CTA.
 struct Piece {
-  int g, head, pair;
-  int s0, s1;          // steps of the pair, [s0, s1)
+  int head, pair;
+  int b0, b1;          // blocks, [b0, b1)
   bool single;
+  int64_t row0;        // padded rows before the pair's
 };
 
 // Walks this CTA's steps piece by piece; every warp runs one.
@@ -249,16 +256,17 @@ struct PieceWalker {
   __device__ __forceinline__ Piece next(const SharedParams& p) {
     while (sg.pages == 0 || x >= sg.step0 + static_cast<int64_t>(sg.steps_head) * p.Hkv) sg = p.groups[++g];
     Piece c;
-    c.g = g;
     const int64_t off = x - sg.step0;
     c.head = static_cast<int>(off / sg.steps_head);
-    const int in_head = static_cast<int>(off - static_cast<int64_t>(c.head) * sg.steps_head);
-    c.pair = min(in_head / sg.blocks, sg.pairs - 1);
-    c.s0 = in_head - c.pair * sg.blocks;
+    int at = static_cast<int>(off - static_cast<int64_t>(c.head) * sg.steps_head);
+    c.pair = min(at / sg.blocks, sg.pairs - 1);
+    at -= c.pair * sg.blocks;
     c.single = shared_single(sg, c.pair);
-    const int n = shared_steps(sg, c.pair);
-    c.s1 = static_cast<int>(min(static_cast<int64_t>(n), c.s0 + (end - x)));
-    x += c.s1 - c.s0;
+    const int n = static_cast<int>(min(static_cast<int64_t>(shared_steps(sg, c.pair) - at), end - x));
+    c.b0 = c.single ? 2 * at : at;
+    c.b1 = c.single ? min(2 * (at + n), sg.blocks) : at + n;
+    c.row0 = sg.row0 + static_cast<int64_t>(c.head) * sg.rows_head + static_cast<int64_t>(c.pair) * kSharedPair;
+    x += n;
     return c;
   }
 };
@@ -282,12 +290,6 @@ __device__ __forceinline__ void after_wait(uint32_t (&r)[N]) {
   tmem_wait_ld();
 #pragma unroll
   for (int e = 0; e < N; ++e) asm volatile("" : "+r"(r[e]));
-}
-
-// Blocks of a piece, [b0, b1).
-__device__ __forceinline__ int first_block(const Piece& c) { return c.single ? 2 * c.s0 : c.s0; }
-__device__ __forceinline__ int end_block(const Piece& c, const SharedGroup& sg) {
-  return c.single ? min(2 * c.s1, sg.blocks) : c.s1;
 }
 
 // Page ids of a group's blocks for a warp: those of four blocks, a lane each, and the four
@@ -315,8 +317,8 @@ struct PageIds {
 // Sub-blocks of a slot in a piece, and the pages of the last one.  A single tile's slots
 // take a half of each block's pages.
 __device__ __forceinline__ int subs_in(const Piece& c, const SharedGroup& sg, int slot, int& last) {
-  const int b1 = end_block(c, sg), n = b1 - first_block(c);
-  const int np = min(kBlockPages, sg.pages - (b1 - 1) * kBlockPages);
+  const int n = c.b1 - c.b0;
+  const int np = min(kBlockPages, sg.pages - (c.b1 - 1) * kBlockPages);
   if (!c.single) {
     last = np > kSubPages ? np - kSubPages : np;
     return 2 * n - (np > kSubPages ? 0 : 1);
@@ -343,43 +345,55 @@ __device__ __forceinline__ uint32_t idesc_f16(int M, int N, bool b_mn_major) {
   return umma_idesc_bf16(M, N, b_mn_major) & ~((1u << 7) | (1u << 10));
 }
 
+template <int N>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 template <int D, bool FP8>
 __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
     pa_shared_prefix_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                             const SharedParams p) {
   using GG = PrefixGeo<D, FP8>;
   constexpr int NH = D / 64;
-  constexpr int RING = GG::RING, RAWS = GG::RAWS;
+  constexpr int RING = GG::KR + GG::VR, RAWS = GG::RAWS;
   constexpr uint32_t TILE = GG::TILE, PAGE = Geo2<D>::PAGE, GROUP = Geo2<D>::GROUP;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* const gbase = smem_raw;
   const uint32_t base = smem_addr(smem_raw);
   const uint32_t ring0 = base + GG::OFF_RING;
   const uint32_t bar0 = base + GG::OFF_BAR;
-  auto full_bar = [&](int e) { return bar0 + 8u * e; };             // ring entries: K or V of a block
+  auto full_bar = [&](int e) { return bar0 + 8u * e; };             // rings' places: K blocks, V blocks
   auto empty_bar = [&](int e) { return bar0 + 8u * (RING + e); };
+  // place of the n-th K or V block of this CTA, and the phase of its barriers
+  auto place = [&](int is_v, uint32_t n) -> uint32_t { return is_v ? GG::KR + n % GG::VR : n % GG::KR; };
+  auto phase = [&](int is_v, uint32_t n) -> uint32_t { return is_v ? n / GG::VR : n / GG::KR; };
   const uint32_t xb = bar0 + 8u * (2 * RING);
   // of a slot: S of a sub-block (by its parity), its P, its P V done; query rows staged; all drained
   auto sfull_bar = [&](int slot, uint32_t n) { return xb + 8u * (2 * slot + (n & 1)); };
   auto pfull_bar = [&](int slot, uint32_t n) { return xb + 8u * (4 + 2 * slot + (n & 1)); };
   auto odone_bar = [&](int slot, uint32_t n) { return xb + 8u * (8 + 2 * slot + (n & 1)); };
   auto qfull_bar = [&](int slot) { return xb + 8u * (12 + slot); };
-  auto drain_bar = [&](int slot) { return xb + 8u * (14 + slot); };
-  auto rawfull_bar = [&](int e) { return xb + 8u * (16 + e); };     // fp8: codes of an entry
-  auto rawempty_bar = [&](int e) { return xb + 8u * (16 + RAWS + e); };
-  static_assert(2 * RING + 16 + 2 * RAWS <= 63, "barriers");
+  auto drain_bar = [&](int issuer) { return xb + 8u * (14 + issuer); };
+  auto rawfull_bar = [&](int e) { return xb + 8u * (18 + e); };     // fp8: codes of K blocks, of V blocks
+  auto rawempty_bar = [&](int e) { return xb + 8u * (18 + 2 * RAWS + e); };
+  static_assert(2 * RING + 18 + 4 * RAWS <= 63, "barriers");
   uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(gbase + GG::OFF_BAR + 504);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     prefetch_tensormap(&tmap_k);
     prefetch_tensormap(&tmap_v);
     for (int e = 0; e < RING; ++e) {
-      mbar_init(full_bar(e), FP8 ? kConverters : kLoaders);
+      mbar_init(full_bar(e), FP8 ? kConverters / 2 : 1);
       mbar_init(empty_bar(e), 2);
     }
-    for (int e = 0; e < RAWS; ++e) {
-      mbar_init(rawfull_bar(e), kLoaders);
-      mbar_init(rawempty_bar(e), kConverters);
+    for (int e = 0; e < 2 * RAWS; ++e) {
+      mbar_init(rawfull_bar(e), 1);
+      mbar_init(rawempty_bar(e), kConverters / 2);
     }
     for (int s = 0; s < 2; ++s) {
       for (int k = 0; k < 2; ++k) {
@@ -389,6 +403,7 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
       }
       mbar_init(qfull_bar(s), kSoftmaxWarps / 2);
       mbar_init(drain_bar(s), 1);
+      mbar_init(drain_bar(2 + s), 1);
     }
     fence_mbar_init();
   }
@@ -412,205 +427,190 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
   PieceWalker wk;
   wk.start(p, from, to);
 
-  if (warp >= kIssuers && warp < kIssuers + kLoaders) {
+  if (warp >= kIssuers && warp < kConverter0) {
     // =============================== loaders =================================
-    const int me = warp - kIssuers;
-    constexpr int SLOTS = FP8 ? RAWS : RING;
-    int e = 0;
-    uint32_t round = 0;
-    bool ok = true;
-    PageIds ids;
-    while (ok && wk.more()) {
-      const Piece c = wk.next(p);
-      ids.start(p, wk.sg);
-      const int b1 = end_block(c, wk.sg);
-      for (int b = first_block(c); ok && b < b1; ++b) {
-        const int np = min(kBlockPages, wk.sg.pages - b * kBlockPages);
-        for (int is_v = 0; is_v < 2; ++is_v) {
-          // boxes dealt over the warps, a lane each: a page, or (split boxes: heads that
-          // are not contiguous) eight slots and 64 features of one
-          const int per = !FP8 && NH == 2 && p.split_boxes ? 4 : 1;
-          const int x = kLoaders * lane + me, pg = x / per, part = x - pg * per;
+    registers_down<GG::R_LOAD>();
+    if (warp < kIssuers + kLoaders) {
+      // One warp loads the K blocks, the other the V blocks.
+      const int is_v = warp - kIssuers;
+      constexpr int kRaws = RAWS > 0 ? RAWS : 1;
+      const CUtensorMap* const map = is_v ? &tmap_v : &tmap_k;
+      // boxes, a lane each: a page, or (split boxes: heads that are not contiguous) eight
+      // slots and 64 features of one
+      const int per = !FP8 && NH == 2 && p.split_boxes ? 4 : 1;
+      const int pg = lane / per, part = lane - pg * per;
+      const uint32_t bytes = (FP8 ? 16u * D : PAGE) / per;
+      const uint32_t to = FP8 ? base + GG::OFF_RAW + pg * bytes : ring0 + pg * PAGE + part * 1024u;
+      uint32_t n = 0;                                          // blocks before
+      bool ok = true;
+      PageIds ids;
+      while (ok && wk.more()) {
+        const Piece c = wk.next(p);
+        ids.start(p, wk.sg);
+        for (int b = c.b0; b < c.b1; ++b, ++n) {
+          const int np = min(kBlockPages, wk.sg.pages - b * kBlockPages);
           ids.turn_to(b >> 2);
           const int page = ids.of(b, pg);
+          const uint32_t e = FP8 ? is_v * RAWS + n % kRaws : place(is_v, n);
+          const uint32_t round = FP8 ? n / kRaws : phase(is_v, n);
+          const uint32_t full = FP8 ? rawfull_bar(e) : full_bar(e);
           if (round > 0 && !warp_wait(FP8 ? rawempty_bar(e) : empty_bar(e), (round - 1) & 1u, p.wait_ns)) {
             if (lane == 0) atomicOr(p.err, kErrTimeout);
             ok = false;
             break;
           }
-          const uint32_t bytes = (FP8 ? 16u * D : PAGE) / per;
-          const uint32_t full = FP8 ? rawfull_bar(e) : full_bar(e);
-          const int mine = np * per > me ? (np * per - me + kLoaders - 1) / kLoaders : 0;
-          if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(mine) * bytes);
+          if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(np * per) * bytes);
           __syncwarp();
           if (pg < np) {
             if ((page < 0 || page >= p.num_pages) && part == 0) atomicOr(p.err, kErrPageRange);
             // (a page id out of range reads as zeros: TMA fills outside the tensor)
-            const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
             if constexpr (FP8) {
-              tma_load_4d(base + GG::OFF_RAW + static_cast<uint32_t>(e) * GG::RAW + static_cast<uint32_t>(pg) * bytes,
-                          map, 0, 0, c.head, page, full);
+              tma_load_4d(to + e * GG::RAW, map, 0, 0, c.head, page, full);
             } else {
-              const uint32_t dst = ring0 + static_cast<uint32_t>(e) * TILE + static_cast<uint32_t>(pg) * PAGE;
               if (NH == 1)
-                tma_load_4d(dst, map, 0, 0, c.head, page, full);
+                tma_load_4d(to + e * TILE, map, 0, 0, c.head, page, full);
               else if (per == 1)
-                tma_load_5d(dst, map, 0, 0, NH * c.head, 0, page, full);
-              else                                          // part = 2 (slot / 8) + half
-                tma_load_4d(dst + part * 1024u, map, 64 * (part & 1), 8 * (part >> 1), c.head, page, full);
+                tma_load_5d(to + e * TILE, map, 0, 0, NH * c.head, 0, page, full);
+              else                                              // part = 2 (slot / 8) + half
+                tma_load_4d(to + e * TILE, map, 64 * (part & 1), 8 * (part >> 1), c.head, page, full);
             }
-          }
-          if (++e == SLOTS) {
-            e = 0;
-            ++round;
           }
         }
       }
     }
-  } else if (FP8 && warp >= kIssuers + kLoaders && warp < GG::SOFT0) {
+  } else if (FP8 && warp >= kConverter0 && warp < GG::SOFT0) {
     // ============================== converters ===============================
-    // e4m3 codes to f16 (exact), into the products' layout: a thread takes 16 codes of a
-    // row of each page (two pages at a time for 64 features), all into registers before it
-    // waits for a free entry.  Its two stores are swapped between the halves of a row: no
-    // bank conflict.  The codes' place is given back after the proxy fence: the copy that
-    // fills it next is not ordered behind plain loads without one (given back right after
-    // the loads, 127 against 126 us for the five groups below, with a fence of its own).
-    const int ct = tid - 32 * (kIssuers + kLoaders);
-    constexpr int CPR = D / 16;                              // 16-code chunks a row
-    constexpr int ITER = kKeys * CPR / (32 * kConverters);
-    constexpr int PPI = kBlockPages / ITER;                  // pages an iteration
+    // e4m3 codes to f16 (exact), into the products' layout.  A thread takes 16 codes of a
+    // row at a time.  Eight lanes (a phase of 128 bytes of the loads and stores) take four
+    // chunks of two rows, of 128 features different halves of them: no bank conflict on
+    // either side.  The codes' place is given back after the proxy fence: the copy that
+    // fills it next is not ordered behind plain loads without one.
+    registers_down<GG::R_CONVERT>();
+    const int is_v = warp >= kConverter0 + kConverters / 2;
+    const int ct = (tid - 32 * kConverter0) & (16 * kConverters - 1);
+    constexpr int ITER = kKeys * (D / 16) / (16 * kConverters), HALF = ITER / 2;
     constexpr int kRaws = RAWS > 0 ? RAWS : 1;
-    const int cc = ct % CPR, slot16 = (ct / CPR) % 16, pg0 = ct / (16 * CPR);
-    const int q = 2 * (cc & 3), swap = (cc >> 2) & 1;
-    const uint32_t to = static_cast<uint32_t>(pg0) * PAGE + (slot16 >> 3) * GROUP + (cc >> 2) * 1024u;
-    const uint32_t to0 = to + swz<128>(slot16 & 7, q + swap), to1 = to + swz<128>(slot16 & 7, q + 1 - swap);
-    uint32_t n = 0;                                          // entries before
+    const int cc = ct & 3, odd = (ct >> 2) & 1;
+    uint32_t n = 0;                                          // blocks before
     bool ok = true;
     while (ok && wk.more()) {
       const Piece c = wk.next(p);
-      const int pages = wk.sg.pages, b1 = end_block(c, wk.sg);
-      for (int b = first_block(c); ok && b < b1; ++b)
-        for (int k = 0; k < 2; ++k, ++n) {
-          const int np = min(kBlockPages, pages - b * kBlockPages);
-          const int er = static_cast<int>(n % kRaws), e = static_cast<int>(n % RING);
-          ok = warp_wait(rawfull_bar(er), (n / kRaws) & 1u, p.wait_ns);
-          uint4 v[ITER];
-          if (ok) {
+      for (int b = c.b0; b < c.b1; ++b, ++n) {
+        const int np = min(kBlockPages, wk.sg.pages - b * kBlockPages);
+        const uint32_t er = is_v * RAWS + n % kRaws, e = place(is_v, n);
+        ok = warp_wait(rawfull_bar(er), (n / kRaws) & 1u, p.wait_ns);
 #pragma unroll
-            for (int i = 0; i < ITER; ++i)
-              v[i] = *reinterpret_cast<const uint4*>(gbase + GG::OFF_RAW + er * GG::RAW + 16 * ct + 2048 * i);
-            if (n >= RING) ok = warp_wait(empty_bar(e), (n / RING - 1) & 1u, p.wait_ns);
-          }
-          if (!ok) {
-            if (lane == 0) atomicOr(p.err, kErrTimeout);
-            break;
-          }
+        for (int h = 0; h < 2; ++h) {
+          if (!ok) break;
+          const uint8_t* src = gbase + GG::OFF_RAW + er * GG::RAW;
           uint8_t* dst = gbase + GG::OFF_RING + e * TILE;
+          auto row_of = [&](int i) { return NH == 2 ? 32 * (i >> 1) + 2 * (ct >> 3) + (odd ^ (i & 1)) : 32 * i + (ct >> 2); };
+          const int half = NH == 2 ? odd : 0;
+          uint4 v[HALF];
 #pragma unroll
-          for (int i = 0; i < ITER; ++i) {
-            if (PPI * i + pg0 >= np) continue;
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            const uint4 h0 = make_uint4(e4m3x2_to_f16x2(w[0]), e4m3x2_to_f16x2(w[0] >> 16), e4m3x2_to_f16x2(w[1]),
-                                        e4m3x2_to_f16x2(w[1] >> 16));
-            const uint4 h1 = make_uint4(e4m3x2_to_f16x2(w[2]), e4m3x2_to_f16x2(w[2] >> 16), e4m3x2_to_f16x2(w[3]),
-                                        e4m3x2_to_f16x2(w[3] >> 16));
-            *reinterpret_cast<uint4*>(dst + to0 + PPI * i * PAGE) = swap ? h1 : h0;
-            *reinterpret_cast<uint4*>(dst + to1 + PPI * i * PAGE) = swap ? h0 : h1;
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(full_bar(e));
-            mbar_arrive(rawempty_bar(er));
+          for (int i = 0; i < HALF; ++i)
+            v[i] = *reinterpret_cast<const uint4*>(src + row_of(h * HALF + i) * D + 64 * half + 16 * cc);
+          if (h == 0 && phase(is_v, n) > 0) ok = warp_wait(empty_bar(e), (phase(is_v, n) - 1) & 1u, p.wait_ns);
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < HALF; ++i) {
+            const int row = row_of(h * HALF + i);
+            if ((row >> 4) >= np) continue;
+            uint8_t* g = dst + (row >> 3) * GROUP + half * 1024u;
+            *reinterpret_cast<uint4*>(g + swz<128>(row & 7, 2 * cc)) =
+                make_uint4(e4m3x2_to_f16x2(v[i].x), e4m3x2_to_f16x2(v[i].x >> 16), e4m3x2_to_f16x2(v[i].y),
+                           e4m3x2_to_f16x2(v[i].y >> 16));
+            *reinterpret_cast<uint4*>(g + swz<128>(row & 7, 2 * cc + 1)) =
+                make_uint4(e4m3x2_to_f16x2(v[i].z), e4m3x2_to_f16x2(v[i].z >> 16), e4m3x2_to_f16x2(v[i].w),
+                           e4m3x2_to_f16x2(v[i].w >> 16));
           }
         }
+        if (!ok) {
+          if (lane == 0) atomicOr(p.err, kErrTimeout);
+          break;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(full_bar(e));
+          mbar_arrive(rawempty_bar(er));
+        }
+      }
     }
-  } else if (warp < 2) {
+  } else if (warp < kIssuers) {
     // =========================== product issuers =============================
-    const int slot = warp;
-    const uint32_t idesc_o = FP8 ? idesc_f16(128, D, true) : umma_idesc_bf16(128, D, true);
-    const uint32_t idesc_s = (FP8 ? idesc_f16(128, 16, false) : umma_idesc_bf16(128, 16, false)) & ~(0x3Fu << 17);
+    registers_down<GG::R_ISSUE>();
+    const int slot = warp & 1, is_v = warp >> 1;
+    const uint32_t idesc = !is_v ? (FP8 ? idesc_f16(128, 16, false) : umma_idesc_bf16(128, 16, false)) & ~(0x3Fu << 17)
+                                 : (FP8 ? idesc_f16(128, D, true) : umma_idesc_bf16(128, D, true));
     const uint64_t qd = umma_sdesc_sw128(warp_uniform(base + slot * TILE), 16u, GROUP);
     const uint32_t tS = warp_uniform(tbase + kColS + 128u * slot), tO = warp_uniform(tbase + kColO + 128u * slot);
-    uint32_t entries = 0;          // ring entries of the pieces before
-    uint32_t tiles = 0, ns = 0, npv = 0;   // query tiles seen, S and P V products
+    uint32_t before = 0;           // blocks of the pieces before
+    uint32_t tiles = 0, n = 0;     // query tiles seen, sub-blocks
     bool ok = true;
     while (ok && wk.more()) {
       const Piece c = wk.next(p);
       int last = 0;
       const int subs = subs_in(c, wk.sg, slot, last);
-      // Ring entry of sub-block i's K or V.  It is free once both issuers' products have
-      // read it: each commits at its last sub-block of the entry.
-      auto entry = [&](int i, int v) { return entries + 2u * (c.single ? i : i >> 1) + v; };
-      auto half_of = [&](int i) { return c.single ? slot : i & 1; };
-      auto opens = [&](int i) { return c.single || (i & 1) == 0; };
-      auto closes = [&](int i) { return c.single || (i & 1) == 1 || i == subs - 1; };
-      auto issue_s = [&](int i) -> bool {
-        const uint32_t e = entry(i, 0), at = e % RING;
-        const int part = half_of(i);
-        if (i == 0 && !warp_wait(qfull_bar(slot), tiles++ & 1u, p.wait_ns)) return false;
-        if (opens(i) && !warp_wait(full_bar(at), (e / RING) & 1u, p.wait_ns)) return false;
-        tc_fence_after();
-        const uint64_t kd = umma_sdesc_sw128(warp_uniform(ring0 + at * TILE + part * (kSubPages * PAGE)), 16u, GROUP);
-        const int np = i == subs - 1 ? last : kSubPages;
-        const uint32_t idesc = warp_uniform(idesc_s | (static_cast<uint32_t>(2 * np) << 17));
-        const uint32_t d = warp_uniform(tS + 64u * (ns & 1u));
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = ((k >> 2) * 1024u + (k & 3) * 32u) >> 4;
-            umma_ss(d, qd + off, kd + off, idesc, k > 0);
-          }
-          umma_commit(sfull_bar(slot, ns));
-          if (closes(i)) umma_commit(empty_bar(at));
-        }
-        __syncwarp();
-        ++ns;
-        return true;
-      };
-      auto issue_pv = [&](int i) -> bool {
-        const uint32_t e = entry(i, 1), at = e % RING;
-        const int part = half_of(i);
-        if ((opens(i) && !warp_wait(full_bar(at), (e / RING) & 1u, p.wait_ns)) ||
-            !warp_wait(pfull_bar(slot, npv), (npv >> 1) & 1u, p.wait_ns))
-          return false;
-        tc_fence_after();
-        const uint64_t vd = umma_sdesc_sw128(warp_uniform(ring0 + at * TILE + part * (kSubPages * PAGE)), 1024u, GROUP);
+      if (subs > 0 && !is_v) ok = warp_wait(qfull_bar(slot), tiles++ & 1u, p.wait_ns);
+      for (int i = 0; ok && i < subs; ++i, ++n) {
+        // The sub-block's block; its place is free once both slots' products have read it:
+        // each commits at its last sub-block of the block.
+        const uint32_t b = before + static_cast<uint32_t>(c.single ? i : i >> 1), at = place(is_v, b);
+        const int part = c.single ? slot : i & 1;
+        const bool opens = c.single || (i & 1) == 0, closes = c.single || (i & 1) == 1 || i == subs - 1;
+        if (opens) ok = warp_wait(full_bar(at), phase(is_v, b) & 1u, p.wait_ns);
         const int np = static_cast<int>(warp_uniform(static_cast<uint32_t>(i == subs - 1 ? last : kSubPages)));
-        const uint32_t a = warp_uniform(tS + 64u * (npv & 1u));
-        if (elect_one()) {
+        const uint32_t sp = warp_uniform(tS + 64u * (n & 1u));
+        const uint32_t src = warp_uniform(ring0 + at * TILE + part * (kSubPages * PAGE));
+        if (!is_v) {
+          // over P of two sub-blocks ago, which its P V has read
+          if (ok && n >= 2) ok = warp_wait(odone_bar(slot, n), ((n >> 1) - 1) & 1u, p.wait_ns);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t kd = umma_sdesc_sw128(src, 16u, GROUP);
+          const uint32_t id = warp_uniform(idesc | (static_cast<uint32_t>(2 * np) << 17));
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kSubPages; ++k)                // (a piece's first overwrites O)
-            if (k < np) umma_ts(tO, a + 8u * k, vd + static_cast<uint64_t>((k * PAGE) >> 4), idesc_o, k > 0 || i > 0);
-          umma_commit(odone_bar(slot, npv));
-          if (closes(i)) umma_commit(empty_bar(at));
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = ((k >> 2) * 1024u + (k & 3) * 32u) >> 4;
+              umma_ss(sp, qd + off, kd + off, id, k > 0);
+            }
+            umma_commit(sfull_bar(slot, n));
+            if (closes) umma_commit(empty_bar(at));
+          }
+        } else {
+          if (ok) ok = warp_wait(pfull_bar(slot, n), (n >> 1) & 1u, p.wait_ns);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vd = umma_sdesc_sw128(src, 1024u, GROUP);
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kSubPages; ++k)              // (a piece's first overwrites O)
+              if (k < np) umma_ts(tO, sp + 8u * k, vd + static_cast<uint64_t>((k * PAGE) >> 4), idesc, k > 0 || i > 0);
+            umma_commit(odone_bar(slot, n));
+            if (closes) umma_commit(empty_bar(at));
+          }
         }
         __syncwarp();
-        ++npv;
-        return true;
-      };
-      // S runs two sub-blocks ahead of P V: the softmax of one runs beside S of the next.
-      // (Not into the next piece: its K may come into the ring only once this V has left.)
-      ok = (subs < 1 || issue_s(0)) && (subs < 2 || issue_s(1));
-      for (int i = 0; ok && i < subs; ++i) ok = issue_pv(i) && (i + 2 >= subs || issue_s(i + 2));
-      const uint32_t blocks = end_block(c, wk.sg) - first_block(c);
+      }
+      const uint32_t blocks = c.b1 - c.b0;
       if (ok && c.single && static_cast<uint32_t>(subs) < blocks) {
         // a last block without pages for this slot
-        for (int v = 0; ok && v < 2; ++v) {
-          const uint32_t e = entry(subs, v), at = e % RING;
-          ok = warp_wait(full_bar(at), (e / RING) & 1u, p.wait_ns);
-          if (ok && lane == 0) mbar_arrive(empty_bar(at));
-        }
+        const uint32_t b = before + static_cast<uint32_t>(subs), at = place(is_v, b);
+        ok = warp_wait(full_bar(at), phase(is_v, b) & 1u, p.wait_ns);
+        if (ok && lane == 0) mbar_arrive(empty_bar(at));
       }
-      entries += 2 * blocks;
+      before += blocks;
     }
     if (!ok && lane == 0) atomicOr(p.err, kErrTimeout);
     // every product must be complete before tensor memory is freed
-    if (elect_one()) umma_commit(drain_bar(slot));
+    if (elect_one()) umma_commit(drain_bar(warp));
     __syncwarp();
-    if (!warp_wait(drain_bar(slot), 0u, p.wait_ns) && lane == 0) atomicOr(p.err, kErrTimeout);
+    if (!warp_wait(drain_bar(warp), 0u, p.wait_ns) && lane == 0) atomicOr(p.err, kErrTimeout);
   } else {
     // ================================ softmax ================================
+    registers_up<GG::R_SOFT>();
     const int slot = (warp - GG::SOFT0) >> 2;
     const int quarter = warp & 3;
     const int rho = 32 * quarter + lane;                      // row of the tile = tensor-memory lane
@@ -755,8 +755,7 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
       const int done = subs;
       // the slot's tile of partial rows: chunk d / 4 of all its rows, then the next chunk (a
       // warp's stores are whole lines)
-      const int64_t tile0 = sg.row0 + static_cast<int64_t>(c.head) * sg.rows_head +
-                            static_cast<int64_t>(c.pair) * kSharedPair + static_cast<int64_t>(cta) * kSharedPair +
+      const int64_t tile0 = c.row0 + static_cast<int64_t>(cta) * kSharedPair +
                             slot * (c.single ? sg.last_rows : kSharedTile);
       const int tile_rows = shared_tile_rows(sg, c.pair, slot);
       // the next piece's rows while this one's last products run: its Q K^T products are

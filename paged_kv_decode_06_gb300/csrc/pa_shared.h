@@ -4,8 +4,9 @@
 // The rows of one (group, KV head), G query heads of every query token of the group's
 // sequences, are cut into pairs of 128-row tiles, one tile a slot; a last pair of at most
 // 128 rows has one tile, which both slots take, each a half of every block of keys.  A step
-// is one block of 128 keys for both tiles, or two blocks for the single tile.  Steps stand end to end in (group, head, pair, block)
-// order, X in all; CTA c of the NG in use takes [c X / NG, (c + 1) X / NG).
+// is one block of 128 keys for both tiles, or two blocks for the single tile.  Steps stand
+// end to end in (group, head, pair, block) order, X in all; CTA c of the NG in use takes
+// [c X / NG, (c + 1) X / NG).
 //
 // The sequences' own pages are attended beside the shared ones, by the split kernel on the
 // SMs that the prefix kernel leaves: the plan cuts the SMs in two by the work of each.
@@ -81,7 +82,7 @@ struct SharedParams {
   int32_t ctas;               // CTAs of the prefix kernel
   int32_t own_ctas;           // CTAs of the split kernel
   int32_t beside;             // they run side by side on `ctas` SMs
-  int32_t step_cost, page_cost;   // time of a step, and of a sequence's page for one head, on one SM
+  int32_t step_cost, page_cost, unit_cost;   // time of a step, a sequence's page and a sequence, for one head on one SM
   int32_t split_boxes;        // 128 features, bf16: heads are not contiguous, pages come in four boxes
   float scale_log2;
   uint64_t wait_ns;
