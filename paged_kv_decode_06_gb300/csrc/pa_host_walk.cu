@@ -280,7 +280,13 @@ int decode_window(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
 }
 
 // ------------------------------------------------------------ shared prefixes
-constexpr int kMinSharedPages = 1;
+// Prefixes that are left to the sequences, where both parts run side by side (elsewhere every
+// prefix is shared): of fewer than 16 pages (200 sequences of 32 / 8 heads of 128 behind 100
+// tokens: 61 us shared, 46 not; behind 300, 52 and 68), and all of a call that would cost an
+// SM less than 2 us (4 sequences behind 1000 tokens: 21.1 and 23 us; of 2 heads of 64, 21 and
+// 19.3).
+constexpr int kMinSharedPages = 16;
+constexpr int kAloneCost = 2000;          // ns, as below
 // What the plan cuts the SMs by (nanoseconds on one SM).  Measured with 4 and 128 of 152 SMs
 // for one part: a step (pa_shared.h) takes 1.6 us (fp8 codes 2.3, of 64 features 1.75), a
 // page for one head and 16 query rows 0.165 us (64 features 0.06, fp8 0.064; 128, fp8,
@@ -399,17 +405,18 @@ int decode_shared(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
   hp.num_pages = sp.num_pages;
   hp.G = sp.G;
   hp.Hkv = sp.Hkv;
-  hp.min_pages = kMinSharedPages;
   hp.split_boxes = split_k;
   hp.ctas = pl.grid;
   hp.own_ctas = pl.split.grid;
   // Both grids are then one CTA an SM at most, the plan's shares add up to the SMs, and the
   // split kernel may start when the plan is made.
   hp.beside = pdl && pl.grid == dev.num_sms && pl.split.grid == dev.num_sms;
+  hp.min_pages = hp.beside ? kMinSharedPages : 1;
   const Costs cost = costs_of(s.D, s.esz == 1);
   hp.step_cost = cost.step;
   hp.page_cost = cost.page * ((sp.R_max + 15) / 16);
   hp.unit_cost = 3 * hp.page_cost;
+  hp.alone_cost = kAloneCost;
   hp.scale_log2 = sp.scale_log2;
   hp.wait_ns = sp.wait_ns;
   hp.err = dev.status;

@@ -138,6 +138,26 @@ __global__ void __launch_bounds__(kPlanThreads) pa_shared_plan_kernel(const Shar
     }
   }
   __syncthreads();
+  // What the sequences' own pages cost, and what the shared ones would if nothing were
+  // shared: where that is little, it is less than the shared part's own start and end.
+  int64_t own = 0, alone = 0, all_own = 0, all_alone = 0;
+  if (p.beside) {
+    for (int i = tid; i < p.num_seqs; i += kPlanThreads) {
+      const int L = p.seq_lens[i], skip = p.skip[i];
+      const int n = (L > 0 ? min((L - 1) / kPage + 1, p.max_blocks) : 0) - skip;
+      if (n > 0) own += static_cast<int64_t>(n) * p.page_cost + p.unit_cost;
+      alone += static_cast<int64_t>(skip) * p.page_cost;
+    }
+    block_scan(own, s_warp, &all_own);
+    block_scan(alone, s_warp, &all_alone);
+    if (all_alone * p.Hkv < static_cast<int64_t>(p.alone_cost) * p.ctas) {
+      for (int i = tid; i < p.num_seqs; i += kPlanThreads) {
+        p.skip[i] = 0;
+        p.seq_group[i] = -1;
+      }
+      for (int g = tid; g < p.num_groups; g += kPlanThreads) p.groups[g] = SharedGroup{};
+    }
+  }
   int64_t step0 = 0, row0 = 0;
   for (int g0 = 0; g0 < p.num_groups; g0 += kPlanThreads) {
     const int g = g0 + tid;
@@ -158,14 +178,6 @@ __global__ void __launch_bounds__(kPlanThreads) pa_shared_plan_kernel(const Shar
   // The SMs for each part, in proportion to its work; some more for the sequences' own pages,
   // whose many short walks pay more for memory the longer the other part runs, and four at
   // least (8 sequences of 500 tokens behind 65536: 57 us with one, 46 with four, 48 with 28).
-  int64_t own = 0, all_own;
-  if (p.beside)
-    for (int i = tid; i < p.num_seqs; i += kPlanThreads) {
-      const int L = p.seq_lens[i];
-      const int n = (L > 0 ? min((L - 1) / kPage + 1, p.max_blocks) : 0) - p.skip[i];
-      if (n > 0) own += static_cast<int64_t>(n) * p.page_cost + p.unit_cost;
-    }
-  block_scan(own, s_warp, &all_own);
   int n = p.ctas;
   if (p.beside && all_own > 0 && step0 > 0) {
     const float a = static_cast<float>(step0) * p.step_cost, b = static_cast<float>(all_own) * p.Hkv;

@@ -275,3 +275,41 @@ def test_many_pieces_a_cta(kv, d, ctas):
     lens = np.concatenate([s + r.integers(1, 30, n) for n, s in zip(sizes, shared)])
     b = Batch(lens, hq=16, hkv=2, d=d, kv=kv, groups=(np.concatenate([[0], np.cumsum(sizes)]).tolist(), shared), seed=1)
     b.check(*_run(b, num_ctas=ctas))
+
+
+_FORMS = {"one after the other": {"disable_pdl": True}, "side by side": {}, "cut to 40": {"num_ctas": 40}}
+
+
+@pytest.mark.parametrize("form", list(_FORMS))
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,shared,hq,hkv", [(2, 16, 1, 1), (3, 130, 16, 2), (16, 128, 8, 1), (17, 255, 8, 1),
+                                             (33, 272, 8, 2), (40, 1000, 8, 1), (7, 2100, 5, 5), (90, 650, 16, 4)])
+def test_every_form_of_one_group(n, shared, hq, hkv, d, kv, form):
+    """Short prefixes are left to the sequences where both parts run side by side, and shared elsewhere."""
+    r = np.random.default_rng(n + shared)
+    b = Batch(shared + r.integers(1, 90, n), hq=hq, hkv=hkv, d=d, kv=kv, groups=([0, n], [shared]), seed=n)
+    b.check(*_run(b, **_FORMS[form]))
+
+
+@pytest.mark.parametrize("kv,d", [("bf16", 64), ("fp8", 128)])
+def test_short_and_long_prefixes_side_by_side(kv, d):
+    """Groups on both sides of the shortest shared prefix, and sequences of no group."""
+    sizes, shared = [30, 20, 40, 10], [255, 256, 500, 1600]
+    r = np.random.default_rng(d)
+    lens = np.concatenate([s + r.integers(1, 200, n) for n, s in zip(sizes, shared)] + [r.integers(1, 900, 20)])
+    b = Batch(lens, hq=16, hkv=4, d=d, kv=kv, groups=(np.concatenate([[0], np.cumsum(sizes)]).tolist(), shared), seed=2)
+    b.check(*_run(b))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_the_same_rows_every_time(kv):
+    """The two parts run beside each other: no call's result depends on their timing."""
+    r = np.random.default_rng(5)
+    lens = 1300 + r.integers(1, 300, 60)
+    b = Batch(lens, hq=32, hkv=4, d=128, kv=kv, groups=([0, 25, 60], [1290, 1000]), seed=3)
+    out, lse = _run(b)
+    b.check(out, lse)
+    for _ in range(20):
+        o, l = _run(b)
+        assert torch.equal(o, out) and torch.equal(l, lse)
