@@ -26,6 +26,7 @@
 // Waits are bounded, and each is made once a phase in order, so its barrier is never more
 // than one phase behind (mbarrier parities cannot tell further).
 #include "pa_device.cuh"
+#include "pa_host.h"
 #include "pa_kernels.h"
 #include "pa_pack.cuh"
 #include "pa_quant.cuh"
@@ -36,81 +37,81 @@ namespace pa {
 namespace {
 
 // ---------------------------------------------------------------- plan kernel
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;        // at most
+constexpr int kPlanInts = 7;              // shared memory a sequence
 
-// Inclusive sum over the block of one value a thread; *total gets the sum of all.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s_warp, int64_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Sum over the block (in a fixed order).
+__device__ __forceinline__ float2 block_sum(float2 v, float2* s_warp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += y;
+  for (int o = 16; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
   }
-  if (lane == 31) s_warp[warp] = v;
+  if (lane == 0) s_warp[warp] = v;
   __syncthreads();
-  if (warp == 0) {
-    int64_t x = s_warp[lane];
+  v = lane < warps ? s_warp[lane] : make_float2(0.f, 0.f);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    s_warp[lane] = x;
+  for (int o = 16; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
   }
-  __syncthreads();
-  if (warp > 0) v += s_warp[warp - 1];
-  *total = s_warp[31];
-  __syncthreads();
   return v;
 }
 
+// Bound by latency: the arrays are read once, everything after that is in shared memory.
 __global__ void __launch_bounds__(kPlanThreads) pa_shared_plan_kernel(const SharedParams p) {
-  __shared__ int64_t s_warp[32];
+  __shared__ float2 s_sum[32];
+  extern __shared__ int32_t s_plan[];
+  const int B = p.num_seqs, NG = p.num_groups;
+  int32_t* const s_len = s_plan;                  // [B] each
+  int32_t* const s_t0 = s_len + B;
+  int32_t* const s_t1 = s_t0 + B;
+  int32_t* const s_skip = s_t1 + B;
+  int32_t* const s_group = s_skip + B;
+  int32_t* const s_steps = s_group + B;           // of a group (NG <= B), a head
+  int32_t* const s_rows = s_steps + B;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < p.num_seqs; i += kPlanThreads) {
-    p.skip[i] = 0;
-    p.seq_group[i] = -1;
-  }
   // Groups are consecutive ranges of sequences; with any other list nothing is shared.
   bool bad = false;
-  for (int g = tid; g < p.num_groups; g += kPlanThreads) {
+  for (int g = tid; g < NG; g += threads) {
     const int a = p.group_start[g], b = p.group_start[g + 1];
-    bad |= a < 0 || b < a || b > p.num_seqs;
+    bad |= a < 0 || b < a || b > B;
   }
   // A query_start_loc that is no cumulative sum could spread a group's tokens (each
   // partial row has its place by them).
-  for (int i = tid; i < p.num_seqs; i += kPlanThreads) {
+  for (int i = tid; i < B; i += threads) {
     const int a = p.qsl != nullptr ? p.qsl[i] : i, b = p.qsl != nullptr ? p.qsl[i + 1] : i + 1;
+    s_len[i] = p.seq_lens[i];
+    s_t0[i] = a;
+    s_t1[i] = b;
+    s_skip[i] = 0;
+    s_group[i] = -1;
     bad |= a < 0 || b < a || b > p.num_tokens || b - a > p.max_qlen;
   }
   bad = __syncthreads_or(bad);
   if (bad && tid == 0) atomicOr(p.err, kErrQueryLen);
-  for (int g = warp; g < p.num_groups; g += kPlanThreads / 32) {
+  for (int g = warp; g < NG; g += threads / 32) {
     const int a = bad ? 0 : p.group_start[g], b = bad ? 0 : p.group_start[g + 1];
     // members: sequences with query tokens, all at positions of their own
     int pages = max(0, p.shared_lens[g]) / kPage, members = 0, t_lo = INT_MAX, t_hi = 0, first = INT_MAX;
     pages = min(pages, p.max_blocks);
+    auto member = [&](int i) { return s_t1[i] > s_t0[i] && s_len[i] >= s_t1[i] - s_t0[i]; };
     for (int i = a + lane; i < b; i += 32) {
-      const int L = p.seq_lens[i];
-      const int t0 = p.qsl != nullptr ? p.qsl[i] : i, t1 = p.qsl != nullptr ? p.qsl[i + 1] : i + 1;
-      const bool in = t1 > t0 && L >= t1 - t0;
-      if (!in) continue;
+      if (!member(i)) continue;
       ++members;
       first = min(first, i);
-      pages = min(pages, (L - (t1 - t0)) / kPage);
-      t_lo = min(t_lo, t0);
-      t_hi = max(t_hi, t1);
+      pages = min(pages, (s_len[i] - (s_t1[i] - s_t0[i])) / kPage);
+      t_lo = min(t_lo, s_t0[i]);
+      t_hi = max(t_hi, s_t1[i]);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      members += __shfl_xor_sync(0xffffffffu, members, o);
-      pages = min(pages, __shfl_xor_sync(0xffffffffu, pages, o));
-      first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
-      t_lo = min(t_lo, __shfl_xor_sync(0xffffffffu, t_lo, o));
-      t_hi = max(t_hi, __shfl_xor_sync(0xffffffffu, t_hi, o));
-    }
+    members = __reduce_add_sync(0xffffffffu, members);
+    pages = __reduce_min_sync(0xffffffffu, pages);
+    first = __reduce_min_sync(0xffffffffu, first);
+    t_lo = __reduce_min_sync(0xffffffffu, t_lo);
+    t_hi = __reduce_max_sync(0xffffffffu, t_hi);
     if (members < 2 || pages < p.min_pages) pages = 0;
     SharedGroup sg = {};
     sg.seq = first;
@@ -125,73 +126,75 @@ __global__ void __launch_bounds__(kPlanThreads) pa_shared_plan_kernel(const Shar
       sg.steps_head = (sg.pairs - 1) * sg.blocks + shared_steps(sg, sg.pairs - 1);
       sg.rows_head = kSharedPair * (sg.pairs - 1) + (single ? 2 * sg.last_rows : sg.last_rows);
     }
-    if (lane == 0) p.groups[g] = sg;
-    if (pages == 0) continue;
-    for (int i = a + lane; i < b; i += 32) {
-      const int L = p.seq_lens[i];
-      const int t0 = p.qsl != nullptr ? p.qsl[i] : i, t1 = p.qsl != nullptr ? p.qsl[i + 1] : i + 1;
-      const bool in = t1 > t0 && L >= t1 - t0;
-      if (in) {
-        p.skip[i] = pages;
-        p.seq_group[i] = g;
-      }
+    if (lane == 0) {
+      p.groups[g] = sg;
+      s_steps[g] = sg.steps_head;
+      s_rows[g] = sg.rows_head;
     }
+    for (int i = a + lane; pages > 0 && i < b; i += 32)
+      if (member(i)) {
+        s_skip[i] = pages;
+        s_group[i] = g;
+      }
   }
   __syncthreads();
-  // What the sequences' own pages cost, and what the shared ones would if nothing were
-  // shared: where that is little, it is less than the shared part's own start and end.
-  int64_t own = 0, alone = 0, all_own = 0, all_alone = 0;
+  // What the sequences' own pages cost (x), and what the shared ones would if nothing were
+  // shared (y): where that is little, it is less than the shared part's own start and end.
+  float2 cost = make_float2(0.f, 0.f);
   if (p.beside) {
-    for (int i = tid; i < p.num_seqs; i += kPlanThreads) {
-      const int L = p.seq_lens[i], skip = p.skip[i];
-      const int n = (L > 0 ? min((L - 1) / kPage + 1, p.max_blocks) : 0) - skip;
-      if (n > 0) own += static_cast<int64_t>(n) * p.page_cost + p.unit_cost;
-      alone += static_cast<int64_t>(skip) * p.page_cost;
+    for (int i = tid; i < B; i += threads) {
+      const int n = (s_len[i] > 0 ? min((s_len[i] - 1) / kPage + 1, p.max_blocks) : 0) - s_skip[i];
+      if (n > 0) cost.x += static_cast<float>(n) * p.page_cost + p.unit_cost;
+      cost.y += static_cast<float>(s_skip[i]) * p.page_cost;
     }
-    block_scan(own, s_warp, &all_own);
-    block_scan(alone, s_warp, &all_alone);
-    if (all_alone * p.Hkv < static_cast<int64_t>(p.alone_cost) * p.ctas) {
-      for (int i = tid; i < p.num_seqs; i += kPlanThreads) {
-        p.skip[i] = 0;
-        p.seq_group[i] = -1;
+    cost = block_sum(cost, s_sum);
+  }
+  const bool alone = p.beside && cost.y * p.Hkv < static_cast<float>(p.alone_cost) * p.ctas;
+  for (int i = tid; i < B; i += threads) {
+    p.skip[i] = alone ? 0 : s_skip[i];
+    p.seq_group[i] = alone ? -1 : s_group[i];
+  }
+  if (alone)
+    for (int g = tid; g < NG; g += threads) p.groups[g] = SharedGroup{};
+  if (warp != 0) return;
+  // The groups' places, 32 at a time.
+  int64_t steps = 0, rows = 0;
+  for (int g0 = 0; g0 < NG && !alone; g0 += 32) {
+    const int g = g0 + lane;
+    const int64_t n = g < NG ? static_cast<int64_t>(s_steps[g]) * p.Hkv : 0;
+    const int64_t r = g < NG ? static_cast<int64_t>(s_rows[g]) * p.Hkv : 0;
+    int64_t ns = n, rs = r;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, ns, o), z = __shfl_up_sync(0xffffffffu, rs, o);
+      if (lane >= o) {
+        ns += y;
+        rs += z;
       }
-      for (int g = tid; g < p.num_groups; g += kPlanThreads) p.groups[g] = SharedGroup{};
     }
+    if (g < NG) {
+      p.groups[g].step0 = steps + ns - n;
+      p.groups[g].row0 = rows + rs - r;
+    }
+    steps += __shfl_sync(0xffffffffu, ns, 31);
+    rows += __shfl_sync(0xffffffffu, rs, 31);
   }
-  int64_t step0 = 0, row0 = 0;
-  for (int g0 = 0; g0 < p.num_groups; g0 += kPlanThreads) {
-    const int g = g0 + tid;
-    int64_t steps = 0, rows = 0;
-    if (g < p.num_groups) {
-      steps = static_cast<int64_t>(p.groups[g].steps_head) * p.Hkv;
-      rows = static_cast<int64_t>(p.groups[g].rows_head) * p.Hkv;
-    }
-    int64_t all_steps, all_rows;
-    const int64_t s1 = block_scan(steps, s_warp, &all_steps), r1 = block_scan(rows, s_warp, &all_rows);
-    if (g < p.num_groups) {
-      p.groups[g].step0 = step0 + s1 - steps;
-      p.groups[g].row0 = row0 + r1 - rows;
-    }
-    step0 += all_steps;
-    row0 += all_rows;
-  }
+  if (lane != 0) return;
   // The SMs for each part, in proportion to its work; some more for the sequences' own pages,
   // whose many short walks pay more for memory the longer the other part runs, and four at
   // least (8 sequences of 500 tokens behind 65536: 57 us with one, 46 with four, 48 with 28).
   int n = p.ctas;
-  if (p.beside && all_own > 0 && step0 > 0) {
-    const float a = static_cast<float>(step0) * p.step_cost, b = static_cast<float>(all_own) * p.Hkv;
+  if (cost.x > 0.f && steps > 0) {
+    const float a = static_cast<float>(steps) * p.step_cost, b = cost.x * p.Hkv;
     const float each = (a + b) / p.ctas;                     // ns
     const float more = 0.2f * a / (a + b) * fmaxf(0.f, each - 20000.f);
     n = min(max(1, p.ctas - 4), max(1, p.ctas - static_cast<int>(b / (each - more) + 0.5f)));
   }
-  if (n > step0) n = static_cast<int>(step0);
-  if (tid == 0) {
-    p.totals->steps = step0;
-    p.totals->rows = row0;
-    p.totals->ctas = n;
-    p.totals->own_ctas = p.beside ? max(1, min(p.own_ctas, p.ctas - n)) : p.own_ctas;
-  }
+  if (n > steps) n = static_cast<int>(steps);
+  p.totals->steps = steps;
+  p.totals->rows = rows;
+  p.totals->ctas = n;
+  p.totals->own_ctas = p.beside ? max(1, min(p.own_ctas, p.ctas - n)) : p.own_ctas;
 }
 
 // ------------------------------------------------------------- prefix kernel
@@ -834,7 +837,8 @@ cudaLaunchConfig_t config(int grid, int threads, size_t smem, bool pdl, cudaStre
 
 cudaError_t launch_shared_plan(const SharedParams& p, bool pdl, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = config(1, kPlanThreads, 0, pdl, stream, attr);
+  const int threads = min(kPlanThreads, max(128, (max(p.num_seqs, 32 * p.num_groups) + 31) / 32 * 32));
+  const cudaLaunchConfig_t cfg = config(1, threads, 4 * kPlanInts * static_cast<size_t>(p.num_seqs), pdl, stream, attr);
   return cudaLaunchKernelEx(&cfg, pa_shared_plan_kernel, p);
 }
 
@@ -866,6 +870,9 @@ cudaError_t launch_shared_prefix(int head_dim, bool fp8, const CUtensorMap& tk, 
 }
 
 cudaError_t set_shared_smem_limits() {
+  const cudaError_t plan = cudaFuncSetAttribute(reinterpret_cast<const void*>(pa_shared_plan_kernel),
+                                                cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kPlanInts * kMaxSeqsHost);
+  if (plan != cudaSuccess) return plan;
   for (int form = 0; form < 4; ++form) {
     const PrefixForm f = prefix_form_of(form & 1 ? 128 : 64, form & 2);
     const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(f.kernel),
