@@ -181,6 +181,12 @@ void fill_merge(MergeRowsParams* mp, const SplitParams& sp, int grid) {
   mp->whole_row0 = sp.whole_row0;
 }
 
+// Pages a CTA takes at least: two, where a few sequences do not fill the CTAs (5 short ones:
+// 10.4 us with one or two, 14.5 with four; 3 of 200 tokens, 64 / 8 heads, fp8: 15.4 and 16.6).
+int min_pages_of(const pa_options_t* opts) {
+  return opts && opts->min_pages_per_cta > 0 ? opts->min_pages_per_cta : 2;
+}
+
 // The options' split events (external nodes under capture).
 struct Events {
   cudaEvent_t start, stop;
@@ -247,6 +253,7 @@ int decode_window(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
   if ((st = host_cache_map(&tk, kc, s.esz, D, Hkv, pl.sp.HC, s.NB)) != PA_OK) return st;
   if ((st = host_cache_map(&tv, vc, s.esz, D, Hkv, pl.sp.HC, s.NB)) != PA_OK) return st;
   SplitParams& sp = pl.sp;
+  sp.min_pages = min_pages_of(opts);
   fill_split(&sp, s, q, bt, sl, qsl, scale, k_scale, v_scale, out, lse, opts, dev.status);
   // Nothing changes once a window or the first tokens hold every position a row of the
   // block table has; the kernels' sums of positions and windows stay within 32 bits.
@@ -373,6 +380,7 @@ int decode_shared(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
   CUtensorMap tk, tv, pk, pv;
   const int D = static_cast<int>(s.D), Hkv = static_cast<int>(s.Hkv);
   SplitParams& sp = pl.split.sp;
+  sp.min_pages = min_pages_of(opts);
   if ((st = host_cache_map(&tk, kc, s.esz, D, Hkv, sp.HC, s.NB)) != PA_OK) return st;
   if ((st = host_cache_map(&tv, vc, s.esz, D, Hkv, sp.HC, s.NB)) != PA_OK) return st;
   bool split_k = false, split_v = false;
