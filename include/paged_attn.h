@@ -86,7 +86,8 @@ typedef struct pa_tensor_t {
 /* Optional controls for paged_attn_decode_ex.  Zero-initialise for defaults. */
 typedef struct pa_options_t {
   int32_t num_ctas;            /* >0: launch this many split CTAs instead of one per SM */
-  int32_t min_pages_per_cta;   /* >0: override the minimum pages of work per CTA (default 4) */
+  int32_t min_pages_per_cta;   /* >0: override the minimum pages of work per CTA (default 4;
+                                  paged_attn_decode_window and _shared: 2) */
   int32_t heads_per_cta;       /* >0: KV heads per CTA (must divide Hkv); 0 = planner's choice */
   int32_t disable_pdl;         /* !=0: launch both kernels without programmatic dependent launch */
   int32_t page_pairing;        /* 0: planner's choice; 1: never; 2: always process two pages at once */
@@ -267,7 +268,10 @@ int paged_attn_decode_window(const pa_tensor_t* q, const pa_tensor_t* k_cache, c
  *                   name the same pages for their first shared_lens[g] tokens.  Whole
  *                   pages of these are shared; any value is valid as far as the rows agree,
  *                   also one past a sequence's length.  The pages are read from the row of
- *                   the group's first sequence that has query tokens.
+ *                   the group's first sequence that has query tokens.  Prefixes that are not
+ *                   worth a part of their own (with default options those below 256 tokens,
+ *                   and all of a call with little in common) are attended with the sequences:
+ *                   the same result but for the order of its sums.
  *   The other arguments, layouts and errors as for paged_attn_decode, except that
  *   - G * max_query_len <= 64 for every cache; max_blocks <= 2^27 - 64; T * Hq < 2^30;
  *   - padded batches, rows without a key and sinks are as for paged_attn_decode_window;

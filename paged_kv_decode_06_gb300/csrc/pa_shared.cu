@@ -492,6 +492,11 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
           }
         }
       }
+      // No copy may be on its way when the CTA ends (one is only where a wait ran out).
+      const uint32_t places = FP8 ? kRaws : is_v ? GG::VR : GG::KR;
+      for (uint32_t k = n > places ? n - places : 0; k < n; ++k)
+        warp_wait(FP8 ? rawfull_bar(is_v * RAWS + k % kRaws) : full_bar(place(is_v, k)),
+                  (FP8 ? k / kRaws : phase(is_v, k)) & 1u, p.wait_ns);
     }
   } else if (FP8 && warp >= kConverter0 && warp < GG::SOFT0) {
     // ============================== converters ===============================

@@ -313,3 +313,15 @@ def test_the_same_rows_every_time(kv):
     for _ in range(20):
         o, l = _run(b)
         assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+def test_as_many_sequences_as_a_call_takes():
+    r = np.random.default_rng(8)
+    sizes = r.integers(1, 60, 400)
+    sizes = sizes[np.cumsum(sizes) <= 8000]
+    shared = r.choice([0, 17, 250, 256, 300, 700], len(sizes))
+    lens = np.concatenate([s + r.integers(1, 20, n) for n, s in zip(sizes, shared)])
+    lens = np.concatenate([lens, r.integers(1, 40, 8192 - len(lens))])
+    at = np.concatenate([[0], np.cumsum(sizes)]).tolist()
+    b = Batch(lens, hq=2, hkv=1, d=64, kv="bf16", groups=(at, shared.tolist()), seed=4)
+    b.check(*_run(b))
