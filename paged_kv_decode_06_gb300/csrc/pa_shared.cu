@@ -3,28 +3,35 @@
 //
 // Plan (one block): the pages that a group shares are those of shared_lens, cut to what
 // every member sees whole ((L_i - q_i) / 16 pages, so that a sequence keeps a page of its
-// own and no mask is needed), none for a group with fewer than two members; and each
-// group's place in the order of steps and partial rows (pa_shared.h).
+// own and no mask is needed), none for a group with fewer than two members; each group's
+// place in the order of steps and partial rows (pa_shared.h); and the SMs for each part.
 //
 // Attention (tcgen05): with R rows a head the products cost 4 R D flops a key against
 // 4 D bytes (bf16), so from about 280 rows on the tensor cores bound it, below that
 // memory does.  A CTA holds two 128-row tiles ("slots") of query rows in
 // shared memory and S / P (128 columns) and O (128 columns) of each in tensor memory, all
-// 512 columns; blocks of 128 keys, K and V apart, pass through a ring.  While one slot's
-// softmax runs, the tensor cores work for the other.
+// 512 columns; blocks of 128 keys pass through a ring of K and a ring of V.  While one
+// slot's softmax runs, the tensor cores work for the other.
 //
-// Warps: 0 and 1 issue a slot's products each (one issuer for both: 5300 cycles a step) and
-// 0 owns tensor memory; 2 and 3 load pages; of an fp8 cache 4 to 7 convert codes to f16
-// (exact); the last eight are the slots' softmax, thread = row of tensor memory.  S of 64
-// keys, twice in each slot, P over it in 16 bits (f16 beside an fp8 cache): S of the next
-// 64 keys is there when a softmax ends.  O is rescaled only where the running maximum grew
-// by more than 2^8.
+// Warps: 0 and 1 issue a slot's S each, 2 and 3 its P V (a product takes its issuer 90 to 130
+// cycles, most of it the tensor pipe's: one warp for both of a slot 1.9 us a step, one for
+// both slots 2.8, these four 1.6) and 0 owns tensor memory; 4 loads K pages, 5 V pages; of
+// an fp8 cache 8 to 15 convert codes to f16 (exact); the last eight are the slots' softmax,
+// thread = row of tensor memory.  Registers are dealt by role.  S of 64 keys, twice in each
+// slot, P over it in 16 bits (f16 beside an fp8 cache): S of the next 64 keys is there when a
+// softmax ends.  O is rescaled only where the running maximum grew by more than 2^8.
+//
+// What bounds a step of 128 keys (1.6 us at 1.9 GHz, D 128, bf16): 2048 cycles of products;
+// 2500 of shared memory, as S of 64 keys reads Q anew (fp8: 3000, and 2.3 us); per slot and 64
+// keys about 1200 of softmax, of which 256 are exponentials.  256 sequences behind 32768
+// tokens, 277 GFLOP: 215 us on 128 SMs where nothing else runs.
 //
 // S of a sub-block overwrites the P of two before once P V has read it; so a softmax warp
 // that sees S of sub-block b knows P V of b - 2 in O.
 //
-// Waits are bounded, and each is made once a phase in order, so its barrier is never more
-// than one phase behind (mbarrier parities cannot tell further).
+// Waits are bounded, and each is made once a phase in order (every K and every V block by both
+// slots' issuers, by its loader and its converters), so its barrier is never more than one
+// phase behind (mbarrier parities cannot tell further).
 #include "pa_device.cuh"
 #include "pa_host.h"
 #include "pa_kernels.h"
