@@ -380,9 +380,12 @@ def _arguments(codes, tensors, num_caches=0):
             args = [array, num_caches] + args
         if len(_MARSHALLED.by_layout) >= _DESC_CACHE_MAX:
             _MARSHALLED.by_layout.clear()
-        _MARSHALLED.by_layout[key] = hit = (tuple(args), descs)
-    for d, t in zip(hit[1], tensors):
-        d.data = t.data_ptr()
+        _MARSHALLED.by_layout[key] = hit = (tuple(args), descs, [])
+    pointers = [t.data_ptr() for t in tensors]
+    if pointers != hit[2]:                           # (a repeated call's are there already)
+        for d, p in zip(hit[1], pointers):
+            d.data = p
+        hit[2][:] = pointers
     return hit[0], dev
 
 

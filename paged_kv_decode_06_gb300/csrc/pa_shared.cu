@@ -237,8 +237,8 @@ struct PrefixGeo {
   // Registers a thread of each role's warps; together what the launch has (4 x 128 and 6 x 80
   // of 128 threads: an increase beyond that would wait for ever)
   static constexpr int R_ISSUE = FP8 ? 64 : 80, R_LOAD = FP8 ? 48 : 80, R_CONVERT = 56, R_SOFT = FP8 ? 128 : 176;
-  static_assert(FP8 ? R_ISSUE + R_LOAD + 2 * R_CONVERT + 2 * R_SOFT == 6 * 80 : R_ISSUE + R_LOAD + 2 * R_SOFT == 4 * 128,
-                "register shares");
+  static constexpr int R_LAUNCH = FP8 ? 80 : 128;
+  static_assert(R_ISSUE + R_LOAD + (FP8 ? 2 * R_CONVERT : 0) + 2 * R_SOFT == THREADS / 128 * R_LAUNCH, "register shares");
   static constexpr uint32_t OFF_RING = 2 * TILE;
   static constexpr uint32_t RAW = kKeys * D;             // fp8: codes of a block
   static constexpr int RAWS = FP8 ? (D == 128 ? 2 : 4) : 0;   // code blocks of K, as many of V
@@ -859,12 +859,13 @@ namespace {
 using PrefixKernel = void (*)(CUtensorMap, CUtensorMap, SharedParams);
 struct PrefixForm {
   PrefixKernel kernel;
-  int threads;
+  int threads, registers;
   uint32_t smem;
 };
 template <int D, bool FP8>
 PrefixForm prefix_form() {
-  return {pa_shared_prefix_kernel<D, FP8>, PrefixGeo<D, FP8>::THREADS, PrefixGeo<D, FP8>::SMEM};
+  using GG = PrefixGeo<D, FP8>;
+  return {pa_shared_prefix_kernel<D, FP8>, GG::THREADS, GG::R_LAUNCH, GG::SMEM};
 }
 PrefixForm prefix_form_of(int head_dim, bool fp8) {
   if (head_dim == 128) return fp8 ? prefix_form<128, true>() : prefix_form<128, false>();
@@ -890,6 +891,11 @@ cudaError_t set_shared_smem_limits() {
     const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(f.kernel),
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(f.smem));
     if (e != cudaSuccess) return e;
+    // a build that launches with fewer registers than the roles are dealt would never end
+    cudaFuncAttributes attr;
+    const cudaError_t a = cudaFuncGetAttributes(&attr, reinterpret_cast<const void*>(f.kernel));
+    if (a != cudaSuccess) return a;
+    if (attr.numRegs < f.registers) return cudaErrorInvalidKernelImage;
   }
   return cudaSuccess;
 }

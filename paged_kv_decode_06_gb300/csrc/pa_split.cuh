@@ -96,7 +96,7 @@ __device__ __forceinline__ int first_visible_page(int L, int qn, int window) {
 
 // Which pages of a sequence a kernel walks.  kAll: those that a sliding window leaves, or
 // all.  kFirst: a window and the first tokens before it.  kOwn: those behind the pages
-// that its group shares (pa_shared.cuh).
+// that its group shares (pa_shared.h).
 enum class Walk { kAll, kFirst, kOwn };
 
 // kFirst and kOwn: the pages walked are the logical pages 0 .. keep - 1 and keep + skip
