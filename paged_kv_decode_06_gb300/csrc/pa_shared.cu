@@ -211,6 +211,7 @@ constexpr int kConverter0 = 8, kConverters = 8;   // fp8 caches: warps 8 .. 11 f
 constexpr int kSoftmaxWarps = 8;          // the last: a slot's four, a thread a row
 constexpr int kBlockPages = kSharedBlockPages;   // K or V of 128 keys in a place of its ring
 constexpr int kKeys = 16 * kBlockPages;
+constexpr uint64_t kDrainNs = 200000000;  // for copies and products that are on their way at the end
 constexpr int kSubPages = 4;              // a product and its softmax: 64 keys
 constexpr uint32_t kCols = 512;
 constexpr uint32_t kColS = 0;             // + 128 slot + 64 (sub-block % 2): S, its P over the first 32 columns
@@ -499,11 +500,12 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
           }
         }
       }
-      // No copy may be on its way when the CTA ends (one is only where a wait ran out).
+      // No copy may be on its way when the CTA ends (one is only where a wait ran out, which
+      // a caller's limit may be too short for).
       const uint32_t places = FP8 ? kRaws : is_v ? GG::VR : GG::KR;
       for (uint32_t k = n > places ? n - places : 0; k < n; ++k)
         warp_wait(FP8 ? rawfull_bar(is_v * RAWS + k % kRaws) : full_bar(place(is_v, k)),
-                  (FP8 ? k / kRaws : phase(is_v, k)) & 1u, p.wait_ns);
+                  (FP8 ? k / kRaws : phase(is_v, k)) & 1u, kDrainNs);
     }
   } else if (FP8 && warp >= kConverter0 && warp < GG::SOFT0) {
     // ============================== converters ===============================
@@ -634,7 +636,7 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
     // every product must be complete before tensor memory is freed
     if (elect_one()) umma_commit(drain_bar(warp));
     __syncwarp();
-    if (!warp_wait(drain_bar(warp), 0u, p.wait_ns) && lane == 0) atomicOr(p.err, kErrTimeout);
+    if (!warp_wait(drain_bar(warp), 0u, kDrainNs) && lane == 0) atomicOr(p.err, kErrTimeout);
   } else {
     // ================================ softmax ================================
     registers_up<GG::R_SOFT>();

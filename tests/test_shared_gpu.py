@@ -325,3 +325,12 @@ def test_as_many_sequences_as_a_call_takes():
     at = np.concatenate([[0], np.cumsum(sizes)]).tolist()
     b = Batch(lens, hq=2, hkv=1, d=64, kv="bf16", groups=(at, shared.tolist()), seed=4)
     b.check(*_run(b))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_a_wait_limit_alone_changes_nothing(kv):
+    b = Batch(900 + np.arange(50), hq=16, hkv=2, d=128, kv=kv, groups=([0, 50], [890]), seed=6)
+    out, lse = _run(b)
+    o, l = _run(b, wait_limit_us=50000)
+    b.check(o, l)
+    assert torch.equal(o, out) and torch.equal(l, lse)
