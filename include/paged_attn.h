@@ -115,7 +115,8 @@ typedef struct pa_options_t {
                                   past a sequence's end may hold anything, even non-finite values */
   const struct pa_tensor_t* v_token_scales;  /* the same for V (value = code * v_scale * scale) */
   int32_t wait_limit_us;       /* >0: every pipeline wait inside the decode kernels gives up after this
-                                  many microseconds (status bit 3, the kernel returns); 0 = 2 seconds */
+                                  many microseconds (status bit 3; the kernel returns behind the copies
+                                  that are on their way); 0 = 2 seconds */
   int32_t test_starve_cta;     /* testing aid for the give-up path, 0 = off.  k > 0: the producer warp
                                   of split CTA k-1 issues no copies, so that CTA's consumer warps wait
                                   out wait_limit_us, set status bit 3 and return; the call's results

@@ -20,6 +20,9 @@ constexpr uint32_t kErrPosition = 64u;
 // A pipeline wait gives up after this long (nanoseconds of %globaltimer)
 // unless the call sets its own limit.
 constexpr uint64_t kWaitTimeoutNs = 2000000000ull;
+// Copies and products that are on their way when a kernel's loops end have a limit of their
+// own, whatever the call's: a CTA must not end before them.
+constexpr uint64_t kDrainNs = 200000000;
 
 constexpr int kPage = 16;
 

@@ -211,7 +211,6 @@ constexpr int kConverter0 = 8, kConverters = 8;   // fp8 caches: warps 8 .. 11 f
 constexpr int kSoftmaxWarps = 8;          // the last: a slot's four, a thread a row
 constexpr int kBlockPages = kSharedBlockPages;   // K or V of 128 keys in a place of its ring
 constexpr int kKeys = 16 * kBlockPages;
-constexpr uint64_t kDrainNs = 200000000;  // for copies and products that are on their way at the end
 constexpr int kSubPages = 4;              // a product and its softmax: 64 keys
 constexpr uint32_t kCols = 512;
 constexpr uint32_t kColS = 0;             // + 128 slot + 64 (sub-block % 2): S, its P over the first 32 columns

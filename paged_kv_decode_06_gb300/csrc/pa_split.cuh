@@ -814,6 +814,18 @@ __global__ void __launch_bounds__(kSplitMaxThreads, 1)
         ++round;
       }
     }
+    // No copy may be on its way when the CTA ends: consumer warps that gave up on a wait do
+    // not see theirs land.  (Each place's last phase; a place is filled again only here.)
+    bool landed = true;
+    for (int s = 0; s < nstage; ++s) {
+      const uint32_t fills = round + (s < stage ? 1u : 0u);
+      if (fills > 0) landed &= mbar_wait(full_bar(s), (fills - 1) & 1u, kDrainNs);
+    }
+    for (int s = 0; s < 2; ++s) {
+      const int fills = (qseg + 1 - s) >> 1;
+      if (fills > 0) landed &= mbar_wait(qfull_bar(s), static_cast<uint32_t>(fills - 1) & 1u, kDrainNs);
+    }
+    if (!landed && lane == 0) atomicOr(p.err, kErrTimeout);
     // (the merge, which waits for this grid, reads what the shared part's kernel leaves)
     if (WALK == Walk::kOwn && g == 0) grid_dependency_wait();
     return;
