@@ -121,14 +121,19 @@ typedef struct pa_options_t {
                                   of split CTA k-1 issues no copies, so that CTA's consumer warps wait
                                   out wait_limit_us, set status bit 3 and return; the call's results
                                   are then undefined (the affected rows keep stale partials).  The
-                                  mma.sync split kernel only (PA_ERR_UNSUPPORTED for the tcgen05 and
-                                  MLA kernels) */
+                                  mma.sync split kernel only (PA_ERR_UNSUPPORTED for the tcgen05, MLA
+                                  and 4-bit kernels and for shared prefixes) */
   int32_t segment_cost_pages;  /* tensor-memory MLA kernel: the work split charges
                                   every unit (sequence, head chunk) a CTA starts this many pages on
                                   top of its pages, so CTAs that open more units get fewer pages
                                   (a unit costs a Q staging and an epilogue).  0 = the planner's
                                   value for the shape; < 0 = an equal page split.  Ignored by the
                                   other kernels */
+  int32_t test_give_up_cta;    /* testing aid for the give-up path, 0 = off.  k > 0: the consumer warps
+                                  of split CTA k-1 take a wait as one that ran out while copies are on
+                                  their way; what else waits for them waits out wait_limit_us.  Status
+                                  bit 3 is set, the call's results are undefined.  The mma.sync split
+                                  kernel only (PA_ERR_UNSUPPORTED for the others) */
 } pa_options_t;
 
 /* Launch plan the library picks for a problem shape (for tests, tuning and

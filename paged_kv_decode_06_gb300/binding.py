@@ -39,7 +39,7 @@ class PaOptions(ctypes.Structure):
                 ("use_tcgen05", ctypes.c_int32),
                 ("k_token_scales", ctypes.POINTER(PaTensor)), ("v_token_scales", ctypes.POINTER(PaTensor)),
                 ("wait_limit_us", ctypes.c_int32), ("test_starve_cta", ctypes.c_int32),
-                ("segment_cost_pages", ctypes.c_int32)]
+                ("segment_cost_pages", ctypes.c_int32), ("test_give_up_cta", ctypes.c_int32)]
 
 
 class PaPlan(ctypes.Structure):
@@ -215,13 +215,15 @@ def make_options(num_ctas=0, min_pages_per_cta=0, heads_per_cta=0, disable_pdl=F
                  workspace_bytes=0, split_start_event=None, split_stop_event=None, page_pairing=0,
                  sliding_window=0, sinks=None, use_tcgen05=0, k_token_scales=None,
                  v_token_scales=None, wait_limit_us=0, test_starve_cta=0,
-                 segment_cost_pages=0) -> PaOptions:
+                 segment_cost_pages=0, test_give_up_cta=0) -> PaOptions:
     """Options for paged_attn_decode_ex.  sinks: CUDA float32 tensor [Hq] (kept
     alive by the caller) or None.  use_tcgen05: 0 planner's choice, 1 never,
     2 always (bf16 caches).  k_token_scales / v_token_scales: CUDA float32
     [NB, Hkv, 16] per-token scales of an fp8 cache (kept alive by the caller).
     wait_limit_us: pipeline wait limit (0 = 2 s).  test_starve_cta: testing aid,
     k > 0 makes split CTA k-1 receive no pages (its waits run out).
+    test_give_up_cta: testing aid, k > 0 makes the consumers of split CTA k-1
+    give up while its pages are on their way.
     segment_cost_pages: tensor-memory MLA work split, pages charged per unit a
     CTA starts (0 planner's value, < 0 equal page split)."""
     o = PaOptions()
@@ -235,6 +237,7 @@ def make_options(num_ctas=0, min_pages_per_cta=0, heads_per_cta=0, disable_pdl=F
     o.wait_limit_us = wait_limit_us
     o.test_starve_cta = test_starve_cta
     o.segment_cost_pages = segment_cost_pages
+    o.test_give_up_cta = test_give_up_cta
     if sinks is not None:
         if sinks.dtype != torch.float32 or not sinks.is_contiguous():
             raise TypeError("sinks must be a contiguous float32 tensor")

@@ -78,6 +78,16 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
   }
 }
 
+// Waits at a kernel's end, for what may still be on its way: all of them within kDrainNs.
+struct Drain {
+  uint64_t t0;
+  __device__ __forceinline__ Drain() : t0(global_timer_ns()) {}
+  __device__ __forceinline__ void wait(uint32_t bar, uint32_t parity) const {
+    const uint64_t used = global_timer_ns() - t0;
+    mbar_wait(bar, parity, used < kDrainNs ? kDrainNs - used : 0);
+  }
+};
+
 // ------------------------------------------------------------------ TMA
 // Order this thread's earlier generic-proxy shared-memory accesses before
 // later async-proxy (TMA) accesses.

@@ -39,11 +39,12 @@ constexpr int kTcBlockPages = 4;
 constexpr int kTcThreads = 384;
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;   // pipeline wait limit without wait_limit_us
 
-// Wait limit and starved CTA of a call (pa_options_t.wait_limit_us, test_starve_cta).
+// Wait limit, starved CTA and CTA that gives up of a call (pa_options_t.wait_limit_us, test_*_cta).
 uint64_t wait_limit_ns(const pa_options_t* opts) {
   return (opts && opts->wait_limit_us > 0) ? static_cast<uint64_t>(opts->wait_limit_us) * 1000ull : kDefaultWaitNs;
 }
 int starved_cta(const pa_options_t* opts) { return (opts && opts->test_starve_cta > 0) ? opts->test_starve_cta - 1 : -1; }
+int give_up_cta(const pa_options_t* opts) { return (opts && opts->test_give_up_cta > 0) ? opts->test_give_up_cta - 1 : -1; }
 
 thread_local std::string t_last_error;
 
@@ -518,8 +519,8 @@ int decode_impl(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* 
   if (!std::isfinite(scale) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
     return fail(PA_ERR_INVALID_ARG, "scale, k_scale and v_scale must be finite");
   if (opts && opts->sinks && !aligned(opts->sinks, 4)) return fail(PA_ERR_INVALID_ARG, "sinks must be 4-byte aligned");
-  if (opts && (opts->wait_limit_us < 0 || opts->test_starve_cta < 0))
-    return fail(PA_ERR_INVALID_ARG, "wait_limit_us and test_starve_cta must not be negative");
+  if (opts && (opts->wait_limit_us < 0 || opts->test_starve_cta < 0 || opts->test_give_up_cta < 0))
+    return fail(PA_ERR_INVALID_ARG, "wait_limit_us, test_starve_cta and test_give_up_cta must not be negative");
   const bool tok = has_token_scales(opts);
   if (tok) {
     if (kc->dtype != PA_FP8_E4M3) return fail(PA_ERR_INVALID_ARG, "per-token scales need an fp8 cache");
@@ -616,8 +617,9 @@ int decode_impl(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* 
   }
   sp.wait_ns = wait_limit_ns(opts);
   sp.starve_cta = starved_cta(opts);
-  if (sp.starve_cta >= 0 && pl.tc)
-    return fail(PA_ERR_UNSUPPORTED, "test_starve_cta applies to the mma.sync split kernel only");
+  sp.give_up_cta = give_up_cta(opts);
+  if ((sp.starve_cta >= 0 || sp.give_up_cta >= 0) && pl.tc)
+    return fail(PA_ERR_UNSUPPORTED, "test_starve_cta and test_give_up_cta apply to the mma.sync split kernel only");
 
   pa::MergeParams mp = {};
   mp.out = sp.out;
@@ -710,9 +712,9 @@ int check_mla_options(const pa_options_t* opts) {
   if (opts->segment_cost_pages > kMaxSegCost)
     return fail(PA_ERR_INVALID_ARG, "segment_cost_pages %d > %d", opts->segment_cost_pages, kMaxSegCost);
   if (opts->heads_per_cta != 0 || opts->sliding_window > 0 || opts->sinks != nullptr || has_token_scales(opts) ||
-      opts->test_starve_cta != 0)
+      opts->test_starve_cta != 0 || opts->test_give_up_cta != 0)
     return fail(PA_ERR_UNSUPPORTED, "MLA decode takes none of heads_per_cta, sliding_window, sinks, token scales, "
-                "test_starve_cta");
+                "test_starve_cta, test_give_up_cta");
   return PA_OK;
 }
 
@@ -977,7 +979,7 @@ int mla_decode_impl(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor
   sp.team_bytes = pl.team_bytes;
   sp.q_slots = pl.q_slots;
   sp.wait_ns = wait_limit_ns(opts);
-  sp.starve_cta = -1;
+  sp.starve_cta = sp.give_up_cta = -1;
   sp.pair_pages = pl.pair;
   sp.off_buf = pl.off_buf;
   sp.off_qring = pl.off_qring;
@@ -1100,6 +1102,7 @@ int host_split_plan(int B, int Hq, int Hkv, int D, int kv_dtype, int max_qlen, c
   r.sp.tok_bytes = pl.tok_bytes;
   r.sp.wait_ns = wait_limit_ns(opts);
   r.sp.starve_cta = starved_cta(opts);
+  r.sp.give_up_cta = give_up_cta(opts);
   r.threads = pl.threads;
   r.grid = pl.grid;
   r.smem = static_cast<int>(pl.smem);

@@ -38,9 +38,10 @@ int check_shape(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_qlen,
                      static_cast<long long>(Hq / Hkv), static_cast<long long>(max_qlen), kMaxRows);
   if (o == nullptr) return PA_OK;
   const bool tok = (o->k_token_scales && o->k_token_scales->data) || (o->v_token_scales && o->v_token_scales->data);
-  if (o->use_tcgen05 != 0 || o->page_pairing != 0 || tok || o->test_starve_cta != 0 || o->segment_cost_pages != 0)
+  if (o->use_tcgen05 != 0 || o->page_pairing != 0 || tok || o->test_starve_cta != 0 || o->segment_cost_pages != 0 ||
+      o->test_give_up_cta != 0)
     return host_fail(PA_ERR_UNSUPPORTED, "4-bit decode takes none of use_tcgen05, page_pairing, token scales, "
-                     "test_starve_cta, segment_cost_pages");
+                     "test_starve_cta, segment_cost_pages, test_give_up_cta");
   if (o->num_ctas < 0 || o->num_ctas > kMaxCtas || o->min_pages_per_cta < 0)
     return host_fail(PA_ERR_INVALID_ARG, "num_ctas must be in [0, %d] and min_pages_per_cta not negative", kMaxCtas);
   if (o->heads_per_cta < 0 || (o->heads_per_cta > 0 && Hkv % o->heads_per_cta != 0))

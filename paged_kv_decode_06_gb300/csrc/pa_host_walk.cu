@@ -36,8 +36,8 @@ int check_options(const pa_options_t* o, int64_t Hkv, bool tokens_too) {
     return host_fail(PA_ERR_INVALID_ARG, "num_ctas must be in [0, %d] and min_pages_per_cta not negative", kMaxCtas);
   if (o->heads_per_cta < 0 || (o->heads_per_cta > 0 && Hkv % o->heads_per_cta != 0))
     return host_fail(PA_ERR_INVALID_ARG, "heads_per_cta %d must divide num_kv_heads %lld", o->heads_per_cta, ll(Hkv));
-  if (o->wait_limit_us < 0 || o->test_starve_cta < 0)
-    return host_fail(PA_ERR_INVALID_ARG, "wait_limit_us and test_starve_cta must not be negative");
+  if (o->wait_limit_us < 0 || o->test_starve_cta < 0 || o->test_give_up_cta < 0)
+    return host_fail(PA_ERR_INVALID_ARG, "wait_limit_us, test_starve_cta and test_give_up_cta must not be negative");
   if (o->sinks && !host_aligned(o->sinks, 4)) return host_fail(PA_ERR_INVALID_ARG, "sinks must be 4-byte aligned");
   return PA_OK;
 }

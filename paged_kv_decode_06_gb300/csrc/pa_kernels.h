@@ -72,6 +72,8 @@ struct SplitParams {
   // testing aid (mma.sync kernel): the producer of split CTA starve_cta issues
   // no copies, so that CTA's consumers run into the wait limit; -1 = none
   int32_t starve_cta;
+  // testing aid: the consumers of split CTA give_up_cta take a wait as one that ran out (-1 = off)
+  int32_t give_up_cta;
   // tensor-memory MLA kernel: the Q staging ring; pages the work split
   // charges for every unit a CTA starts (0: an equal page split)
   uint32_t off_qring;

@@ -814,18 +814,6 @@ __global__ void __launch_bounds__(kSplitMaxThreads, 1)
         ++round;
       }
     }
-    // No copy may be on its way when the CTA ends: consumer warps that gave up on a wait do
-    // not see theirs land.  (Each place's last phase; a place is filled again only here.)
-    bool landed = true;
-    for (int s = 0; s < nstage; ++s) {
-      const uint32_t fills = round + (s < stage ? 1u : 0u);
-      if (fills > 0) landed &= mbar_wait(full_bar(s), (fills - 1) & 1u, kDrainNs);
-    }
-    for (int s = 0; s < 2; ++s) {
-      const int fills = (qseg + 1 - s) >> 1;
-      if (fills > 0) landed &= mbar_wait(qfull_bar(s), static_cast<uint32_t>(fills - 1) & 1u, kDrainNs);
-    }
-    if (!landed && lane == 0) atomicOr(p.err, kErrTimeout);
     // (the merge, which waits for this grid, reads what the shared part's kernel leaves)
     if (WALK == Walk::kOwn && g == 0) grid_dependency_wait();
     return;
@@ -861,21 +849,15 @@ __global__ void __launch_bounds__(kSplitMaxThreads, 1)
   int stage = 0;
   uint32_t round = 0;              // k / nstage for the page at `stage`
   int64_t k = 0;
-  while (k < count) {
-    if (!mbar_wait(full_bar(stage), round & 1u, p.wait_ns)) {
-      if (lane == 0) atomicOr(p.err, kErrTimeout);
-      break;
-    }
+  if (g != p.give_up_cta) while (k < count) {   // (testing aid: that CTA's consumers give up at once)
+    if (!mbar_wait(full_bar(stage), round & 1u, p.wait_ns)) break;
     if (k == 0 || cu.j == 0) {
       // ---- new segment: query rows into registers, state reset ----
       si = seq_info(p, s_len, s_qsl, cu.i, lane == 0 && hh == 0 && w == 0, window);
       seg_k0 = k;
       seg_j0 = cu.j;
       const int qs = qseg & 1;
-      if (!mbar_wait(qfull_bar(qs), static_cast<uint32_t>(qseg >> 1) & 1u, p.wait_ns)) {
-        if (lane == 0) atomicOr(p.err, kErrTimeout);
-        break;
-      }
+      if (!mbar_wait(qfull_bar(qs), static_cast<uint32_t>(qseg >> 1) & 1u, p.wait_ns)) break;
       if (seg_j0 == 0 && cw == 0 && lane == 0) {
         // This CTA holds the unit's first page: describe the unit for the merge.
         const int64_t a = static_cast<int64_t>(NC) * s_pre[cu.i] + static_cast<int64_t>(cu.c) * cu.n;
@@ -925,10 +907,7 @@ __global__ void __launch_bounds__(kSplitMaxThreads, 1)
     }
     const bool pair = p.pair_pages && (k + 1 < count) && (cu.j + 1 < cu.n) &&
                       (WALK != Walk::kFirst || view.skip == 0 || cu.j + 1 != view.keep);
-    if (pair && !mbar_wait(full_bar(stage2), round2 & 1u, p.wait_ns)) {
-      if (lane == 0) atomicOr(p.err, kErrTimeout);
-      break;
-    }
+    if (pair && !mbar_wait(full_bar(stage2), round2 & 1u, p.wait_ns)) break;
     const int tb = kPage * (kHole ? view.page(cu.j) : si.js + cu.j);
     const int first = WALK == Walk::kFirst ? p.first_tokens : 0;
     if (active) {
@@ -1026,6 +1005,21 @@ __global__ void __launch_bounds__(kSplitMaxThreads, 1)
       }
     }
     k += np;
+  }
+  if (k < count) {
+    // This warp gave up on a wait.  No copy may be on its way when the CTA ends: those of the pages
+    // that the ring holds from this one on, and of the next two segments' query rows (no
+    // place is filled again before this warp gives it back).
+    if (lane == 0) atomicOr(p.err, kErrTimeout);
+    const Drain drain;
+    for (int64_t x = k; x < count && x < k + nstage; ++x) {
+      drain.wait(full_bar(stage), round & 1u);
+      if (++stage == nstage) {
+        stage = 0;
+        ++round;
+      }
+    }
+    for (int s = qseg; s < qseg + 2; ++s) drain.wait(qfull_bar(s & 1), static_cast<uint32_t>(s >> 1) & 1u);
   }
 }
 

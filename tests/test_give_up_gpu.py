@@ -1,5 +1,6 @@
-"""Decode calls whose waits are allowed a microsecond: some of them give up while copies
-are on their way.  The call ends soon, within its buffers, and the next one is right."""
+"""Decode calls in which warps give up on a wait while copies are on their way: the
+consumers of one CTA do at once (test_give_up_cta), so the warps that wait for them wait
+out the limit.  The call ends soon, within its buffers, and the next one is right."""
 import time
 
 import numpy as np
@@ -36,37 +37,34 @@ def _shared(b, dev, out, lse, **kw):
                                      lse=lse, options=b.options(**kw))
 
 
-def _hurried(call, b, view, **kw):
-    """Calls with a limit of 1 us over caches that no L2 line holds, then an ordinary one."""
+def _given_up(call, b, view, ctas=(1, 6), **kw):
     dev = b.on_gpu()
-    big = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
-    out, lse = b.buffers()
-    t0 = time.perf_counter()
-    for _ in range(5):
-        big.zero_()
-        call(b, dev, out, lse, wait_limit_us=1, **kw)
-    torch.cuda.synchronize()
-    assert time.perf_counter() - t0 < 5.0
-    assert binding.paged_attn_device_status(clear=True) in (0, binding.STATUS_TIMEOUT)
-    out, lse = b.buffers()
-    call(b, dev, out, lse, **kw)
-    b.check(out, lse, *view)
+    for k in ctas:
+        out, lse = b.buffers()
+        t0 = time.perf_counter()
+        call(b, dev, out, lse, wait_limit_us=1000, test_give_up_cta=k, **kw)
+        torch.cuda.synchronize()
+        assert time.perf_counter() - t0 < 2.0
+        assert binding.paged_attn_device_status(clear=True) == binding.STATUS_TIMEOUT
+        out, lse = b.buffers()
+        call(b, dev, out, lse, **kw)
+        b.check(out, lse, *view)
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 @pytest.mark.parametrize("call,view", [(_decode, ()), (_window, (700, 20))])
 def test_split_kernel(call, view, kv):
     b = Batch(1000 + 37 * np.arange(24), 1 + np.arange(24) % 3, hq=8, hkv=4, kv=kv, seed=1)
-    _hurried(call, b, view)
-
-
-@pytest.mark.parametrize("kv", ["bf16", "fp8"])
-def test_shared_prefix(kv):
-    b = Batch(1400 + np.arange(40), hq=16, hkv=2, kv=kv, groups=([0, 40], [1390]), seed=2)
-    _hurried(_shared, b, ())
-    _hurried(_shared, b, (), num_ctas=20)
+    _given_up(call, b, view)
 
 
 def test_token_scales():
     b = Batch(600 + 37 * np.arange(12), hq=8, hkv=4, kv="fp8", tokens=True, seed=3)
-    _hurried(_window, b, (700, 20))
+    _given_up(_window, b, (700, 20))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_sequences_behind_a_shared_prefix(kv):
+    b = Batch(1400 + np.arange(40), hq=16, hkv=2, kv=kv, groups=([0, 40], [1390]), seed=2)
+    _given_up(_shared, b, ())
+    _given_up(_shared, b, (), num_ctas=20)
