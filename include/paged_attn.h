@@ -131,9 +131,10 @@ typedef struct pa_options_t {
                                   other kernels */
   int32_t test_give_up_cta;    /* testing aid for the give-up path, 0 = off.  k > 0: the consumer warps
                                   of split CTA k-1 take a wait as one that ran out while copies are on
-                                  their way; what else waits for them waits out wait_limit_us.  Status
-                                  bit 3 is set, the call's results are undefined.  The mma.sync split
-                                  kernel only (PA_ERR_UNSUPPORTED for the others) */
+                                  their way (of the tensor-memory kernel the softmax warps); what else
+                                  waits for them waits out wait_limit_us.  Status bit 3 is set, the
+                                  call's results are undefined.  The split kernels only
+                                  (PA_ERR_UNSUPPORTED for the MLA and 4-bit kernels) */
 } pa_options_t;
 
 /* Launch plan the library picks for a problem shape (for tests, tuning and

@@ -618,8 +618,8 @@ int decode_impl(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t* 
   sp.wait_ns = wait_limit_ns(opts);
   sp.starve_cta = starved_cta(opts);
   sp.give_up_cta = give_up_cta(opts);
-  if ((sp.starve_cta >= 0 || sp.give_up_cta >= 0) && pl.tc)
-    return fail(PA_ERR_UNSUPPORTED, "test_starve_cta and test_give_up_cta apply to the mma.sync split kernel only");
+  if (sp.starve_cta >= 0 && pl.tc)
+    return fail(PA_ERR_UNSUPPORTED, "test_starve_cta applies to the mma.sync split kernel only");
 
   pa::MergeParams mp = {};
   mp.out = sp.out;

@@ -308,6 +308,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ++round;
       }
     }
+    // No copy may be on its way when the CTA ends: warps that gave up on a wait do not see
+    // theirs land.  (A place's last phase; one that another producer's part never reached
+    // runs into the limit, and every copy has landed by then.)
+    const Drain drain;
+    for (int s = 0; s < nstage; ++s) {
+      const uint32_t fills = round + (s < stage ? 1u : 0u);
+      if (fills > 0) drain.wait(full_bar(s), (fills - 1) & 1u);
+    }
   } else if (warp == kTcMmaWarp) {
     // ============================ Q K^T issuer =============================
     const uint32_t idesc_s_base = umma_idesc_bf16(128, 16, false) & ~(0x3Fu << 17);
@@ -349,7 +357,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // Every MMA this warp issued must be complete before tensor memory is freed.
     if (lane == 0) umma_commit(drain_bar);
     __syncwarp();
-    if (!warp_wait(drain_bar, 0u, p.wait_ns) && lane == 0) atomicOr(p.err, kErrTimeout);
+    if (!warp_wait(drain_bar, 0u, kDrainNs) && lane == 0) atomicOr(p.err, kErrTimeout);
   } else if (warp == kTcPvWarp) {
     // ============================ P V issuer ===============================
     // Runs beside the Q K^T issuer, so the two MMA streams do not wait on
@@ -421,7 +429,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (!ok && lane == 0) atomicOr(p.err, kErrTimeout);
     if (lane == 0) umma_commit(drain2_bar);
     __syncwarp();
-    if (!warp_wait(drain2_bar, 0u, p.wait_ns) && lane == 0) atomicOr(p.err, kErrTimeout);
+    if (!warp_wait(drain2_bar, 0u, kDrainNs) && lane == 0) atomicOr(p.err, kErrTimeout);
   } else {
     // ============================ softmax ==================================
     // Two groups of four warps; group gi = (warp - 4) / 4 takes the blocks b
@@ -438,7 +446,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     float4* const xstat = reinterpret_cast<float4*>(gbase + p.off_xchg);   // [segment % 2][group][128] (max, sum, rounded sum)
     constexpr int HD = D / 2;              // O columns each group's thread writes out
     constexpr int NP4 = kTcMaxBlockPages;
-    BlockWalker wk(s_pre, B, NC, start, count, kTcMaxBlockPages);
+    const bool quit = g == p.give_up_cta;  // testing aid: this CTA's softmax gives up at once
+    BlockWalker wk(s_pre, B, NC, start, quit ? 0 : count, kTcMaxBlockPages);
     int b = 0, seg = -1, b0 = 0;
     SeqInfo si = {0, 0, 0, 0};
     bool row_ok = false;
@@ -446,7 +455,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int64_t seg_k0 = 0;
     float m = -INFINITY, l = 0.f;          // this group's running max (log2 units) and sum of the row
     float lr = 0.f;                        // the sum of the weights as rounded into P (O's normaliser)
-    bool ok = true;
+    bool ok = !quit;
 
     // This thread's half (by group) of row rho of the segment starting at
     // block t, into TMEM Q slot `slot` (rows past G * qn are zero); q_full

@@ -11,7 +11,7 @@ from paged_kv_decode_06_gb300 import binding
 from paged_kv_decode_06_gb300 import build as builder
 from tests import test_abi, test_walk_abi
 
-KERNELS = ["pa_split.cuh", "pa_shared.cu"]
+KERNELS = ["pa_split.cuh", "pa_split_tc.cuh", "pa_shared.cu"]
 
 
 def _code(name):

@@ -68,3 +68,9 @@ def test_sequences_behind_a_shared_prefix(kv):
     b = Batch(1400 + np.arange(40), hq=16, hkv=2, kv=kv, groups=([0, 40], [1390]), seed=2)
     _given_up(_shared, b, ())
     _given_up(_shared, b, (), num_ctas=20)
+
+
+@pytest.mark.parametrize("runs", [1, 5])
+def test_tensor_memory_split_kernel(runs):
+    b = Batch(1000 + 37 * np.arange(24), 1 + np.arange(24) % runs, hq=16, hkv=2, seed=4)
+    _given_up(_decode, b, (), use_tcgen05=2)
