@@ -133,8 +133,8 @@ typedef struct pa_options_t {
                                   of split CTA k-1 take a wait as one that ran out while copies are on
                                   their way (of the tensor-memory kernel the softmax warps); what else
                                   waits for them waits out wait_limit_us.  Status bit 3 is set, the
-                                  call's results are undefined.  The split kernels only
-                                  (PA_ERR_UNSUPPORTED for the MLA and 4-bit kernels) */
+                                  call's results are undefined.  Not for the tensor-memory MLA and
+                                  4-bit kernels (PA_ERR_UNSUPPORTED) */
 } pa_options_t;
 
 /* Launch plan the library picks for a problem shape (for tests, tuning and

@@ -708,13 +708,14 @@ int check_mla_options(const pa_options_t* opts) {
     return fail(PA_ERR_INVALID_ARG, "use_tcgen05 %d not in {0, 1, 2}", opts->use_tcgen05);
   if (opts->page_pairing < 0 || opts->page_pairing > 2)
     return fail(PA_ERR_INVALID_ARG, "page_pairing %d not in {0, 1, 2}", opts->page_pairing);
-  if (opts->wait_limit_us < 0) return fail(PA_ERR_INVALID_ARG, "wait_limit_us %d is negative", opts->wait_limit_us);
+  if (opts->wait_limit_us < 0 || opts->test_give_up_cta < 0)
+    return fail(PA_ERR_INVALID_ARG, "wait_limit_us and test_give_up_cta must not be negative");
   if (opts->segment_cost_pages > kMaxSegCost)
     return fail(PA_ERR_INVALID_ARG, "segment_cost_pages %d > %d", opts->segment_cost_pages, kMaxSegCost);
   if (opts->heads_per_cta != 0 || opts->sliding_window > 0 || opts->sinks != nullptr || has_token_scales(opts) ||
-      opts->test_starve_cta != 0 || opts->test_give_up_cta != 0)
+      opts->test_starve_cta != 0)
     return fail(PA_ERR_UNSUPPORTED, "MLA decode takes none of heads_per_cta, sliding_window, sinks, token scales, "
-                "test_starve_cta, test_give_up_cta");
+                "test_starve_cta");
   return PA_OK;
 }
 
@@ -979,7 +980,10 @@ int mla_decode_impl(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor
   sp.team_bytes = pl.team_bytes;
   sp.q_slots = pl.q_slots;
   sp.wait_ns = wait_limit_ns(opts);
-  sp.starve_cta = sp.give_up_cta = -1;
+  sp.starve_cta = -1;
+  sp.give_up_cta = give_up_cta(opts);
+  if (sp.give_up_cta >= 0 && pl.tc)
+    return fail(PA_ERR_UNSUPPORTED, "test_give_up_cta does not apply to the tensor-memory MLA kernel");
   sp.pair_pages = pl.pair;
   sp.off_buf = pl.off_buf;
   sp.off_qring = pl.off_qring;

@@ -512,21 +512,15 @@ __global__ void __launch_bounds__(MlaTeams<RT>::THREADS, 1)
   int stage = 0;
   uint32_t round = 0;
   int k = 0;
-  while (k < count) {
-    if (!mbar_wait(full_bar(stage), round & 1u, p.wait_ns)) {
-      if (lane == 0) atomicOr(p.err, kErrTimeout);
-      break;
-    }
+  if (static_cast<int>(blockIdx.x) != p.give_up_cta) while (k < count) {   // (testing aid: its consumers give up at once)
+    if (!mbar_wait(full_bar(stage), round & 1u, p.wait_ns)) break;
     if (k == 0 || cu.j == 0) {
       // ---- new segment: query rows into registers, state reset ----
       si = seq_info(p, s_len, s_qsl, cu.i, lane == 0 && cw == 0, 0);
       seg_first_page = k == 0;
       seg_j0 = cu.j;
       const int qs = qseg % p.q_slots;
-      if (!mbar_wait(qfull_bar(qs), static_cast<uint32_t>(qseg / p.q_slots) & 1u, p.wait_ns)) {
-        if (lane == 0) atomicOr(p.err, kErrTimeout);
-        break;
-      }
+      if (!mbar_wait(qfull_bar(qs), static_cast<uint32_t>(qseg / p.q_slots) & 1u, p.wait_ns)) break;
       if (seg_j0 == 0 && cw == 0 && lane == 0) {
         // This worker holds the unit's first page: describe the unit for the merge.
         const int64_t xt = total_pages();
@@ -560,10 +554,7 @@ __global__ void __launch_bounds__(MlaTeams<RT>::THREADS, 1)
       ++round2;
     }
     const bool pair = p.pair_pages && (k + 1 < count) && (cu.j + 1 < cu.n);
-    if (pair && !mbar_wait(full_bar(stage2), round2 & 1u, p.wait_ns)) {
-      if (lane == 0) atomicOr(p.err, kErrTimeout);
-      break;
-    }
+    if (pair && !mbar_wait(full_bar(stage2), round2 & 1u, p.wait_ns)) break;
     const int tb = kPage * cu.j;
     if (active) {
       // exchange buffer b = step parity is used for the (step >> 1)-th time
@@ -580,10 +571,7 @@ __global__ void __launch_bounds__(MlaTeams<RT>::THREADS, 1)
         ok = mla_pages<FP8, 1>(ws, sts, xb, xfull_bar(b, rt), (step >> 1) & 1u, cq, tb, si.L, si.L - si.qn, lim0,
                                lim1, p.scale_log2, lane, p.wait_ns);
       }
-      if (!ok) {
-        if (lane == 0) atomicOr(p.err, kErrTimeout);
-        break;
-      }
+      if (!ok) break;
       ++step;
     }
     __syncwarp();
@@ -667,6 +655,21 @@ __global__ void __launch_bounds__(MlaTeams<RT>::THREADS, 1)
       }
     }
     k += np;
+  }
+  if (k < count) {
+    // This warp gave up on a wait.  No copy may be on its way when the CTA ends: those of
+    // the pages that the ring holds from this one on, and of the next segments' query rows.
+    if (lane == 0) atomicOr(p.err, kErrTimeout);
+    const Drain drain;
+    for (int x = k; x < count && x < k + nstage; ++x) {
+      drain.wait(full_bar(stage), round & 1u);
+      if (++stage == nstage) {
+        stage = 0;
+        ++round;
+      }
+    }
+    for (int s = qseg; s < qseg + p.q_slots; ++s)
+      drain.wait(qfull_bar(s % p.q_slots), static_cast<uint32_t>(s / p.q_slots) & 1u);
   }
 }
 

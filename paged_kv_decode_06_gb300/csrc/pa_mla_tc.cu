@@ -436,6 +436,11 @@ __global__ void __launch_bounds__(kMtcThreads, 1)
       ++b;
     }
     if (!ok && lane == 0) atomicOr(p.err, kErrTimeout);
+    // No copy may be on its way when the CTA ends: warps that gave up on a wait do not see
+    // theirs land.  (A buffer's last phase; one that another producer's part never reached
+    // runs into the limit, and every copy has landed by then.)
+    for (int x = max(0, b - kMtcNbuf); x < b; ++x)
+      if (!mtc_wait(cfull_bar(x % kMtcNbuf), static_cast<uint32_t>(x / kMtcNbuf) & 1u, kDrainNs)) break;
   } else if (FP8 && warp == kMtcProducer) {
     // ==================== fp8: page producer ===============================
     Cursor cu = locate(s_pre, B, NC, start);
@@ -460,6 +465,11 @@ __global__ void __launch_bounds__(kMtcThreads, 1)
         stage = 0;
         ++round;
       }
+    }
+    // no copy may be on its way when the CTA ends: a place's last phase
+    for (int s = 0; s < nstage; ++s) {
+      const uint32_t fills = round + (s < stage ? 1u : 0u);
+      if (fills > 0 && !mtc_wait(full_bar(s), (fills - 1) & 1u, kDrainNs)) break;
     }
   } else if (FP8 && (warp == 3 || warp >= kMtcSoftmax0 + 4)) {
     // ==================== fp8: converters ==================================
@@ -569,7 +579,7 @@ __global__ void __launch_bounds__(kMtcThreads, 1)
     if (!ok && lane == 0) atomicOr(p.err, kErrTimeout);
     if (lane == 0) umma_commit(drain_bar);
     __syncwarp();
-    if (!mtc_wait(drain_bar, 0u, p.wait_ns) && lane == 0) atomicOr(p.err, kErrTimeout);
+    if (!mtc_wait(drain_bar, 0u, kDrainNs) && lane == 0) atomicOr(p.err, kErrTimeout);
   } else if (warp == kMtcPvWarp) {
     // ============================ P V issuer ===============================
     const uint32_t idesc = mtc_idesc(128, RP, !FP8, true, false);
@@ -636,7 +646,7 @@ __global__ void __launch_bounds__(kMtcThreads, 1)
     if (!ok && lane == 0) atomicOr(p.err, kErrTimeout);
     if (lane == 0) umma_commit(drain2_bar);
     __syncwarp();
-    if (!mtc_wait(drain2_bar, 0u, p.wait_ns) && lane == 0) atomicOr(p.err, kErrTimeout);
+    if (!mtc_wait(drain2_bar, 0u, kDrainNs) && lane == 0) atomicOr(p.err, kErrTimeout);
   } else {
     // ============================ softmax ==================================
     // Segment s keeps its Q rows, and so its S rows, in tensor-memory lane
@@ -1043,6 +1053,7 @@ __global__ void __launch_bounds__(kMtcThreads, 1)
       ++b;
     }
     if (!fine) atomicOr(p.err, kErrF16Range);
+    asm volatile("cp.async.wait_all;" ::: "memory");   // query slices that were staged for nobody
     if (!ok && lane == 0) atomicOr(p.err, kErrTimeout);
   }
 

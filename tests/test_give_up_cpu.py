@@ -11,7 +11,8 @@ from paged_kv_decode_06_gb300 import binding
 from paged_kv_decode_06_gb300 import build as builder
 from tests import test_abi, test_walk_abi
 
-KERNELS = ["pa_split.cuh", "pa_split_tc.cuh", "pa_shared.cu"]
+KERNELS = ["pa_split.cuh", "pa_split_tc.cuh", "pa_mla.cu", "pa_mla_tc.cu",
+           "pa_shared.cu"]
 
 
 def _code(name):
@@ -40,3 +41,10 @@ def test_give_up_option(lib):
         assert test_abi._opt_call(lib, o) == want
         for call in test_walk_abi.CALLS:
             assert call(lib, dict(test_walk_abi._args(), opts=o)) == want
+
+
+def test_give_up_option_of_mla(lib):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    for k, want in ((-1, binding.PA_ERR_INVALID_ARG), (2, binding.PA_ERR_CUDA)):
+        assert test_abi._mla_call(lib, dict(test_abi._mla_args(), opts=binding.make_options(test_give_up_cta=k))) == want

@@ -7,7 +7,9 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 from paged_kv_decode_06_gb300 import binding
+from paged_kv_decode_06_gb300 import workloads as wl
 from tests.walk_cases import Batch
 
 pytestmark = pytest.mark.gpu
@@ -74,3 +76,23 @@ def test_sequences_behind_a_shared_prefix(kv):
 def test_tensor_memory_split_kernel(runs):
     b = Batch(1000 + 37 * np.arange(24), 1 + np.arange(24) % runs, hq=16, hkv=2, seed=4)
     _given_up(_decode, b, (), use_tcgen05=2)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_mla(kv):
+    scale = 0.05 if kv == "fp8" else 1.0
+    w = wl.make_mla_workload(wl.custom_mla_spec(num_q_heads=16, kv_dtype=kv, seq_lens=(700, 1000, 333, 901, 640, 1023),
+                                                query_len_choices=(2,), kv_scale=scale, fp8_source_scale=scale, seed=5),
+                             device="cuda")
+    ref = oracle.run_mla_workload(w)
+    for k in (1, 6):
+        t0 = time.perf_counter()
+        binding.mla_decode_workload(w, options=binding.make_options(use_tcgen05=1, wait_limit_us=1000, test_give_up_cta=k))
+        torch.cuda.synchronize()
+        assert time.perf_counter() - t0 < 2.0
+        assert binding.paged_attn_device_status(clear=True) & binding.STATUS_TIMEOUT
+        out, lse = binding.mla_decode_workload(w, options=binding.make_options(use_tcgen05=1))
+        assert binding.paged_attn_device_status() == 0
+        # the bounds of the parity tests of these kernels
+        assert np.abs(out.float().cpu().numpy() - ref[0]).max() <= (2e-2 if kv == "fp8" else 1e-2)
+        assert np.abs(lse.cpu().numpy() - ref[1]).max() <= 1e-3
