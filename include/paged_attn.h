@@ -131,10 +131,11 @@ typedef struct pa_options_t {
                                   other kernels */
   int32_t test_give_up_cta;    /* testing aid for the give-up path, 0 = off.  k > 0: the consumer warps
                                   of split CTA k-1 take a wait as one that ran out while copies are on
-                                  their way (of the tensor-memory kernel the softmax warps); what else
-                                  waits for them waits out wait_limit_us.  Status bit 3 is set, the
-                                  call's results are undefined.  Not for the tensor-memory MLA and
-                                  4-bit kernels (PA_ERR_UNSUPPORTED) */
+                                  their way (of the tensor-memory kernel the softmax warps, of a shared
+                                  prefix those of one of CTA k-1's two tiles); what else waits for
+                                  them waits out wait_limit_us.  Status bit 3 is set, the call's
+                                  results are undefined.  Not for the tensor-memory MLA and 4-bit
+                                  kernels (PA_ERR_UNSUPPORTED) */
 } pa_options_t;
 
 /* Launch plan the library picks for a problem shape (for tests, tuning and

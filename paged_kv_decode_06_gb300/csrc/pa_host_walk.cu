@@ -427,6 +427,7 @@ int decode_shared(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
   hp.alone_cost = kAloneCost;
   hp.scale_log2 = sp.scale_log2;
   hp.wait_ns = sp.wait_ns;
+  hp.give_up_cta = sp.give_up_cta;
   hp.err = dev.status;
   hp.skip = reinterpret_cast<int32_t*>(wsb + pl.skip);
   hp.seq_group = reinterpret_cast<int32_t*>(wsb + pl.group_of);

@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
     const uint32_t tS0 = tbase + lane_off + kColS + 128u * slot, tO = tbase + lane_off + kColO + 128u * slot;
     uint32_t n = 0;                                           // sub-blocks of the pieces before
     float next_scale = 1.f;                                   // fp8: what the staged row was divided by
-    bool ok = true;
+    bool ok = cta != p.give_up_cta || slot != 0;              // (testing aid: this slot's warps give up at once)
     // this thread's query row of a piece into the slot's tile (rows past the pair's are
     // zero).  fp8 caches: in f16, divided by a power of two that leaves the largest element
     // in [1, 2).

@@ -87,6 +87,7 @@ struct SharedParams {
   int32_t split_boxes;        // 128 features, bf16: heads are not contiguous, pages come in four boxes
   float scale_log2;
   uint64_t wait_ns;
+  int32_t give_up_cta;        // testing aid: the softmax of this CTA's first slot gives up at once (-1 = off)
   uint32_t* err;
   // workspace: written by the plan kernel ...
   int32_t* skip;              // [B] pages that the group attends for the sequence

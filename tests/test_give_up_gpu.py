@@ -72,6 +72,14 @@ def test_sequences_behind_a_shared_prefix(kv):
     _given_up(_shared, b, (), num_ctas=20)
 
 
+@pytest.mark.parametrize("kv,d", [("bf16", 128), ("bf16", 64), ("fp8", 128), ("fp8", 64)])
+def test_shared_prefix(kv, d):
+    """Four CTAs of many steps each, pairs of tiles and single ones: the loaders, converters, product issuers
+    and the other tile's softmax wait out the limit one after the other."""
+    b = Batch(6000 + np.arange(40), hq=16, hkv=2, d=d, kv=kv, groups=([0, 40], [5990]), seed=6)
+    _given_up(_shared, b, (), ctas=(1, 3), num_ctas=4)
+
+
 @pytest.mark.parametrize("runs", [1, 5])
 def test_tensor_memory_split_kernel(runs):
     b = Batch(1000 + 37 * np.arange(24), 1 + np.arange(24) % runs, hq=16, hkv=2, seed=4)
