@@ -386,8 +386,6 @@ int decode_shared(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
   bool split_k = false, split_v = false;
   if ((st = host_prefix_map(&pk, kc, s.esz, D, Hkv, s.NB, &split_k)) != PA_OK) return st;
   if ((st = host_prefix_map(&pv, vc, s.esz, D, Hkv, s.NB, &split_v)) != PA_OK) return st;
-  if (split_k != split_v)
-    return host_fail(PA_ERR_UNSUPPORTED, "k_cache and v_cache need heads of the same contiguity");
   fill_split(&sp, s, q, bt, sl, qsl, scale, k_scale, v_scale, out, lse, opts, dev.status);
   sp.ws_unit = reinterpret_cast<int4*>(wsb + pl.unit);
   sp.ws_ml = reinterpret_cast<float2*>(wsb + pl.ml);
@@ -413,7 +411,7 @@ int decode_shared(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
   hp.num_pages = sp.num_pages;
   hp.G = sp.G;
   hp.Hkv = sp.Hkv;
-  hp.split_boxes = split_k;
+  hp.split_boxes = (split_k ? 1 : 0) | (split_v ? 2 : 0);
   hp.ctas = pl.grid;
   hp.own_ctas = pl.split.grid;
   // Both grids are then one CTA an SM at most, the plan's shares add up to the SMs, and the

@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(PrefixGeo<D, FP8>::THREADS, 1)
       const CUtensorMap* const map = is_v ? &tmap_v : &tmap_k;
       // boxes, a lane each: a page, or (split boxes: heads that are not contiguous) eight
       // slots and 64 features of one
-      const int per = !FP8 && NH == 2 && p.split_boxes ? 4 : 1;
+      const int per = !FP8 && NH == 2 && ((p.split_boxes >> is_v) & 1) ? 4 : 1;
       const int pg = lane / per, part = lane - pg * per;
       const uint32_t bytes = (FP8 ? 16u * D : PAGE) / per;
       const uint32_t to = FP8 ? base + GG::OFF_RAW + pg * bytes : ring0 + pg * PAGE + part * 1024u;

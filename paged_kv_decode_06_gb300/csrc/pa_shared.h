@@ -84,7 +84,7 @@ struct SharedParams {
   int32_t beside;             // they run side by side on `ctas` SMs
   int32_t step_cost, page_cost, unit_cost;   // time of a step, a sequence's page and a sequence, for one head on one SM
   int32_t alone_cost;         // nothing is shared that takes less on an SM
-  int32_t split_boxes;        // 128 features, bf16: heads are not contiguous, pages come in four boxes
+  int32_t split_boxes;        // 128 features, bf16, bit 0 for K, 1 for V: heads are not contiguous, pages come in four boxes
   float scale_log2;
   uint64_t wait_ns;
   int32_t give_up_cta;        // testing aid: the softmax of this CTA's first slot gives up at once (-1 = off)
