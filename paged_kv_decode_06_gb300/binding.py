@@ -517,6 +517,7 @@ def _with_workspace(options, shape, device, plan=paged_attn_q4_plan):
     o = PaOptions()
     if options is not None:
         ctypes.pointer(o)[0] = options
+        o._source = options                          # (the copy points to its token scales' descriptors)
     # every option that a plan's bytes depend on (token scales ride in the ring's stages)
     key = (plan, device.index, shape, o.num_ctas, o.min_pages_per_cta, o.heads_per_cta, o.page_pairing, o.use_tcgen05,
            bool(o.k_token_scales), bool(o.v_token_scales))

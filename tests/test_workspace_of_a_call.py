@@ -1,5 +1,9 @@
 """The workspace that a decode call takes where its options have none: its size is kept
-by everything it depends on (no GPU: a plan that stands in for the library's)."""
+by everything it depends on (no GPU: a plan that stands in for the library's).
+The descriptors of token scales live as long as the options that point to them."""
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -34,3 +38,15 @@ def test_a_size_is_kept_for_its_own_options(kw, first):
     calls = [None, binding.make_options(**kw)]
     for o in calls[::-1] if first else calls:
         assert _bytes(o) == _plan(1, 2, 3, options=o)["workspace_bytes"]
+
+
+def test_the_token_scales_descriptors_live_as_long_as_a_calls_options():
+    scales = torch.zeros(1, 2, 16)
+    o = binding.make_options(k_token_scales=scales, v_token_scales=scales)
+    kept = [weakref.ref(d) for d in o._tok_descs]
+    mine, ws = binding._with_workspace(o, (1, 2, 3), CPU, _plan)
+    del o
+    binding._DESC_CACHE.clear()                      # (another place that may keep them for a while)
+    gc.collect()
+    assert all(d() is not None for d in kept)
+    assert mine.k_token_scales.contents.data == scales.data_ptr()
