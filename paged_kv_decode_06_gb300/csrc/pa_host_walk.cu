@@ -15,6 +15,7 @@ namespace {
 constexpr int kPageTokens = 16;
 constexpr int kMaxRows = 64;                       // query rows per KV head
 constexpr int kMaxCtas = 1 << 14;
+static_assert(kMaxCtas < 1 << kReadyBits, "the split kernel's CTAs stand below a call's number");
 constexpr int64_t kMaxBlocks = (int64_t(1) << 27) - 64;   // positions stay below 2^31 - 1024
 
 size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -309,7 +310,7 @@ Costs costs_of(int64_t D, bool fp8) {
 struct SharedPlan {
   HostSplitPlan split;
   int grid;                      // of the prefix kernel
-  size_t skip, group_of, groups, totals, pre_ml, pre_o, unit, ml, o, bytes;
+  size_t skip, ready, group_of, groups, totals, pre_ml, pre_o, unit, ml, o, bytes;
 };
 
 // Grids and the workspace of a call.
@@ -327,6 +328,7 @@ int plan_shared(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int kv
     return here;
   };
   p.skip = take(4 * static_cast<size_t>(B));
+  p.ready = take(sizeof(uint64_t));
   p.group_of = take(4 * static_cast<size_t>(B));
   p.groups = take(sizeof(SharedGroup) * static_cast<size_t>(B));
   p.totals = take(sizeof(SharedTotals));
@@ -431,6 +433,10 @@ int decode_shared(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
   hp.seq_group = reinterpret_cast<int32_t*>(wsb + pl.group_of);
   hp.groups = reinterpret_cast<SharedGroup*>(wsb + pl.groups);
   hp.totals = reinterpret_cast<SharedTotals*>(wsb + pl.totals);
+  hp.ready = reinterpret_cast<uint64_t*>(wsb + pl.ready);
+  // (odd multiples: no two calls have the same 48 bits, and few look like what a workspace holds)
+  static uint64_t calls = 0;
+  hp.call = (++calls * 0x9E3779B97F4A7C15ull) & ((uint64_t(1) << (64 - kReadyBits)) - 1);
   hp.ws_ml = reinterpret_cast<float2*>(wsb + pl.pre_ml);
   hp.ws_o = reinterpret_cast<float*>(wsb + pl.pre_o);
 
@@ -441,7 +447,9 @@ int decode_shared(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
   mp.totals = hp.totals;
   mp.pre_ml = hp.ws_ml;
   mp.pre_o = hp.ws_o;
-  sp.own_ctas = &hp.totals->own_ctas;
+  mp.ready = hp.ready;
+  sp.ready = hp.ready;
+  sp.call = hp.call;
 
   Events ev;
   if ((st = events_of(opts, stream, &ev)) != PA_OK) return st;

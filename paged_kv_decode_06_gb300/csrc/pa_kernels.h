@@ -7,6 +7,11 @@
 
 namespace pa {
 
+// Shared prefixes: the split kernel runs beside the prefix kernel and so waits for neither.
+// The plan's last store, of one word, tells it that the plan is there: the call's number, and
+// in the low bits the CTAs that take the sequences' own pages.  The merge takes the word back.
+constexpr int kReadyBits = 16;
+
 struct SplitParams {
   // query / outputs
   const uint16_t* q;        // bf16 [T, Hq, D], head stride D
@@ -81,11 +86,12 @@ struct SplitParams {
   // windows with first tokens that stay visible (Walk::kFirst)
   int32_t first_tokens;
   // sequences behind a shared prefix (Walk::kOwn): pages each skips (int32 [B]), the row of
-  // ws_ml / ws_o from which rows of whole units stand by (token, query head), and the number
-  // of CTAs that take part (on the device)
+  // ws_ml / ws_o from which rows of whole units stand by (token, query head), the word that
+  // says that the plan is there, and the call's number
   const int32_t* skip;
   int64_t whole_row0;
-  const int32_t* own_ctas;
+  const uint64_t* ready;
+  uint64_t call;
 };
 
 struct MergeParams {
@@ -123,6 +129,7 @@ struct MergeRowsParams : MergeParams {
   const int32_t* seq_group;
   const SharedGroup* groups;
   const SharedTotals* totals;
+  uint64_t* ready;
   const float2* pre_ml;
   const float* pre_o;
 };

@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(kRowThreads) pa_merge_rows_kernel(const MergeR
   constexpr bool kShared = WALK == Walk::kOwn;
   grid_dependency_wait();
   grid_launch_dependents();
+  if (kShared && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.ready = 0;   // (a graph's next replay has the same number)
   const int lane = threadIdx.x % TPR;
   const int row = TPR == 32 ? blockIdx.y * (kRowThreads / 32) + threadIdx.x / 32 : blockIdx.y;
   const int u = blockIdx.x;

@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kPlanThreads) pa_shared_plan_kernel(const Shar
   }
   if (alone)
     for (int g = tid; g < NG; g += threads) p.groups[g] = SharedGroup{};
+  __syncthreads();                                // (all of it before the release at the end)
   if (warp != 0) return;
   // The groups' places, 32 at a time.
   int64_t steps = 0, rows = 0;
@@ -201,7 +202,8 @@ __global__ void __launch_bounds__(kPlanThreads) pa_shared_plan_kernel(const Shar
   p.totals->steps = steps;
   p.totals->rows = rows;
   p.totals->ctas = n;
-  p.totals->own_ctas = p.beside ? max(1, min(p.own_ctas, p.ctas - n)) : p.own_ctas;
+  const int own = p.beside ? max(1, min(p.own_ctas, p.ctas - n)) : p.own_ctas;
+  store_release(p.ready, (p.call << kReadyBits) | static_cast<uint64_t>(own));
 }
 
 // ------------------------------------------------------------- prefix kernel

@@ -45,7 +45,6 @@ struct SharedTotals {
   int64_t steps;
   int64_t rows;
   int32_t ctas;         // CTAs that take the steps
-  int32_t own_ctas;     // CTAs that take the sequences' own pages
 };
 
 __host__ __device__ inline bool shared_single(const SharedGroup& g, int pair) {
@@ -94,6 +93,8 @@ struct SharedParams {
   int32_t* seq_group;         // [B] its group, -1: none
   SharedGroup* groups;
   SharedTotals* totals;
+  uint64_t* ready;
+  uint64_t call;              // number of this call, never 0
   // ... and by the prefix kernel: partial rows
   float2* ws_ml;
   float* ws_o;

@@ -688,11 +688,18 @@ __global__ void __launch_bounds__(kSplitMaxThreads, 1)
   const int B = p.num_seqs;
   int most = gridDim.x;
   if constexpr (WALK == Walk::kOwn) {
-    // Runs beside the kernel of the shared part: that kernel lets this one start once it has
-    // seen the plan's kernel complete, and everything read here was there before.  (The fence
-    // drops what this SM may still hold of it from before.)  CTA 0 waits for it at the end.
-    __threadfence();
-    most = min(most, __ldcg(p.own_ctas));
+    // Runs beside the kernel of the shared part, which lets this one start once it has seen
+    // the plan's kernel complete.  That start orders no memory; the plan's last store does,
+    // which each thread reads here: what the plan wrote and saw (all that came before this
+    // call) is seen after it.  Without this call's number the kernels wait for one another.
+    // CTA 0 waits for the shared part at its end.
+    uint64_t ready = load_acquire(p.ready);
+    if (ready >> kReadyBits != p.call) {
+      grid_dependency_wait();
+      ready = load_acquire(p.ready);
+    }
+    if (warp == 0) fence_proxy_async_global();
+    most = min(most, static_cast<int>(ready & ((1u << kReadyBits) - 1)));
     if (static_cast<int>(blockIdx.x) >= most) return;
   }
   if (tid == 0) {

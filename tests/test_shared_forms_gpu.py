@@ -67,3 +67,45 @@ def test_every_layout_of_keys_beside_every_one_of_values(kv, d, form):
                 first = got
                 b.check(*got)
             assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+
+
+@form
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_replays_over_new_lists(kv, form):
+    """A captured call whose lists, lengths, tables and queries change between its replays: every kernel of it works
+    on this replay's plan.  The word that says that the plan is there (behind the skipped pages) is taken back."""
+    lens = np.concatenate([1200 + 5 * np.arange(60), [40] * 4])
+    batches = [Batch(lens, hq=16, hkv=4, d=64, kv=kv, groups=g, seed=7)
+               for g in (([0, 30, 60], [1190, 1000]), ([10, 50, 60], [1195, 160]), ([0, 60, 64], [700, 0]))]
+    assert all((x.lens == lens).all() and x.bt.shape == batches[0].bt.shape for x in batches)
+    pages = max(x.k.shape[0] for x in batches)
+    dev = batches[0].on_gpu()
+    for x in (1, 2):
+        dev[x] = torch.zeros(pages, *dev[x].shape[1:], dtype=dev[x].dtype, device="cuda")
+    lists = [_i32([0, 0, 0]), _i32([0, 0])]
+    out, lse = batches[0].buffers()
+    code = binding.PA_FP8_E4M3 if kv == "fp8" else binding.PA_BF16
+    n = binding.paged_attn_shared_workspace_size(64, 64, 16, 4, 64, code, 1, batches[0].options(**FORMS[form]))
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    call = binding.prepare_decode_shared(*dev, 1, *lists, batches[0].scale, batches[0].ks, batches[0].vs, out=out, lse=lse,
+                                         options=batches[0].options(workspace=ws.data_ptr(), workspace_bytes=n, **FORMS[form]))
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    word = ws[256:264].view(torch.int64)
+    for again in range(3):
+        for b in batches:
+            new = b.on_gpu() + [_i32(b.groups[0]), _i32(b.groups[1])]
+            for x, y in zip(dev + lists, new):
+                if y is not None:
+                    x[:y.shape[0]].copy_(y)
+            out.fill_(7.0)
+            graph.replay()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert int(word) == 0 and ws[:256].view(torch.int32).any()
+            if again == 0:
+                b.check(out, lse)
+                b.got = out.clone(), lse.clone()
+            assert torch.equal(out, b.got[0]) and torch.equal(lse, b.got[1])
