@@ -66,6 +66,7 @@ struct DeviceState {
   bool ready = false;
   int num_sms = 0;
   int smem_optin = 0;
+  cudaError_t shared_prefix = cudaSuccess;   // the prefix kernel's set-up
   uint32_t* status = nullptr;
   void* ws = nullptr;
   size_t ws_bytes = 0;
@@ -116,7 +117,8 @@ int device_state(DeviceState** out, int* dev_out) {
     if ((e = pa::set_split_smem_limits_first(s.smem_optin)) != cudaSuccess ||
         (e = pa::set_split_smem_limits_own(s.smem_optin)) != cudaSuccess)
       return cuda_fail(e, "cudaFuncSetAttribute(split over a walk with a hole)");
-    if ((e = pa::set_shared_smem_limits()) != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(shared prefix)");
+    // (a build whose prefix kernel cannot run refuses the shared calls, and only these)
+    if ((s.shared_prefix = pa::set_shared_smem_limits()) != cudaSuccess) cudaGetLastError();
     pa::init_cache_write_occupancy();
     void* ptr = nullptr;
     if ((e = cudaGetSymbolAddress(&ptr, g_status_word)) != cudaSuccess)
@@ -1068,6 +1070,7 @@ int host_device(HostDevice* out) {
   out->num_sms = ds->num_sms;
   out->smem_optin = ds->smem_optin;
   out->status = ds->status;
+  out->shared_prefix = ds->shared_prefix;
   return PA_OK;
 }
 int host_workspace(const pa_options_t* opts, size_t bytes, cudaStream_t stream, const char* reserve_fn, void** ws) {

@@ -29,6 +29,7 @@ struct HostDevice {
   int num_sms;
   int smem_optin;      // dynamic shared memory a kernel may ask for
   uint32_t* status;    // device status word
+  cudaError_t shared_prefix;   // whether the prefix kernel can run
 };
 
 // Serialises the library's host state.  Hold it across host_device,

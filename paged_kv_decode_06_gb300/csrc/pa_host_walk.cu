@@ -316,6 +316,7 @@ struct SharedPlan {
 // Grids and the workspace of a call.
 int plan_shared(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int kv_dtype, int max_qlen,
                 const pa_options_t* opts, const HostDevice& dev, SharedPlan* out) {
+  if (dev.shared_prefix != cudaSuccess) return host_cuda_fail(dev.shared_prefix, "set-up of the shared prefix kernel");
   SharedPlan p = {};
   const int st = host_split_plan(static_cast<int>(B), static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(D),
                                  kv_dtype, max_qlen, opts, 4, dev, &p.split);
