@@ -200,7 +200,6 @@ __global__ void __launch_bounds__(kPlanThreads) pa_shared_plan_kernel(const Shar
   }
   if (n > steps) n = static_cast<int>(steps);
   p.totals->steps = steps;
-  p.totals->rows = rows;
   p.totals->ctas = n;
   const int own = p.beside ? max(1, min(p.own_ctas, p.ctas - n)) : p.own_ctas;
   store_release(p.ready, (p.call << kReadyBits) | static_cast<uint64_t>(own));

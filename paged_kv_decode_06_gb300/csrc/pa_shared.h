@@ -43,7 +43,6 @@ struct SharedGroup {
 
 struct SharedTotals {
   int64_t steps;
-  int64_t rows;
   int32_t ctas;         // CTAs that take the steps
 };
 

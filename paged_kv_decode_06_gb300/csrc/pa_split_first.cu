@@ -41,7 +41,6 @@ cudaError_t set_split_smem_limits_first(int smem) {
   for (int d = 64; d <= 128; d += 64)
     for (int form = 0; form < 3; ++form) {
       const Kernel k = kernel_of(d, form > 0, form == 2);
-      if (k == nullptr) continue;
       const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k),
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return e;

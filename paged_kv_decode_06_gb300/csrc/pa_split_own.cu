@@ -6,8 +6,7 @@ namespace {
 
 using Kernel = void (*)(CUtensorMap, CUtensorMap, SplitParams);
 
-Kernel kernel_of(int d, bool fp8, bool tok) {
-  if (tok) return nullptr;
+Kernel kernel_of(int d, bool fp8) {
   if (d == 128)
     return fp8 ? pa_split_kernel<128, true, false, false, Walk::kOwn>
                : pa_split_kernel<128, false, false, false, Walk::kOwn>;
@@ -21,7 +20,7 @@ Kernel kernel_of(int d, bool fp8, bool tok) {
 
 cudaError_t launch_split_own(int head_dim, bool fp8, const CUtensorMap& tk, const CUtensorMap& tv,
                               const SplitParams& p, int grid, int threads, int smem, bool pdl, cudaStream_t stream) {
-  const Kernel k = kernel_of(head_dim, fp8, p.k_tok != nullptr);
+  const Kernel k = kernel_of(head_dim, fp8);
   if (k == nullptr) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
@@ -38,9 +37,8 @@ cudaError_t launch_split_own(int head_dim, bool fp8, const CUtensorMap& tk, cons
 
 cudaError_t set_split_smem_limits_own(int smem) {
   for (int d = 64; d <= 128; d += 64)
-    for (int form = 0; form < 3; ++form) {
-      const Kernel k = kernel_of(d, form > 0, form == 2);
-      if (k == nullptr) continue;
+    for (int fp8 = 0; fp8 < 2; ++fp8) {
+      const Kernel k = kernel_of(d, fp8 != 0);
       const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k),
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (e != cudaSuccess) return e;
