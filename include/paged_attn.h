@@ -313,8 +313,8 @@ int paged_attn_shared_reserve(int32_t num_tokens, int32_t num_seqs, int32_t num_
  *   slot_mapping    int32 [T] contiguous.  Token t goes to page slot_mapping[t] / 16,
  *                   slot slot_mapping[t] % 16; a negative entry (padding) writes
  *                   nothing; an entry >= 16 * NB writes nothing and sets bit 0 of the
- *                   device status word.  Two tokens with the same slot: which one
- *                   lands is unspecified.
+ *                   device status word.  Two tokens with the same slot: what each
+ *                   element (and scale) holds is one token's, whose is unspecified.
  *   k_cache, v_cache bf16 or fp8e4m3 [NB, 16, Hkv, D]: stride[3] == 1, other
  *                   strides multiples of 16 bytes, data 16-byte aligned.  D is any
  *                   multiple of 8 up to 512 (of 16 for fp8 caches, by the stride
