@@ -194,7 +194,8 @@ __device__ __forceinline__ int page_prefix(const SplitParams& p, int window, int
       const int L = p.seq_lens[i];
       s_len[i] = L;
       s_qsl[i] = p.qsl != nullptr ? p.qsl[i] : i;
-      v = L > 0 ? (L + kPage - 1) / kPage : 0;
+      // (the second form for lengths from 2^31 - 15 on too)
+      v = L > 0 ? (WALK == Walk::kAll ? (L + kPage - 1) / kPage : (L - 1) / kPage + 1) : 0;
       if (v > p.max_blocks) {       // context longer than its block-table row: never read past the row
         atomicOr(p.err, kErrSeqLen);
         v = p.max_blocks;
