@@ -182,8 +182,9 @@ void fill_merge(MergeRowsParams* mp, const SplitParams& sp, int grid) {
   mp->whole_row0 = sp.whole_row0;
 }
 
-// Pages a CTA takes at least: two, where a few sequences do not fill the CTAs (5 short ones:
-// 10.4 us with one or two, 14.5 with four; 3 of 200 tokens, 64 / 8 heads, fp8: 15.4 and 16.6).
+// Pages a CTA takes at least: two, where a few sequences do not fill the CTAs (in a graph, 5
+// short ones: 8.5 us, 10.4 with four; 3 of 200 tokens, 64 / 8 heads, fp8: 11.8 and 13.3).  One
+// would take 7.2 and 9.3 there.
 int min_pages_of(const pa_options_t* opts) {
   return opts && opts->min_pages_per_cta > 0 ? opts->min_pages_per_cta : 2;
 }
@@ -290,9 +291,9 @@ int decode_window(const pa_tensor_t* q, const pa_tensor_t* kc, const pa_tensor_t
 // ------------------------------------------------------------ shared prefixes
 // Prefixes that are left to the sequences, where both parts run side by side (elsewhere every
 // prefix is shared): of fewer than 16 pages (200 sequences of 32 / 8 heads of 128 behind 100
-// tokens: 61 us shared, 46 not; behind 300, 52 and 68), and all of a call that would cost an
-// SM less than 2 us (4 sequences behind 1000 tokens: 21.1 and 23 us; of 2 heads of 64, 21 and
-// 19.3).
+// tokens, in a graph: 99 us shared, 52 not; behind 300, 62 and 73), and all of a call that
+// would cost an SM less than 2 us (4 sequences behind 1000 tokens: 15.8 and 16.7 us, of 2 heads
+// of 64, 14.3 and 14.6; of those behind 100, 14.2 and 13.2).
 constexpr int kMinSharedPages = 16;
 constexpr int kAloneCost = 2000;          // ns, as below
 // What the plan cuts the SMs by (nanoseconds on one SM).  Measured with 4 and 128 of 152 SMs

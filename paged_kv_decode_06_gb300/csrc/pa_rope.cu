@@ -14,7 +14,7 @@
 // A thread takes one chunk of 2 W features of a head (W pairs, or 2 W features that
 // do not rotate) for one or more heads of a token: the angles are loaded once for
 // all of them.  Bound by memory: 16384 tokens of 32 / 8 heads of 128, fp8 cache, 378 MB,
-// take 65 us, 86 % of the rate of a copy (bf16 cache 65.5 us, 93 %).
+// take 64 us in a graph, 87 % of the rate of a copy (bf16 cache, 411 MB, 62 us, 98 %).
 #include <algorithm>
 #include <cmath>
 
@@ -29,8 +29,8 @@ namespace {
 constexpr int kMaxAxes = 3;
 constexpr int kThreads = 256;
 constexpr int kMaxHeadDim = 512;
-// Heads of a thread on the way.  With four CTAs an SM three are enough (16384 tokens, fp8: 67.2
-// us, 67.7 with four; 68.4 and 69.8 with three CTAs).
+// Heads of a thread on the way.  With four CTAs an SM three are enough (16384 tokens, fp8: 64.2
+// us, 64.4 with four; with three CTAs 67.2 for three, 66.7 for four).
 constexpr int kDepth = 3;
 
 struct RopeParams {
@@ -440,8 +440,9 @@ int rope_cache_write(const pa_tensor_t* query, const pa_tensor_t* key, const pa_
   const int64_t heads = Hq + 2 * Hkv;
   // Heads a thread: enough threads for an SM's 512 or so, then more heads for each, so that
   // what waits in turn (positions, then angles) is paid once for them, up to 12 (16384 tokens
-  // of 48 heads: 69 us for 12, 79 for 8, 81 for 24, 152 for one; 500 tokens: 8.3 us for 5,
-  // 10.3 for one).
+  // of 48 heads, fp8: 64 us for 12, 66 for 8, 68 for 24, 149 for one; 500 tokens: 6.5 us for
+  // 2, 7.0 for one).  With 4-byte accesses (24 features rotate) 24 heads would take 105 us,
+  // 12 take 114 (bf16 85 and 94).
   const int64_t threads = T * heads * p.chunks;
   const int64_t turns = std::min<int64_t>(std::min<int64_t>(heads, 12), threads / (dev.num_sms * int64_t(512)));
   const bool many = turns > 1;

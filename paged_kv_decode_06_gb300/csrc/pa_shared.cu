@@ -190,7 +190,8 @@ __global__ void __launch_bounds__(kPlanThreads) pa_shared_plan_kernel(const Shar
   if (lane != 0) return;
   // The SMs for each part, in proportion to its work; some more for the sequences' own pages,
   // whose many short walks pay more for memory the longer the other part runs, and four at
-  // least (8 sequences of 500 tokens behind 65536: 57 us with one, 46 with four, 48 with 28).
+  // least (8 sequences of 500 tokens behind 65536, in a graph: 50 us with one, 40 with four, 43
+  // with 28).
   int n = p.ctas;
   if (cost.x > 0.f && steps > 0) {
     const float a = static_cast<float>(steps) * p.step_cost, b = cost.x * p.Hkv;
